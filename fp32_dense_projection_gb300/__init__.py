@@ -14,6 +14,15 @@ first call raises.
   router_fwd / router_dgrad / router_wgrad: the same on FP32 operands through
   BF16x3 emulation, FP32 output.
 
+  dp_gemm_{fwd,dgrad,wgrad}_grouped
+                           rows sorted by expert times their expert's weights, ragged
+                           groups given by offsets on the device
+  fp8_quantize             8-bit floating point with a scale per 128 values
+  dp_gemm_{fwd,dgrad,wgrad}_fp8
+                           the three products of operands quantised so
+  AdamW                    the weights' update over many tensors in one launch, moments in
+                           32 or 8 bits
+
 Outputs are bf16 (``out_dtype=torch.bfloat16``) or fp32 for the BF16 ops.  An
 ``out=`` tensor may be a column slice of a wider buffer (padded row stride).
 """
@@ -93,6 +102,8 @@ def lib():
         L.dp_gemm_bwd.argtypes = [P, I, P, I, P, I, P, I, S, P, I, S, I, I, I, S, P, Z, P]
         L.dp_plan_query_bwd.argtypes = [I, I, I, S, S, S, ctypes.POINTER(BwdPlanInfo)]
         L.dp_workspace_size_bwd.argtypes = [I, I, I, S, S, S, ctypes.POINTER(ctypes.c_size_t)]
+        for m in (grouped, fp8, adamw):
+            m._bind(L)
         L.dp_init.argtypes = [S]
         L.dp_device_error.argtypes = [S]
         L.dp_status_string.argtypes = [S]
@@ -506,3 +517,9 @@ def dp_gemm_wgrad_noalloc(dY, X, out, out_dtype=None, deterministic=True, stream
                     DP_OUT_F32 if out_f32 else DP_OUT_BF16, int(bool(deterministic)), _stream(dY.device, stream))
     _check(status, "dp_gemm_wgrad_noalloc")
     return out
+
+
+from . import adamw, fp8, grouped  # noqa: E402  (they use the definitions above)
+from .adamw import AdamW  # noqa: E402
+from .fp8 import dp_gemm_dgrad_fp8, dp_gemm_fwd_fp8, dp_gemm_wgrad_fp8, fp8_quantize  # noqa: E402
+from .grouped import dp_gemm_dgrad_grouped, dp_gemm_fwd_grouped, dp_gemm_wgrad_grouped  # noqa: E402

@@ -1,0 +1,324 @@
+// AdamW over many tensors in one launch, first and second moments in 32 or 8 bits.
+//
+//   g' = g * grad_scale
+//   m  = beta1 m + (1 - beta1) g',      v = beta2 v + (1 - beta2) g'^2
+//   p  = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+//
+// in FP32, each operation rounded once (no contraction into fused multiply-adds), whatever
+// the storage types; the parameter is rounded once to its type, and its optional BF16 copy
+// (the working weight of the GEMMs) from the rounded parameter.
+//
+// 8-bit moments: 128 consecutive elements of a tensor share a scale.  m is held as E4M3
+// codes of m / s with s = max|m| / 448.  sqrt(v), not v, is held the same way: the root
+// halves the exponents' range, so E4M3's 2^17.8 covers v over 2^35; a v above zero never
+// becomes zero (the smallest code is kept), since a lost v would blow up m / sqrt(v).
+// A code's rounding is up to 1/16 of the value; a second moment that moves by less than
+// half a code relative to its block's maximum keeps its code.
+//
+// Bound: HBM bytes (16 to 30 per element).  A CTA takes chunks of 2048 elements, a
+// thread 8 consecutive ones: every load of the chunk is in flight before the first use,
+// and a block's maximum is a shuffle reduction over 16 lanes.  The tensors' table travels
+// as a kernel parameter: no copy to the device, no state between calls.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "api_internal.h"
+#include "ptx.cuh"
+
+namespace dp {
+namespace {
+
+constexpr int kBlockElems = 128;   // 8-bit moments: elements per scale
+constexpr int kChunkElems = 2048;  // elements per CTA step (256 threads x 8)
+constexpr float kTop = 448.0f, kTinyMax = 1e-30f, kSmallest = 0.001953125f;  // E4M3: largest, smallest > 0
+
+struct Entry {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  uint16_t* copy;
+  int64_t n;
+  int32_t flags;  // bit 0: p BF16, bit 1: g BF16, bit 2: every pointer 16-byte aligned
+};
+
+template <int MAX>
+struct Table {
+  Entry e[MAX];
+  int64_t chunk0[MAX + 1];  // first chunk of each tensor
+  int32_t count;
+  float beta1, one_beta1, beta2, one_beta2, eps, keep, root_scale, lr;
+  float grad_scale;
+  const float* grad_scale_ptr;
+};
+
+__device__ __forceinline__ float bf16_at(uint32_t w, int half) {
+  return __uint_as_float(half ? (w & 0xFFFF0000u) : (w << 16));
+}
+
+// Eight values of a thread, from aligned storage or one by one (n of them exist).
+__device__ __forceinline__ void load8(const void* base, int64_t at, bool bf16, bool fast, int n, float (&x)[8]) {
+  if (fast) {
+    if (bf16) {
+      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = bf16_at(u[j >> 1], j & 1);
+    } else {
+      const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+      const float4 a = __ldcs(f), b = __ldcs(f + 1);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    x[j] = 0.0f;
+    if (j < n)
+      x[j] = bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[at + j]) << 16)
+                  : static_cast<const float*>(base)[at + j];
+  }
+}
+
+__device__ __forceinline__ void store8(void* base, int64_t at, bool bf16, bool fast, int n, const float (&x)[8]) {
+  if (fast) {
+    if (bf16) {
+      __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at),
+             make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+    } else {
+      float4* f = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+      __stcs(f, make_float4(x[0], x[1], x[2], x[3]));
+      __stcs(f + 1, make_float4(x[4], x[5], x[6], x[7]));
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) {
+      if (bf16)
+        static_cast<uint16_t*>(base)[at + j] = static_cast<uint16_t>(pack_bf16x2(x[j], 0.0f) & 0xFFFFu);
+      else
+        static_cast<float*>(base)[at + j] = x[j];
+    }
+}
+
+__device__ __forceinline__ uint2 load_codes(const void* base, int64_t at, bool fast, int n) {
+  const uint8_t* p = static_cast<const uint8_t*>(base) + at;
+  if (fast) return __ldcs(reinterpret_cast<const uint2*>(p));
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) w[j >> 2] |= static_cast<uint32_t>(p[j]) << (8 * (j & 3));
+  return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void store_codes(void* base, int64_t at, bool fast, int n, uint2 w) {
+  uint8_t* p = static_cast<uint8_t*>(base) + at;
+  if (fast) {
+    __stcs(reinterpret_cast<uint2*>(p), w);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) p[j] = static_cast<uint8_t>((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+}
+
+__device__ __forceinline__ void decode4(uint32_t w, float s, float* x) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t f16x2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f16x2) : "h"(static_cast<uint16_t>(w >> (16 * h))));
+    float lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(f16x2));
+    x[2 * h] = __fmul_rn(lo, s);
+    x[2 * h + 1] = __fmul_rn(hi, s);
+  }
+}
+
+__device__ __forceinline__ uint32_t encode4(const float* x) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1]), "f"(x[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// max |x| over the 16 lanes of a block, with its lower bound; NaN counts as the largest.
+__device__ __forceinline__ float block_max(const float (&x)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float a = __uint_as_float(m);
+  return a < kTinyMax ? kTinyMax : a;
+}
+
+template <int MAX, bool EIGHT>
+__global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Table<MAX> t) {
+  const float gs = t.grad_scale_ptr ? __fmul_rn(t.grad_scale, __ldg(t.grad_scale_ptr)) : t.grad_scale;
+  const int64_t chunks = t.chunk0[t.count];
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    int lo = 0, hi = t.count - 1;  // the last tensor whose first chunk is <= c
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (t.chunk0[mid] <= c)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const Entry& e = t.e[lo];
+    const int64_t at = (c - t.chunk0[lo]) * kChunkElems + static_cast<int64_t>(threadIdx.x) * 8;
+    const int64_t left = e.n - at;
+    const int n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
+    const bool fast = (e.flags & 4) != 0 && n == 8;
+    const bool p16 = (e.flags & 1) != 0, g16 = (e.flags & 2) != 0;
+    float p[8], g[8], m[8], v[8];
+    load8(e.p, at, p16, fast, n, p);
+    load8(e.g, at, g16, fast, n, g);
+    const int64_t blk = at / kBlockElems;
+    if (EIGHT) {
+      const uint2 mq = load_codes(e.m, at, fast, n), vq = load_codes(e.v, at, fast, n);
+      const float ms = n > 0 ? e.ms[blk] : 0.0f, vs = n > 0 ? e.vs[blk] : 0.0f;
+      decode4(mq.x, ms, m);
+      decode4(mq.y, ms, m + 4);
+      decode4(vq.x, vs, v);
+      decode4(vq.y, vs, v + 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
+    } else {
+      load8(e.m, at, false, fast, n, m);
+      load8(e.v, at, false, fast, n, v);
+    }
+    float root[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = __fmul_rn(g[j], gs);
+      m[j] = __fadd_rn(__fmul_rn(m[j], t.beta1), __fmul_rn(x, t.one_beta1));
+      v[j] = __fadd_rn(__fmul_rn(v[j], t.beta2), __fmul_rn(__fmul_rn(x, x), t.one_beta2));
+      root[j] = __fsqrt_rn(v[j]);
+      const float u = __fdiv_rn(m[j], __fadd_rn(__fmul_rn(root[j], t.root_scale), t.eps));
+      p[j] = __fsub_rn(__fmul_rn(p[j], t.keep), __fmul_rn(u, t.lr));
+    }
+    store8(e.p, at, p16, fast, n, p);
+    if (e.copy) store8(e.copy, at, true, fast, n, p);
+    if (EIGHT) {
+      if (n < 8) {  // elements past the end are no part of the block's maximum
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j >= n) m[j] = root[j] = 0.0f;
+      }
+      const float ma = block_max(m), va = block_max(root);
+      const float mf = __fdiv_rn(kTop, ma), vf = __fdiv_rn(kTop, va);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[j] = __fmul_rn(m[j], mf);
+        const float y = __fmul_rn(root[j], vf);
+        root[j] = root[j] > 0.0f && y < kSmallest ? kSmallest : y;
+      }
+      store_codes(e.m, at, fast, n, make_uint2(encode4(m), encode4(m + 4)));
+      store_codes(e.v, at, fast, n, make_uint2(encode4(root), encode4(root + 4)));
+      if ((threadIdx.x & 15) == 0 && n > 0) {
+        e.ms[blk] = __fdiv_rn(ma, kTop);
+        e.vs[blk] = __fdiv_rn(va, kTop);
+      }
+    } else {
+      store8(e.m, at, false, fast, n, m);
+      store8(e.v, at, false, fast, n, v);
+    }
+  }
+}
+
+template <int MAX, bool EIGHT>
+cudaError_t launch_adamw(const dp_adamw_tensor* t, int64_t count, const dp_adamw_hyper& h, int sm_count,
+                         cudaStream_t stream) {
+  static_assert(sizeof(Table<MAX>) <= 32764, "kernel parameters");
+  for (int64_t first = 0; first < count; first += MAX) {
+    Table<MAX> tab;
+    const int n = static_cast<int>(std::min<int64_t>(MAX, count - first));
+    int64_t chunks = 0;
+    for (int i = 0; i < n; ++i) {
+      const dp_adamw_tensor& x = t[first + i];
+      Entry& e = tab.e[i];
+      e.p = x.param;
+      e.g = x.grad;
+      e.m = x.exp_avg;
+      e.v = x.exp_avg_sq;
+      e.ms = x.exp_avg_scale;
+      e.vs = x.exp_avg_sq_scale;
+      e.copy = static_cast<uint16_t*>(x.copy);
+      e.n = x.grad == nullptr ? 0 : x.numel;
+      const bool aligned = is_aligned16(x.param) && is_aligned16(x.grad) && is_aligned16(x.exp_avg) &&
+                           is_aligned16(x.exp_avg_sq) && is_aligned16(x.copy);
+      e.flags = (x.param_bf16 ? 1 : 0) | (x.grad_bf16 ? 2 : 0) | (aligned ? 4 : 0);
+      tab.chunk0[i] = chunks;
+      chunks += (e.n + kChunkElems - 1) / kChunkElems;
+    }
+    tab.chunk0[n] = chunks;
+    if (chunks == 0) continue;
+    tab.count = n;
+    tab.beta1 = static_cast<float>(h.beta1);
+    tab.one_beta1 = static_cast<float>(1.0 - h.beta1);
+    tab.beta2 = static_cast<float>(h.beta2);
+    tab.one_beta2 = static_cast<float>(1.0 - h.beta2);
+    tab.eps = static_cast<float>(h.eps);
+    tab.keep = static_cast<float>(1.0 - h.lr * h.weight_decay);
+    tab.root_scale = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(h.beta2, static_cast<double>(h.step))));
+    tab.lr = static_cast<float>(h.lr / (1.0 - std::pow(h.beta1, static_cast<double>(h.step))));
+    tab.grad_scale = static_cast<float>(h.grad_scale);
+    tab.grad_scale_ptr = h.grad_scale_ptr;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(chunks, int64_t{sm_count} * 8));
+    adamw_kernel<MAX, EIGHT><<<grid, 256, 0, stream>>>(tab);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+}  // namespace dp
+
+extern "C" dp_status dp_adamw_step(const dp_adamw_tensor* tensors, int64_t count, int state_bits,
+                                   const dp_adamw_hyper* hyper, dp_stream stream) {
+  using namespace dp;
+  if (count < 0 || (count > 0 && tensors == nullptr) || hyper == nullptr) return DP_ERR_INVALID_ARG;
+  if (state_bits != 8 && state_bits != 32) return DP_ERR_INVALID_ARG;
+  const dp_adamw_hyper& h = *hyper;
+  // (negated comparisons: a NaN is refused too)
+  if (!(h.lr >= 0.0) || !(h.beta1 >= 0.0 && h.beta1 < 1.0) || !(h.beta2 >= 0.0 && h.beta2 < 1.0) || !(h.eps >= 0.0) ||
+      !(h.weight_decay >= 0.0) || h.step < 1)
+    return DP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(h.grad_scale_ptr) & 3) != 0) return DP_ERR_ALIGNMENT;
+  for (int64_t i = 0; i < count; ++i) {
+    const dp_adamw_tensor& t = tensors[i];
+    if (t.numel < 0) return DP_ERR_INVALID_ARG;
+    if (t.numel == 0 || t.grad == nullptr) continue;
+    if (!t.param || !t.exp_avg || !t.exp_avg_sq) return DP_ERR_INVALID_ARG;
+    if (state_bits == 8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale)) return DP_ERR_INVALID_ARG;
+    const uintptr_t p = t.param_bf16 ? 1 : 3, g = t.grad_bf16 ? 1 : 3, s = state_bits == 8 ? 0 : 3;
+    if ((reinterpret_cast<uintptr_t>(t.param) & p) || (reinterpret_cast<uintptr_t>(t.grad) & g) ||
+        (reinterpret_cast<uintptr_t>(t.exp_avg) & s) || (reinterpret_cast<uintptr_t>(t.exp_avg_sq) & s) ||
+        (reinterpret_cast<uintptr_t>(t.exp_avg_scale) & 3) || (reinterpret_cast<uintptr_t>(t.exp_avg_sq_scale) & 3) ||
+        (reinterpret_cast<uintptr_t>(t.copy) & 1))
+      return DP_ERR_ALIGNMENT;
+  }
+  DeviceContext ctx;
+  const dp_status st = device_context(&ctx);
+  if (st != DP_OK) return st;
+  cudaStream_t str = static_cast<cudaStream_t>(stream);
+  // (a small table for few tensors: its launch carries 2 KB of parameters instead of 20)
+  cudaError_t e;
+  if (count <= 24)
+    e = state_bits == 8 ? launch_adamw<24, true>(tensors, count, h, ctx.sm_count, str)
+                        : launch_adamw<24, false>(tensors, count, h, ctx.sm_count, str);
+  else
+    e = state_bits == 8 ? launch_adamw<256, true>(tensors, count, h, ctx.sm_count, str)
+                        : launch_adamw<256, false>(tensors, count, h, ctx.sm_count, str);
+  return e == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+}

@@ -12,9 +12,11 @@
 #include <utility>
 #include <vector>
 
+#include "api_internal.h"
 #include "dp_gemm.h"
 #include "gemm_kernel.cuh"
 #include "planner.h"
+#include "promoted_gemm.cuh"
 
 namespace {
 
@@ -61,6 +63,8 @@ dp_status init_device(int dev, DeviceState** out) {
       if (e == cudaSuccess) e = set_attributes_ffma();
       if (e == cudaSuccess) e = set_attributes_split();
       if (e == cudaSuccess) e = set_attributes_reduce();
+      if (e == cudaSuccess) e = set_attributes_grouped();
+      if (e == cudaSuccess) e = set_attributes_fp8();
       if (e == cudaSuccess) e = cudaGetSymbolAddress(&fault, g_fault_word);
       if (cur != dev) cudaSetDevice(cur);
       if (e != cudaSuccess) return DP_ERR_LAUNCH;
@@ -802,6 +806,41 @@ __global__ void wait_probe_kernel(uint32_t* fault, uint64_t limit_ns, int arrive
 
 }  // namespace
 
+// ------------------------------------------- shared with the other entry points
+
+namespace dp {
+
+dp_status device_context(DeviceContext* ctx) {
+  DeviceState* d = nullptr;
+  const dp_status st = current_device(&d);
+  if (st != DP_OK) return st;
+  ctx->sm_count = d->sm_count;
+  ctx->fault = d->fault;
+  return DP_OK;
+}
+
+bool is_aligned16(const void* p) { return aligned16(p); }
+
+dp_status check_operand(const void* p, int64_t rows, int64_t cols, int64_t* ld, int esize) {
+  return check_matrix(p, rows, cols, ld, esize);
+}
+
+bool encode_operand(CUtensorMap* map, const void* ptr, CUtensorMapDataType type, int esize, int64_t rows, int64_t cols,
+                    int64_t ld, int64_t batch, int64_t bstride, uint32_t box_cols, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * esize, static_cast<cuuint64_t>(bstride) * esize};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, type, batch > 0 ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace dp
+
 // =================================================================== C ABI
 
 extern "C" {
@@ -1033,7 +1072,8 @@ dp_status dp_device_error(int clear) {
     const uint32_t zero = 0;
     if (cudaMemcpyToSymbol(g_fault_word, &zero, sizeof(zero)) != cudaSuccess) return DP_ERR_LAUNCH;
   }
-  return word ? DP_ERR_TIMEOUT : DP_OK;
+  if (word & ~kFaultOffsets) return DP_ERR_TIMEOUT;
+  return word ? DP_ERR_INVALID_ARG : DP_OK;
 }
 
 dp_status dp_wait_probe(uint64_t limit_ns, int arrive, dp_stream stream) {

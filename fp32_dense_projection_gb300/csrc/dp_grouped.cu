@@ -1,0 +1,257 @@
+// C ABI of the products grouped by expert and of the 8-bit products (declared in
+// include/dp_gemm.h): argument checks, tile width, tensor maps, one launch.  Nothing here
+// allocates device memory, copies or synchronises.
+#include <algorithm>
+#include <cstring>
+
+#include "api_internal.h"
+#include "promoted_gemm.cuh"
+
+namespace {
+
+using namespace dp;
+
+constexpr int64_t kMaxInt = 0x7FFFFFFF;
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tile width: the widest whose tiles still give every SM one.  Wide tiles read A less
+// often and keep the tensor cores fed (a 128 x 256 tile needs 96 bytes of operands per
+// cycle, a 128 x 64 tile 192); narrow ones spread a few rows' weights over the SMs.
+int tile_width(int64_t tiles_m, int64_t gn, int sm_count, int narrowest) {
+  for (int bn = 256; bn > narrowest; bn /= 2)
+    if (tiles_m * cdiv(gn, bn) >= sm_count) return bn;
+  return narrowest;
+}
+
+// Row tiles per raster group: as many rows of A as fill a share of L2 beside the weights.
+int raster_rows(int64_t k_bytes) {
+  const int64_t rows = (int64_t{48} << 20) / std::max<int64_t>(1, 128 * k_bytes);
+  return static_cast<int>(std::min<int64_t>(64, std::max<int64_t>(4, rows)));
+}
+
+dp_status zero_rows(void* out, int64_t rows, int64_t cols, int64_t ld, int esize, cudaStream_t stream) {
+  if (rows == 0) return DP_OK;
+  return cudaMemset2DAsync(out, static_cast<size_t>(ld) * esize, 0, static_cast<size_t>(cols) * esize,
+                           static_cast<size_t>(rows), stream) == cudaSuccess
+             ? DP_OK
+             : DP_ERR_LAUNCH;
+}
+
+enum GroupedOp { kFwd, kDgrad, kWgrad };
+
+// fwd:   a = X [T][K],  b = W,        out = Y [T][N]
+// dgrad: a = dY [T][N], b = W,        out = dX [T][K]
+// wgrad: a = dY [T][N], b = X [T][K], out = dW
+// W and dW: [E][N][K], or [E][K][N] with kn.
+dp_status run_grouped(GroupedOp op, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t bsb,
+                      const void* offsets, int offset_bits, void* out, int64_t ldo, int64_t bso, int kn, int64_t E,
+                      int64_t T, int64_t N, int64_t K, int out_f32, cudaStream_t stream) {
+  if (out_f32 != DP_OUT_BF16 && out_f32 != DP_OUT_F32) return DP_ERR_INVALID_ARG;
+  if ((kn != 0 && kn != 1) || E < 0 || T < 0 || N < 1 || K < 1 || bsb < 0 || bso < 0) return DP_ERR_INVALID_ARG;
+  if (offset_bits != 32 && offset_bits != 64) return DP_ERR_INVALID_ARG;
+  if (N % 8 != 0 || K % 8 != 0) return DP_ERR_UNSUPPORTED;
+  if (E > kMaxExperts || T > kMaxInt - 256 || N > kMaxInt - 256 || K > kMaxInt - 256) return DP_ERR_UNSUPPORTED;
+  const int osize = out_f32 ? 4 : 2;
+  const int64_t a_cols = op == kFwd ? K : N;
+  const int64_t w_rows = kn ? K : N, w_cols = kn ? N : K;
+  const int64_t out_rows = op == kWgrad ? w_rows : T, out_cols = op == kFwd ? N : op == kDgrad ? K : w_cols;
+  dp_status st = check_operand(a, T, a_cols, &lda, 2);
+  if (st == DP_OK) st = op == kWgrad ? check_operand(b, T, K, &ldb, 2) : check_operand(b, E * w_rows, w_cols, &ldb, 2);
+  if (st == DP_OK) st = check_operand(out, op == kWgrad ? E * out_rows : out_rows, out_cols, &ldo, osize);
+  if (st != DP_OK) return st;
+  if (offsets == nullptr && E > 0) return DP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(offsets) & (offset_bits / 8 - 1)) != 0) return DP_ERR_ALIGNMENT;
+  if (bsb == 0) bsb = w_rows * ldb;
+  if (bso == 0) bso = w_rows * ldo;
+  if (op != kWgrad && bsb * 2 % 16 != 0) return DP_ERR_ALIGNMENT;
+  if (op == kWgrad && bso * osize % 16 != 0) return DP_ERR_ALIGNMENT;
+  DeviceContext ctx;
+  if ((st = device_context(&ctx)) != DP_OK) return st;
+  if (E == 0) return op == kWgrad ? DP_OK : zero_rows(out, T, out_cols, ldo, osize, stream);
+  if (T == 0) {
+    if (op != kWgrad) return DP_OK;
+    for (int64_t e = 0; e < E; ++e)
+      if ((st = zero_rows(static_cast<char*>(out) + e * bso * osize, out_rows, out_cols, ldo, osize, stream)) != DP_OK)
+        return st;
+    return DP_OK;
+  }
+
+  PgLaunch l;
+  std::memset(&l, 0, sizeof(l));
+  PgArgs& g = l.args;
+  g.rows = static_cast<int32_t>(T);
+  g.experts = static_cast<int32_t>(E);
+  g.offsets = offsets;
+  g.offsets64 = offset_bits == 64;
+  g.out = out;
+  g.ldo = ldo;
+  g.out_gstride = bso;
+  g.out_f32 = out_f32;
+  g.fault = ctx.fault;
+  g.wait_ns = kWaitLimitNs;
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  int kind, bn;
+  int64_t tiles;
+  bool ok;
+  if (op == kWgrad) {
+    // dW[n][k] with A = dY, B = X; dW stored [K][N]: A = X, B = dY
+    const int64_t gm = w_rows, gn = w_cols;
+    kind = kGroupMM;
+    g.gm = static_cast<int32_t>(gm);
+    g.gn = static_cast<int32_t>(gn);
+    bn = tile_width(E * cdiv(gm, 128), gn, ctx.sm_count, 64);
+    g.tiles_m = static_cast<int32_t>(cdiv(gm, 128));
+    g.tiles_n = static_cast<int32_t>(cdiv(gn, bn));
+    g.group_m = 8;
+    tiles = E * g.tiles_m * g.tiles_n;
+    const void *pa = kn ? b : a, *pb = kn ? a : b;
+    const int64_t la = kn ? ldb : lda, lb = kn ? lda : ldb;
+    ok = encode_operand(&l.tmA, pa, bf16, 2, T, gm, la, 0, 0, 64, 64) &&
+         encode_operand(&l.tmB, pb, bf16, 2, T, gn, lb, 0, 0, 64, 64);
+  } else {
+    const int64_t gk = a_cols, gn = out_cols;
+    const bool b_mn = (op == kFwd) == (kn != 0);  // W's rows are contraction rows
+    kind = b_mn ? kGroupKM : kGroupKK;
+    g.gn = static_cast<int32_t>(gn);
+    g.gk = static_cast<int32_t>(gk);
+    // (the groups' sizes are known on the device only: at most one partial tile per group)
+    const int64_t tiles_m = T / 128 + std::min(E, T);
+    bn = tile_width(std::max(cdiv(T, 128), std::min(E, T)), gn, ctx.sm_count, 64);
+    g.tiles_n = static_cast<int32_t>(cdiv(gn, bn));
+    g.group_m = raster_rows(gk * 2);
+    tiles = tiles_m * g.tiles_n;
+    ok = encode_operand(&l.tmA, a, bf16, 2, T, gk, lda, 0, 0, 64, 128) &&
+         (b_mn ? encode_operand(&l.tmB, b, bf16, 2, w_rows, w_cols, ldb, E, bsb, 64, 64)
+               : encode_operand(&l.tmB, b, bf16, 2, w_rows, w_cols, ldb, E, bsb, 64, static_cast<uint32_t>(bn)));
+  }
+  if (!ok) return DP_ERR_LAUNCH;
+  if (tiles > kMaxInt) return DP_ERR_UNSUPPORTED;
+  g.idesc = idesc_bf16_f32(128, bn, kind == kGroupMM, kind != kGroupKK);
+  l.grid = static_cast<int>(std::min<int64_t>(ctx.sm_count, tiles));
+  return launch_grouped(kind, bn, l, stream) == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+}
+
+struct Scales {
+  const float* p;
+  int64_t row, blk;
+};
+
+dp_status check_scales(const Scales& s) {
+  if (s.p == nullptr || s.row < 0 || s.blk < 0) return DP_ERR_INVALID_ARG;
+  return (reinterpret_cast<uintptr_t>(s.p) & 3) != 0 ? DP_ERR_ALIGNMENT : DP_OK;
+}
+
+dp_status run_fp8(GroupedOp op, const void* a, int64_t lda, int a_fmt, Scales sa, const void* b, int64_t ldb, int b_fmt,
+                  Scales sb, void* out, int64_t ldo, int64_t T, int64_t N, int64_t K, int out_f32,
+                  cudaStream_t stream) {
+  if (out_f32 != DP_OUT_BF16 && out_f32 != DP_OUT_F32) return DP_ERR_INVALID_ARG;
+  if (a_fmt < DP_FP8_E4M3 || a_fmt > DP_FP8_E5M2 || b_fmt < DP_FP8_E4M3 || b_fmt > DP_FP8_E5M2)
+    return DP_ERR_INVALID_ARG;
+  if (T < 0 || N < 1 || K < 1) return DP_ERR_INVALID_ARG;
+  if (N % 16 != 0 || K % 16 != 0) return DP_ERR_UNSUPPORTED;
+  if (T > kMaxInt - 256 || N > kMaxInt - 256 || K > kMaxInt - 256) return DP_ERR_UNSUPPORTED;
+  const int osize = out_f32 ? 4 : 2;
+  const int64_t gm = op == kWgrad ? N : T, gn = op == kFwd ? N : K, gk = op == kFwd ? K : op == kDgrad ? N : T;
+  dp_status st = check_operand(a, T, op == kFwd ? K : N, &lda, 1);
+  if (st == DP_OK) st = op == kWgrad ? check_operand(b, T, K, &ldb, 1) : check_operand(b, N, K, &ldb, 1);
+  if (st == DP_OK) st = check_operand(out, gm, gn, &ldo, osize);
+  if (st != DP_OK) return st;
+  if (T > 0) {
+    if ((st = check_scales(sa)) != DP_OK || (st = check_scales(sb)) != DP_OK) return st;
+  }
+  DeviceContext ctx;
+  if ((st = device_context(&ctx)) != DP_OK) return st;
+  if (T == 0) return op == kWgrad ? zero_rows(out, gm, gn, ldo, osize, stream) : DP_OK;
+
+  PgLaunch l;
+  std::memset(&l, 0, sizeof(l));
+  PgArgs& g = l.args;
+  const int kind = op == kFwd ? kFp8KK : op == kDgrad ? kFp8KM : kFp8MM;
+  const int bn = tile_width(cdiv(gm, 128), gn, ctx.sm_count, kind == kFp8KK ? 64 : 128);
+  g.rows = static_cast<int32_t>(gm);
+  g.gm = static_cast<int32_t>(gm);
+  g.gn = static_cast<int32_t>(gn);
+  g.gk = static_cast<int32_t>(gk);
+  g.experts = 1;
+  g.out = out;
+  g.ldo = ldo;
+  g.out_f32 = out_f32;
+  g.tiles_m = static_cast<int32_t>(cdiv(gm, 128));
+  g.tiles_n = static_cast<int32_t>(cdiv(gn, bn));
+  g.group_m = raster_rows(gk);
+  g.idesc = idesc_fp8_f32(128, bn, kind == kFp8MM, kind != kFp8KK, a_fmt == DP_FP8_E5M2, b_fmt == DP_FP8_E5M2);
+  g.sa = sa.p;
+  g.sa_row = sa.row;
+  g.sa_blk = sa.blk;
+  g.sb = sb.p;
+  // (input gradient: the contraction runs along W's rows, so their block index is the chunk)
+  g.sb_row = op == kDgrad ? sb.blk : sb.row;
+  g.sb_blk = op == kDgrad ? sb.row : sb.blk;
+  g.fault = ctx.fault;
+  g.wait_ns = kWaitLimitNs;
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const bool ok =
+      (kind == kFp8MM ? encode_operand(&l.tmA, a, u8, 1, gk, gm, lda, 0, 0, 128, 128)
+                      : encode_operand(&l.tmA, a, u8, 1, gm, gk, lda, 0, 0, 128, 128)) &&
+      (kind == kFp8KK ? encode_operand(&l.tmB, b, u8, 1, gn, gk, ldb, 0, 0, 128, static_cast<uint32_t>(bn))
+                      : encode_operand(&l.tmB, b, u8, 1, gk, gn, ldb, 0, 0, 128, 128));
+  if (!ok) return DP_ERR_LAUNCH;
+  const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
+  if (tiles > kMaxInt) return DP_ERR_UNSUPPORTED;
+  l.grid = static_cast<int>(std::min<int64_t>(ctx.sm_count, tiles));
+  return launch_fp8(kind, bn, l, stream) == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+dp_status dp_gemm_fwd_grouped(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t bsw, int weight_kn,
+                              const void* offsets, int offset_bits, void* Y, int64_t ldy, int64_t E, int64_t T,
+                              int64_t N, int64_t K, dp_out_dtype out, dp_stream stream) {
+  return run_grouped(kFwd, X, ldx, W, ldw, bsw, offsets, offset_bits, Y, ldy, 0, weight_kn, E, T, N, K,
+                     static_cast<int>(out), static_cast<cudaStream_t>(stream));
+}
+
+dp_status dp_gemm_dgrad_grouped(const void* dY, int64_t ldg, const void* W, int64_t ldw, int64_t bsw, int weight_kn,
+                                const void* offsets, int offset_bits, void* dX, int64_t ldx, int64_t E, int64_t T,
+                                int64_t N, int64_t K, dp_out_dtype out, dp_stream stream) {
+  return run_grouped(kDgrad, dY, ldg, W, ldw, bsw, offsets, offset_bits, dX, ldx, 0, weight_kn, E, T, N, K,
+                     static_cast<int>(out), static_cast<cudaStream_t>(stream));
+}
+
+dp_status dp_gemm_wgrad_grouped(const void* dY, int64_t ldg, const void* X, int64_t ldx, const void* offsets,
+                                int offset_bits, void* dW, int64_t ldw, int64_t bsw, int weight_kn, int64_t E,
+                                int64_t T, int64_t N, int64_t K, dp_out_dtype out, dp_stream stream) {
+  return run_grouped(kWgrad, dY, ldg, X, ldx, 0, offsets, offset_bits, dW, ldw, bsw, weight_kn, E, T, N, K,
+                     static_cast<int>(out), static_cast<cudaStream_t>(stream));
+}
+
+dp_status dp_gemm_fwd_fp8(const void* Xq, int64_t ldx, dp_fp8_format x_format, const float* Xs, int64_t xs_row,
+                          int64_t xs_blk, const void* Wq, int64_t ldw, dp_fp8_format w_format, const float* Ws,
+                          int64_t ws_row, int64_t ws_col, void* Y, int64_t ldy, int64_t T, int64_t N, int64_t K,
+                          dp_out_dtype out, dp_stream stream) {
+  return run_fp8(kFwd, Xq, ldx, static_cast<int>(x_format), {Xs, xs_row, xs_blk}, Wq, ldw, static_cast<int>(w_format),
+                 {Ws, ws_row, ws_col}, Y, ldy, T, N, K, static_cast<int>(out), static_cast<cudaStream_t>(stream));
+}
+
+dp_status dp_gemm_dgrad_fp8(const void* dYq, int64_t ldg, dp_fp8_format dy_format, const float* dYs, int64_t gs_row,
+                            int64_t gs_blk, const void* Wq, int64_t ldw, dp_fp8_format w_format, const float* Ws,
+                            int64_t ws_row, int64_t ws_col, void* dX, int64_t ldx, int64_t T, int64_t N, int64_t K,
+                            dp_out_dtype out, dp_stream stream) {
+  return run_fp8(kDgrad, dYq, ldg, static_cast<int>(dy_format), {dYs, gs_row, gs_blk}, Wq, ldw,
+                 static_cast<int>(w_format), {Ws, ws_row, ws_col}, dX, ldx, T, N, K, static_cast<int>(out),
+                 static_cast<cudaStream_t>(stream));
+}
+
+dp_status dp_gemm_wgrad_fp8(const void* dYq, int64_t ldg, dp_fp8_format dy_format, const float* dYs, int64_t gs_blk,
+                            int64_t gs_col, const void* Xq, int64_t ldx, dp_fp8_format x_format, const float* Xs,
+                            int64_t xs_blk, int64_t xs_col, void* dW, int64_t ldw, int64_t T, int64_t N, int64_t K,
+                            dp_out_dtype out, dp_stream stream) {
+  return run_fp8(kWgrad, dYq, ldg, static_cast<int>(dy_format), {dYs, gs_col, gs_blk}, Xq, ldx,
+                 static_cast<int>(x_format), {Xs, xs_col, xs_blk}, dW, ldw, T, N, K, static_cast<int>(out),
+                 static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -18,6 +18,7 @@ constexpr uint32_t kFaultMmaWait = 1u << 1;
 constexpr uint32_t kFaultEpilogueWait = 1u << 2;
 constexpr uint32_t kFaultDrainWait = 1u << 3;
 constexpr uint32_t kFaultProbeWait = 1u << 4;  // the wait probe (dp_wait_probe) gave up
+constexpr uint32_t kFaultOffsets = 1u << 5;    // group offsets that decrease or leave [0, T] (clamped by the kernel)
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -269,6 +269,121 @@ dp_status router_wgrad_ex(const float* dY, int64_t ldg, const float* X, int64_t 
                           float* dW, int64_t ldw, int64_t T, int64_t N, int64_t K, int deterministic,
                           void* workspace, size_t workspace_bytes, dp_stream stream);
 
+/* ------------------------------------------- products grouped by expert (BF16) */
+/* The projections of a layer of experts: the T rows of X (or dY) are sorted by expert,
+ * expert e owns the rows [offsets[e], offsets[e + 1]), and each row meets its expert's
+ * weights:
+ *   forward          Y[t]  = X[t] W_e^T          W_e: N x K
+ *   input gradient   dX[t] = dY[t] W_e
+ *   weight gradient  dW_e  = sum over the expert's rows of dY[t]^T X[t]
+ * No counterpart on the pages; operands, outputs and errors as the calls above.
+ * offsets: E + 1 values in DEVICE memory, int32 or int64 (offset_bits), never read by the
+ *   host: the call needs no synchronisation and can be captured before the router's choice
+ *   is known.  They should not decrease and lie in [0, T].  Values that do not are clamped
+ *   (to [0, T] and to the running maximum) and reported as DP_ERR_INVALID_ARG by
+ *   dp_device_error().
+ * Rows before offsets[0] and from offsets[E] on (padding of a buffer with room to spare)
+ *   belong to no expert: their output rows are zero and no weight gradient sees them.
+ *   Infinities and NaN there, or in another expert's rows, reach no other output.
+ * Experts without rows: dW_e = 0.
+ * weight_kn: W_e and dW_e are [N][K] (0) or [K][N] (1) matrices, ldw apart by rows and bsw
+ *   apart by experts (elements; 0 = packed).
+ * FP32 accumulation in pieces of 2048 contraction elements that are added in FP32 with
+ * round-to-nearest, whatever the group's size; every output is deterministic.  One launch,
+ * no workspace.  At most 1024 experts. */
+dp_status dp_gemm_fwd_grouped(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t bsw, int weight_kn,
+                              const void* offsets, int offset_bits, void* Y, int64_t ldy,
+                              int64_t E, int64_t T, int64_t N, int64_t K, dp_out_dtype out, dp_stream stream);
+dp_status dp_gemm_dgrad_grouped(const void* dY, int64_t ldg, const void* W, int64_t ldw, int64_t bsw, int weight_kn,
+                                const void* offsets, int offset_bits, void* dX, int64_t ldx,
+                                int64_t E, int64_t T, int64_t N, int64_t K, dp_out_dtype out, dp_stream stream);
+dp_status dp_gemm_wgrad_grouped(const void* dY, int64_t ldg, const void* X, int64_t ldx,
+                                const void* offsets, int offset_bits, void* dW, int64_t ldw, int64_t bsw,
+                                int weight_kn, int64_t E, int64_t T, int64_t N, int64_t K, dp_out_dtype out,
+                                dp_stream stream);
+
+/* ------------------------------- 8-bit floating point, a scale per 128 elements */
+typedef enum dp_fp8_format {
+    DP_FP8_E4M3 = 0,          /* largest value 448 */
+    DP_FP8_E5M2 = 1           /* largest value 57344 */
+} dp_fp8_format;
+
+typedef enum dp_fp8_scaling {
+    DP_FP8_ROW = 0,           /* blocks of 128 elements of a row */
+    DP_FP8_COL = 1,           /* blocks of 128 elements of a column */
+    DP_FP8_BLOCK = 2,         /* blocks of 128 x 128 */
+    DP_FP8_BOTH = 3           /* row blocks into q, s and column blocks into q_col, s_colwise */
+} dp_fp8_scaling;
+
+/* Quantise x [rows][cols] (BF16, or FP32 with x_f32):
+ *   a = max(max |x| over the block, 1e-30), s = a / top, q = rn(x * (top / a))
+ * with top the format's largest value; the last blocks may be partial.  A block that holds a
+ * NaN gets a NaN scale, one that holds an infinity an infinite scale.
+ *   q, s          row or 128 x 128 blocks: the scale of row (or row block) r and column block
+ *                 c goes to s[r * s_row + c * s_col]
+ *   q_col, s_colwise  column blocks: row block r, column c at s_colwise[r * sc_row + c]
+ *                 (16-byte aligned rows)
+ * The unused pair may be null.  cols a multiple of 16. */
+dp_status dp_fp8_quantize(const void* x, int64_t ldx, int x_f32, int64_t rows, int64_t cols, dp_fp8_scaling scaling,
+                          dp_fp8_format format, void* q, int64_t ldq, float* s, int64_t s_row, int64_t s_col,
+                          void* q_col, int64_t ldq_col, float* s_colwise, int64_t sc_row, dp_stream stream);
+
+/* Products of quantised operands, x = q * s.  The 128-element blocks run along the
+ * contraction; each block's sum is scaled and added in FP32:
+ *   forward          Y  = X W^T   X: row blocks, W: 128 x 128 blocks
+ *   input gradient   dX = dY W    dY: row blocks (along N), W as in the forward pass (the
+ *                                 same bytes: no transposed copy)
+ *   weight gradient  dW = dY^T X  dY and X: column blocks (along T)
+ * Scales lie at any non-negative strides: row blocks at s[t * row + block * blk], 128 x 128
+ * blocks at s[row block * row + column block * col], column blocks at
+ * s[block * blk + column * col].  N, K and leading dimensions multiples of 16.  T == 0 as
+ * for the BF16 calls.  Deterministic; one launch, no workspace. */
+dp_status dp_gemm_fwd_fp8(const void* Xq, int64_t ldx, dp_fp8_format x_format, const float* Xs, int64_t xs_row,
+                          int64_t xs_blk, const void* Wq, int64_t ldw, dp_fp8_format w_format, const float* Ws,
+                          int64_t ws_row, int64_t ws_col, void* Y, int64_t ldy,
+                          int64_t T, int64_t N, int64_t K, dp_out_dtype out, dp_stream stream);
+dp_status dp_gemm_dgrad_fp8(const void* dYq, int64_t ldg, dp_fp8_format dy_format, const float* dYs, int64_t gs_row,
+                            int64_t gs_blk, const void* Wq, int64_t ldw, dp_fp8_format w_format, const float* Ws,
+                            int64_t ws_row, int64_t ws_col, void* dX, int64_t ldx,
+                            int64_t T, int64_t N, int64_t K, dp_out_dtype out, dp_stream stream);
+dp_status dp_gemm_wgrad_fp8(const void* dYq, int64_t ldg, dp_fp8_format dy_format, const float* dYs, int64_t gs_blk,
+                            int64_t gs_col, const void* Xq, int64_t ldx, dp_fp8_format x_format, const float* Xs,
+                            int64_t xs_blk, int64_t xs_col, void* dW, int64_t ldw,
+                            int64_t T, int64_t N, int64_t K, dp_out_dtype out, dp_stream stream);
+
+/* ------------------------------------------------------- AdamW over many tensors */
+typedef struct dp_adamw_tensor {
+    void* param;              /* FP32, or BF16 with param_bf16; updated in place */
+    const void* grad;         /* FP32, or BF16 with grad_bf16; null: the tensor is skipped */
+    void* exp_avg;            /* FP32, or E4M3 codes (state_bits = 8); updated in place */
+    void* exp_avg_sq;         /* FP32, or E4M3 codes of the square root */
+    float* exp_avg_scale;     /* state_bits = 8: one scale per 128 elements */
+    float* exp_avg_sq_scale;
+    void* copy;               /* BF16 copy of the updated parameter, or null */
+    int64_t numel;
+    int32_t param_bf16;
+    int32_t grad_bf16;
+} dp_adamw_tensor;
+
+typedef struct dp_adamw_hyper {
+    double lr, beta1, beta2, eps, weight_decay;
+    double grad_scale;            /* gradients are multiplied by this */
+    const float* grad_scale_ptr;  /* and, if not null, by this DEVICE value */
+    int64_t step;                 /* 1 for the first update (bias corrections) */
+} dp_adamw_hyper;
+
+/* One AdamW update of `count` dense tensors (the table is read on the host during the call):
+ *   g' = g * scale;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   p  = p (1 - lr wd) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in FP32, each operation rounded once; p is rounded once to its type.
+ * state_bits = 8: m is held as E4M3 codes with a scale max|m| / 448 for each 128 consecutive
+ * elements, and sqrt(v) likewise; a v above zero is never held as zero.  A non-finite
+ * gradient makes its element (32 bits) or its 128 elements' state (8 bits) non-finite.
+ * 16-byte aligned tensors are faster; any element alignment works.  One launch per 256
+ * tensors, no workspace. */
+dp_status dp_adamw_step(const dp_adamw_tensor* tensors, int64_t count, int state_bits, const dp_adamw_hyper* hyper,
+                        dp_stream stream);
+
 /* ------------------------------------------------------------ planning, misc */
 /* Tuning and test overrides.  They are read from the environment only in a
  * process that has DP_TUNING set when the library first plans a call; such a
@@ -391,7 +506,8 @@ dp_status dp_workspace_size_bwd(int64_t T, int64_t N, int64_t K, dp_out_dtype ou
 dp_status dp_init(int device);
 
 /* Debug read-out: synchronise the current device and report whether any kernel
- * of this library gave up waiting (DP_ERR_TIMEOUT) since the last clear.
+ * of this library gave up waiting (DP_ERR_TIMEOUT), or else was given group offsets
+ * that decrease or leave [0, T] (DP_ERR_INVALID_ARG), since the last clear.
  * `clear` != 0 resets the flag.  Not for use inside stream capture. */
 dp_status dp_device_error(int clear);
 
