@@ -86,7 +86,12 @@ struct PgCfg {
   static constexpr int STAGES = (192 * 1024) / STAGE_BYTES < 8 ? (192 * 1024) / STAGE_BYTES : 8;
   static constexpr int HALF = BN / 2;  // columns of one epilogue warp
   static constexpr int EPI_BYTES = 8 * 2048;
-  static constexpr int SCALE_BYTES = KIND == kFp8MM ? 8 * HALF * 4 : 0;
+  // 8-bit products: every epilogue warp keeps the scales of its 32 rows and of its columns
+  // (one value where a 128 x 128 block covers them) for the chunk at work and the two ahead
+  static constexpr bool COL_SCALES = KIND == kFp8MM;
+  static constexpr int SCALE_SLOTS = 3;
+  static constexpr int SCALE_FLOATS = 32 + (COL_SCALES ? HALF : 4);
+  static constexpr int SCALE_BYTES = FP8 ? 8 * SCALE_SLOTS * SCALE_FLOATS * 4 : 0;
   static constexpr int TABLE_BYTES = (ROW_GROUPS || K_GROUPS) ? 2 * (kMaxExperts + 4) * 4 : 0;
   static constexpr int NUM_BARS = 2 * STAGES + 5;
   static constexpr int TMEM_COLS = 2 * BN;
@@ -262,9 +267,45 @@ __device__ __forceinline__ void build_group_table(const PgArgs& a, int32_t* star
   __syncthreads();
 }
 
-__device__ __forceinline__ void add_scaled(float (&acc)[32], const uint32_t (&r)[32], float s) {
-#pragma unroll
-  for (int j = 0; j < 32; ++j) acc[j] = fmaf(__uint_as_float(r[j]), s, acc[j]);
+// Pairs of FP32 values in one 64-bit register: one instruction for two operations.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  return (static_cast<uint64_t>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ uint64_t pack_u32x2(uint32_t lo, uint32_t hi) { return (static_cast<uint64_t>(hi) << 32) | lo; }
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Four bytes from global to shared memory without a register; zero where !valid.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Registers move between the warpgroups: 384 x 168 at launch = 128 x 72 + 256 x 216.
+template <int N>
+__device__ __forceinline__ void regs_give() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <int BN, int KIND>
@@ -323,6 +364,9 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
   const int units = walk.units();
   const int step = static_cast<int>(gridDim.x);
 
+  // (Narrower tiles need fewer registers than every thread has at launch.)
+  if (warp < 4) {
+  if (BN == 256) regs_give<72>();
   if (warp == 0 || warp == 2) {
     // -------------------------------------------------------------- producers
     if (lane == 0) {
@@ -458,39 +502,72 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
       if (!mbar_wait(drain_bar, 0, args.wait_ns)) atomicOr(args.fault, kFaultDrainWait);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  }
+  } else {
     // -------------------------------------------------- promotion and epilogue
+    if (BN == 256) regs_take<216>();
     const int q = warp & 3, h = (warp - 4) >> 2;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * C::HALF);
     const uint32_t ebuf = ebase + static_cast<uint32_t>(warp - 4) * 2048u;
-    const uint32_t sbuf = scbase + static_cast<uint32_t>(warp - 4) * (C::HALF * 4);
+    constexpr uint32_t SLOT = C::SCALE_FLOATS * 4;
+    const uint32_t sring = scbase + static_cast<uint32_t>(warp - 4) * (C::SCALE_SLOTS * SLOT);
     int buf = 0;
     uint32_t bphase = 0;
     bool ok = true;
+    // The scales' cursor walks the same tiles and chunks two ahead of the promotion.
+    int pu = static_cast<int>(blockIdx.x), pc = 0, pslot = 0;
+    PgTile pt = {};
+    if (C::FP8 && pu < units) pt = walk.at(pu);
+    auto fetch_scales = [&]() {
+      if (pu < units) {
+        const uint32_t dst = sring + static_cast<uint32_t>(pslot) * SLOT;
+        const int pm = pt.tm * C::BM + q * 32 + lane, pn = pt.tn * BN + h * C::HALF;
+        // (rows and columns past the edges have zero operands: any finite scale will do)
+        cp_async4(dst + lane * 4, args.sa + (pm < args.gm ? pm * args.sa_row + pc * args.sa_blk : 0), pm < args.gm);
+        if (C::COL_SCALES) {
+#pragma unroll
+          for (int j = 0; j < C::HALF; j += 32) {
+            const bool in = pn + j + lane < args.gn;
+            cp_async4(dst + (32 + j + lane) * 4, args.sb + (in ? (pn + j + lane) * args.sb_row + pc * args.sb_blk : 0), in);
+          }
+        } else if (lane == 0) {
+          const bool in = pn < args.gn;
+          cp_async4(dst + 32 * 4, args.sb + (in ? (pn / 128) * args.sb_row + pc * args.sb_blk : 0), in);
+        }
+        if (++pslot == C::SCALE_SLOTS) pslot = 0;
+        if (++pc == pt.nkb) {
+          pc = 0;
+          pu += step;
+          if (pu < units) pt = walk.at(pu);
+        }
+      }
+      cp_async_commit();
+    };
+    int slot = 0;
+    if (C::FP8) {
+      fetch_scales();
+      fetch_scales();
+    }
     for (int u = static_cast<int>(blockIdx.x); ok && u < units; u += step) {
       const PgTile t = walk.at(u);
       const int n0 = t.tn * BN + h * C::HALF;  // this warp's first column
-      float acc[C::HALF / 32][32];
+      uint64_t acc[C::HALF / 2];               // pairs of columns
 #pragma unroll
-      for (int c = 0; c < C::HALF / 32; ++c)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) acc[c][j] = 0.0f;
-      const int m = t.tm * C::BM + q * 32 + lane;  // this thread's row in the dense output
+      for (int j = 0; j < C::HALF / 2; ++j) acc[j] = 0;
       for (int c0 = 0; c0 < t.nkb; c0 += CHUNK) {
-        float s = 1.0f;
+        uint64_t s = 0;
+        uint32_t xcol = 0;
         if (C::FP8) {
-          // (columns and rows past the edges have zero operands; their scale is not read)
-          s = m < args.gm ? __ldg(args.sa + m * args.sa_row + c0 * args.sa_blk) : 0.0f;
-          if (KIND != kFp8MM) {
-            if (n0 < args.gn) s *= __ldg(args.sb + (n0 / 128) * args.sb_row + c0 * args.sb_blk);
-          } else {
-            __syncwarp();
-            for (int j = lane; j < C::HALF; j += 32) {
-              const float x = n0 + j < args.gn ? __ldg(args.sb + (n0 + j) * args.sb_row + c0 * args.sb_blk) : 0.0f;
-              asm volatile("st.shared.f32 [%0], %1;" ::"r"(sbuf + j * 4), "f"(x) : "memory");
-            }
-            __syncwarp();
-          }
+          __syncwarp();  // every lane has read the slot that the next fetch fills
+          fetch_scales();
+          cp_async_wait<2>();
+          __syncwarp();
+          const uint32_t at = sring + static_cast<uint32_t>(slot) * SLOT;
+          float f = ld_shared_f32(at + lane * 4);
+          if (!C::COL_SCALES) f *= ld_shared_f32(at + 32 * 4);
+          s = pack_f32x2(f, f);
+          xcol = at + 32 * 4;
+          if (++slot == C::SCALE_SLOTS) slot = 0;
         }
         if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(buf), bphase, args.wait_ns))) {
           if (lane == 0) atomicOr(args.fault, kFaultEpilogueWait);
@@ -499,31 +576,34 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
         }
         tc_fence_after();
         const uint32_t t_addr = lane_addr + static_cast<uint32_t>(buf * BN);
+        // columns read from TMEM together (column scales take the registers of the second 32)
+        constexpr int BATCH = C::HALF < 64 ? C::HALF : C::COL_SCALES ? 32 : 64;
 #pragma unroll
-        for (int c = 0; c < C::HALF / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(t_addr + c * 32, r);
+        for (int c = 0; c < C::HALF; c += BATCH) {
+          uint32_t r[BATCH / 32][32];
+#pragma unroll
+          for (int i = 0; i < BATCH / 32; ++i) tmem_ld_32x32b_x32(t_addr + c + 32 * i, r[i]);
           tmem_wait_ld();
-          if (c == C::HALF / 32 - 1) {  // the accumulator is read: the next chunk may use it
+          if (c + BATCH == C::HALF) {  // the accumulator is read: the next chunk may use it
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty_bar(buf));
           }
-          if (!C::FP8) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[c][j] += __uint_as_float(r[j]);
-          } else if (KIND != kFp8MM) {
-            add_scaled(acc[c], r, s);
-          } else {
+          for (int i = 0; i < BATCH / 32; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 x = ld_shared_f4(sbuf + (c * 32 + j * 4) * 4);
-              acc[c][4 * j + 0] = fmaf(__uint_as_float(r[4 * j + 0]) * x.x, s, acc[c][4 * j + 0]);
-              acc[c][4 * j + 1] = fmaf(__uint_as_float(r[4 * j + 1]) * x.y, s, acc[c][4 * j + 1]);
-              acc[c][4 * j + 2] = fmaf(__uint_as_float(r[4 * j + 2]) * x.z, s, acc[c][4 * j + 2]);
-              acc[c][4 * j + 3] = fmaf(__uint_as_float(r[4 * j + 3]) * x.w, s, acc[c][4 * j + 3]);
+            for (int j = 0; j < 32; j += 4) {
+              uint64_t lo = pack_u32x2(r[i][j], r[i][j + 1]), hi = pack_u32x2(r[i][j + 2], r[i][j + 3]);
+              uint64_t& a0 = acc[(c + 32 * i + j) / 2];
+              uint64_t& a1 = acc[(c + 32 * i + j) / 2 + 1];
+              if (C::COL_SCALES) {
+                const float4 x = ld_shared_f4(xcol + (c + 32 * i + j) * 4);
+                lo = mul_f32x2(lo, pack_f32x2(x.x, x.y));
+                hi = mul_f32x2(hi, pack_f32x2(x.z, x.w));
+              }
+              a0 = C::FP8 ? fma_f32x2(lo, s, a0) : add_f32x2(lo, a0);
+              a1 = C::FP8 ? fma_f32x2(hi, s, a1) : add_f32x2(hi, a1);
             }
-          }
         }
         if (++buf == 2) {
           buf = 0;
@@ -550,35 +630,35 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
             *reinterpret_cast<uint4*>(out + (r * args.ldo + col) * esize) = x;
         }
       };
+      auto lo32 = [&](int j) { return static_cast<uint32_t>(acc[j]); };
+      auto hi32 = [&](int j) { return static_cast<uint32_t>(acc[j] >> 32); };
+      auto bf16x2 = [&](int j) { return pack_bf16x2(__uint_as_float(lo32(j)), __uint_as_float(hi32(j))); };
+      if (args.out_f32) {
 #pragma unroll
-      for (int c = 0; c < C::HALF / 32; ++c) {
-        const int col0 = n0 + c * 32;
-        if (args.out_f32) {
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              st_shared_u4(ebuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4),
-                           make_uint4(__float_as_uint(acc[c][16 * p + 4 * j]), __float_as_uint(acc[c][16 * p + 4 * j + 1]),
-                                      __float_as_uint(acc[c][16 * p + 4 * j + 2]),
-                                      __float_as_uint(acc[c][16 * p + 4 * j + 3])));
-            __syncwarp();
-            flush(col0 + 16 * p, 4);
-          }
-        } else {
+        for (int c = 0; c < C::HALF; c += 16) {
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             st_shared_u4(ebuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4),
-                         make_uint4(pack_bf16x2(acc[c][8 * j], acc[c][8 * j + 1]), pack_bf16x2(acc[c][8 * j + 2], acc[c][8 * j + 3]),
-                                    pack_bf16x2(acc[c][8 * j + 4], acc[c][8 * j + 5]),
-                                    pack_bf16x2(acc[c][8 * j + 6], acc[c][8 * j + 7])));
+                         make_uint4(lo32(c / 2 + 2 * j), hi32(c / 2 + 2 * j), lo32(c / 2 + 2 * j + 1), hi32(c / 2 + 2 * j + 1)));
           __syncwarp();
-          flush(col0, 8);
+          flush(n0 + c, 4);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < C::HALF; c += 32) {
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            st_shared_u4(ebuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4),
+                         make_uint4(bf16x2(c / 2 + 4 * j), bf16x2(c / 2 + 4 * j + 1), bf16x2(c / 2 + 4 * j + 2),
+                                    bf16x2(c / 2 + 4 * j + 3)));
+          __syncwarp();
+          flush(n0 + c, 8);
         }
       }
     }
+    if (C::FP8) cp_async_wait<0>();
     // Rows before the first group and after the last one belong to no expert: zeros.
     if (C::ROW_GROUPS) {
       const int lo = start[0], hi = start[args.experts], esize = args.out_f32 ? 4 : 2;
@@ -627,6 +707,13 @@ cudaError_t set_attr_pg() {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(promoted_gemm_kernel<BN, KIND>, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared);
+  if (BN == 256 && e == cudaSuccess) {
+    // the warpgroups trade exactly the registers of a launch at 168 a thread (regs_take
+    // would wait for ever on fewer): refuse to run a build that launches with another count
+    cudaFuncAttributes f;
+    e = cudaFuncGetAttributes(&f, promoted_gemm_kernel<BN, KIND>);
+    if (e == cudaSuccess && f.numRegs < 168) e = cudaErrorInvalidConfiguration;
+  }
   return e;
 }
 
