@@ -8,6 +8,7 @@
 //   warp 1       TMEM allocation and tcgen05.mma; for ragged contractions it also zeroes
 //                the rows of the last block that belong to the next group
 //   warp 2       TMA loads of B
+//   warp 3       8-bit products: the chunks' scales, by asynchronous copies into a ring
 //   warps 4..11  promotion and epilogue: read a finished chunk's accumulator from TMEM,
 //                add it (scaled) to FP32 registers; after the last chunk, round once and
 //                store.  Warp w holds rows 32 (w % 4) .. + 32 and one half of the columns.
@@ -47,6 +48,7 @@ enum PgKind : int {
 };
 
 constexpr int kMaxExperts = 1024;
+constexpr int kScaleSlots = 8;  // 8-bit products: chunks whose scales are in shared memory
 constexpr int kPgChunk = 32;  // BF16: contraction blocks of 64 per accumulator
 
 struct PgArgs {
@@ -86,14 +88,14 @@ struct PgCfg {
   static constexpr int STAGES = (192 * 1024) / STAGE_BYTES < 8 ? (192 * 1024) / STAGE_BYTES : 8;
   static constexpr int HALF = BN / 2;  // columns of one epilogue warp
   static constexpr int EPI_BYTES = 8 * 2048;
-  // 8-bit products: every epilogue warp keeps the scales of its 32 rows and of its columns
-  // (one value where a 128 x 128 block covers them) for the chunk at work and the two ahead
+  // 8-bit products: a ring of the scales of a chunk's 128 rows and BN columns (one value per
+  // 128 columns where blocks of 128 x 128 cover them)
   static constexpr bool COL_SCALES = KIND == kFp8MM;
-  static constexpr int SCALE_SLOTS = 3;
-  static constexpr int SCALE_FLOATS = 32 + (COL_SCALES ? HALF : 4);
-  static constexpr int SCALE_BYTES = FP8 ? 8 * SCALE_SLOTS * SCALE_FLOATS * 4 : 0;
+  static constexpr int SCALE_SLOTS = FP8 ? kScaleSlots : 0;
+  static constexpr int SCALE_FLOATS = 128 + (COL_SCALES ? BN : 4);
+  static constexpr int SCALE_BYTES = SCALE_SLOTS * SCALE_FLOATS * 4;
   static constexpr int TABLE_BYTES = (ROW_GROUPS || K_GROUPS) ? 2 * (kMaxExperts + 4) * 4 : 0;
-  static constexpr int NUM_BARS = 2 * STAGES + 5;
+  static constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * SCALE_SLOTS;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int SMEM_BYTES =
       1024 + STAGES * STAGE_BYTES + EPI_BYTES + SCALE_BYTES + TABLE_BYTES + NUM_BARS * 8 + 256;
@@ -267,24 +269,26 @@ __device__ __forceinline__ void build_group_table(const PgArgs& a, int32_t* star
   __syncthreads();
 }
 
-// Pairs of FP32 values in one 64-bit register: one instruction for two operations.
+// Pairs of FP32 values in one 64-bit register: one instruction for two operations.  Volatile,
+// so that they stay behind the wait for the TMEM loads whose values they take (passing the
+// values through the wait instead costs a register copy each).
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
   return (static_cast<uint64_t>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
 }
 __device__ __forceinline__ uint64_t pack_u32x2(uint32_t lo, uint32_t hi) { return (static_cast<uint64_t>(hi) << 32) | lo; }
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  asm volatile("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  asm volatile("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  asm volatile("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 
@@ -292,13 +296,14 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Arrive on `bar` when this thread's copies so far have landed (counted among the
+// arrivals the barrier was initialised with).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Registers move between the warpgroups: 384 x 168 at launch = 128 x 72 + 256 x 216.
+// Registers move between the warpgroups: 384 x 168 at launch = 128 x 88 + 256 x 208.
 template <int N>
 __device__ __forceinline__ void regs_give() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -334,6 +339,8 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
   auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
   auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
   const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+  auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
+  auto sempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + C::SCALE_SLOTS + s); };
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
   const int lane = static_cast<int>(threadIdx.x) & 31;
@@ -347,6 +354,10 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
       mbar_init(tempty_bar(b), 8);  // one arrival per epilogue warp
+    }
+    for (int s = 0; s < C::SCALE_SLOTS; ++s) {
+      mbar_init(sfull_bar(s), 32);  // every lane's copies
+      mbar_init(sempty_bar(s), 8);
     }
     mbar_init(drain_bar, 1);
     fence_mbar_init();
@@ -366,7 +377,7 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
 
   // (Narrower tiles need fewer registers than every thread has at launch.)
   if (warp < 4) {
-  if (BN == 256) regs_give<72>();
+  if (BN == 256) regs_give<88>();
   if (warp == 0 || warp == 2) {
     // -------------------------------------------------------------- producers
     if (lane == 0) {
@@ -466,9 +477,9 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
               __syncwarp();
             }
           }
-          if (lane == 0) {
-            tc_fence_after();
-            for (int kk = 0; kk < slices; ++kk) {
+          tc_fence_after();
+          if (elect_one()) {
+            auto issue = [&](int kk) {
               const uint64_t ad = C::A_MN ? sdesc_sw128(sa + kk * (C::SLICE * 128), C::BK * 128, 1024)
                                           : sdesc_sw128(sa + kk * 32, 16, 1024);
               const uint64_t bd = C::B_MN ? sdesc_sw128(sb + kk * (C::SLICE * 128), C::BK * 128, 1024)
@@ -478,8 +489,15 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
                 mma_fp8(d_tmem, ad, bd, args.idesc, more);
               else
                 mma_bf16(d_tmem, ad, bd, args.idesc, more);
+            };
+            if (C::K_GROUPS && slices < C::BK / C::SLICE) {
+              for (int kk = 0; kk < slices; ++kk) issue(kk);
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < C::BK / C::SLICE; ++kk) issue(kk);
             }
             mma_commit(empty_bar(stage));
+            if (kb + 1 == c1) mma_commit(tfull_bar(buf));
           }
           __syncwarp();
           if (++stage == STAGES) {
@@ -488,129 +506,151 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
           }
         }
         if (!ok) break;
-        if (lane == 0) mma_commit(tfull_bar(buf));
-        __syncwarp();
         if (++buf == 2) {
           buf = 0;
           bphase ^= 1u;
         }
       }
     }
-    // every MMA has finished before TMEM is freed
-    if (lane == 0) {
+    // every MMA has finished before TMEM is freed (each commit covers the MMAs of the lane
+    // that issues it: the elected lane is the same one throughout)
+    if (elect_one()) {
       mma_commit(drain_bar);
       if (!mbar_wait(drain_bar, 0, args.wait_ns)) atomicOr(args.fault, kFaultDrainWait);
     }
     __syncwarp();
+  } else if (C::FP8) {
+    // ------------------------------------------------------------------ scales
+    int slot = 0;
+    uint32_t sphase = 0;
+    bool ok = true;
+    for (int u = static_cast<int>(blockIdx.x); ok && u < units; u += step) {
+      const PgTile t = walk.at(u);
+      // (rows and columns past the edges have zero operands: their scale is zero)
+      const float* pa[4];
+      bool in_a[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int m = t.tm * C::BM + 32 * j + lane;
+        in_a[j] = m < args.gm;
+        pa[j] = args.sa + (in_a[j] ? m * args.sa_row : 0);
+      }
+      constexpr int NB = C::COL_SCALES ? BN / 32 : 1;
+      const float* pb[NB];
+      bool in_b[NB];
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int n = t.tn * BN + (C::COL_SCALES ? 32 * j + lane : 128 * lane);
+        in_b[j] = n < args.gn;
+        pb[j] = args.sb + (in_b[j] ? (C::COL_SCALES ? n : n / 128) * args.sb_row : 0);
+      }
+      for (int kb = 0; kb < t.nkb; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(sempty_bar(slot), sphase ^ 1u, args.wait_ns))) {
+          if (lane == 0) atomicOr(args.fault, kFaultProducerWait);
+          ok = false;
+          break;
+        }
+        const uint32_t dst = scbase + static_cast<uint32_t>(slot) * (C::SCALE_FLOATS * 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          cp_async4(dst + (32 * j + lane) * 4, pa[j], in_a[j]);
+          pa[j] += in_a[j] ? args.sa_blk : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          if (C::COL_SCALES || lane < (BN + 127) / 128) cp_async4(dst + (128 + 32 * j + lane) * 4, pb[j], in_b[j]);
+          pb[j] += in_b[j] ? args.sb_blk : 0;
+        }
+        cp_async_arrive(sfull_bar(slot));
+        if (++slot == C::SCALE_SLOTS) {
+          slot = 0;
+          sphase ^= 1u;
+        }
+      }
+    }
+    // one empty slot past the last chunk: the epilogue looks one ahead
+    if (ok && __all_sync(0xffffffffu, mbar_wait(sempty_bar(slot), sphase ^ 1u, args.wait_ns)))
+      cp_async_arrive(sfull_bar(slot));
+    cp_async_wait_all();
   }
   } else {
     // -------------------------------------------------- promotion and epilogue
-    if (BN == 256) regs_take<216>();
+    if (BN == 256) regs_take<208>();
     const int q = warp & 3, h = (warp - 4) >> 2;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * C::HALF);
     const uint32_t ebuf = ebase + static_cast<uint32_t>(warp - 4) * 2048u;
-    constexpr uint32_t SLOT = C::SCALE_FLOATS * 4;
-    const uint32_t sring = scbase + static_cast<uint32_t>(warp - 4) * (C::SCALE_SLOTS * SLOT);
-    int buf = 0;
-    uint32_t bphase = 0;
+    // (Beside 128 accumulators registers are short: one counter gives every ring position, and
+    // the tile is decoded again for the store.)
+    uint32_t it = 0;  // chunks done by this CTA
     bool ok = true;
-    // The scales' cursor walks the same tiles and chunks two ahead of the promotion.
-    int pu = static_cast<int>(blockIdx.x), pc = 0, pslot = 0;
-    PgTile pt = {};
-    if (C::FP8 && pu < units) pt = walk.at(pu);
-    auto fetch_scales = [&]() {
-      if (pu < units) {
-        const uint32_t dst = sring + static_cast<uint32_t>(pslot) * SLOT;
-        const int pm = pt.tm * C::BM + q * 32 + lane, pn = pt.tn * BN + h * C::HALF;
-        // (rows and columns past the edges have zero operands: any finite scale will do)
-        cp_async4(dst + lane * 4, args.sa + (pm < args.gm ? pm * args.sa_row + pc * args.sa_blk : 0), pm < args.gm);
-        if (C::COL_SCALES) {
-#pragma unroll
-          for (int j = 0; j < C::HALF; j += 32) {
-            const bool in = pn + j + lane < args.gn;
-            cp_async4(dst + (32 + j + lane) * 4, args.sb + (in ? (pn + j + lane) * args.sb_row + pc * args.sb_blk : 0), in);
-          }
-        } else if (lane == 0) {
-          const bool in = pn < args.gn;
-          cp_async4(dst + 32 * 4, args.sb + (in ? (pn / 128) * args.sb_row + pc * args.sb_blk : 0), in);
-        }
-        if (++pslot == C::SCALE_SLOTS) pslot = 0;
-        if (++pc == pt.nkb) {
-          pc = 0;
-          pu += step;
-          if (pu < units) pt = walk.at(pu);
-        }
-      }
-      cp_async_commit();
+    float next = 1.0f;  // this row's factor for chunk `it`, read one chunk ahead
+    auto read_scale = [&](uint32_t i) {
+      const bool in = mbar_wait(sfull_bar(i % kScaleSlots), (i / kScaleSlots) & 1u, args.wait_ns);
+      const uint32_t at = scbase + (i % kScaleSlots) * (C::SCALE_FLOATS * 4);
+      next = ld_shared_f32(at + (q * 32 + lane) * 4);
+      if (!C::COL_SCALES) next *= ld_shared_f32(at + (128 + (BN == 256 ? h : 0)) * 4);
+      return in;
     };
-    int slot = 0;
-    if (C::FP8) {
-      fetch_scales();
-      fetch_scales();
-    }
-    for (int u = static_cast<int>(blockIdx.x); ok && u < units; u += step) {
-      const PgTile t = walk.at(u);
-      const int n0 = t.tn * BN + h * C::HALF;  // this warp's first column
-      uint64_t acc[C::HALF / 2];               // pairs of columns
+    if (C::FP8) ok = read_scale(0);
+    for (int u = static_cast<int>(blockIdx.x); u < units; u += step) {
+      uint64_t acc[C::HALF / 2];  // pairs of columns
 #pragma unroll
       for (int j = 0; j < C::HALF / 2; ++j) acc[j] = 0;
-      for (int c0 = 0; c0 < t.nkb; c0 += CHUNK) {
-        uint64_t s = 0;
-        uint32_t xcol = 0;
-        if (C::FP8) {
-          __syncwarp();  // every lane has read the slot that the next fetch fills
-          fetch_scales();
-          cp_async_wait<2>();
-          __syncwarp();
-          const uint32_t at = sring + static_cast<uint32_t>(slot) * SLOT;
-          float f = ld_shared_f32(at + lane * 4);
-          if (!C::COL_SCALES) f *= ld_shared_f32(at + 32 * 4);
-          s = pack_f32x2(f, f);
-          xcol = at + 32 * 4;
-          if (++slot == C::SCALE_SLOTS) slot = 0;
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(buf), bphase, args.wait_ns))) {
+      for (int left = (walk.at(u).nkb + CHUNK - 1) / CHUNK; left > 0; --left, ++it) {
+        const uint64_t s = pack_f32x2(next, next);
+        const uint32_t xcol = scbase + (it % kScaleSlots) * (C::SCALE_FLOATS * 4) + (128 + h * C::HALF) * 4;
+        if (C::FP8) ok = read_scale(it + 1) && ok;
+        ok = mbar_wait(tfull_bar(it & 1u), (it >> 1) & 1u, args.wait_ns) && ok;
+        if (!__all_sync(0xffffffffu, ok)) {
           if (lane == 0) atomicOr(args.fault, kFaultEpilogueWait);
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t t_addr = lane_addr + static_cast<uint32_t>(buf * BN);
-        // columns read from TMEM together (column scales take the registers of the second 32)
-        constexpr int BATCH = C::HALF < 64 ? C::HALF : C::COL_SCALES ? 32 : 64;
+        const uint32_t t_addr = lane_addr + (it & 1u) * BN;
+        // 32 columns at a time.  Where the registers allow it the next 32 are on their way from
+        // TMEM while these are added; beside 128 accumulators they do not (the pairs would be
+        // copied to make room: 107 moves a chunk, 85 against 61 us at T = 4031, 4096 -> 4096),
+        // and the other warp of the SM sub-partition adds while this one loads.
+        constexpr int AHEAD = C::HALF <= 64 ? 1 : 0;
+        uint32_t r[1 + AHEAD][32];
+        if (AHEAD) tmem_ld_32x32b_x32(t_addr, r[0]);
 #pragma unroll
-        for (int c = 0; c < C::HALF; c += BATCH) {
-          uint32_t r[BATCH / 32][32];
-#pragma unroll
-          for (int i = 0; i < BATCH / 32; ++i) tmem_ld_32x32b_x32(t_addr + c + 32 * i, r[i]);
+        for (int c = 0; c < C::HALF; c += 32) {
+          uint32_t(&v)[32] = r[AHEAD ? (c / 32) & 1 : 0];
+          if (!AHEAD) tmem_ld_32x32b_x32(t_addr + c, v);
           tmem_wait_ld();
-          if (c + BATCH == C::HALF) {  // the accumulator is read: the next chunk may use it
+          if (c + 32 < C::HALF) {
+            if (AHEAD) tmem_ld_32x32b_x32(t_addr + c + 32, r[(c / 32 + 1) & 1]);
+          } else {  // the accumulator is read: the next chunk but one may use it
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(tempty_bar(buf));
+            if (lane == 0) mbar_arrive(tempty_bar(it & 1u));
           }
 #pragma unroll
-          for (int i = 0; i < BATCH / 32; ++i)
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              uint64_t lo = pack_u32x2(r[i][j], r[i][j + 1]), hi = pack_u32x2(r[i][j + 2], r[i][j + 3]);
-              uint64_t& a0 = acc[(c + 32 * i + j) / 2];
-              uint64_t& a1 = acc[(c + 32 * i + j) / 2 + 1];
-              if (C::COL_SCALES) {
-                const float4 x = ld_shared_f4(xcol + (c + 32 * i + j) * 4);
-                lo = mul_f32x2(lo, pack_f32x2(x.x, x.y));
-                hi = mul_f32x2(hi, pack_f32x2(x.z, x.w));
-              }
-              a0 = C::FP8 ? fma_f32x2(lo, s, a0) : add_f32x2(lo, a0);
-              a1 = C::FP8 ? fma_f32x2(hi, s, a1) : add_f32x2(hi, a1);
+          for (int j = 0; j < 32; j += 4) {
+            uint64_t lo = pack_u32x2(v[j], v[j + 1]), hi = pack_u32x2(v[j + 2], v[j + 3]);
+            uint64_t& a0 = acc[(c + j) / 2];
+            uint64_t& a1 = acc[(c + j) / 2 + 1];
+            if (C::COL_SCALES) {
+              const float4 x = ld_shared_f4(xcol + (c + j) * 4);
+              lo = mul_f32x2(lo, pack_f32x2(x.x, x.y));
+              hi = mul_f32x2(hi, pack_f32x2(x.z, x.w));
             }
+            a0 = C::FP8 ? fma_f32x2(lo, s, a0) : add_f32x2(lo, a0);
+            a1 = C::FP8 ? fma_f32x2(hi, s, a1) : add_f32x2(hi, a1);
+          }
         }
-        if (++buf == 2) {
-          buf = 0;
-          bphase ^= 1u;
+        if (C::FP8) {
+          __syncwarp();  // every lane has read its scales
+          if (lane == 0) mbar_arrive(sempty_bar(it % kScaleSlots));
         }
       }
       if (!ok) break;
+      int us = u;
+      asm volatile("" : "+r"(us));
+      const PgTile t = walk.at(us);
+      const int n0 = t.tn * BN + h * C::HALF;  // this warp's first column
       // Store 32 rows x HALF columns through the warp's 2 KB block: 64-byte rows (32 BF16 or
       // 16 FP32 columns), 16-byte chunks XOR-swizzled by row, read back so that four lanes
       // write 64 consecutive bytes of a row.
@@ -658,7 +698,6 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
         }
       }
     }
-    if (C::FP8) cp_async_wait<0>();
     // Rows before the first group and after the last one belong to no expert: zeros.
     if (C::ROW_GROUPS) {
       const int lo = start[0], hi = start[args.experts], esize = args.out_f32 ? 4 : 2;
