@@ -105,15 +105,30 @@ struct PgCfg {
   static_assert(!(FP8 && B_MN) || BN >= 128, "8-bit MN-major boxes are 128 columns wide");
 };
 
-// tcgen05.mma on 8-bit operands (E4M3 or E5M2 each, as the instruction descriptor says).
-__device__ __forceinline__ void mma_fp8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// tcgen05.mma on operands given by the halves of their shared-memory descriptors.  The low
+// half holds the start address >> 4 and the leading offset, the high half (constant over a
+// kernel) the stride and the layout: stepping through stages and slices is one 32-bit add, which
+// stays in uniform registers.  (8-bit operands: E4M3 or E5M2 each, as the instruction
+// descriptor says.)
+template <bool FP8>
+__device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+  if (FP8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // Instruction descriptor, kind::f8f6f4 with FP32 D: as idesc_bf16_f32, formats 0 = E4M3, 1 = E5M2.
@@ -442,6 +457,13 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
     int stage = 0, buf = 0;
     uint32_t phase = 0, bphase = 0;
     bool ok = true;
+    // descriptors of stage 0 and their step per slice: K-major 32 bytes along the swizzled row,
+    // MN-major SLICE rows of 128 bytes (see sdesc_sw128)
+    constexpr uint32_t A_STEP = C::A_MN ? C::SLICE * 8 : 2, B_STEP = C::B_MN ? C::SLICE * 8 : 2;
+    const uint64_t a_desc = sdesc_sw128(base, C::A_MN ? C::BK * 128 : 16, 1024);
+    const uint64_t b_desc = sdesc_sw128(base + C::A_BYTES, C::B_MN ? C::BK * 128 : 16, 1024);
+    const uint32_t a_lo = static_cast<uint32_t>(a_desc), a_hi = static_cast<uint32_t>(a_desc >> 32);
+    const uint32_t b_lo = static_cast<uint32_t>(b_desc), b_hi = static_cast<uint32_t>(b_desc >> 32);
     for (int u = static_cast<int>(blockIdx.x); ok && u < units; u += step) {
       const PgTile t = walk.at(u);
       for (int c0 = 0; ok && c0 < t.nkb; c0 += CHUNK) {
@@ -458,7 +480,6 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
             ok = false;
             break;
           }
-          const uint32_t sa = base + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
           int slices = C::BK / C::SLICE;
           if (C::K_GROUPS) {
             // the last block's rows past the group's end belong to the next group: contract
@@ -471,7 +492,7 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
               constexpr int BOXES = (C::BM + BN) / C::MN;
               for (int i = lane; i < rows * 8 * BOXES; i += 32) {
                 const int box = i / (rows * 8), j = i - box * (rows * 8);
-                st_shared_u4(sa + box * (C::BK * 128) + (valid + (j >> 3)) * 128 + (j & 7) * 16, make_uint4(0, 0, 0, 0));
+                st_shared_u4(base + stage * C::STAGE_BYTES + box * (C::BK * 128) + (valid + (j >> 3)) * 128 + (j & 7) * 16, make_uint4(0, 0, 0, 0));
               }
               fence_proxy_async_shared();
               __syncwarp();
@@ -479,16 +500,10 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
           }
           tc_fence_after();
           if (elect_one()) {
+            const uint32_t at = static_cast<uint32_t>(stage) * (C::STAGE_BYTES >> 4);
             auto issue = [&](int kk) {
-              const uint64_t ad = C::A_MN ? sdesc_sw128(sa + kk * (C::SLICE * 128), C::BK * 128, 1024)
-                                          : sdesc_sw128(sa + kk * 32, 16, 1024);
-              const uint64_t bd = C::B_MN ? sdesc_sw128(sb + kk * (C::SLICE * 128), C::BK * 128, 1024)
-                                          : sdesc_sw128(sb + kk * 32, 16, 1024);
-              const uint32_t more = (kb > c0 || kk > 0) ? 1u : 0u;
-              if (C::FP8)
-                mma_fp8(d_tmem, ad, bd, args.idesc, more);
-              else
-                mma_bf16(d_tmem, ad, bd, args.idesc, more);
+              mma_lo<C::FP8>(d_tmem, a_lo + at + kk * A_STEP, a_hi, b_lo + at + kk * B_STEP, b_hi, args.idesc,
+                             (kb > c0 || kk > 0) ? 1u : 0u);
             };
             if (C::K_GROUPS && slices < C::BK / C::SLICE) {
               for (int kk = 0; kk < slices; ++kk) issue(kk);
