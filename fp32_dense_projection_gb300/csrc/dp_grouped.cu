@@ -168,7 +168,9 @@ dp_status run_fp8(GroupedOp op, const void* a, int64_t lda, int a_fmt, Scales sa
   std::memset(&l, 0, sizeof(l));
   PgArgs& g = l.args;
   const int kind = op == kFwd ? kFp8KK : op == kDgrad ? kFp8KM : kFp8MM;
-  const int bn = tile_width(cdiv(gm, 128), gn, ctx.sm_count, kind == kFp8KK ? 64 : 128);
+  const bool pair = cdiv(gm, 256) * cdiv(gn, 256) * 2 >= ctx.sm_count;
+  const int bn = pair ? 256 : tile_width(cdiv(gm, 128), gn, ctx.sm_count, kind == kFp8KK ? 64 : 128);
+  const int tm = pair ? 256 : 128;
   g.rows = static_cast<int32_t>(gm);
   g.gm = static_cast<int32_t>(gm);
   g.gn = static_cast<int32_t>(gn);
@@ -177,10 +179,10 @@ dp_status run_fp8(GroupedOp op, const void* a, int64_t lda, int a_fmt, Scales sa
   g.out = out;
   g.ldo = ldo;
   g.out_f32 = out_f32;
-  g.tiles_m = static_cast<int32_t>(cdiv(gm, 128));
+  g.tiles_m = static_cast<int32_t>(cdiv(gm, tm));
   g.tiles_n = static_cast<int32_t>(cdiv(gn, bn));
   g.group_m = raster_rows(gk);
-  g.idesc = idesc_fp8_f32(128, bn, kind == kFp8MM, kind != kFp8KK, a_fmt == DP_FP8_E5M2, b_fmt == DP_FP8_E5M2);
+  g.idesc = idesc_fp8_f32(tm, std::min(bn, 128), kind == kFp8MM, kind != kFp8KK, a_fmt == DP_FP8_E5M2, b_fmt == DP_FP8_E5M2);
   g.sa = sa.p;
   g.sa_row = sa.row;
   g.sa_blk = sa.blk;
@@ -194,13 +196,13 @@ dp_status run_fp8(GroupedOp op, const void* a, int64_t lda, int a_fmt, Scales sa
   const bool ok =
       (kind == kFp8MM ? encode_operand(&l.tmA, a, u8, 1, gk, gm, lda, 0, 0, 128, 128)
                       : encode_operand(&l.tmA, a, u8, 1, gm, gk, lda, 0, 0, 128, 128)) &&
-      (kind == kFp8KK ? encode_operand(&l.tmB, b, u8, 1, gn, gk, ldb, 0, 0, 128, static_cast<uint32_t>(bn))
+      (kind == kFp8KK ? encode_operand(&l.tmB, b, u8, 1, gn, gk, ldb, 0, 0, 128, static_cast<uint32_t>(pair ? bn / 2 : bn))
                       : encode_operand(&l.tmB, b, u8, 1, gk, gn, ldb, 0, 0, 128, 128));
   if (!ok) return DP_ERR_LAUNCH;
   const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
   if (tiles > kMaxInt) return DP_ERR_UNSUPPORTED;
-  l.grid = static_cast<int>(std::min<int64_t>(ctx.sm_count, tiles));
-  return launch_fp8(kind, bn, l, stream) == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+  l.grid = static_cast<int>(pair ? 2 * std::min<int64_t>(ctx.sm_count / 2, tiles) : std::min<int64_t>(ctx.sm_count, tiles));
+  return launch_fp8(kind, bn, pair, l, stream) == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
 }
 
 }  // namespace

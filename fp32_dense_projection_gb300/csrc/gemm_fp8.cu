@@ -4,7 +4,14 @@
 
 namespace dp {
 
-cudaError_t launch_fp8(int kind, int bn, const PgLaunch& l, cudaStream_t stream) {
+cudaError_t launch_fp8(int kind, int bn, bool pair, const PgLaunch& l, cudaStream_t stream) {
+  if (pair) {
+    if (bn != 256) return cudaErrorInvalidValue;
+    if (kind == kFp8KK) return launch_pg<256, kFp8KK, true>(l, stream);
+    if (kind == kFp8KM) return launch_pg<256, kFp8KM, true>(l, stream);
+    if (kind == kFp8MM) return launch_pg<256, kFp8MM, true>(l, stream);
+    return cudaErrorInvalidValue;
+  }
   switch (kind) {
     case kFp8KK:
       if (bn == 64) return launch_pg<64, kFp8KK>(l, stream);
@@ -31,6 +38,9 @@ cudaError_t set_attributes_fp8() {
   if (e == cudaSuccess) e = set_attr_pg<256, kFp8KM>();
   if (e == cudaSuccess) e = set_attr_pg<128, kFp8MM>();
   if (e == cudaSuccess) e = set_attr_pg<256, kFp8MM>();
+  if (e == cudaSuccess) e = set_attr_pg<256, kFp8KK, true>();
+  if (e == cudaSuccess) e = set_attr_pg<256, kFp8KM, true>();
+  if (e == cudaSuccess) e = set_attr_pg<256, kFp8MM, true>();
   return e;
 }
 

@@ -8,7 +8,7 @@
 //   warp 1       TMEM allocation and tcgen05.mma; for ragged contractions it also zeroes
 //                the rows of the last block that belong to the next group
 //   warp 2       TMA loads of B
-//   warp 3       8-bit products: the chunks' scales, by asynchronous copies into a ring
+//   warp 3       8-bit products: the chunks' scales, through registers into a ring
 //   warps 4..11  promotion and epilogue: read a finished chunk's accumulator from TMEM,
 //                add it (scaled) to FP32 registers; after the last chunk, round once and
 //                store.  Warp w holds rows 32 (w % 4) .. + 32 and one half of the columns.
@@ -48,7 +48,7 @@ enum PgKind : int {
 };
 
 constexpr int kMaxExperts = 1024;
-constexpr int kScaleSlots = 8;  // 8-bit products: chunks whose scales are in shared memory
+constexpr int kScaleAhead = 3;  // 8-bit products: how many chunks ahead scales are loaded
 constexpr int kPgChunk = 32;  // BF16: contraction blocks of 64 per accumulator
 
 struct PgArgs {
@@ -71,8 +71,13 @@ struct PgArgs {
   uint64_t wait_ns;
 };
 
-template <int BN, int KIND>
+// PAIR: a cluster of two CTAs computes one tile of 256 x BN.  Each loads its 128 rows of A
+// and half of the tile's columns of B, the leader (rank 0) issues the MMAs over both, and each
+// promotes its 128 x BN half of the accumulator: a third less operand traffic per SM.
+template <int BN, int KIND, bool PAIR = false>
 struct PgCfg {
+  static constexpr int TM = PAIR ? 256 : 128;     // rows of a tile
+  static constexpr int BNL = PAIR ? BN / 2 : BN;  // columns of B a CTA loads
   static constexpr bool FP8 = KIND >= kFp8KK;
   static constexpr bool A_MN = KIND == kGroupMM || KIND == kFp8MM;
   static constexpr bool B_MN = KIND != kGroupKK && KIND != kFp8KK;
@@ -83,26 +88,36 @@ struct PgCfg {
   static constexpr int MN = FP8 ? 128 : 64;  // columns of one MN-major box (128 bytes)
   static constexpr int SLICE = FP8 ? 32 : 16;  // contraction elements of one MMA
   static constexpr int A_BYTES = BM * 128;
-  static constexpr int B_BYTES = BN * 128;
+  static constexpr int B_BYTES = BNL * 128;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int STAGES = (192 * 1024) / STAGE_BYTES < 8 ? (192 * 1024) / STAGE_BYTES : 8;
+  // Accumulator buffers.  8-bit products commit every block: their MMAs are 128 columns wide
+  // (as fast as 256) into four buffers, so that the tensor cores go on while two blocks are
+  // promoted; with two buffers of 256 the promotion of a block had to end within the MMAs of the
+  // next one.  At 256 columns the two groups of epilogue warps take one half each.
+  static constexpr int SUB = FP8 && BN == 256 ? 128 : BN;  // columns of one MMA
+  static constexpr int NSUB = BN / SUB;
+  static constexpr int NBUF = FP8 ? 4 : 2;
+  static constexpr int EPI_ARRIVALS = (NSUB == 2 ? 4 : 8) * (PAIR ? 2 : 1);  // per buffer
   static constexpr int HALF = BN / 2;  // columns of one epilogue warp
   static constexpr int EPI_BYTES = 8 * 2048;
-  // 8-bit products: a ring of the scales of a chunk's 128 rows and BN columns (one value per
-  // 128 columns where blocks of 128 x 128 cover them)
+  // 8-bit products: a ring of the chunks' scales, filled by warp 3: for each of the 128 rows its
+  // scale times that of the tile's first and second 128 columns (128 x 128 blocks of B), or
+  // the scales of the rows and then of the BN columns.
   static constexpr bool COL_SCALES = KIND == kFp8MM;
-  static constexpr int SCALE_SLOTS = FP8 ? kScaleSlots : 0;
-  static constexpr int SCALE_FLOATS = 128 + (COL_SCALES ? BN : 4);
-  static constexpr int SCALE_BYTES = SCALE_SLOTS * SCALE_FLOATS * 4;
+  static constexpr int SCALE_FLOATS = COL_SCALES ? 128 + BN : 256;
+  static constexpr int SCALE_SLOTS = !FP8 ? 1 : NSUB == 2 ? 8 : 16;
+  static constexpr int SCALE_BYTES = FP8 ? SCALE_SLOTS * SCALE_FLOATS * 4 : 0;
   static constexpr int TABLE_BYTES = (ROW_GROUPS || K_GROUPS) ? 2 * (kMaxExperts + 4) * 4 : 0;
-  static constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * SCALE_SLOTS;
-  static constexpr int TMEM_COLS = 2 * BN;
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * NBUF + 1;
+  static constexpr int TMEM_COLS = NBUF * SUB;
   static constexpr int SMEM_BYTES =
       1024 + STAGES * STAGE_BYTES + EPI_BYTES + SCALE_BYTES + TABLE_BYTES + NUM_BARS * 8 + 256;
   static constexpr int THREADS = 384;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
   static_assert(BN == 64 || BN == 128 || BN == 256, "tile width");
-  static_assert(!(FP8 && B_MN) || BN >= 128, "8-bit MN-major boxes are 128 columns wide");
+  static_assert(!(PAIR && K_GROUPS), "the leader zeroes ragged rows in its own shared memory only");
+  static_assert(!(FP8 && B_MN) || BNL >= 128, "8-bit MN-major boxes are 128 columns wide");
 };
 
 // tcgen05.mma on operands given by the halves of their shared-memory descriptors.  The low
@@ -110,25 +125,26 @@ struct PgCfg {
 // kernel) the stride and the layout: stepping through stages and slices is one 32-bit add, which
 // stays in uniform registers.  (8-bit operands: E4M3 or E5M2 each, as the instruction
 // descriptor says.)
-template <bool FP8>
+template <bool FP8, bool PAIR>
 __device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
                                        uint32_t idesc, uint32_t accumulate) {
-  if (FP8)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
-        : "memory");
+#define DP_MMA(GROUP, TYPE)                                                                      \
+  asm volatile(                                                                                  \
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"                                              \
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"                                       \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                                \
+      "tcgen05.mma.cta_group::" GROUP ".kind::" TYPE " [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem), \
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)                    \
+      : "memory")
+  if (FP8 && PAIR)
+    DP_MMA("2", "f8f6f4");
+  else if (FP8)
+    DP_MMA("1", "f8f6f4");
+  else if (PAIR)
+    DP_MMA("2", "f16");
   else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
-        : "memory");
+    DP_MMA("1", "f16");
+#undef DP_MMA
 }
 
 // Instruction descriptor, kind::f8f6f4 with FP32 D: as idesc_bf16_f32, formats 0 = E4M3, 1 = E5M2.
@@ -147,9 +163,9 @@ struct PgTile {
   int k_left;  // contraction elements
 };
 
-template <int BN, int KIND>
+template <int BN, int KIND, bool PAIR>
 struct PgWalk {
-  using C = PgCfg<BN, KIND>;
+  using C = PgCfg<BN, KIND, PAIR>;
   const PgArgs& a;
   const int32_t* start;  // [experts + 1] first row of each group
   const int32_t* first;  // [experts + 1] first tile of each group (row-grouped)
@@ -174,7 +190,7 @@ struct PgWalk {
       t.e = lo;
       local = u - first[lo];
       const int cnt = start[lo + 1] - start[lo];
-      tiles_m = (cnt + C::BM - 1) / C::BM;
+      tiles_m = (cnt + C::TM - 1) / C::TM;
       t.m_left = cnt;
       t.row0 = start[lo];
       t.k_left = a.gk;
@@ -201,8 +217,8 @@ struct PgWalk {
     const int l2 = local - g * per_group;
     t.tm = m0 + l2 % width;
     t.tn = l2 / width;
-    t.m_left -= t.tm * C::BM;
-    if (C::ROW_GROUPS) t.row0 += t.tm * C::BM;
+    t.m_left -= t.tm * C::TM;
+    if (C::ROW_GROUPS) t.row0 += t.tm * C::TM;
     t.nkb = (t.k_left + C::BK - 1) / C::BK;
     return t;
   }
@@ -211,9 +227,9 @@ struct PgWalk {
 // The groups' table: start[i] = running maximum of the offsets, clamped to [0, rows], and
 // (row-grouped) first[i] = tiles of the groups before i.  Offsets that decrease or leave
 // [0, rows] set kFaultOffsets.  All 384 threads call it; each takes `per` consecutive entries.
-template <int BN, int KIND>
+template <int BN, int KIND, bool PAIR>
 __device__ __forceinline__ void build_group_table(const PgArgs& a, int32_t* start, int32_t* first, int32_t* scan) {
-  using C = PgCfg<BN, KIND>;
+  using C = PgCfg<BN, KIND, PAIR>;
   constexpr int NW = C::THREADS / 32;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int n = a.experts + 1;
@@ -262,7 +278,7 @@ __device__ __forceinline__ void build_group_table(const PgArgs& a, int32_t* star
   for (int j = 0; j < 3; ++j) {
     const int i = tid * per + j;
     tiles[j] = 0;
-    if (j < per && i < a.experts) tiles[j] = (start[i + 1] - start[i] + C::BM - 1) / C::BM * a.tiles_n;
+    if (j < per && i < a.experts) tiles[j] = (start[i + 1] - start[i] + C::TM - 1) / C::TM * a.tiles_n;
     sum += tiles[j];
   }
   int32_t tot = sum;
@@ -307,15 +323,16 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Four bytes from global to shared memory without a register; zero where !valid.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+__device__ __forceinline__ void st_shared_f2(uint32_t addr, float a, float b) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// Arrive on `bar` when this thread's copies so far have landed (counted among the
-// arrivals the barrier was initialised with).
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ float2 ld_shared_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // Registers move between the warpgroups: 384 x 168 at launch = 128 x 88 + 256 x 208.
@@ -328,11 +345,11 @@ __device__ __forceinline__ void regs_take() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int BN, int KIND>
-__global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
+template <int BN, int KIND, bool PAIR>
+__global__ void __launch_bounds__(PgCfg<BN, KIND, PAIR>::THREADS, 1)
     promoted_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ PgArgs args) {
-  using C = PgCfg<BN, KIND>;
+  using C = PgCfg<BN, KIND, PAIR>;
   constexpr int STAGES = C::STAGES;
   constexpr int CHUNK = C::FP8 ? 1 : kPgChunk;
   extern __shared__ uint8_t smem_raw[];
@@ -352,10 +369,8 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
-  auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
-  auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
-  auto sempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + C::SCALE_SLOTS + s); };
+  auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + C::NBUF + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * C::NBUF);
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
   const int lane = static_cast<int>(threadIdx.x) & 31;
@@ -366,29 +381,35 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
       mbar_init(full_bar(s), 2);  // one expect-tx arrival from each producer
       mbar_init(empty_bar(s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), 8);  // one arrival per epilogue warp
-    }
-    for (int s = 0; s < C::SCALE_SLOTS; ++s) {
-      mbar_init(sfull_bar(s), 32);  // every lane's copies
-      mbar_init(sempty_bar(s), 8);
+    for (int b = 0; b < C::NBUF; ++b) {
+      mbar_init(tfull_bar(b), C::FP8 ? 2 : 1);  // the MMAs' commit and, 8-bit, the scales
+      mbar_init(tempty_bar(b), C::EPI_ARRIVALS);
     }
     mbar_init(drain_bar, 1);
     fence_mbar_init();
   }
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
   if (warp == 1) {
-    tmem_alloc(smem_addr(tmem_slot), C::TMEM_COLS);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(smem_addr(tmem_slot), C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_addr(tmem_slot), C::TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if (PAIR)
+    cluster_sync();  // both CTAs' barriers are initialised before either signals the other
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  if (C::ROW_GROUPS || C::K_GROUPS) build_group_table<BN, KIND>(args, start, first, scan);
-  const PgWalk<BN, KIND> walk{args, start, first};
+  if (C::ROW_GROUPS || C::K_GROUPS) build_group_table<BN, KIND, PAIR>(args, start, first, scan);
+  const PgWalk<BN, KIND, PAIR> walk{args, start, first};
   const int units = walk.units();
-  const int step = static_cast<int>(gridDim.x);
+  const int unit0 = static_cast<int>(blockIdx.x) / (PAIR ? 2 : 1);
+  const int step = static_cast<int>(gridDim.x) / (PAIR ? 2 : 1);
 
   // (Narrower tiles need fewer registers than every thread has at launch.)
   if (warp < 4) {
@@ -400,42 +421,53 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
-      for (int u = static_cast<int>(blockIdx.x); ok && u < units; u += step) {
+      for (int u = unit0; ok && u < units; u += step) {
         const PgTile t = walk.at(u);
         for (int kb = 0; kb < t.nkb; ++kb) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, args.wait_ns)) {
+          if (!mbar_wait<PAIR>(empty_bar(stage), phase ^ 1u, args.wait_ns)) {
             atomicOr(args.fault, kFaultProducerWait);
             ok = false;
             break;
           }
-          const uint32_t fb = full_bar(stage);
+          // (a pair's loads all complete on the leader's barrier)
+          const uint32_t fb = PAIR ? map_shared_rank(full_bar(stage), 0) : full_bar(stage);
           const uint32_t sa = base + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+          auto load2 = [&](uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y) {
+            if (PAIR)
+              tma_load_2d_pair(dst, map, fb, x, y);
+            else
+              tma_load_2d(dst, map, fb, x, y);
+          };
+          auto load3 = [&](uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z) {
+            if (PAIR)
+              tma_load_3d_pair(dst, map, fb, x, y, z);
+            else
+              tma_load_3d(dst, map, fb, x, y, z);
+          };
+          const int k0 = (C::K_GROUPS ? t.row0 : 0) + kb * C::BK;
+          if (rank == 0) mbar_expect_tx(full_bar(stage), (PAIR ? 2 : 1) * (load_a ? C::A_BYTES : C::B_BYTES));
           if (load_a) {
-            mbar_expect_tx(fb, C::A_BYTES);
+            const int m0 = t.tm * C::TM + static_cast<int>(rank) * C::BM;
             if (C::A_MN) {
-              const int k0 = (C::K_GROUPS ? t.row0 : 0) + kb * C::BK;
 #pragma unroll
-              for (int g = 0; g < C::BM / C::MN; ++g)
-                tma_load_2d(sa + g * (C::BK * 128), &tmA, fb, t.tm * C::BM + g * C::MN, k0);
+              for (int g = 0; g < C::BM / C::MN; ++g) load2(sa + g * (C::BK * 128), &tmA, m0 + g * C::MN, k0);
             } else {
-              tma_load_2d(sa, &tmA, fb, kb * C::BK, C::ROW_GROUPS ? t.row0 : t.tm * C::BM);
+              load2(sa, &tmA, kb * C::BK, C::ROW_GROUPS ? t.row0 + static_cast<int>(rank) * C::BM : m0);
             }
           } else {
-            mbar_expect_tx(fb, C::B_BYTES);
-            const int n0 = t.tn * BN;
+            const int n0 = t.tn * BN + static_cast<int>(rank) * C::BNL;
             if (C::B_MN) {
-              const int k0 = (C::K_GROUPS ? t.row0 : 0) + kb * C::BK;
 #pragma unroll
-              for (int g = 0; g < BN / C::MN; ++g) {
+              for (int g = 0; g < C::BNL / C::MN; ++g) {
                 if (C::ROW_GROUPS)
-                  tma_load_3d(sb + g * (C::BK * 128), &tmB, fb, n0 + g * C::MN, k0, t.e);
+                  load3(sb + g * (C::BK * 128), &tmB, n0 + g * C::MN, k0, t.e);
                 else
-                  tma_load_2d(sb + g * (C::BK * 128), &tmB, fb, n0 + g * C::MN, k0);
+                  load2(sb + g * (C::BK * 128), &tmB, n0 + g * C::MN, k0);
               }
             } else if (C::ROW_GROUPS) {
-              tma_load_3d(sb, &tmB, fb, kb * C::BK, n0, t.e);
+              load3(sb, &tmB, kb * C::BK, n0, t.e);
             } else {
-              tma_load_2d(sb, &tmB, fb, kb * C::BK, n0);
+              load2(sb, &tmB, kb * C::BK, n0);
             }
           }
           issued |= 1u << stage;
@@ -446,38 +478,51 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
           }
         }
       }
-      // every load has landed before the CTA may exit
+      // every load has landed before the CTA may exit (a pair's: the MMAs that read it are done)
       for (int s = 0; s < STAGES; ++s)
         if ((issued >> s) & 1u)
-          if (!mbar_wait(full_bar(s), (issued_phase >> s) & 1u, args.wait_ns)) atomicOr(args.fault, kFaultDrainWait);
+          if (!mbar_wait<PAIR>(PAIR ? empty_bar(s) : full_bar(s), (issued_phase >> s) & 1u, args.wait_ns))
+            atomicOr(args.fault, kFaultDrainWait);
     }
   } else if (warp == 1) {
+    if (rank == 0) {
     // ------------------------------------------------------------- MMA issuer
-    // (the whole warp walks the list: its lanes zero the rows of a ragged last block)
+    // One elected thread walks the list (297 cycles a block with nothing to wait for, against
+    // 415 where the whole warp walks it, votes and elects for each block: a block's MMAs take
+    // 512).  Ragged contractions need the warp: its lanes zero the rows of a last block.
+    constexpr bool SOLO = !C::K_GROUPS;
+    if (!SOLO || elect_one()) {
+    auto all = [](bool in) { return SOLO ? in : __all_sync(0xffffffffu, in) != 0; };
+    auto one = []() { return SOLO || elect_one(); };
+    auto give_up = [&]() {
+      if (SOLO || lane == 0) atomicOr(args.fault, kFaultMmaWait);
+      return false;
+    };
     int stage = 0, buf = 0;
     uint32_t phase = 0, bphase = 0;
     bool ok = true;
     // descriptors of stage 0 and their step per slice: K-major 32 bytes along the swizzled row,
     // MN-major SLICE rows of 128 bytes (see sdesc_sw128)
     constexpr uint32_t A_STEP = C::A_MN ? C::SLICE * 8 : 2, B_STEP = C::B_MN ? C::SLICE * 8 : 2;
+    // B of the second 128-column MMA: 128 K-major rows further, or the next MN-major box.  A
+    // pair's MMA takes 64 of its columns from each CTA: 64 rows further, or 64 bytes along the
+    // rows of the one box (see tile_col for the columns this makes).
+    constexpr uint32_t SUB_STEP = !PAIR ? 128 * 128 / 16 : C::B_MN ? 64 / 16 : 64 * 128 / 16;
     const uint64_t a_desc = sdesc_sw128(base, C::A_MN ? C::BK * 128 : 16, 1024);
     const uint64_t b_desc = sdesc_sw128(base + C::A_BYTES, C::B_MN ? C::BK * 128 : 16, 1024);
     const uint32_t a_lo = static_cast<uint32_t>(a_desc), a_hi = static_cast<uint32_t>(a_desc >> 32);
     const uint32_t b_lo = static_cast<uint32_t>(b_desc), b_hi = static_cast<uint32_t>(b_desc >> 32);
-    for (int u = static_cast<int>(blockIdx.x); ok && u < units; u += step) {
+    for (int u = unit0; ok && u < units; u += step) {
       const PgTile t = walk.at(u);
       for (int c0 = 0; ok && c0 < t.nkb; c0 += CHUNK) {
         const int c1 = min(c0 + CHUNK, t.nkb);
-        if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar(buf), bphase ^ 1u, args.wait_ns))) {
-          if (lane == 0) atomicOr(args.fault, kFaultMmaWait);
-          ok = false;
-          break;
-        }
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * BN);
+        auto wait_empty = [&](int b) {
+          return all(mbar_wait_soon<PAIR>(tempty_bar(b), bphase ^ 1u, args.wait_ns)) || give_up();
+        };
+        if (!(ok = wait_empty(buf))) break;
         for (int kb = c0; kb < c1; ++kb) {
-          if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, args.wait_ns))) {
-            if (lane == 0) atomicOr(args.fault, kFaultMmaWait);
-            ok = false;
+          if (!all(mbar_wait_soon<PAIR>(full_bar(stage), phase, args.wait_ns))) {
+            ok = give_up();
             break;
           }
           int slices = C::BK / C::SLICE;
@@ -498,179 +543,228 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
               __syncwarp();
             }
           }
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t at = static_cast<uint32_t>(stage) * (C::STAGE_BYTES >> 4);
-            auto issue = [&](int kk) {
-              mma_lo<C::FP8>(d_tmem, a_lo + at + kk * A_STEP, a_hi, b_lo + at + kk * B_STEP, b_hi, args.idesc,
-                             (kb > c0 || kk > 0) ? 1u : 0u);
-            };
-            if (C::K_GROUPS && slices < C::BK / C::SLICE) {
-              for (int kk = 0; kk < slices; ++kk) issue(kk);
-            } else {
 #pragma unroll
-              for (int kk = 0; kk < C::BK / C::SLICE; ++kk) issue(kk);
+          for (int sub = 0; sub < C::NSUB; ++sub) {
+            if (sub > 0 && !(ok = wait_empty(buf + sub))) break;
+            tc_fence_after();
+            if (one()) {
+              const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((buf + sub) * C::SUB);
+              const uint32_t at = static_cast<uint32_t>(stage) * (C::STAGE_BYTES >> 4);
+              auto issue = [&](int kk) {
+                mma_lo<C::FP8, PAIR>(d_tmem, a_lo + at + kk * A_STEP, a_hi, b_lo + at + sub * SUB_STEP + kk * B_STEP, b_hi,
+                                     args.idesc, (kb > c0 || kk > 0) ? 1u : 0u);
+              };
+              if (C::K_GROUPS && slices < C::BK / C::SLICE) {
+                for (int kk = 0; kk < slices; ++kk) issue(kk);
+              } else {
+#pragma unroll
+                for (int kk = 0; kk < C::BK / C::SLICE; ++kk) issue(kk);
+              }
+              auto commit = [&](uint32_t bar) {  // (in both CTAs of a pair)
+                if (PAIR)
+                  mma_commit_pair_multicast(bar, 0x3);
+                else
+                  mma_commit(bar);
+              };
+              if (sub == C::NSUB - 1) commit(empty_bar(stage));
+              if (kb + 1 == c1) commit(tfull_bar(buf + sub));
             }
-            mma_commit(empty_bar(stage));
-            if (kb + 1 == c1) mma_commit(tfull_bar(buf));
+            if (!SOLO) __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        if (++buf == 2) {
+        if ((buf += C::NSUB) == C::NBUF) {
           buf = 0;
           bphase ^= 1u;
         }
       }
     }
-    // every MMA has finished before TMEM is freed (each commit covers the MMAs of the lane
-    // that issues it: the elected lane is the same one throughout)
-    if (elect_one()) {
-      mma_commit(drain_bar);
+    // every MMA has finished before TMEM is freed (a commit covers the MMAs of the thread that
+    // issues it: the elected one is the same throughout)
+    if (one()) {
+      if (PAIR)
+        mma_commit_pair(drain_bar);
+      else
+        mma_commit(drain_bar);
       if (!mbar_wait(drain_bar, 0, args.wait_ns)) atomicOr(args.fault, kFaultDrainWait);
     }
+    }
     __syncwarp();
+    }
   } else if (C::FP8) {
     // ------------------------------------------------------------------ scales
-    int slot = 0;
-    uint32_t sphase = 0;
+    // A chunk's accumulator barriers take an arrival of this warp beside the MMAs' commit, so the
+    // epilogue waits once for the sums and their scales.  The arrival may be made once the
+    // barrier's phase before is over (the chunk NBUF / NSUB earlier); the loads run kScaleAhead
+    // chunks ahead of it, in registers.  A ring slot's last readers are done by then: they gave
+    // back the accumulator of a later chunk, which the MMAs of that earlier phase overwrote.
+    static_assert(!C::FP8 || C::SCALE_SLOTS > 2 * C::NBUF / C::NSUB, "scale ring");
+    constexpr int NB = C::COL_SCALES ? BN / 32 : 2, NV = 4 + NB;
+    float v[kScaleAhead][NV];
+    int lu = unit0, left = 0;  // tile of the next load, chunks left in it
+    const float* at[NV];
+    bool in[NV];
+    // (rows and columns past the edges have zero operands: their scale is zero)
+    auto load = [&](float (&x)[NV]) {
+      if (left == 0) {
+        if (lu >= units) return;
+        const PgTile t = walk.at(lu);
+        lu += step;
+        left = t.nkb;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int m = t.tm * C::TM + static_cast<int>(rank) * C::BM + 32 * j + lane;
+          in[j] = m < args.gm;
+          at[j] = args.sa + (in[j] ? m * args.sa_row : 0);
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const int n = t.tn * BN + (C::COL_SCALES ? 32 * j + lane : 128 * j);
+          in[4 + j] = n < args.gn;
+          at[4 + j] = args.sb + (in[4 + j] ? (C::COL_SCALES ? n : n / 128) * args.sb_row : 0);
+        }
+      }
+      --left;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        x[j] = in[j] ? __ldg(at[j]) : 0.0f;
+        at[j] += j < 4 ? args.sa_blk : args.sb_blk;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kScaleAhead; ++i) load(v[i]);
+    const int nkb = (args.gk + C::BK - 1) / C::BK;  // (the same for every tile)
+    const int total = unit0 < units ? ((units - unit0 + step - 1) / step) * nkb : 0;
     bool ok = true;
-    for (int u = static_cast<int>(blockIdx.x); ok && u < units; u += step) {
-      const PgTile t = walk.at(u);
-      // (rows and columns past the edges have zero operands: their scale is zero)
-      const float* pa[4];
-      bool in_a[4];
+    for (int i0 = 0; ok && i0 < total; i0 += kScaleAhead) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = t.tm * C::BM + 32 * j + lane;
-        in_a[j] = m < args.gm;
-        pa[j] = args.sa + (in_a[j] ? m * args.sa_row : 0);
-      }
-      constexpr int NB = C::COL_SCALES ? BN / 32 : 1;
-      const float* pb[NB];
-      bool in_b[NB];
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const int n = t.tn * BN + (C::COL_SCALES ? 32 * j + lane : 128 * lane);
-        in_b[j] = n < args.gn;
-        pb[j] = args.sb + (in_b[j] ? (C::COL_SCALES ? n : n / 128) * args.sb_row : 0);
-      }
-      for (int kb = 0; kb < t.nkb; ++kb) {
-        if (!__all_sync(0xffffffffu, mbar_wait(sempty_bar(slot), sphase ^ 1u, args.wait_ns))) {
+      for (int k = 0; k < kScaleAhead; ++k) {
+        const int i = i0 + k;
+        if (i >= total) break;
+        const int b = i * C::NSUB % C::NBUF;
+        const uint32_t parity = ((i * C::NSUB / C::NBUF) & 1) ^ 1;
+        bool free = mbar_wait_soon<PAIR>(tfull_bar(b), parity, args.wait_ns);
+        if (C::NSUB == 2) free = free && mbar_wait_soon<PAIR>(tfull_bar(b + 1), parity, args.wait_ns);
+        if (!__all_sync(0xffffffffu, free)) {
           if (lane == 0) atomicOr(args.fault, kFaultProducerWait);
           ok = false;
           break;
         }
-        const uint32_t dst = scbase + static_cast<uint32_t>(slot) * (C::SCALE_FLOATS * 4);
+        const uint32_t dst = scbase + static_cast<uint32_t>(i % C::SCALE_SLOTS) * (C::SCALE_FLOATS * 4);
+        if (C::COL_SCALES) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          cp_async4(dst + (32 * j + lane) * 4, pa[j], in_a[j]);
-          pa[j] += in_a[j] ? args.sa_blk : 0;
-        }
+          for (int j = 0; j < NV; ++j) st_shared_f32(dst + (32 * j + lane) * 4, v[k][j]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          if (C::COL_SCALES || lane < (BN + 127) / 128) cp_async4(dst + (128 + 32 * j + lane) * 4, pb[j], in_b[j]);
-          pb[j] += in_b[j] ? args.sb_blk : 0;
+          for (int j = 0; j < 4; ++j) st_shared_f2(dst + (32 * j + lane) * 8, v[k][j] * v[k][4], v[k][j] * v[k][5]);
         }
-        cp_async_arrive(sfull_bar(slot));
-        if (++slot == C::SCALE_SLOTS) {
-          slot = 0;
-          sphase ^= 1u;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(tfull_bar(b));
+          if (C::NSUB == 2) mbar_arrive(tfull_bar(b + 1));
         }
+        load(v[k]);
       }
     }
-    // one empty slot past the last chunk: the epilogue looks one ahead
-    if (ok && __all_sync(0xffffffffu, mbar_wait(sempty_bar(slot), sphase ^ 1u, args.wait_ns)))
-      cp_async_arrive(sfull_bar(slot));
-    cp_async_wait_all();
   }
   } else {
     // -------------------------------------------------- promotion and epilogue
     if (BN == 256) regs_take<208>();
     const int q = warp & 3, h = (warp - 4) >> 2;
-    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * C::HALF);
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                               static_cast<uint32_t>(C::NSUB == 2 ? 0 : h * C::HALF);
     const uint32_t ebuf = ebase + static_cast<uint32_t>(warp - 4) * 2048u;
+    // The tile's column of this warp's accumulator c.  A pair's MMA h has 64 columns from the
+    // first and 64 from the second half of the tile.
+    auto tile_col = [&](int c) { return !PAIR ? h * C::HALF + c : 64 * h + c + (c < 64 ? 0 : 64); };
     // (Beside 128 accumulators registers are short: one counter gives every ring position, and
     // the tile is decoded again for the store.)
     uint32_t it = 0;  // chunks done by this CTA
     bool ok = true;
-    float next = 1.0f;  // this row's factor for chunk `it`, read one chunk ahead
-    auto read_scale = [&](uint32_t i) {
-      const bool in = mbar_wait(sfull_bar(i % kScaleSlots), (i / kScaleSlots) & 1u, args.wait_ns);
-      const uint32_t at = scbase + (i % kScaleSlots) * (C::SCALE_FLOATS * 4);
-      next = ld_shared_f32(at + (q * 32 + lane) * 4);
-      if (!C::COL_SCALES) next *= ld_shared_f32(at + (128 + (BN == 256 ? h : 0)) * 4);
-      return in;
-    };
-    if (C::FP8) ok = read_scale(0);
-    for (int u = static_cast<int>(blockIdx.x); u < units; u += step) {
+    for (int u = unit0; u < units; u += step) {
       uint64_t acc[C::HALF / 2];  // pairs of columns
 #pragma unroll
       for (int j = 0; j < C::HALF / 2; ++j) acc[j] = 0;
       for (int left = (walk.at(u).nkb + CHUNK - 1) / CHUNK; left > 0; --left, ++it) {
-        const uint64_t s = pack_f32x2(next, next);
-        const uint32_t xcol = scbase + (it % kScaleSlots) * (C::SCALE_FLOATS * 4) + (128 + h * C::HALF) * 4;
-        if (C::FP8) ok = read_scale(it + 1) && ok;
-        ok = mbar_wait(tfull_bar(it & 1u), (it >> 1) & 1u, args.wait_ns) && ok;
-        if (!__all_sync(0xffffffffu, ok)) {
+        const uint32_t buf = C::NSUB == 2 ? 2 * (it & 1u) + static_cast<uint32_t>(h) : it % C::NBUF;
+        const uint32_t parity = (it * C::NSUB / C::NBUF) & 1u;
+        if (!__all_sync(0xffffffffu, mbar_wait_soon<PAIR>(tfull_bar(buf), parity, args.wait_ns))) {
           if (lane == 0) atomicOr(args.fault, kFaultEpilogueWait);
           ok = false;
           break;
         }
+        const uint32_t sc = scbase + (it % C::SCALE_SLOTS) * (C::SCALE_FLOATS * 4);
+        float f0 = 1.0f, f1 = 1.0f;  // this row's factors (f1: a pair's second 64 columns)
+        if (C::COL_SCALES) {
+          f0 = f1 = ld_shared_f32(sc + (q * 32 + lane) * 4);
+        } else if (C::FP8) {
+          const float2 f = ld_shared_f2(sc + (q * 32 + lane) * 8);
+          f0 = !PAIR && C::NSUB == 2 && h == 1 ? f.y : f.x;
+          f1 = f.y;
+        }
+        const uint64_t s0 = pack_f32x2(f0, f0), s1 = pack_f32x2(f1, f1);
         tc_fence_after();
-        const uint32_t t_addr = lane_addr + (it & 1u) * BN;
-        // 32 columns at a time.  Where the registers allow it the next 32 are on their way from
-        // TMEM while these are added; beside 128 accumulators they do not (the pairs would be
-        // copied to make room: 107 moves a chunk, 85 against 61 us at T = 4031, 4096 -> 4096),
-        // and the other warp of the SM sub-partition adds while this one loads.
-        constexpr int AHEAD = C::HALF <= 64 ? 1 : 0;
-        uint32_t r[1 + AHEAD][32];
-        if (AHEAD) tmem_ld_32x32b_x32(t_addr, r[0]);
-#pragma unroll
-        for (int c = 0; c < C::HALF; c += 32) {
-          uint32_t(&v)[32] = r[AHEAD ? (c / 32) & 1 : 0];
-          if (!AHEAD) tmem_ld_32x32b_x32(t_addr + c, v);
-          tmem_wait_ld();
-          if (c + 32 < C::HALF) {
-            if (AHEAD) tmem_ld_32x32b_x32(t_addr + c + 32, r[(c / 32 + 1) & 1]);
-          } else {  // the accumulator is read: the next chunk but one may use it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tempty_bar(it & 1u));
-          }
+        const uint32_t t_addr = lane_addr + buf * C::SUB;
+        // 32 columns at a time through two register blocks: both are loaded, then each is refilled
+        // as soon as its columns are added, so that a chunk waits for TMEM twice at most.
+        auto add32 = [&](uint32_t (&v)[32], int c) {
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             uint64_t lo = pack_u32x2(v[j], v[j + 1]), hi = pack_u32x2(v[j + 2], v[j + 3]);
             uint64_t& a0 = acc[(c + j) / 2];
             uint64_t& a1 = acc[(c + j) / 2 + 1];
             if (C::COL_SCALES) {
-              const float4 x = ld_shared_f4(xcol + (c + j) * 4);
+              const float4 x = ld_shared_f4(sc + (128 + tile_col(c) + j) * 4);
               lo = mul_f32x2(lo, pack_f32x2(x.x, x.y));
               hi = mul_f32x2(hi, pack_f32x2(x.z, x.w));
             }
+            const uint64_t s = PAIR && c >= 64 ? s1 : s0;
             a0 = C::FP8 ? fma_f32x2(lo, s, a0) : add_f32x2(lo, a0);
             a1 = C::FP8 ? fma_f32x2(hi, s, a1) : add_f32x2(hi, a1);
           }
-        }
-        if (C::FP8) {
-          __syncwarp();  // every lane has read its scales
-          if (lane == 0) mbar_arrive(sempty_bar(it % kScaleSlots));
+        };
+        auto release = [&]() {  // the accumulator is read: later MMAs may use the buffer
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR)
+              mbar_arrive_remote(map_shared_rank(tempty_bar(buf), 0));
+            else
+              mbar_arrive(tempty_bar(buf));
+          }
+        };
+        uint32_t r0[32], r1[32];
+        tmem_ld_32x32b_x32(t_addr, r0);
+        if (C::HALF >= 64) tmem_ld_32x32b_x32(t_addr + 32, r1);
+        tmem_wait_ld();
+        if (C::HALF <= 64) release();
+        add32(r0, 0);
+        if (C::HALF == 128) tmem_ld_32x32b_x32(t_addr + 64, r0);
+        if (C::HALF >= 64) add32(r1, 32);
+        if (C::HALF == 128) {
+          tmem_ld_32x32b_x32(t_addr + 96, r1);
+          tmem_wait_ld();
+          release();
+          add32(r0, 64);
+          add32(r1, 96);
         }
       }
       if (!ok) break;
       int us = u;
       asm volatile("" : "+r"(us));
       const PgTile t = walk.at(us);
-      const int n0 = t.tn * BN + h * C::HALF;  // this warp's first column
+      const int n0 = t.tn * BN;
       // Store 32 rows x HALF columns through the warp's 2 KB block: 64-byte rows (32 BF16 or
       // 16 FP32 columns), 16-byte chunks XOR-swizzled by row, read back so that four lanes
       // write 64 consecutive bytes of a row.
-      const int rows_left = t.m_left - q * 32;
-      const int64_t row = (C::ROW_GROUPS ? static_cast<int64_t>(t.row0) : static_cast<int64_t>(t.tm) * C::BM) + q * 32;
+      const int half_row = static_cast<int>(rank) * C::BM + q * 32;  // of the tile's rows
+      const int rows_left = t.m_left - half_row;
+      const int64_t row = (C::ROW_GROUPS ? static_cast<int64_t>(t.row0) : static_cast<int64_t>(t.tm) * C::TM) + half_row;
       const int esize = args.out_f32 ? 4 : 2;
       char* out = static_cast<char*>(args.out) +
                   ((C::K_GROUPS ? t.e * args.out_gstride : int64_t{0}) + row * args.ldo) * esize;
@@ -697,7 +791,7 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
             st_shared_u4(ebuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4),
                          make_uint4(lo32(c / 2 + 2 * j), hi32(c / 2 + 2 * j), lo32(c / 2 + 2 * j + 1), hi32(c / 2 + 2 * j + 1)));
           __syncwarp();
-          flush(n0 + c, 4);
+          flush(n0 + tile_col(c), 4);
         }
       } else {
 #pragma unroll
@@ -709,7 +803,7 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
                          make_uint4(bf16x2(c / 2 + 4 * j), bf16x2(c / 2 + 4 * j + 1), bf16x2(c / 2 + 4 * j + 2),
                                     bf16x2(c / 2 + 4 * j + 3)));
           __syncwarp();
-          flush(n0 + c, 8);
+          flush(n0 + tile_col(c), 8);
         }
       }
     }
@@ -717,7 +811,7 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
     if (C::ROW_GROUPS) {
       const int lo = start[0], hi = start[args.experts], esize = args.out_f32 ? 4 : 2;
       const int64_t idle = static_cast<int64_t>(lo) + (args.rows - hi);
-      for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (warp - 4); i < idle; i += static_cast<int64_t>(step) * 8) {
+      for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (warp - 4); i < idle; i += static_cast<int64_t>(gridDim.x) * 8) {
         const int64_t r = i < lo ? i : hi + (i - lo);
         char* p = static_cast<char*>(args.out) + r * args.ldo * esize;
         for (int b = lane * 16; b < args.gn * esize; b += 512) *reinterpret_cast<uint4*>(p + b) = make_uint4(0, 0, 0, 0);
@@ -726,10 +820,17 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND>::THREADS, 1)
   }
 
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  if (PAIR)
+    cluster_sync();  // neither CTA leaves while the other may still signal it or read its operands
+  else
+    __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, C::TMEM_COLS);
+    if (PAIR)
+      tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
 }
 
@@ -741,31 +842,41 @@ struct PgLaunch {
   int grid;
 };
 
-// gemm_grouped.cu / gemm_fp8.cu: one launch of the kernel of that kind and tile width.
+// gemm_grouped.cu / gemm_fp8.cu: one launch of the kernel of that kind, tile width and form.
 cudaError_t launch_grouped(int kind, int bn, const PgLaunch& l, cudaStream_t stream);
-cudaError_t launch_fp8(int kind, int bn, const PgLaunch& l, cudaStream_t stream);
+cudaError_t launch_fp8(int kind, int bn, bool pair, const PgLaunch& l, cudaStream_t stream);
 cudaError_t set_attributes_grouped();
 cudaError_t set_attributes_fp8();
 
-template <int BN, int KIND>
+template <int BN, int KIND, bool PAIR = false>
 cudaError_t launch_pg(const PgLaunch& l, cudaStream_t stream) {
-  promoted_gemm_kernel<BN, KIND><<<static_cast<unsigned>(l.grid), PgCfg<BN, KIND>::THREADS, PgCfg<BN, KIND>::SMEM_BYTES,
-                                   stream>>>(l.tmA, l.tmB, l.args);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(l.grid), 1, 1);
+  cfg.blockDim = dim3(PgCfg<BN, KIND, PAIR>::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = PgCfg<BN, KIND, PAIR>::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, promoted_gemm_kernel<BN, KIND, PAIR>, l.tmA, l.tmB, l.args);
 }
 
-template <int BN, int KIND>
+template <int BN, int KIND, bool PAIR = false>
 cudaError_t set_attr_pg() {
-  cudaError_t e = cudaFuncSetAttribute(promoted_gemm_kernel<BN, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       PgCfg<BN, KIND>::SMEM_BYTES);
+  const auto kernel = promoted_gemm_kernel<BN, KIND, PAIR>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       PgCfg<BN, KIND, PAIR>::SMEM_BYTES);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(promoted_gemm_kernel<BN, KIND>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (BN == 256 && e == cudaSuccess) {
     // the warpgroups trade exactly the registers of a launch at 168 a thread (regs_take
     // would wait for ever on fewer): refuse to run a build that launches with another count
     cudaFuncAttributes f;
-    e = cudaFuncGetAttributes(&f, promoted_gemm_kernel<BN, KIND>);
+    e = cudaFuncGetAttributes(&f, kernel);
     if (e == cudaSuccess && f.numRegs < 168) e = cudaErrorInvalidConfiguration;
   }
   return e;

@@ -115,6 +115,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
   }
 }
 
+// The same with a non-suspending test first: ~20 cycles where the phase has completed, against
+// ~50 for a satisfied try_wait (measured on GB300).
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  return (CLUSTER ? mbar_peek_cluster(bar, parity) : mbar_peek(bar, parity)) || mbar_wait<CLUSTER>(bar, parity, limit_ns);
+}
+
 // Programmatic dependent launch: let the grid launched after this one on the
 // stream (with the programmatic-serialisation attribute) start its prologue now;
 // and, in that dependent grid, wait until this grid has completed and its memory

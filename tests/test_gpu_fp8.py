@@ -153,10 +153,21 @@ def test_exact_products(op, T, N, K):
     assert dp.device_error() == 0
 
 
+@pytest.mark.parametrize("T,N,K", [(2500, 2064, 2064), (2305, 2320, 2576), (4096, 2048, 1664)])
+@pytest.mark.parametrize("op", OPS)
+def test_exact_products_on_many_tiles(op, T, N, K):
+    """Sizes whose tiles fill the device: two SMs share a tile of 256 x 256, ragged at its edges."""
+    (a, da), (b, db) = operands(op, T, N, K, T + N, ints=True)
+    ref = product(op, da, db)
+    assert torch.equal(call(op, a, b, out_dtype=torch.float32), ref.float())
+    assert torch.equal(call(op, a, b), ref.to(torch.bfloat16))
+    assert dp.device_error() == 0
+
+
 @pytest.mark.parametrize("fa,fb", [(E4, E4), (E5, E4), (E4, E5), (E5, E5)])
 @pytest.mark.parametrize("op", OPS)
 def test_real_products(op, fa, fb):
-    for T, N, K in ((1, 272, 528), (333, 1040, 656), (2000, 256, 4112)):
+    for T, N, K in ((1, 272, 528), (333, 1040, 656), (2000, 256, 4112), (2600, 2064, 2192)):
         (a, da), (b, db) = operands(op, T, N, K, T, fa, fb)
         ref, mag = product(op, da, db), product(op, da.abs(), db.abs())
         tol = (24 + 2 * blocks({"fwd": K, "dgrad": N, "wgrad": T}[op])) * 2.0 ** -23 * mag
