@@ -5,14 +5,17 @@
 // weight gradient), or 128 x 128 (weights).  Row and column blocks together come from one
 // read of x.
 //
-// Bound: HBM bytes (2 or 4 read, 1 or 2 written per value).  One CTA takes a 128 x 128 tile
-// and keeps it in registers (64 values a thread: 16 rows x 4 columns), so x is read once
-// whatever the blocks; a thread's 16 loads are in flight together.  A row's maximum is a
-// shuffle reduction of one warp, a column's a maximum over the warps in shared memory.
+// Bound: HBM bytes (2 or 4 read, 1 or 2 written per value).  One CTA of 16 warps takes a
+// 128 x 128 tile and keeps it in registers (BF16 pairs packed), so x is read once whatever the
+// blocks; a thread's loads are in flight together and several CTAs share an SM, so that one
+// tile's loads run beside another's stores.  What stands beside the bytes is instructions: the
+// first form (FP32 in registers, a division per lane and row) took 32 a value and 107 us for
+// 16384 x 4096 BF16, rows and columns.  A row's maximum is a shuffle reduction of two rows at a
+// time, a column's a maximum over the warps in shared memory.
 //
-// Maxima are taken on the bits of |x| as integers: that order puts NaN above infinity, so
-// a block with a NaN gets a NaN scale (and one with an infinity an infinite scale, whose
-// products are NaN) instead of hiding it.
+// Maxima are taken on the bits of |x| as integers (two BF16 at a time): that order puts NaN
+// above infinity, so a block with a NaN gets a NaN scale (and one with an infinity an
+// infinite scale, whose products are NaN) instead of hiding it.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -54,94 +57,147 @@ __device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) {
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
 // The block's maximum with its lower bound (a NaN stays).
 __device__ __forceinline__ float block_max(uint32_t bits) {
   const float a = __uint_as_float(bits);
   return a < kTinyMax ? kTinyMax : a;
 }
 
+// Maxima of |x| as bits: one 32-bit word per FP32 value, or two BF16 in the halves of a word.
+template <bool F32>
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint32_t x) {
+  return F32 ? max(m, x & 0x7FFFFFFFu) : __vmaxu2(m, x & 0x7FFF7FFFu);
+}
+
+constexpr int kWarps = 16;  // warps of a CTA, 8 rows each
+
+// A thread holds 16 bytes (4 FP32 or 8 BF16 columns) of each of ITERS rows: a warp's load covers
+// one FP32 row or two BF16 rows of the tile.
 template <int MODE, bool F32, bool E5M2>
-__global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 2) quantize_kernel(const __grid_constant__ QuantArgs a) {
   constexpr float kTop = E5M2 ? 57344.0f : 448.0f;
   constexpr bool COL = MODE == kCol || MODE == kBoth, ROW = MODE == kRow || MODE == kBoth;
-  __shared__ uint32_t part[8][128];
+  constexpr int CPL = F32 ? 4 : 8, LPR = 128 / CPL, RPI = 32 / LPR, ITERS = 8 / RPI;
+  __shared__ __align__(16) uint32_t part[COL ? kWarps * RPI : 1][COL ? LPR * 4 : 32];
+  __shared__ __align__(16) float factors[COL ? 128 : 4];
   const int lane = static_cast<int>(threadIdx.x) & 31, warp = static_cast<int>(threadIdx.x) >> 5;
   const int cb = static_cast<int>(blockIdx.x) % a.blk_cols, rb = static_cast<int>(blockIdx.x) / a.blk_cols;
-  const int col = cb * 128 + lane * 4, row0 = rb * 128 + warp * 16;
-  const bool col_ok = col < a.cols;  // (cols is a multiple of 16: a thread's four columns exist together)
-  float v[16][4];
+  const int tcol = lane % LPR * CPL, col = cb * 128 + tcol;
+  const int row0 = rb * 128 + warp * 8 + lane / LPR;  // this thread's rows: row0 + RPI * i
+  // (cols is a multiple of 16: a thread's columns exist together)
+  const int rows = col < a.cols ? a.rows - row0 : 0;
+  uint32_t v[ITERS][4];
+  {
+    const int esize = F32 ? 4 : 2;
+    const char* p = static_cast<const char*>(a.x) + (row0 * a.ldx + col) * esize;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.0f;
-    if (col_ok && row0 + i < a.rows) {
-      const int64_t at = (row0 + i) * a.ldx + col;
-      if (F32) {
-        const float4 x = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + at));
-        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-      } else {
-        const uint2 x = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + at));
-        v[i][0] = __uint_as_float(x.x << 16), v[i][1] = __uint_as_float(x.x & 0xFFFF0000u);
-        v[i][2] = __uint_as_float(x.y << 16), v[i][3] = __uint_as_float(x.y & 0xFFFF0000u);
-      }
+    for (int i = 0; i < ITERS; ++i, p += RPI * a.ldx * esize) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (RPI * i < rows) x = __ldg(reinterpret_cast<const uint4*>(p));
+      v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
     }
   }
-  if (ROW) {
-    float mine = 0.0f;  // lane i keeps row i's scale
+  auto value = [&](int i, int j) {
+    if (F32) return __uint_as_float(v[i][j & 3]);
+    return __uint_as_float(j & 1 ? v[i][j >> 1] & 0xFFFF0000u : v[i][j >> 1] << 16);
+  };
+  // row i's codes: values times factors (one for the row, or one per column)
+  auto store = [&](uint8_t* p, int i, auto factor) {
+    if (RPI * i >= rows) return;
+    uint32_t w[CPL / 4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      uint32_t m = max(max(abs_bits(v[i][0]), abs_bits(v[i][1])), max(abs_bits(v[i][2]), abs_bits(v[i][3])));
-      m = __reduce_max_sync(0xffffffffu, m);
-      const float top = block_max(m), f = __fdiv_rn(kTop, top);
-      if (lane == i) mine = __fdiv_rn(top, kTop);
-      if (col_ok && row0 + i < a.rows)
-        *reinterpret_cast<uint32_t*>(a.q + (row0 + i) * a.ldq + col) =
-            cvt4<E5M2>(__fmul_rn(v[i][0], f), __fmul_rn(v[i][1], f), __fmul_rn(v[i][2], f), __fmul_rn(v[i][3], f));
+    for (int j = 0; j < CPL; j += 4)
+      w[j / 4] = cvt4<E5M2>(__fmul_rn(value(i, j), factor(j)), __fmul_rn(value(i, j + 1), factor(j + 1)),
+                            __fmul_rn(value(i, j + 2), factor(j + 2)), __fmul_rn(value(i, j + 3), factor(j + 3)));
+    if (F32)
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[CPL / 4 - 1]);
+  };
+  // (Quotients are IEEE divisions of ~10 instructions: each is taken once and passed on.)
+  if (ROW) {
+    uint32_t m[ITERS];
+#pragma unroll
+    for (int i = 0; i < ITERS; ++i) {
+      m[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[i] = max_bits<F32>(m[i], v[i][j]);
     }
-    if (lane < 16 && row0 + lane < a.rows) a.s[(row0 + lane) * a.s_row + cb * a.s_col] = mine;
+    uint32_t mine = 0;  // the maximum of row row0 + RPI * (lane % ITERS)
+    if (F32) {
+#pragma unroll
+      for (int i = 0; i < ITERS; ++i) {
+        const uint32_t r = __reduce_max_sync(0xffffffffu, m[i]);
+        if (lane % ITERS == i) mine = r;
+      }
+    } else {
+      // two rows' maxima in the halves of a word, reduced over the 16 lanes of a row
+#pragma unroll
+      for (int i = 0; i < ITERS; i += 2) {
+        const uint32_t lo = __vmaxu2(m[i], m[i] >> 16) & 0xFFFFu, hi = __vmaxu2(m[i + 1], m[i + 1] << 16) & 0xFFFF0000u;
+        uint32_t r = lo | hi;
+#pragma unroll
+        for (int d = 1; d < LPR; d <<= 1) r = __vmaxu2(r, __shfl_xor_sync(0xffffffffu, r, d));
+        if (lane % ITERS == i) mine = r << 16;
+        if (lane % ITERS == i + 1) mine = r & 0xFFFF0000u;
+      }
+    }
+    const float top = block_max(mine), f = __fdiv_rn(kTop, top);
+    const int srow = row0 + RPI * (lane % ITERS);
+    if (lane % LPR < ITERS && srow < a.rows) a.s[srow * a.s_row + cb * a.s_col] = __fdiv_rn(top, kTop);
+    uint8_t* p = a.q + row0 * a.ldq + col;
+#pragma unroll
+    for (int i = 0; i < ITERS; ++i, p += RPI * a.ldq) {
+      const float fi = __shfl_sync(0xffffffffu, f, lane / LPR * LPR + i);
+      store(p, i, [&](int) { return fi; });
+    }
   }
   if (MODE != kRow) {
-    uint32_t m[4] = {0, 0, 0, 0};
+    uint32_t m[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int j = 0; j < 4; ++j) {
+      m[j] = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) m[j] = max(m[j], abs_bits(v[i][j]));
+      for (int i = 0; i < ITERS; ++i) m[j] = max_bits<F32>(m[j], v[i][j]);
+    }
     if (MODE == kBlock) {
-      const uint32_t w = __reduce_max_sync(0xffffffffu, max(max(m[0], m[1]), max(m[2], m[3])));
+#pragma unroll
+      for (int j = 1; j < 4; ++j) m[0] = max_bits<F32>(m[0], m[j]);
+      if (!F32) m[0] = max(m[0] << 16, m[0] & 0xFFFF0000u);
+      const uint32_t w = __reduce_max_sync(0xffffffffu, m[0]);
       if (lane == 0) part[0][warp] = w;
       __syncthreads();
-      uint32_t all = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) all = max(all, part[0][k]);
-      const float top = block_max(all), f = __fdiv_rn(kTop, top);
+      const float top = block_max(__reduce_max_sync(0xffffffffu, part[0][lane % kWarps])), f = __fdiv_rn(kTop, top);
       if (threadIdx.x == 0) a.s[rb * a.s_row + cb * a.s_col] = __fdiv_rn(top, kTop);
+      uint8_t* p = a.q + row0 * a.ldq + col;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (col_ok && row0 + i < a.rows)
-          *reinterpret_cast<uint32_t*>(a.q + (row0 + i) * a.ldq + col) =
-              cvt4<E5M2>(__fmul_rn(v[i][0], f), __fmul_rn(v[i][1], f), __fmul_rn(v[i][2], f), __fmul_rn(v[i][3], f));
+      for (int i = 0; i < ITERS; ++i, p += RPI * a.ldq) store(p, i, [&](int) { return f; });
     }
     if (COL) {
-      *reinterpret_cast<uint4*>(&part[warp][lane * 4]) = make_uint4(m[0], m[1], m[2], m[3]);
+      *reinterpret_cast<uint4*>(&part[warp * RPI + lane / LPR][lane % LPR * 4]) = make_uint4(m[0], m[1], m[2], m[3]);
       __syncthreads();
-      float f[4];
-      float4 sc;
+      // one thread per word of maxima: 1 FP32 or 2 BF16 columns and their factors
+      if (threadIdx.x < LPR * 4) {
+        const int t = static_cast<int>(threadIdx.x);
+        uint32_t w = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t all = 0;
+        for (int k = 0; k < kWarps * RPI; ++k) w = max_bits<F32>(w, part[k][t]);
+        constexpr int PER = CPL / 4;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) all = max(all, part[k][lane * 4 + j]);
-        const float top = block_max(all);
-        f[j] = __fdiv_rn(kTop, top);
-        (&sc.x)[j] = __fdiv_rn(top, kTop);
+        for (int j = 0; j < PER; ++j) {
+          const int c = t * PER + j;
+          const float top = block_max(F32 ? w : j ? w & 0xFFFF0000u : w << 16);
+          factors[c] = __fdiv_rn(kTop, top);
+          if (cb * 128 + c < a.cols) a.sc[rb * a.sc_row + cb * 128 + c] = __fdiv_rn(top, kTop);
+        }
       }
-      if (warp == 0 && col_ok) *reinterpret_cast<float4*>(a.sc + rb * a.sc_row + col) = sc;
+      __syncthreads();
+      float f[CPL];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (col_ok && row0 + i < a.rows)
-          *reinterpret_cast<uint32_t*>(a.qc + (row0 + i) * a.ldqc + col) = cvt4<E5M2>(
-              __fmul_rn(v[i][0], f[0]), __fmul_rn(v[i][1], f[1]), __fmul_rn(v[i][2], f[2]), __fmul_rn(v[i][3], f[3]));
+      for (int j = 0; j < CPL; ++j) f[j] = factors[tcol + j];
+      uint8_t* p = a.qc + row0 * a.ldqc + col;
+#pragma unroll
+      for (int i = 0; i < ITERS; ++i, p += RPI * a.ldqc) store(p, i, [&](int j) { return f[j]; });
     }
   }
 }
@@ -150,16 +206,16 @@ template <bool F32, bool E5M2>
 void launch_quantize(int mode, const QuantArgs& a, unsigned grid, cudaStream_t stream) {
   switch (mode) {
     case kRow:
-      quantize_kernel<kRow, F32, E5M2><<<grid, 256, 0, stream>>>(a);
+      quantize_kernel<kRow, F32, E5M2><<<grid, kWarps * 32, 0, stream>>>(a);
       break;
     case kCol:
-      quantize_kernel<kCol, F32, E5M2><<<grid, 256, 0, stream>>>(a);
+      quantize_kernel<kCol, F32, E5M2><<<grid, kWarps * 32, 0, stream>>>(a);
       break;
     case kBlock:
-      quantize_kernel<kBlock, F32, E5M2><<<grid, 256, 0, stream>>>(a);
+      quantize_kernel<kBlock, F32, E5M2><<<grid, kWarps * 32, 0, stream>>>(a);
       break;
     default:
-      quantize_kernel<kBoth, F32, E5M2><<<grid, 256, 0, stream>>>(a);
+      quantize_kernel<kBoth, F32, E5M2><<<grid, kWarps * 32, 0, stream>>>(a);
       break;
   }
 }
