@@ -1,60 +1,70 @@
-"""Marshalling shared by the grouped, 8-bit and AdamW bindings."""
+"""Marshalling shared by the grouped, 8-bit and AdamW bindings.
+
+A call of a few microseconds on the GPU is bound by what the host does before it, so checks
+are plain comparisons, and their messages are put together only when one of them fails.
+"""
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
 
 P, I, S = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+BF16, F32 = torch.bfloat16, torch.float32
+OUT_CODES = {BF16: 0, F32: 1}  # dp_out_dtype
+
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def need(ok: bool, what: str, kind=ValueError):
-    if not ok:
-        raise kind(what)
-
-
-def one_device(name: str, tensors: dict) -> torch.device:
-    """The CUDA device that every given tensor is on."""
-    device = None
+def refuse_devices(name: str, tensors: dict):
+    """Say which of the tensors is not on the first one's CUDA device (one of them is not)."""
+    first = None
     for what, t in tensors.items():
-        need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name}: {what} must be a CUDA tensor")
-        if device is None:
-            device = t.device
-        need(t.device == device, f"{name}: {what} is on {t.device}, the first operand on {device}")
-    return device
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name}: {what} must be a CUDA tensor")
+        first = t.device if first is None else first
+        if t.device != first:
+            raise ValueError(f"{name}: {what} is on {t.device}, the first operand on {first}")
 
 
-@contextlib.contextmanager
-def on_stream(device: torch.device, stream, tensors=()):
-    """The device and, if one is given, the stream of a call: memory that the call
-    allocates belongs to that stream, and its operands' memory is not handed out again
-    before the stream's work on them is done."""
-    if stream is None and device.index == torch.cuda.current_device():
-        yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        return
-    with torch.cuda.device(device):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-            return
-        with torch.cuda.stream(stream):
-            yield ctypes.c_void_p(stream.cuda_stream)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-
-
-def matrix(t: torch.Tensor, name: str, what: str):
+def ld(t: torch.Tensor, name: str, what: str) -> int:
     """Leading dimension of a 2-D view with unit column stride."""
-    need(t.dim() == 2 and (t.size(1) <= 1 or t.stride(1) == 1), f"{name}: {what} must be 2-D with unit column stride")
-    return t.stride(0) if t.size(0) > 1 else max(t.stride(0), t.size(1))
+    strides, shape = t.stride(), t.shape
+    if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name}: {what} must be 2-D with unit column stride")
+    return strides[0] if shape[0] > 1 else max(strides[0], shape[1])
 
 
-def output(out, shape, dtype, device, name: str, allowed):
+def output(out, shape, dtype, index: int, device, name: str):
+    """The given output, checked, or a new one; and its type's code."""
     if out is None:
-        need(dtype in allowed, f"{name}: out_dtype must be one of {allowed}", TypeError)
-        return torch.empty(shape, dtype=dtype, device=device)
-    need(tuple(out.shape) == tuple(shape), f"{name}: out must have shape {tuple(shape)}")
-    need(out.dtype in allowed, f"{name}: out must be one of {allowed}", TypeError)
-    need(out.is_cuda and out.device == device, f"{name}: out must be on {device}")
-    return out
+        code = OUT_CODES.get(dtype)
+        if code is None:
+            raise TypeError(f"{name}: out_dtype must be bfloat16 or float32")
+        return torch.empty(shape, dtype=dtype, device=device), code
+    code = OUT_CODES.get(out.dtype)
+    if code is None:
+        raise TypeError(f"{name}: out must be bfloat16 or float32")
+    if out.shape != shape:
+        raise ValueError(f"{name}: out must have shape {tuple(shape)}")
+    if out.get_device() != index:
+        raise ValueError(f"{name}: out must be on {device}")
+    return out, code
+
+
+def on_stream(index: int, stream, tensors, work):
+    """work(raw stream) with the device current and, if one is given, on that stream: memory
+    that the call allocates belongs to it, and its operands' memory is not handed out again
+    before the stream's work on them is done."""
+    if stream is None:
+        if _current_device() == index:
+            return work(_raw_stream(index))
+        with torch.cuda.device(index):
+            return work(_raw_stream(index))
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        result = work(stream.cuda_stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return result

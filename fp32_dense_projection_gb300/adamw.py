@@ -10,6 +10,7 @@ receive the updated parameter: the working weights of the GEMMs beside fp32 mast
 from __future__ import annotations
 
 import ctypes
+from operator import attrgetter
 
 import numpy as np
 import torch
@@ -26,8 +27,22 @@ class _Hyper(ctypes.Structure):
         ("grad_scale_ptr", ctypes.c_void_p), ("step", ctypes.c_int64)]
 
 
+_fn = {}
+
+
 def _bind(L):
+    _fn["step"] = L.dp_adamw_step
     L.dp_adamw_step.argtypes = [c.P, c.I, c.S, ctypes.POINTER(_Hyper), c.P]
+
+
+_data_ptr, _is_contiguous, _get_device = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
+_shape, _dtype = attrgetter("shape"), attrgetter("dtype")
+_F32, _BF16 = torch.float32, torch.bfloat16
+
+
+def _need(ok, what, kind=ValueError):
+    if not ok:
+        raise kind(f"AdamW: {what}")
 
 
 class AdamW:
@@ -35,58 +50,78 @@ class AdamW:
 
     state_bits=32 keeps both moments in fp32.  state_bits=8 keeps them as float8_e4m3fn
     codes with an fp32 scale per 128 consecutive elements: ``exp_avg`` holds m / scale,
-    ``exp_avg_sq`` holds sqrt(v) / scale.  The moments are attributes (lists of tensors) and
-    may be passed in, with ``step`` the updates already done, to resume a run.
+    ``exp_avg_sq`` holds sqrt(v) / scale.  The moments are attributes (tuples of tensors) and
+    may be passed in, with ``step`` the updates already done, to resume a run.  The updates
+    are made in place, outside autograd.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32, copies=None,
                  exp_avg=None, exp_avg_sq=None, exp_avg_scale=None, exp_avg_sq_scale=None, step=0):
-        self.params = list(params)
-        c.need(state_bits in (8, 32), "AdamW: state_bits must be 8 or 32")
-        c.need(len(betas) == 2 and all(0.0 <= b < 1.0 for b in betas), "AdamW: betas must lie in [0, 1)")
-        c.need(lr >= 0 and eps >= 0 and weight_decay >= 0, "AdamW: lr, eps and weight_decay must not be negative")
-        c.need(step >= 0, "AdamW: step must not be negative")
+        _need(state_bits in (8, 32), "state_bits must be 8 or 32")
+        _need(len(betas) == 2 and all(0.0 <= b < 1.0 for b in betas), "betas must lie in [0, 1)")
+        _need(lr >= 0 and eps >= 0 and weight_decay >= 0, "lr, eps and weight_decay must not be negative")
+        _need(step >= 0, "step must not be negative")
+        self.params = tuple(params)
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
         self.state_bits, self.step_count = state_bits, int(step)
-        self.device = c.one_device("AdamW", {f"params[{i}]": p for i, p in enumerate(self.params)})
-        for i, p in enumerate(self.params):
-            c.need(p.dtype in (torch.float32, torch.bfloat16), f"AdamW: params[{i}] must be float32 or bfloat16", TypeError)
-            c.need(p.is_contiguous(), f"AdamW: params[{i}] must be contiguous")
         n = len(self.params)
+        self.device = None
+        for i, p in enumerate(self.params):
+            _need(isinstance(p, torch.Tensor) and p.is_cuda, f"params[{i}] must be a CUDA tensor")
+            self.device = self.device or p.device
+            _need(p.device == self.device, f"params[{i}] is on {p.device}, params[0] on {self.device}")
+        self.copies = None if copies is None else tuple(copies)
+        _need(copies is None or len(self.copies) == n, "copies must have one entry (a tensor or None) per parameter")
+        self._table = np.zeros(n, _ENTRY)
         self._shapes = [p.shape for p in self.params]
-        kind = torch.float8_e4m3fn if state_bits == 8 else torch.float32
+        self._pointers = None
+        self._check_params()
+        kind = torch.float8_e4m3fn if state_bits == 8 else _F32
         self.exp_avg = self._state("exp_avg", exp_avg, kind, False)
         self.exp_avg_sq = self._state("exp_avg_sq", exp_avg_sq, kind, False)
         self.exp_avg_scale = self.exp_avg_sq_scale = None
         if state_bits == 8:
-            self.exp_avg_scale = self._state("exp_avg_scale", exp_avg_scale, torch.float32, True)
-            self.exp_avg_sq_scale = self._state("exp_avg_sq_scale", exp_avg_sq_scale, torch.float32, True)
+            self.exp_avg_scale = self._state("exp_avg_scale", exp_avg_scale, _F32, True)
+            self.exp_avg_sq_scale = self._state("exp_avg_sq_scale", exp_avg_sq_scale, _F32, True)
         else:
-            c.need(exp_avg_scale is None and exp_avg_sq_scale is None, "AdamW: scales belong to state_bits=8")
-        self.copies = None
-        if copies is not None:
-            self.copies = list(copies)
-            c.need(len(self.copies) == n, "AdamW: copies must have one entry (a tensor or None) per parameter")
-            for i, (t, p) in enumerate(zip(self.copies, self.params)):
-                if t is not None:
-                    self._alike(f"copies[{i}]", t, p.shape, torch.bfloat16)
-        self._table = np.zeros(n, _ENTRY)
-        self._table["numel"] = [p.numel() for p in self.params]
-        self._table["param_bf16"] = [p.dtype == torch.bfloat16 for p in self.params]
+            _need(exp_avg_scale is None and exp_avg_sq_scale is None, "scales belong to state_bits=8")
 
-    def _alike(self, what, t, shape, dtype):
-        c.need(isinstance(t, torch.Tensor) and t.device == self.device, f"AdamW: {what} must be on {self.device}")
-        c.need(t.dtype == dtype, f"AdamW: {what} must be {dtype}", TypeError)
-        c.need(t.shape == shape and t.is_contiguous(), f"AdamW: {what} must be contiguous with shape {tuple(shape)}")
+    def _alike(self, what, t, shape, dtypes):
+        _need(isinstance(t, torch.Tensor) and t.device == self.device, f"{what} must be on {self.device}")
+        _need(t.dtype in dtypes, f"{what} must be {' or '.join(map(str, dtypes))}", TypeError)
+        _need(t.shape == shape and t.is_contiguous(), f"{what} must be contiguous with shape {tuple(shape)}")
+
+    def _check_params(self):
+        """Check the parameters and copies and enter them in the table: at construction, and
+        again whenever one of them has moved (a module's .data may have been replaced)."""
+        for i, (p, shape) in enumerate(zip(self.params, self._shapes)):
+            self._alike(f"params[{i}]", p, shape, (_F32, _BF16))
+        for i, (x, shape) in enumerate(zip(self.copies or (), self._shapes)):
+            if x is not None:
+                self._alike(f"copies[{i}]", x, shape, (_BF16,))
+        t = self._table
+        t["numel"] = [p.numel() for p in self.params]
+        t["param"] = [p.data_ptr() for p in self.params]
+        t["param_bf16"] = [p.dtype is _BF16 for p in self.params]
+        t["copy"] = [0 if x is None else x.data_ptr() for x in self.copies or (None,) * len(self.params)]
+        self._pointers = self._where()
+        self._grad_dtypes = None
+
+    def _where(self):
+        where = list(map(_data_ptr, self.params))
+        if self.copies is not None:
+            where += [0 if x is None else x.data_ptr() for x in self.copies]
+        return where
 
     def _state(self, what, given, dtype, scales):
         shapes = [torch.Size((-(-p.numel() // _BLOCK),)) if scales else p.shape for p in self.params]
         if given is None:
-            return [torch.zeros(s, dtype=dtype, device=self.device) for s in shapes]
-        given = list(given)
-        c.need(len(given) == len(shapes), f"AdamW: {what} must have one tensor per parameter")
+            given = tuple(torch.zeros(s, dtype=dtype, device=self.device) for s in shapes)
+        given = tuple(given)
+        _need(len(given) == len(shapes), f"{what} must have one tensor per parameter")
         for i, (t, s) in enumerate(zip(given, shapes)):
-            self._alike(f"{what}[{i}]", t, s, dtype)
+            self._alike(f"{what}[{i}]", t, s, (dtype,))
+        self._table[what] = [t.data_ptr() for t in given]
         return given
 
     def step(self, grads, lr=None, grad_scale=1.0, stream=None):
@@ -95,35 +130,42 @@ class AdamW:
         clipping coefficient computed on the device, read without synchronising)."""
         from . import _check as status, lib
         grads = list(grads)
-        c.need(len(grads) == len(self.params), "AdamW.step: grads must have one entry (a tensor or None) per parameter")
+        _need(len(grads) == len(self.params), "grads must have one entry (a tensor or None) per parameter")
+        if not grads:
+            self.step_count += 1
+            return
+        if self._where() != self._pointers:
+            self._check_params()
+        index = self.device.index
+        some = [g for g in grads if g is not None]
+        shapes = self._shapes if len(some) == len(grads) else [s for g, s in zip(grads, self._shapes) if g is not None]
+        dtypes = list(map(_dtype, some))
+        if (list(map(_shape, some)) != shapes or False in map(_is_contiguous, some) or set(map(_get_device, some)) - {index} or
+                set(dtypes) - {_F32, _BF16}):
+            raise ValueError(f"AdamW.step: every gradient must be contiguous, float32 or bfloat16, on {self.device} and of its "
+                             "parameter's shape")
         t = self._table
-        for g, shape in zip(grads, self._shapes):
-            if g is not None and not (
-                    g.shape == shape and g.is_contiguous() and g.device == self.device and
-                    (g.dtype is torch.bfloat16 or g.dtype is torch.float32)):
-                raise ValueError(f"AdamW.step: a gradient must be contiguous, float32 or bfloat16, on {self.device}, of its "
-                                 f"parameter's shape {tuple(shape)}")
-        t["grad"] = [0 if g is None else g.data_ptr() for g in grads]
-        t["grad_bf16"] = [g is not None and g.dtype is torch.bfloat16 for g in grads]
-        t["param"] = [p.data_ptr() for p in self.params]
-        t["exp_avg"] = [x.data_ptr() for x in self.exp_avg]
-        t["exp_avg_sq"] = [x.data_ptr() for x in self.exp_avg_sq]
-        if self.state_bits == 8:
-            t["exp_avg_scale"] = [x.data_ptr() for x in self.exp_avg_scale]
-            t["exp_avg_sq_scale"] = [x.data_ptr() for x in self.exp_avg_sq_scale]
-        if self.copies is not None:
-            t["copy"] = [0 if x is None else x.data_ptr() for x in self.copies]
+        t["grad"] = list(map(_data_ptr, some)) if len(some) == len(grads) else [0 if g is None else g.data_ptr() for g in grads]
+        if len(some) != len(grads):
+            t["grad_bf16"] = [g is not None and g.dtype is _BF16 for g in grads]
+            self._grad_dtypes = None
+        elif dtypes != self._grad_dtypes:
+            t["grad_bf16"] = [d is _BF16 for d in dtypes]
+            self._grad_dtypes = dtypes
         h = _Hyper(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, 1.0, None,
                    self.step_count + 1)
         if isinstance(grad_scale, torch.Tensor):
-            c.need(grad_scale.numel() == 1 and grad_scale.dtype == torch.float32 and grad_scale.device == self.device,
-                   "AdamW.step: a grad_scale tensor must hold one float32 on the parameters' device")
+            if grad_scale.numel() != 1 or grad_scale.dtype is not _F32 or grad_scale.get_device() != index:
+                raise ValueError("AdamW.step: a grad_scale tensor must hold one float32 on the parameters' device")
             h.grad_scale_ptr = grad_scale.data_ptr()
         else:
             h.grad_scale = float(grad_scale)
-        used = () if stream is None else (*(g for g in grads if g is not None), *self.params, *self.exp_avg, *self.exp_avg_sq,
-                                          *(self.exp_avg_scale or ()), *(self.exp_avg_sq_scale or ()),
-                                          *(x for x in self.copies or () if x is not None))
-        with c.on_stream(self.device, stream, used) as st:
-            status(lib().dp_adamw_step(t.ctypes.data_as(c.P), len(self.params), self.state_bits, ctypes.byref(h), st), "dp_adamw_step")
+        used = () if stream is None else (*some, *self.params, *self.exp_avg, *self.exp_avg_sq, *(self.exp_avg_scale or ()),
+                                          *(self.exp_avg_sq_scale or ()), *(x for x in self.copies or () if x is not None),
+                                          *((grad_scale,) if isinstance(grad_scale, torch.Tensor) else ()))
+        lib()
+        code = c.on_stream(index, stream, used,
+                           lambda st: _fn["step"](t.ctypes.data, len(grads), self.state_bits, ctypes.byref(h), st))
+        if code:
+            status(code, "dp_adamw_step")
         self.step_count += 1

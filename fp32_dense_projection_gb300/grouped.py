@@ -15,77 +15,100 @@ import torch
 
 from . import _call as c
 
-_BF16, _F32 = torch.bfloat16, torch.float32
+_BITS = {torch.int32: 32, torch.int64: 64}
+_fn = {}
 
 
 def _bind(L):
     P, I, S = c.P, c.I, c.S
     for name in ("dp_gemm_fwd_grouped", "dp_gemm_dgrad_grouped"):
-        getattr(L, name).argtypes = [P, I, P, I, I, S, P, S, P, I, I, I, I, I, S, P]
+        _fn[name] = getattr(L, name)
+        _fn[name].argtypes = [P, I, P, I, I, S, P, S, P, I, I, I, I, I, S, P]
+    _fn["dp_gemm_wgrad_grouped"] = L.dp_gemm_wgrad_grouped
     L.dp_gemm_wgrad_grouped.argtypes = [P, I, P, I, P, S, P, I, I, S, I, I, I, I, S, P]
 
 
 def _experts(w: torch.Tensor, name: str, what: str):
     """(leading dimension, expert stride) of an [E, rows, columns] view."""
-    c.need(w.dim() == 3 and (w.size(2) <= 1 or w.stride(2) == 1), f"{name}: {what} must be [E, rows, columns] with unit column stride")
-    ld = w.stride(1) if w.size(1) > 1 else max(w.size(2), 1)
-    bs = w.stride(0) if w.size(0) > 1 else w.size(1) * ld
-    return ld, bs
+    strides, shape = w.stride(), w.shape
+    if len(shape) != 3 or (strides[2] != 1 and shape[2] > 1):
+        raise ValueError(f"{name}: {what} must be [E, rows, columns] with unit column stride")
+    ld = strides[1] if shape[1] > 1 else max(shape[2], 1)
+    return ld, strides[0] if shape[0] > 1 else shape[1] * ld
 
 
-def _check(name, rows: dict, weights, offsets, E):
-    device = c.one_device(name, {**rows, "weights": weights, "offsets": offsets} if weights is not None else {**rows, "offsets": offsets})
-    for what, t in rows.items():
-        c.need(t.dtype == _BF16, f"{name}: {what} must be bfloat16", TypeError)
-    if weights is not None:
-        c.need(weights.dtype == _BF16, f"{name}: weights must be bfloat16", TypeError)
-    c.need(offsets.dtype in (torch.int32, torch.int64), f"{name}: offsets must be int32 or int64", TypeError)
-    c.need(offsets.dim() == 1 and offsets.is_contiguous() and offsets.numel() >= 1 and (E is None or offsets.numel() == E + 1),
-           f"{name}: offsets must be a contiguous vector of E + 1 values")
-    return device
+def _check(name, a, b, b_name, offsets, E):
+    """Devices, types and the offsets' form; the offsets' width and the device's index."""
+    index = a.get_device()
+    if index < 0 or b.get_device() != index or offsets.get_device() != index:
+        c.refuse_devices(name, {"rows": a, b_name: b, "offsets": offsets})
+    if a.dtype is not c.BF16 or b.dtype is not c.BF16:
+        raise TypeError(f"{name}: rows and {b_name} must be bfloat16")
+    bits = _BITS.get(offsets.dtype)
+    if bits is None:
+        raise TypeError(f"{name}: offsets must be int32 or int64")
+    if offsets.dim() != 1 or not offsets.is_contiguous() or offsets.numel() != E + 1:
+        raise ValueError(f"{name}: offsets must be a contiguous vector of E + 1 values")
+    return index, bits
 
 
-def _rows_by_experts(name, op, a, W, offsets, out, out_dtype, weight_layout, stream):
-    from . import DP_OUT_BF16, DP_OUT_F32, _check as status, _layout, _ptr, lib
+def _rows_by_experts(name, forward, a, W, offsets, out, out_dtype, weight_layout, stream):
+    from . import _check as status, _layout, lib
     kn = _layout(weight_layout)
-    c.need(a.dim() == 2 and W.dim() == 3, f"{name}: rows must be 2-D and weights 3-D")
+    if a.dim() != 2 or W.dim() != 3:
+        raise ValueError(f"{name}: rows must be 2-D and weights 3-D")
     T, width = a.shape
-    E = W.shape[0]
-    N, K = (W.shape[2], W.shape[1]) if kn else (W.shape[1], W.shape[2])
-    c.need(width == (K if op == "fwd" else N), f"{name}: the rows' length does not match the weights")
-    device = _check(name, {"rows": a}, W, offsets, E)
+    E, N, K = W.shape
+    if kn:
+        N, K = K, N
+    if width != (K if forward else N):
+        raise ValueError(f"{name}: the rows' length does not match the weights")
+    index, bits = _check(name, a, W, "weights", offsets, E)
     ldw, bsw = _experts(W, name, "weights")
-    with c.on_stream(device, stream, (a, W, offsets, out)) as st:
-        out = c.output(out, (T, N if op == "fwd" else K), out_dtype, device, name, (_BF16, _F32))
-        code = DP_OUT_F32 if out.dtype == _F32 else DP_OUT_BF16
-        status(getattr(lib(), name)(_ptr(a), c.matrix(a, name, "rows"), _ptr(W), ldw, bsw, int(kn), _ptr(offsets),
-                                    offsets.element_size() * 8, _ptr(out), c.matrix(out, name, "out"), E, T, N, K, code, st), name)
-    return out
+    lda = c.ld(a, name, "rows")
+    lib()
+
+    def work(st):
+        y, code = c.output(out, (T, N if forward else K), out_dtype, index, a.device, name)
+        code = _fn[name](a.data_ptr(), lda, W.data_ptr(), ldw, bsw, kn, offsets.data_ptr(), bits, y.data_ptr(),
+                         c.ld(y, name, "out"), E, T, N, K, code, st)
+        if code:
+            status(code, name)
+        return y
+
+    return c.on_stream(index, stream, (a, W, offsets, out), work)
 
 
-def dp_gemm_fwd_grouped(X, W, offsets, out=None, out_dtype=_BF16, weight_layout="nk", stream=None):
+def dp_gemm_fwd_grouped(X, W, offsets, out=None, out_dtype=c.BF16, weight_layout="nk", stream=None):
     """Y[t] = X[t] W_e^T for the rows t of expert e: X [T,K]; W [E,N,K] ("nk") or [E,K,N] ("kn"); Y [T,N]."""
-    return _rows_by_experts("dp_gemm_fwd_grouped", "fwd", X, W, offsets, out, out_dtype, weight_layout, stream)
+    return _rows_by_experts("dp_gemm_fwd_grouped", True, X, W, offsets, out, out_dtype, weight_layout, stream)
 
 
-def dp_gemm_dgrad_grouped(dY, W, offsets, out=None, out_dtype=_BF16, weight_layout="nk", stream=None):
+def dp_gemm_dgrad_grouped(dY, W, offsets, out=None, out_dtype=c.BF16, weight_layout="nk", stream=None):
     """dX[t] = dY[t] W_e for the rows t of expert e: dY [T,N]; W as in the forward pass; dX [T,K]."""
-    return _rows_by_experts("dp_gemm_dgrad_grouped", "dgrad", dY, W, offsets, out, out_dtype, weight_layout, stream)
+    return _rows_by_experts("dp_gemm_dgrad_grouped", False, dY, W, offsets, out, out_dtype, weight_layout, stream)
 
 
-def dp_gemm_wgrad_grouped(dY, X, offsets, out=None, out_dtype=_BF16, weight_layout="nk", stream=None):
+def dp_gemm_wgrad_grouped(dY, X, offsets, out=None, out_dtype=c.BF16, weight_layout="nk", stream=None):
     """dW_e = sum over expert e's rows of dY[t]^T X[t]: dY [T,N]; X [T,K]; dW [E,N,K] ("nk") or [E,K,N] ("kn")."""
-    from . import DP_OUT_BF16, DP_OUT_F32, _check as status, _layout, _ptr, lib
+    from . import _check as status, _layout, lib
     name = "dp_gemm_wgrad_grouped"
     kn = _layout(weight_layout)
-    c.need(dY.dim() == 2 and X.dim() == 2 and dY.shape[0] == X.shape[0], f"{name}: dY[T,N] and X[T,K] must have the same rows")
+    if dY.dim() != 2 or X.dim() != 2 or dY.shape[0] != X.shape[0]:
+        raise ValueError(f"{name}: dY[T,N] and X[T,K] must have the same rows")
     (T, N), K = dY.shape, X.shape[1]
-    device = _check(name, {"dY": dY, "X": X}, None, offsets, None)
     E = offsets.numel() - 1
-    with c.on_stream(device, stream, (dY, X, offsets, out)) as st:
-        out = c.output(out, (E, K, N) if kn else (E, N, K), out_dtype, device, name, (_BF16, _F32))
-        ldo, bso = _experts(out, name, "out")
-        code = DP_OUT_F32 if out.dtype == _F32 else DP_OUT_BF16
-        status(lib().dp_gemm_wgrad_grouped(_ptr(dY), c.matrix(dY, name, "dY"), _ptr(X), c.matrix(X, name, "X"), _ptr(offsets),
-                                           offsets.element_size() * 8, _ptr(out), ldo, bso, int(kn), E, T, N, K, code, st), name)
-    return out
+    index, bits = _check(name, dY, X, "X", offsets, max(E, 0))
+    ldg, ldx = c.ld(dY, name, "dY"), c.ld(X, name, "X")
+    lib()
+
+    def work(st):
+        dW, code = c.output(out, (E, K, N) if kn else (E, N, K), out_dtype, index, dY.device, name)
+        ldw, bsw = _experts(dW, name, "out")
+        code = _fn[name](dY.data_ptr(), ldg, X.data_ptr(), ldx, offsets.data_ptr(), bits, dW.data_ptr(), ldw, bsw, kn, E, T,
+                         N, K, code, st)
+        if code:
+            status(code, name)
+        return dW
+
+    return c.on_stream(index, stream, (dY, X, offsets, out), work)
