@@ -2,6 +2,7 @@
 // include/dp_gemm.h): argument checks, tile width, tensor maps, one launch.  Nothing here
 // allocates device memory, copies or synchronises.
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include "api_internal.h"
@@ -37,6 +38,51 @@ dp_status zero_rows(void* out, int64_t rows, int64_t cols, int64_t ld, int esize
                            static_cast<size_t>(rows), stream) == cudaSuccess
              ? DP_OK
              : DP_ERR_LAUNCH;
+}
+
+// ------------------------------------------------ how an 8-bit product is launched
+
+struct Fp8Plan {
+  int bn, form, split;
+};
+
+// Clusters that run at one time, asked once per kernel, size and device.
+int cluster_capacity(int kind, int bn, int split) {
+  static std::atomic<int> known[64][3][2][9];  // capacity + 1; 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::atomic<int>& entry = known[dev][kind - kFp8KK][bn == 256][split];
+  int n = entry.load(std::memory_order_relaxed);
+  if (n == 0) {
+    n = max_clusters_fp8(kind, bn, split) + 1;
+    entry.store(n, std::memory_order_relaxed);
+  }
+  return n - 1;
+}
+
+// The form of least modelled time.  A CTA's time is its blocks (128 contraction elements) at
+// the rate measured for its tile, whole waves of tiles counted; measured on GB300, ns a block:
+// pair tiles of 256 x 256 430, 128 x 256 405, 128 x 128 250 (430 with column scales, whose
+// promotion costs twice the operations).  A split adds its exchange: ~1.2 us of barriers and
+// the tile's rows through the cluster's shared memory.
+Fp8Plan plan_fp8(int kind, int64_t gm, int64_t gn, int64_t nkb, int sm_count) {
+  const double ns128 = kind == kFp8MM ? 430.0 : 250.0, ns256 = kind == kFp8MM ? 480.0 : 405.0, ns_pair = 430.0;
+  Fp8Plan best = {128, kPlain, 1};
+  double least = 1e30;
+  auto offer = [&](int bn, int form, int split, int64_t tiles, int64_t slots, double ns) {
+    double t = static_cast<double>(cdiv(tiles, slots) * cdiv(nkb, split)) * ns;
+    if (form == kSplit) t += 1200.0 + 12.0 * static_cast<double>(std::min<int64_t>(gm, 128)) * bn / 256;
+    if (t < least) least = t, best = {bn, form, split};
+  };
+  offer(256, kPair, 1, cdiv(gm, 256) * cdiv(gn, 256), sm_count / 2, ns_pair);
+  for (int bn = 256; bn >= 128; bn /= 2) {
+    const int64_t tiles = cdiv(gm, 128) * cdiv(gn, bn);
+    const double ns = bn == 256 ? ns256 : ns128;
+    offer(bn, kPlain, 1, tiles, sm_count, ns);
+    for (int split = 2; split <= 8 && split <= nkb && tiles * split <= sm_count; ++split)
+      if (tiles <= cluster_capacity(kind, bn, split)) offer(bn, kSplit, split, tiles, tiles, ns);
+  }
+  return best;
 }
 
 enum GroupedOp { kFwd, kDgrad, kWgrad };
@@ -169,9 +215,8 @@ dp_status run_fp8(GroupedOp op, const void* a, int64_t lda, int a_fmt, Scales sa
   std::memset(&l, 0, sizeof(l));
   PgArgs& g = l.args;
   const int kind = op == kFwd ? kFp8KK : op == kDgrad ? kFp8KM : kFp8MM;
-  const bool pair = cdiv(gm, 256) * cdiv(gn, 256) * 2 >= ctx.sm_count;
-  const int bn = pair ? 256 : tile_width(cdiv(gm, 128), gn, ctx.sm_count, kind == kFp8KK ? 64 : 128);
-  const int tm = pair ? 256 : 128;
+  const Fp8Plan plan = plan_fp8(kind, gm, gn, cdiv(gk, 128), ctx.sm_count);
+  const int bn = plan.bn, tm = plan.form == kPair ? 256 : 128;
   g.rows = static_cast<int32_t>(gm);
   g.gm = static_cast<int32_t>(gm);
   g.gn = static_cast<int32_t>(gn);
@@ -182,6 +227,7 @@ dp_status run_fp8(GroupedOp op, const void* a, int64_t lda, int a_fmt, Scales sa
   g.out_f32 = out_f32;
   g.tiles_m = static_cast<int32_t>(cdiv(gm, tm));
   g.tiles_n = static_cast<int32_t>(cdiv(gn, bn));
+  g.split = plan.split;
   g.group_m = raster_rows(tm, gk);
   g.idesc = idesc_fp8_f32(tm, std::min(bn, 128), kind == kFp8MM, kind != kFp8KK, a_fmt == DP_FP8_E5M2, b_fmt == DP_FP8_E5M2);
   g.sa = sa.p;
@@ -197,13 +243,15 @@ dp_status run_fp8(GroupedOp op, const void* a, int64_t lda, int a_fmt, Scales sa
   const bool ok =
       (kind == kFp8MM ? encode_operand(&l.tmA, a, u8, 1, gk, gm, lda, 0, 0, 128, 128)
                       : encode_operand(&l.tmA, a, u8, 1, gm, gk, lda, 0, 0, 128, 128)) &&
-      (kind == kFp8KK ? encode_operand(&l.tmB, b, u8, 1, gn, gk, ldb, 0, 0, 128, static_cast<uint32_t>(pair ? bn / 2 : bn))
+      (kind == kFp8KK ? encode_operand(&l.tmB, b, u8, 1, gn, gk, ldb, 0, 0, 128, static_cast<uint32_t>(plan.form == kPair ? bn / 2 : bn))
                       : encode_operand(&l.tmB, b, u8, 1, gk, gn, ldb, 0, 0, 128, 128));
   if (!ok) return DP_ERR_LAUNCH;
   const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
   if (tiles > kMaxInt) return DP_ERR_UNSUPPORTED;
-  l.grid = static_cast<int>(pair ? 2 * std::min<int64_t>(ctx.sm_count / 2, tiles) : std::min<int64_t>(ctx.sm_count, tiles));
-  return launch_fp8(kind, bn, pair, l, stream) == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+  l.grid = static_cast<int>(plan.form == kPair    ? 2 * std::min<int64_t>(ctx.sm_count / 2, tiles)
+                            : plan.form == kSplit ? tiles * plan.split
+                                                  : std::min<int64_t>(ctx.sm_count, tiles));
+  return launch_fp8(kind, bn, plan.form, l, stream) == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
 }
 
 }  // namespace

@@ -4,44 +4,48 @@
 
 namespace dp {
 
-cudaError_t launch_fp8(int kind, int bn, bool pair, const PgLaunch& l, cudaStream_t stream) {
-  if (pair) {
-    if (bn != 256) return cudaErrorInvalidValue;
-    if (kind == kFp8KK) return launch_pg<256, kFp8KK, true>(l, stream);
-    if (kind == kFp8KM) return launch_pg<256, kFp8KM, true>(l, stream);
-    if (kind == kFp8MM) return launch_pg<256, kFp8MM, true>(l, stream);
-    return cudaErrorInvalidValue;
-  }
-  switch (kind) {
-    case kFp8KK:
-      if (bn == 64) return launch_pg<64, kFp8KK>(l, stream);
-      if (bn == 128) return launch_pg<128, kFp8KK>(l, stream);
-      if (bn == 256) return launch_pg<256, kFp8KK>(l, stream);
-      break;
-    case kFp8KM:
-      if (bn == 128) return launch_pg<128, kFp8KM>(l, stream);
-      if (bn == 256) return launch_pg<256, kFp8KM>(l, stream);
-      break;
-    case kFp8MM:
-      if (bn == 128) return launch_pg<128, kFp8MM>(l, stream);
-      if (bn == 256) return launch_pg<256, kFp8MM>(l, stream);
-      break;
-  }
+// (tile width, kind, form) of every kernel of this file
+#define DP_FP8_KERNELS(X) \
+  X(128, kFp8KK, kPlain)  \
+  X(256, kFp8KK, kPlain)  \
+  X(256, kFp8KK, kPair)   \
+  X(128, kFp8KK, kSplit)  \
+  X(256, kFp8KK, kSplit)  \
+  X(128, kFp8KM, kPlain)  \
+  X(256, kFp8KM, kPlain)  \
+  X(256, kFp8KM, kPair)   \
+  X(128, kFp8KM, kSplit)  \
+  X(256, kFp8KM, kSplit)  \
+  X(128, kFp8MM, kPlain)  \
+  X(256, kFp8MM, kPlain)  \
+  X(256, kFp8MM, kPair)   \
+  X(128, kFp8MM, kSplit)  \
+  X(256, kFp8MM, kSplit)
+
+cudaError_t launch_fp8(int kind, int bn, int form, const PgLaunch& l, cudaStream_t stream) {
+#define DP_LAUNCH(BN, KIND, FORM) \
+  if (bn == BN && kind == KIND && form == FORM) return launch_pg<BN, KIND, FORM>(l, stream);
+  DP_FP8_KERNELS(DP_LAUNCH)
+#undef DP_LAUNCH
   return cudaErrorInvalidValue;
 }
 
 cudaError_t set_attributes_fp8() {
-  cudaError_t e = set_attr_pg<64, kFp8KK>();
-  if (e == cudaSuccess) e = set_attr_pg<128, kFp8KK>();
-  if (e == cudaSuccess) e = set_attr_pg<256, kFp8KK>();
-  if (e == cudaSuccess) e = set_attr_pg<128, kFp8KM>();
-  if (e == cudaSuccess) e = set_attr_pg<256, kFp8KM>();
-  if (e == cudaSuccess) e = set_attr_pg<128, kFp8MM>();
-  if (e == cudaSuccess) e = set_attr_pg<256, kFp8MM>();
-  if (e == cudaSuccess) e = set_attr_pg<256, kFp8KK, true>();
-  if (e == cudaSuccess) e = set_attr_pg<256, kFp8KM, true>();
-  if (e == cudaSuccess) e = set_attr_pg<256, kFp8MM, true>();
+  cudaError_t e = cudaSuccess;
+#define DP_SET(BN, KIND, FORM) \
+  if (e == cudaSuccess) e = set_attr_pg<BN, KIND, FORM>();
+  DP_FP8_KERNELS(DP_SET)
+#undef DP_SET
   return e;
+}
+
+// Clusters of `split` CTAs of this kernel that run at one time (0 if the query fails).
+int max_clusters_fp8(int kind, int bn, int split) {
+#define DP_MAX(BN, KIND, FORM) \
+  if (FORM == kSplit && bn == BN && kind == KIND) return max_clusters_pg<BN, KIND, FORM>(split);
+  DP_FP8_KERNELS(DP_MAX)
+#undef DP_MAX
+  return 0;
 }
 
 }  // namespace dp

@@ -62,6 +62,7 @@ struct PgArgs {
   int32_t out_f32;
   int32_t tiles_m, tiles_n;  // (row-grouped: tiles_m unused)
   int32_t group_m;           // raster: row tiles that share a column tile's operand in L2
+  int32_t split;             // kSplit: CTAs that share a tile (2..8)
   uint32_t idesc;
   const float* sa;           // 8-bit products: scale of row m, block c at sa[m * sa_row + c * sa_blk]
   int64_t sa_row, sa_blk;
@@ -71,11 +72,17 @@ struct PgArgs {
   uint64_t wait_ns;
 };
 
-// PAIR: a cluster of two CTAs computes one tile of 256 x BN.  Each loads its 128 rows of A
+// Forms of a launch.  kSplit: clusters of `split` CTAs share a tile's contraction, one range of
+// blocks each, and the first sums the others' tiles from their shared memory in rank order:
+// for few tiles, whose operands one CTA each would stream too slowly.
+// kPair: a cluster of two CTAs computes one tile of 256 x BN.  Each loads its 128 rows of A
 // and half of the tile's columns of B, the leader (rank 0) issues the MMAs over both, and each
 // promotes its 128 x BN half of the accumulator: a third less operand traffic per SM.
-template <int BN, int KIND, bool PAIR = false>
+enum PgForm : int { kPlain = 0, kPair = 1, kSplit = 2 };
+
+template <int BN, int KIND, int FORM = kPlain>
 struct PgCfg {
+  static constexpr bool PAIR = FORM == kPair, SPLIT = FORM == kSplit;
   static constexpr int TM = PAIR ? 256 : 128;     // rows of a tile
   static constexpr int BNL = PAIR ? BN / 2 : BN;  // columns of B a CTA loads
   static constexpr bool FP8 = KIND >= kFp8KK;
@@ -116,6 +123,8 @@ struct PgCfg {
   static constexpr int THREADS = 384;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
   static_assert(BN == 64 || BN == 128 || BN == 256, "tile width");
+  static_assert(!SPLIT || FP8, "split contractions are built for the 8-bit products");
+  static_assert(!SPLIT || STAGES * STAGE_BYTES >= BM * BN * 4, "a split tile passes through the operand ring");
   static_assert(!(PAIR && K_GROUPS), "the leader zeroes ragged rows in its own shared memory only");
   static_assert(!(FP8 && B_MN) || BNL >= 128, "8-bit MN-major boxes are 128 columns wide");
 };
@@ -161,17 +170,18 @@ struct PgTile {
   int m_left;  // rows of the tile that exist (may exceed 128)
   int nkb;     // contraction blocks
   int k_left;  // contraction elements
+  int kb0;     // first contraction block (of this CTA's share)
 };
 
-template <int BN, int KIND, bool PAIR>
+template <int BN, int KIND, int FORM>
 struct PgWalk {
-  using C = PgCfg<BN, KIND, PAIR>;
+  using C = PgCfg<BN, KIND, FORM>;
   const PgArgs& a;
   const int32_t* start;  // [experts + 1] first row of each group
   const int32_t* first;  // [experts + 1] first tile of each group (row-grouped)
   __device__ __forceinline__ int units() const {
     if (C::ROW_GROUPS) return first[a.experts];
-    return a.tiles_m * a.tiles_n * (C::K_GROUPS ? a.experts : 1);
+    return a.tiles_m * a.tiles_n * (C::K_GROUPS ? a.experts : C::SPLIT ? a.split : 1);
   }
   // Tiles are rastered in groups of group_m row tiles, row tiles fastest: the CTAs that run
   // at one time share the column tile's operand and the group's rows in L2.
@@ -204,7 +214,7 @@ struct PgWalk {
       t.k_left = start[t.e + 1] - start[t.e];
     } else {
       t.e = 0;
-      local = u;
+      local = C::SPLIT ? u / a.split : u;
       tiles_m = a.tiles_m;
       t.m_left = a.gm;
       t.row0 = 0;
@@ -220,6 +230,12 @@ struct PgWalk {
     t.m_left -= t.tm * C::TM;
     if (C::ROW_GROUPS) t.row0 += t.tm * C::TM;
     t.nkb = (t.k_left + C::BK - 1) / C::BK;
+    t.kb0 = 0;
+    if (C::SPLIT) {
+      const int s = u % a.split;
+      t.kb0 = s * t.nkb / a.split;
+      t.nkb = (s + 1) * t.nkb / a.split - t.kb0;
+    }
     return t;
   }
 };
@@ -227,9 +243,9 @@ struct PgWalk {
 // The groups' table: start[i] = running maximum of the offsets, clamped to [0, rows], and
 // (row-grouped) first[i] = tiles of the groups before i.  Offsets that decrease or leave
 // [0, rows] set kFaultOffsets.  All 384 threads call it; each takes `per` consecutive entries.
-template <int BN, int KIND, bool PAIR>
+template <int BN, int KIND, int FORM>
 __device__ __forceinline__ void build_group_table(const PgArgs& a, int32_t* start, int32_t* first, int32_t* scan) {
-  using C = PgCfg<BN, KIND, PAIR>;
+  using C = PgCfg<BN, KIND, FORM>;
   constexpr int NW = C::THREADS / 32;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int n = a.experts + 1;
@@ -331,6 +347,15 @@ __device__ __forceinline__ float2 ld_shared_f2(uint32_t addr) {
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ void st_shared_u64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared.b64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+// From a CTA of the cluster (a shared::cluster address).
+__device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -345,11 +370,43 @@ __device__ __forceinline__ void regs_take() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int BN, int KIND, bool PAIR>
-__global__ void __launch_bounds__(PgCfg<BN, KIND, PAIR>::THREADS, 1)
+// The sum of a split tile: the cluster's CTAs share its columns in groups of eight; each of
+// their 256 epilogue threads adds a row's eight values of all ranks, in rank order, and stores
+// them.  `base`: where every CTA keeps its partial tile, [pair of columns][row].
+template <int BN>
+__device__ __forceinline__ void sum_split(const PgArgs& a, const PgTile& t, uint32_t base, int thread) {
+  const int rank = static_cast<int>(cluster_rank()), rows = min(128, t.m_left);
+  const int g0 = rank * (BN / 8) / a.split, g1 = (rank + 1) * (BN / 8) / a.split;
+  for (int i = thread; i < (g1 - g0) * rows; i += 256) {
+    const int g = g0 + i / rows, row = i % rows, col = t.tn * BN + 8 * g;
+    if (col >= a.gn) break;  // (gn is a multiple of 16; later items lie further right)
+    uint64_t sum[4] = {0, 0, 0, 0};
+    for (int r = 0; r < a.split; ++r) {
+      const uint32_t from = map_shared_rank(base + static_cast<uint32_t>(4 * g * 128 + row) * 8, static_cast<uint32_t>(r));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] = add_f32x2(sum[j], ld_cluster_u64(from + j * (128 * 8)));
+    }
+    const int64_t at = (static_cast<int64_t>(t.tm) * 128 + row) * a.ldo + col;
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[2 * j] = static_cast<uint32_t>(sum[j]), w[2 * j + 1] = static_cast<uint32_t>(sum[j] >> 32);
+    if (a.out_f32) {
+      uint4* p = reinterpret_cast<uint4*>(static_cast<float*>(a.out) + at);
+      p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+      auto pack = [&](int j) { return pack_bf16x2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])); };
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) = make_uint4(pack(0), pack(2), pack(4), pack(6));
+    }
+  }
+}
+
+template <int BN, int KIND, int FORM>
+__global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
     promoted_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ PgArgs args) {
-  using C = PgCfg<BN, KIND, PAIR>;
+  using C = PgCfg<BN, KIND, FORM>;
+  constexpr bool PAIR = C::PAIR;
   constexpr int STAGES = C::STAGES;
   constexpr int CHUNK = C::FP8 ? 1 : kPgChunk;
   extern __shared__ uint8_t smem_raw[];
@@ -405,8 +462,8 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, PAIR>::THREADS, 1)
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  if (C::ROW_GROUPS || C::K_GROUPS) build_group_table<BN, KIND, PAIR>(args, start, first, scan);
-  const PgWalk<BN, KIND, PAIR> walk{args, start, first};
+  if (C::ROW_GROUPS || C::K_GROUPS) build_group_table<BN, KIND, FORM>(args, start, first, scan);
+  const PgWalk<BN, KIND, FORM> walk{args, start, first};
   const int units = walk.units();
   const int unit0 = static_cast<int>(blockIdx.x) / (PAIR ? 2 : 1);
   const int step = static_cast<int>(gridDim.x) / (PAIR ? 2 : 1);
@@ -444,7 +501,8 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, PAIR>::THREADS, 1)
             else
               tma_load_3d(dst, map, fb, x, y, z);
           };
-          const int k0 = (C::K_GROUPS ? t.row0 : 0) + kb * C::BK;
+          const int kx = (C::SPLIT ? t.kb0 + kb : kb) * C::BK;
+          const int k0 = (C::K_GROUPS ? t.row0 : 0) + kx;
           if (rank == 0) mbar_expect_tx(full_bar(stage), (PAIR ? 2 : 1) * (load_a ? C::A_BYTES : C::B_BYTES));
           if (load_a) {
             const int m0 = t.tm * C::TM + static_cast<int>(rank) * C::BM;
@@ -452,7 +510,7 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, PAIR>::THREADS, 1)
 #pragma unroll
               for (int g = 0; g < C::BM / C::MN; ++g) load2(sa + g * (C::BK * 128), &tmA, m0 + g * C::MN, k0);
             } else {
-              load2(sa, &tmA, kb * C::BK, C::ROW_GROUPS ? t.row0 + static_cast<int>(rank) * C::BM : m0);
+              load2(sa, &tmA, kx, C::ROW_GROUPS ? t.row0 + static_cast<int>(rank) * C::BM : m0);
             }
           } else {
             const int n0 = t.tn * BN + static_cast<int>(rank) * C::BNL;
@@ -465,9 +523,9 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, PAIR>::THREADS, 1)
                   load2(sb + g * (C::BK * 128), &tmB, n0 + g * C::MN, k0);
               }
             } else if (C::ROW_GROUPS) {
-              load3(sb, &tmB, kb * C::BK, n0, t.e);
+              load3(sb, &tmB, kx, n0, t.e);
             } else {
-              load2(sb, &tmB, kb * C::BK, n0);
+              load2(sb, &tmB, kx, n0);
             }
           }
           issued |= 1u << stage;
@@ -620,13 +678,13 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, PAIR>::THREADS, 1)
         for (int j = 0; j < 4; ++j) {
           const int m = t.tm * C::TM + static_cast<int>(rank) * C::BM + 32 * j + lane;
           in[j] = m < args.gm;
-          at[j] = args.sa + (in[j] ? m * args.sa_row : 0);
+          at[j] = args.sa + (in[j] ? m * args.sa_row + t.kb0 * args.sa_blk : 0);
         }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
           const int n = t.tn * BN + (C::COL_SCALES ? 32 * j + lane : 128 * j);
           in[4 + j] = n < args.gn;
-          at[4 + j] = args.sb + (in[4 + j] ? (C::COL_SCALES ? n : n / 128) * args.sb_row : 0);
+          at[4 + j] = args.sb + (in[4 + j] ? (C::COL_SCALES ? n : n / 128) * args.sb_row + t.kb0 * args.sb_blk : 0);
         }
       }
       --left;
@@ -638,7 +696,8 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, PAIR>::THREADS, 1)
     };
 #pragma unroll
     for (int i = 0; i < kScaleAhead; ++i) load(v[i]);
-    const int nkb = (args.gk + C::BK - 1) / C::BK;  // (the same for every tile)
+    // (every tile has the same number of blocks; a split launch gives each CTA one share)
+    const int nkb = C::SPLIT ? walk.at(unit0).nkb : (args.gk + C::BK - 1) / C::BK;
     const int total = unit0 < units ? ((units - unit0 + step - 1) / step) * nkb : 0;
     bool ok = true;
     for (int i0 = 0; ok && i0 < total; i0 += kScaleAhead) {
@@ -672,6 +731,10 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, PAIR>::THREADS, 1)
       }
     }
   }
+  if (C::SPLIT) {  // (the epilogue warps' exchange)
+    cluster_sync();
+    cluster_sync();
+  }
   } else {
     // -------------------------------------------------- promotion and epilogue
     if (BN == 256) regs_take<208>();
@@ -685,6 +748,7 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, PAIR>::THREADS, 1)
     // (Beside 128 accumulators registers are short: one counter gives every ring position, and
     // the tile is decoded again for the store.)
     uint32_t it = 0;  // chunks done by this CTA
+    bool exchanged = false;
     bool ok = true;
     for (int u = unit0; u < units; u += step) {
       uint64_t acc[C::HALF / 2];  // pairs of columns
@@ -759,6 +823,20 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, PAIR>::THREADS, 1)
       asm volatile("" : "+r"(us));
       const PgTile t = walk.at(us);
       const int n0 = t.tn * BN;
+      if (C::SPLIT) {
+        // This rank's partial tile, [pair of columns][row], into the operand ring (whose loads and
+        // MMAs are done).
+        if (q * 32 + lane < t.m_left) {
+          const uint32_t at = base + static_cast<uint32_t>(h * (C::HALF / 2) * C::BM + q * 32 + lane) * 8;
+#pragma unroll
+          for (int j = 0; j < C::HALF / 2; ++j) st_shared_u64(at + j * (C::BM * 8), acc[j]);
+        }
+        cluster_sync();
+        sum_split<BN>(args, t, base, static_cast<int>(threadIdx.x) - 128);
+        cluster_sync();  // (no CTA leaves while its tile may be read)
+        exchanged = true;
+        break;
+      }
       // Store 32 rows x HALF columns through the warp's 2 KB block: 64-byte rows (32 BF16 or
       // 16 FP32 columns), 16-byte chunks XOR-swizzled by row, read back so that four lanes
       // write 64 consecutive bytes of a row.
@@ -807,6 +885,10 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, PAIR>::THREADS, 1)
         }
       }
     }
+    if (C::SPLIT && !exchanged) {  // (a wait ran out: the others still meet this CTA twice)
+      cluster_sync();
+      cluster_sync();
+    }
     // Rows before the first group and after the last one belong to no expert: zeros.
     if (C::ROW_GROUPS) {
       const int lo = start[0], hi = start[args.experts], esize = args.out_f32 ? 4 : 2;
@@ -844,32 +926,54 @@ struct PgLaunch {
 
 // gemm_grouped.cu / gemm_fp8.cu: one launch of the kernel of that kind, tile width and form.
 cudaError_t launch_grouped(int kind, int bn, const PgLaunch& l, cudaStream_t stream);
-cudaError_t launch_fp8(int kind, int bn, bool pair, const PgLaunch& l, cudaStream_t stream);
+cudaError_t launch_fp8(int kind, int bn, int form, const PgLaunch& l, cudaStream_t stream);
 cudaError_t set_attributes_grouped();
 cudaError_t set_attributes_fp8();
+int max_clusters_fp8(int kind, int bn, int split);
 
-template <int BN, int KIND, bool PAIR = false>
+template <int BN, int KIND, int FORM = kPlain>
 cudaError_t launch_pg(const PgLaunch& l, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(l.grid), 1, 1);
-  cfg.blockDim = dim3(PgCfg<BN, KIND, PAIR>::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = PgCfg<BN, KIND, PAIR>::SMEM_BYTES;
+  cfg.blockDim = dim3(PgCfg<BN, KIND, FORM>::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = PgCfg<BN, KIND, FORM>::SMEM_BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = FORM == kSplit ? static_cast<unsigned>(l.args.split) : 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, promoted_gemm_kernel<BN, KIND, PAIR>, l.tmA, l.tmB, l.args);
+  cfg.numAttrs = FORM == kPlain ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, promoted_gemm_kernel<BN, KIND, FORM>, l.tmA, l.tmB, l.args);
 }
 
-template <int BN, int KIND, bool PAIR = false>
+template <int BN, int KIND, int FORM>
+int max_clusters_pg(int split) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(split), 1, 1);
+  cfg.blockDim = dim3(PgCfg<BN, KIND, FORM>::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = PgCfg<BN, KIND, FORM>::SMEM_BYTES;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, promoted_gemm_kernel<BN, KIND, FORM>, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // clear: no split launches
+    return 0;
+  }
+  return n;
+}
+
+template <int BN, int KIND, int FORM = kPlain>
 cudaError_t set_attr_pg() {
-  const auto kernel = promoted_gemm_kernel<BN, KIND, PAIR>;
+  const auto kernel = promoted_gemm_kernel<BN, KIND, FORM>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       PgCfg<BN, KIND, PAIR>::SMEM_BYTES);
+                                       PgCfg<BN, KIND, FORM>::SMEM_BYTES);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (BN == 256 && e == cudaSuccess) {

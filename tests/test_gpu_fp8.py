@@ -164,6 +164,18 @@ def test_exact_products_on_many_tiles(op, T, N, K):
     assert dp.device_error() == 0
 
 
+@pytest.mark.parametrize("T,N,K", [(16, 4096, 4096), (130, 272, 4112), (3000, 144, 272), (128, 128, 16384), (7, 1040, 656)])
+@pytest.mark.parametrize("op", OPS)
+def test_exact_products_of_few_tiles(op, T, N, K):
+    """Sizes whose tiles do not fill the device: clusters of SMs share a tile's contraction, the
+    shares uneven, rows and columns ragged."""
+    (a, da), (b, db) = operands(op, T, N, K, T + K, ints=True)
+    ref = product(op, da, db)
+    assert torch.equal(call(op, a, b, out_dtype=torch.float32), ref.float())
+    assert torch.equal(call(op, a, b), ref.to(torch.bfloat16))
+    assert dp.device_error() == 0
+
+
 @pytest.mark.parametrize("fa,fb", [(E4, E4), (E5, E4), (E4, E5), (E5, E5)])
 @pytest.mark.parametrize("op", OPS)
 def test_real_products(op, fa, fb):
