@@ -13,6 +13,7 @@ namespace {
 using namespace dp;
 
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
+constexpr int64_t kPairRows = 192;  // rows per expert, on average, from which pairs pay
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -61,17 +62,19 @@ int cluster_capacity(int kind, int bn, int split) {
 }
 
 // The form of least modelled time.  A CTA's time is its blocks (128 contraction elements) at
-// the rate measured for its tile, whole waves of tiles counted; measured on GB300, ns a block:
-// pair tiles of 256 x 256 430, 128 x 256 405, 128 x 128 250 (430 with column scales, whose
-// promotion costs twice the operations).  A split adds its exchange: ~1.2 us of barriers and
-// the tile's rows through the cluster's shared memory.
+// the rate measured for its tile, whole waves of tiles counted.  Measured on GB300 (forced
+// forms, 17 shapes), ns a block: 128 x 128 215, 128 x 256 405, pairs of 256 x 256 440; with
+// column scales, whose promotion takes twice the operations and reads every column's scale,
+// 340 / 650 / 650.  A split adds its exchange: barriers of the cluster, and the tile's rows
+// through its shared memory.
 Fp8Plan plan_fp8(int kind, int64_t gm, int64_t gn, int64_t nkb, int sm_count) {
-  const double ns128 = kind == kFp8MM ? 430.0 : 250.0, ns256 = kind == kFp8MM ? 480.0 : 405.0, ns_pair = 430.0;
+  const bool cols = kind == kFp8MM;
+  const double ns128 = cols ? 340.0 : 215.0, ns256 = cols ? 650.0 : 405.0, ns_pair = cols ? 650.0 : 440.0;
   Fp8Plan best = {128, kPlain, 1};
   double least = 1e30;
   auto offer = [&](int bn, int form, int split, int64_t tiles, int64_t slots, double ns) {
     double t = static_cast<double>(cdiv(tiles, slots) * cdiv(nkb, split)) * ns;
-    if (form == kSplit) t += 1200.0 + 12.0 * static_cast<double>(std::min<int64_t>(gm, 128)) * bn / 256;
+    if (form == kSplit) t += 2300.0 + 200.0 * split + 12.0 * static_cast<double>(std::min<int64_t>(gm, 128)) * bn / 256;
     if (t < least) least = t, best = {bn, form, split};
   };
   offer(256, kPair, 1, cdiv(gm, 256) * cdiv(gn, 256), sm_count / 2, ns_pair);
@@ -138,7 +141,7 @@ dp_status run_grouped(GroupedOp op, const void* a, int64_t lda, const void* b, i
   g.fault = ctx.fault;
   g.wait_ns = kWaitLimitNs;
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  int kind, bn;
+  int kind, bn, form = kPlain;
   int64_t tiles;
   bool ok;
   if (op == kWgrad) {
@@ -163,20 +166,25 @@ dp_status run_grouped(GroupedOp op, const void* a, int64_t lda, const void* b, i
     g.gn = static_cast<int32_t>(gn);
     g.gk = static_cast<int32_t>(gk);
     // (the groups' sizes are known on the device only: at most one partial tile per group)
-    const int64_t tiles_m = T / 128 + std::min(E, T);
-    bn = tile_width(std::max(cdiv(T, 128), std::min(E, T)), gn, ctx.sm_count, 64);
+    // Pairs of SMs on tiles of 256 rows load a third less per SM and keep six stages in flight
+    // instead of four, but round every group up to 256 rows.
+    const bool pair = T >= kPairRows * E && cdiv(T, 256) * cdiv(gn, 256) >= ctx.sm_count / 2;
+    form = pair ? kPair : kPlain;
+    const int64_t tiles_m = T / (pair ? 256 : 128) + std::min(E, T);
+    bn = pair ? 256 : tile_width(std::max(cdiv(T, 128), std::min(E, T)), gn, ctx.sm_count, 64);
     g.tiles_n = static_cast<int32_t>(cdiv(gn, bn));
-    g.group_m = raster_rows(128, gk * 2);
+    g.group_m = raster_rows(pair ? 256 : 128, gk * 2);
     tiles = tiles_m * g.tiles_n;
     ok = encode_operand(&l.tmA, a, bf16, 2, T, gk, lda, 0, 0, 64, 128) &&
          (b_mn ? encode_operand(&l.tmB, b, bf16, 2, w_rows, w_cols, ldb, E, bsb, 64, 64)
-               : encode_operand(&l.tmB, b, bf16, 2, w_rows, w_cols, ldb, E, bsb, 64, static_cast<uint32_t>(bn)));
+               : encode_operand(&l.tmB, b, bf16, 2, w_rows, w_cols, ldb, E, bsb, 64, static_cast<uint32_t>(pair ? bn / 2 : bn)));
   }
   if (!ok) return DP_ERR_LAUNCH;
   if (tiles > kMaxInt) return DP_ERR_UNSUPPORTED;
-  g.idesc = idesc_bf16_f32(128, bn, kind == kGroupMM, kind != kGroupKK);
-  l.grid = static_cast<int>(std::min<int64_t>(ctx.sm_count, tiles));
-  return launch_grouped(kind, bn, l, stream) == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+  g.idesc = idesc_bf16_f32(form == kPair ? 256 : 128, bn, kind == kGroupMM, kind != kGroupKK);
+  l.grid = static_cast<int>(form == kPair ? 2 * std::min<int64_t>(ctx.sm_count / 2, tiles)
+                                          : std::min<int64_t>(ctx.sm_count, tiles));
+  return launch_grouped(kind, bn, form, l, stream) == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
 }
 
 struct Scales {

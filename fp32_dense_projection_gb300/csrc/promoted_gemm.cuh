@@ -742,9 +742,10 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                static_cast<uint32_t>(C::NSUB == 2 ? 0 : h * C::HALF);
     const uint32_t ebuf = ebase + static_cast<uint32_t>(warp - 4) * 2048u;
-    // The tile's column of this warp's accumulator c.  A pair's MMA h has 64 columns from the
-    // first and 64 from the second half of the tile.
-    auto tile_col = [&](int c) { return !PAIR ? h * C::HALF + c : 64 * h + c + (c < 64 ? 0 : 64); };
+    // The tile's column of this warp's accumulator c.  A pair's 128-column MMA h has 64 columns
+    // from the first and 64 from the second half of the tile.
+    constexpr bool MIXED = PAIR && C::NSUB == 2;
+    auto tile_col = [&](int c) { return !MIXED ? h * C::HALF + c : 64 * h + c + (c < 64 ? 0 : 64); };
     // (Beside 128 accumulators registers are short: one counter gives every ring position, and
     // the tile is decoded again for the store.)
     uint32_t it = 0;  // chunks done by this CTA
@@ -787,7 +788,7 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
               lo = mul_f32x2(lo, pack_f32x2(x.x, x.y));
               hi = mul_f32x2(hi, pack_f32x2(x.z, x.w));
             }
-            const uint64_t s = PAIR && c >= 64 ? s1 : s0;
+            const uint64_t s = MIXED && c >= 64 ? s1 : s0;
             a0 = C::FP8 ? fma_f32x2(lo, s, a0) : add_f32x2(lo, a0);
             a1 = C::FP8 ? fma_f32x2(hi, s, a1) : add_f32x2(hi, a1);
           }
@@ -925,7 +926,7 @@ struct PgLaunch {
 };
 
 // gemm_grouped.cu / gemm_fp8.cu: one launch of the kernel of that kind, tile width and form.
-cudaError_t launch_grouped(int kind, int bn, const PgLaunch& l, cudaStream_t stream);
+cudaError_t launch_grouped(int kind, int bn, int form, const PgLaunch& l, cudaStream_t stream);
 cudaError_t launch_fp8(int kind, int bn, int form, const PgLaunch& l, cudaStream_t stream);
 cudaError_t set_attributes_grouped();
 cudaError_t set_attributes_fp8();

@@ -93,6 +93,21 @@ def test_integers_are_exact(op, groups, kn):
     assert dp.device_error() == 0
 
 
+@pytest.mark.parametrize("counts,front,back", [([300, 0, 517, 256, 1, 900, 128, 700], 3, 250), ([4100], 0, 0), ([255, 257, 2000], 5, 1)])
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("kn", [False, True])
+def test_integers_are_exact_on_many_tiles(op, kn, counts, front, back):
+    """Sizes whose tiles fill the device: two SMs share a tile of 256 rows."""
+    edges = edges_of(counts, front)
+    T = int(edges[-1]) + back
+    for N, K in ((2600, 2056), (2056, 2568)):
+        c = tensors(edges, T, N, K, seed=T, kn=kn)
+        ref = reference(op, c, edges, kn)
+        assert torch.equal(call(op, c, kn, out_dtype=torch.float32), ref.float())
+        assert torch.equal(call(op, c, kn), ref.to(torch.bfloat16))
+    assert dp.device_error() == 0
+
+
 @pytest.mark.parametrize("op", OPS)
 @pytest.mark.parametrize("T,E,N,K", [(1, 8, 256, 512), (64, 64, 1024, 512), (700, 4, 520, 4104), (2500, 3, 264, 2056),
                                      (5000, 1, 128, 136), (4031, 32, 1024, 512)])
