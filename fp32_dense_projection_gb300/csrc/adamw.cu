@@ -4,9 +4,13 @@
 //   m  = beta1 m + (1 - beta1) g',      v = beta2 v + (1 - beta2) g'^2
 //   p  = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
 //
-// in FP32 whatever the storage types (the square root and the quotient to two units in the
-// last place: the approximate instructions' bounds); the parameter is rounded once to its
-// type, and its optional BF16 copy (the working weight of the GEMMs) from the rounded parameter.
+// in FP32 whatever the storage types.  The moments' operations are rounded one by one (no
+// fused multiply-add, and for 8-bit moments the IEEE square root and reciprocal): a code on the
+// edge between two values would else depend on how its FP32 value was computed, and a run
+// would not be reproducible elsewhere.  The parameter's quotient, which no state depends on, takes
+// the approximate instructions (two units in the last place of the update).  The parameter is
+// rounded once to its type, and its optional BF16 copy (the working weight of the GEMMs) from
+// the rounded parameter.
 //
 // 8-bit moments: 128 consecutive elements of a tensor share a scale.  m is held as E4M3
 // codes of m / s with s = max|m| / 448.  sqrt(v), not v, is held the same way: the root
@@ -140,8 +144,8 @@ __device__ __forceinline__ void decode4(uint32_t w, float s, float* x) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
         : "=f"(lo), "=f"(hi)
         : "r"(f16x2));
-    x[2 * h] = lo * s;
-    x[2 * h + 1] = hi * s;
+    x[2 * h] = __fmul_rn(lo, s);
+    x[2 * h + 1] = __fmul_rn(hi, s);
   }
 }
 
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Tabl
       decode4(vq.x, vs, v);
       decode4(vq.y, vs, v + 4);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= v[j];
+      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
     } else {
       load8(e.m, at, false, fast, n, m);
       load8(e.v, at, false, fast, n, v);
@@ -222,10 +226,10 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Tabl
     float root[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float x = g[j] * gs;
-      m[j] = fmaf(m[j], t.beta1, x * t.one_beta1);
-      v[j] = fmaf(x * t.one_beta2, x, v[j] * t.beta2);
-      root[j] = sqrt_approx(v[j]);
+      const float x = __fmul_rn(g[j], gs);
+      m[j] = __fadd_rn(__fmul_rn(m[j], t.beta1), __fmul_rn(x, t.one_beta1));
+      v[j] = __fadd_rn(__fmul_rn(v[j], t.beta2), __fmul_rn(__fmul_rn(x, x), t.one_beta2));
+      root[j] = EIGHT ? __fsqrt_rn(v[j]) : sqrt_approx(v[j]);
       const float u = m[j] * rcp_approx(fmaf(root[j], t.root_scale, t.eps));
       p[j] = fmaf(u, -t.lr, p[j] * t.keep);
     }
@@ -238,19 +242,19 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Tabl
           if (j >= n) m[j] = root[j] = 0.0f;
       }
       const float ma = block_max(m), va = block_max(root);
-      const float mf = __fdiv_rn(kTop, ma), vf = __fdiv_rn(kTop, va);
+      const float mf = __fmul_rn(__frcp_rn(ma), kTop), vf = __fmul_rn(__frcp_rn(va), kTop);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        m[j] *= mf;
+        m[j] = __fmul_rn(m[j], mf);
         // (a root above zero is at least 1e-23: the product is above kSmallest, and stays zero
         // for zero)
-        root[j] = fmaxf(root[j] * vf, fminf(root[j] * 1e30f, kSmallest));
+        root[j] = fmaxf(__fmul_rn(root[j], vf), fminf(root[j] * 1e30f, kSmallest));
       }
       store_codes(e.m, at, fast, n, make_uint2(encode4(m), encode4(m + 4)));
       store_codes(e.v, at, fast, n, make_uint2(encode4(root), encode4(root + 4)));
       if ((threadIdx.x & 15) == 0 && n > 0) {
-        e.ms[blk] = __fdiv_rn(ma, kTop);
-        e.vs[blk] = __fdiv_rn(va, kTop);
+        e.ms[blk] = __fmul_rn(ma, 1.0f / kTop);
+        e.vs[blk] = __fmul_rn(va, 1.0f / kTop);
       }
     } else {
       store8(e.m, at, false, fast, n, m);

@@ -375,8 +375,8 @@ typedef struct dp_adamw_hyper {
 /* One AdamW update of `count` dense tensors (the table is read on the host during the call):
  *   g' = g * scale;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
  *   p  = p (1 - lr wd) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * in FP32 (square root and quotient to two units in the last place); p is rounded once to
- * its type.
+ * in FP32: the moments' operations rounded one by one, the parameter's quotient to two units
+ * in the last place; p is rounded once to its type.
  * state_bits = 8: m is held as E4M3 codes with a scale max|m| / 448 for each 128 consecutive
  * elements, and sqrt(v) likewise; a v above zero is never held as zero.  A non-finite
  * gradient makes its element (32 bits) or its 128 elements' state (8 bits) non-finite.
