@@ -135,7 +135,33 @@ __device__ __forceinline__ void store_codes(void* base, int64_t at, bool fast, i
     if (j < n) p[j] = static_cast<uint8_t>((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
 }
 
-__device__ __forceinline__ void decode4(uint32_t w, float s, float* x) {
+// Two FP32 operations in one instruction, each rounded to nearest.
+struct Pair {
+  uint64_t v;
+  __device__ __forceinline__ float lo() const { return __uint_as_float(static_cast<uint32_t>(v)); }
+  __device__ __forceinline__ float hi() const { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+};
+__device__ __forceinline__ Pair pair(float a, float b) {
+  return {(static_cast<uint64_t>(__float_as_uint(b)) << 32) | __float_as_uint(a)};
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a.v), "l"(b.v));
+  return {d};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a.v), "l"(b.v));
+  return {d};
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return {d};
+}
+
+// Four E4M3 codes times their scale (squared: the second moment from its root).
+__device__ __forceinline__ void decode4(uint32_t w, float s, bool square, float* x) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t f16x2;
@@ -144,8 +170,10 @@ __device__ __forceinline__ void decode4(uint32_t w, float s, float* x) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
         : "=f"(lo), "=f"(hi)
         : "r"(f16x2));
-    x[2 * h] = __fmul_rn(lo, s);
-    x[2 * h + 1] = __fmul_rn(hi, s);
+    Pair y = pair(lo, hi) * pair(s, s);
+    if (square) y = y * y;
+    x[2 * h] = y.lo();
+    x[2 * h + 1] = y.hi();
   }
 }
 
@@ -188,7 +216,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 template <int MAX, bool EIGHT>
-__global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Table<MAX> t) {
+__global__ void __launch_bounds__(256, EIGHT ? 6 : 5) adamw_kernel(const __grid_constant__ Table<MAX> t) {
   const float gs = t.grad_scale_ptr ? t.grad_scale * __ldg(t.grad_scale_ptr) : t.grad_scale;
   const int64_t chunks = t.chunk0[t.count];
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
@@ -213,25 +241,29 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Tabl
     if (EIGHT) {
       const uint2 mq = load_codes(e.m, at, fast, n), vq = load_codes(e.v, at, fast, n);
       const float ms = n > 0 ? e.ms[blk] : 0.0f, vs = n > 0 ? e.vs[blk] : 0.0f;
-      decode4(mq.x, ms, m);
-      decode4(mq.y, ms, m + 4);
-      decode4(vq.x, vs, v);
-      decode4(vq.y, vs, v + 4);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
+      decode4(mq.x, ms, false, m);
+      decode4(mq.y, ms, false, m + 4);
+      decode4(vq.x, vs, true, v);
+      decode4(vq.y, vs, true, v + 4);
     } else {
       load8(e.m, at, false, fast, n, m);
       load8(e.v, at, false, fast, n, v);
     }
     float root[8];
+    auto twice = [](float x) { return pair(x, x); };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = __fmul_rn(g[j], gs);
-      m[j] = __fadd_rn(__fmul_rn(m[j], t.beta1), __fmul_rn(x, t.one_beta1));
-      v[j] = __fadd_rn(__fmul_rn(v[j], t.beta2), __fmul_rn(__fmul_rn(x, x), t.one_beta2));
+    for (int j = 0; j < 8; j += 2) {
+      const Pair x = pair(g[j], g[j + 1]) * twice(gs);
+      const Pair mm = pair(m[j], m[j + 1]) * twice(t.beta1) + x * twice(t.one_beta1);
+      const Pair vv = pair(v[j], v[j + 1]) * twice(t.beta2) + (x * x) * twice(t.one_beta2);
+      m[j] = mm.lo(), m[j + 1] = mm.hi();
+      v[j] = vv.lo(), v[j + 1] = vv.hi();
       root[j] = EIGHT ? __fsqrt_rn(v[j]) : sqrt_approx(v[j]);
-      const float u = m[j] * rcp_approx(fmaf(root[j], t.root_scale, t.eps));
-      p[j] = fmaf(u, -t.lr, p[j] * t.keep);
+      root[j + 1] = EIGHT ? __fsqrt_rn(v[j + 1]) : sqrt_approx(v[j + 1]);
+      const Pair den = fma2(pair(root[j], root[j + 1]), twice(t.root_scale), twice(t.eps));
+      const Pair u = mm * pair(rcp_approx(den.lo()), rcp_approx(den.hi()));
+      const Pair pp = fma2(u, twice(-t.lr), pair(p[j], p[j + 1]) * twice(t.keep));
+      p[j] = pp.lo(), p[j + 1] = pp.hi();
     }
     store8(e.p, at, p16, fast, n, p);
     if (e.copy) store8(e.copy, at, true, fast, n, p);
@@ -244,11 +276,13 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Tabl
       const float ma = block_max(m), va = block_max(root);
       const float mf = __fmul_rn(__frcp_rn(ma), kTop), vf = __fmul_rn(__frcp_rn(va), kTop);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = __fmul_rn(m[j], mf);
-        // (a root above zero is at least 1e-23: the product is above kSmallest, and stays zero
-        // for zero)
-        root[j] = fmaxf(__fmul_rn(root[j], vf), fminf(root[j] * 1e30f, kSmallest));
+      for (int j = 0; j < 8; j += 2) {
+        const Pair mm = pair(m[j], m[j + 1]) * twice(mf), r = pair(root[j], root[j + 1]), vv = r * twice(vf);
+        m[j] = mm.lo(), m[j + 1] = mm.hi();
+        // (a root above zero is at least 1e-23: its floor is kSmallest, and zero's stays zero)
+        const Pair floor = r * twice(1e30f);
+        root[j] = fmaxf(vv.lo(), fminf(floor.lo(), kSmallest));
+        root[j + 1] = fmaxf(vv.hi(), fminf(floor.hi(), kSmallest));
       }
       store_codes(e.m, at, fast, n, make_uint2(encode4(m), encode4(m + 4)));
       store_codes(e.v, at, fast, n, make_uint2(encode4(root), encode4(root + 4)));
