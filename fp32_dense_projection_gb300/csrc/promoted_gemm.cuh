@@ -350,6 +350,11 @@ __device__ __forceinline__ float2 ld_shared_f2(uint32_t addr) {
 __device__ __forceinline__ void st_shared_u64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared.b64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
+__device__ __forceinline__ uint64_t ld_shared_u64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr));
+  return v;
+}
 // From a CTA of the cluster (a shared::cluster address).
 __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
   uint64_t v;
@@ -764,15 +769,20 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
           break;
         }
         const uint32_t sc = scbase + (it % C::SCALE_SLOTS) * (C::SCALE_FLOATS * 4);
-        float f0 = 1.0f, f1 = 1.0f;  // this row's factors (f1: a pair's second 64 columns)
+        // This thread's factors: of its row and, in a pair, of the second 64 columns; with column
+        // scales, of its four rows.
+        uint64_t s0 = 0, s1 = 0, srow[4] = {0, 0, 0, 0};
         if (C::COL_SCALES) {
-          f0 = f1 = ld_shared_f32(sc + (q * 32 + lane) * 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float f = ld_shared_f32(sc + (q * 32 + 8 * k + lane / 4) * 4);
+            srow[k] = pack_f32x2(f, f);
+          }
         } else if (C::FP8) {
           const float2 f = ld_shared_f2(sc + (q * 32 + lane) * 8);
-          f0 = !PAIR && C::NSUB == 2 && h == 1 ? f.y : f.x;
-          f1 = f.y;
+          const float f0 = !PAIR && C::NSUB == 2 && h == 1 ? f.y : f.x;
+          s0 = pack_f32x2(f0, f0), s1 = pack_f32x2(f.y, f.y);
         }
-        const uint64_t s0 = pack_f32x2(f0, f0), s1 = pack_f32x2(f1, f1);
         tc_fence_after();
         const uint32_t t_addr = lane_addr + buf * C::SUB;
         // 32 columns at a time through two register blocks: both are loaded, then each is refilled
@@ -783,11 +793,6 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
             uint64_t lo = pack_u32x2(v[j], v[j + 1]), hi = pack_u32x2(v[j + 2], v[j + 3]);
             uint64_t& a0 = acc[(c + j) / 2];
             uint64_t& a1 = acc[(c + j) / 2 + 1];
-            if (C::COL_SCALES) {
-              const float4 x = ld_shared_f4(sc + (128 + tile_col(c) + j) * 4);
-              lo = mul_f32x2(lo, pack_f32x2(x.x, x.y));
-              hi = mul_f32x2(hi, pack_f32x2(x.z, x.w));
-            }
             const uint64_t s = MIXED && c >= 64 ? s1 : s0;
             a0 = C::FP8 ? fma_f32x2(lo, s, a0) : add_f32x2(lo, a0);
             a1 = C::FP8 ? fma_f32x2(hi, s, a1) : add_f32x2(hi, a1);
@@ -803,20 +808,45 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
               mbar_arrive(tempty_bar(buf));
           }
         };
-        uint32_t r0[32], r1[32];
-        tmem_ld_32x32b_x32(t_addr, r0);
-        if (C::HALF >= 64) tmem_ld_32x32b_x32(t_addr + 32, r1);
-        tmem_wait_ld();
-        if (C::HALF <= 64) release();
-        add32(r0, 0);
-        if (C::HALF == 128) tmem_ld_32x32b_x32(t_addr + 64, r0);
-        if (C::HALF >= 64) add32(r1, 32);
-        if (C::HALF == 128) {
-          tmem_ld_32x32b_x32(t_addr + 96, r1);
+        if (C::COL_SCALES) {
+          // Column scales: a thread takes pairs of columns of four rows (16x256b) instead of one
+          // row, so a warp reads a chunk's scales as 16 words of 8 bytes a thread and not as 32
+          // broadcasts of 16 (which took the SM ~1000 cycles of shared-memory bandwidth a chunk).
+#pragma unroll
+          for (int c = 0; c < C::HALF; c += 32) {
+            uint32_t v[2][16];
+            tmem_ld_16x256b_x4(t_addr + c, v[0]);
+            tmem_ld_16x256b_x4(t_addr + c + (16u << 16), v[1]);
+            tmem_wait_ld();
+            if (c + 32 == C::HALF) release();
+            const uint32_t x = sc + (128 + tile_col(c) + 2 * (lane & 3)) * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint64_t col = ld_shared_u64(x + 32 * i);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint64_t& a0 = acc[c / 2 + 4 * i + k];
+                const uint32_t* r = &v[k >> 1][4 * i + 2 * (k & 1)];
+                a0 = fma_f32x2(mul_f32x2(pack_u32x2(r[0], r[1]), col), srow[k], a0);
+              }
+            }
+          }
+        } else {
+          uint32_t r0[32], r1[32];
+          tmem_ld_32x32b_x32(t_addr, r0);
+          if (C::HALF >= 64) tmem_ld_32x32b_x32(t_addr + 32, r1);
           tmem_wait_ld();
-          release();
-          add32(r0, 64);
-          add32(r1, 96);
+          if (C::HALF <= 64) release();
+          add32(r0, 0);
+          if (C::HALF == 128) tmem_ld_32x32b_x32(t_addr + 64, r0);
+          if (C::HALF >= 64) add32(r1, 32);
+          if (C::HALF == 128) {
+            tmem_ld_32x32b_x32(t_addr + 96, r1);
+            tmem_wait_ld();
+            release();
+            add32(r0, 64);
+            add32(r1, 96);
+          }
         }
       }
       if (!ok) break;
@@ -827,7 +857,12 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
       if (C::SPLIT) {
         // This rank's partial tile, [pair of columns][row], into the operand ring (whose loads and
         // MMAs are done).
-        if (q * 32 + lane < t.m_left) {
+        if (C::COL_SCALES) {
+          const uint32_t at = base + static_cast<uint32_t>((h * (C::HALF / 2) + (lane & 3)) * C::BM + q * 32 + lane / 4) * 8;
+#pragma unroll
+          for (int j = 0; j < C::HALF / 2; ++j)
+            st_shared_u64(at + (j / 16 * 16 + (j % 16) / 4 * 4) * (C::BM * 8) + (j & 3) * 64, acc[j]);
+        } else if (q * 32 + lane < t.m_left) {
           const uint32_t at = base + static_cast<uint32_t>(h * (C::HALF / 2) * C::BM + q * 32 + lane) * 8;
 #pragma unroll
           for (int j = 0; j < C::HALF / 2; ++j) st_shared_u64(at + j * (C::BM * 8), acc[j]);
@@ -861,7 +896,20 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
       auto lo32 = [&](int j) { return static_cast<uint32_t>(acc[j]); };
       auto hi32 = [&](int j) { return static_cast<uint32_t>(acc[j] >> 32); };
       auto bf16x2 = [&](int j) { return pack_bf16x2(__uint_as_float(lo32(j)), __uint_as_float(hi32(j))); };
-      if (args.out_f32) {
+      if (C::COL_SCALES) {
+        // (a thread's pairs go straight out: four lanes write 32 (FP32) or 16 consecutive bytes)
+#pragma unroll
+        for (int j = 0; j < C::HALF / 2; ++j) {
+          const int r = 8 * (j & 3) + lane / 4, col = n0 + tile_col(j / 16 * 32) + (j % 16) / 4 * 8 + 2 * (lane & 3);
+          if (r < rows_left && col < args.gn) {
+            char* p = out + (r * args.ldo + col) * esize;
+            if (args.out_f32)
+              *reinterpret_cast<uint64_t*>(p) = acc[j];
+            else
+              *reinterpret_cast<uint32_t*>(p) = bf16x2(j);
+          }
+        }
+      } else if (args.out_f32) {
 #pragma unroll
         for (int c = 0; c < C::HALF; c += 16) {
           __syncwarp();
