@@ -13,18 +13,20 @@ namespace {
 using namespace dp;
 
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
-constexpr int64_t kPairRows = 192;  // rows per expert, on average, from which pairs pay
+constexpr int64_t kPairRows = 384;  // rows per expert, on average, from which pairs pay
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tile width: the widest that gives every SM two tiles.  Wide tiles read A less often and keep
-// the tensor cores fed (a 128 x 256 tile needs 96 bytes of operands per cycle, a 128 x 64 tile
-// 192); narrow ones spread a few rows' weights evenly over the SMs (64 rows over 64 experts,
-// 4096 -> 1024: 256 columns 74 us, 128 columns 53, 64 columns 69; 16384 rows: 263, 299, 408).
-int tile_width(int64_t tiles_m, int64_t gn, int sm_count, int narrowest) {
-  for (int bn = 256; bn > narrowest; bn /= 2)
-    if (tiles_m * cdiv(gn, bn) >= 2 * sm_count) return bn;
-  return narrowest;
+// Tile width: the widest that gives the SMs `least` tiles.  Wide tiles read A less often and keep
+// the tensor cores fed: a 128 x 256 tile needs 96 bytes of operands per cycle, a 128 x 64 tile
+// 192 (16384 rows over 64 experts, 4096 -> 2048: 263 us at 256 columns, 299 at 128, 408 at 64).
+// One tile per SM is enough for them, two where a few rows stream their experts' weights and
+// the last tiles' share of the SMs counts (64 rows over 64 experts, 4096 -> 1024: 74 us at 256
+// columns, 53 to 68 at 128 by how many experts have rows, 69 at 64).
+int tile_width(int64_t tiles_m, int64_t gn, int64_t least) {
+  for (int bn = 256; bn > 64; bn /= 2)
+    if (tiles_m * cdiv(gn, bn) >= least) return bn;
+  return 64;
 }
 
 // Row tiles per raster group: as many rows of A as fill a share of L2 beside the weights.
@@ -150,7 +152,7 @@ dp_status run_grouped(GroupedOp op, const void* a, int64_t lda, const void* b, i
     kind = kGroupMM;
     g.gm = static_cast<int32_t>(gm);
     g.gn = static_cast<int32_t>(gn);
-    bn = tile_width(E * cdiv(gm, 128), gn, ctx.sm_count, 64);
+    bn = tile_width(E * cdiv(gm, 128), gn, ctx.sm_count);
     g.tiles_m = static_cast<int32_t>(cdiv(gm, 128));
     g.tiles_n = static_cast<int32_t>(cdiv(gn, bn));
     g.group_m = 8;
@@ -167,11 +169,14 @@ dp_status run_grouped(GroupedOp op, const void* a, int64_t lda, const void* b, i
     g.gk = static_cast<int32_t>(gk);
     // (the groups' sizes are known on the device only: at most one partial tile per group)
     // Pairs of SMs on tiles of 256 rows load a third less per SM and keep six stages in flight
-    // instead of four, but round every group up to 256 rows.
+    // instead of four, but round every group up to 256 rows (16384 rows, 4096 -> 4096: over 8
+    // experts 311 us against 332 on single SMs, over 32 386 against 402; over 64 at 4096 -> 2048
+    // no difference, over 128 at 2048 -> 2048 205 against 199).
     const bool pair = T >= kPairRows * E && cdiv(T, 256) * cdiv(gn, 256) >= ctx.sm_count / 2;
     form = pair ? kPair : kPlain;
     const int64_t tiles_m = T / (pair ? 256 : 128) + std::min(E, T);
-    bn = pair ? 256 : tile_width(std::max(cdiv(T, 128), std::min(E, T)), gn, ctx.sm_count, 64);
+    bn = pair ? 256 : tile_width(std::max(cdiv(T, 128), std::min(E, T)), gn,
+                                 T <= 32 * E ? 2 * ctx.sm_count : ctx.sm_count);
     g.tiles_n = static_cast<int32_t>(cdiv(gn, bn));
     g.group_m = raster_rows(pair ? 256 : 128, gk * 2);
     tiles = tiles_m * g.tiles_n;
