@@ -11,7 +11,10 @@
 
 namespace dp {
 
+constexpr int kMaxDevices = 64;
+
 struct DeviceContext {
+  int device = 0;  // below kMaxDevices
   int sm_count = 0;
   uint32_t* fault = nullptr;  // device status word
 };

@@ -25,7 +25,6 @@ using namespace dp;
 // Device status word: kernels OR fault bits into it when a bounded wait gives up.
 __device__ uint32_t g_fault_word;
 
-constexpr int kMaxDevices = 64;
 
 struct DeviceState {
   bool initialised = false;
@@ -814,6 +813,7 @@ dp_status device_context(DeviceContext* ctx) {
   DeviceState* d = nullptr;
   const dp_status st = current_device(&d);
   if (st != DP_OK) return st;
+  ctx->device = static_cast<int>(d - g_devices);
   ctx->sm_count = d->sm_count;
   ctx->fault = d->fault;
   return DP_OK;

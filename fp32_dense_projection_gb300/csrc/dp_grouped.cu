@@ -35,6 +35,10 @@ int raster_rows(int64_t tile_rows, int64_t k_bytes) {
   return static_cast<int>(std::min<int64_t>(64, std::max<int64_t>(4, rows)));
 }
 
+// Rows of A a load brings: where there are fewer than a tile's 128, just those, in whole swizzle
+// rows of 8 (the accumulator's other rows come from stale shared memory and are not stored).
+int rows_loaded(int64_t rows) { return static_cast<int>(std::min<int64_t>(128, cdiv(rows, 8) * 8)); }
+
 dp_status zero_rows(void* out, int64_t rows, int64_t cols, int64_t ld, int esize, cudaStream_t stream) {
   if (rows == 0) return DP_OK;
   return cudaMemset2DAsync(out, static_cast<size_t>(ld) * esize, 0, static_cast<size_t>(cols) * esize,
@@ -50,10 +54,8 @@ struct Fp8Plan {
 };
 
 // Clusters that run at one time, asked once per kernel, size and device.
-int cluster_capacity(int kind, int bn, int split) {
-  static std::atomic<int> known[64][3][2][9];  // capacity + 1; 0: not asked yet
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+int cluster_capacity(int dev, int kind, int bn, int split) {
+  static std::atomic<int> known[kMaxDevices][3][2][9];  // capacity + 1; 0: not asked yet
   std::atomic<int>& entry = known[dev][kind - kFp8KK][bn == 256][split];
   int n = entry.load(std::memory_order_relaxed);
   if (n == 0) {
@@ -65,27 +67,35 @@ int cluster_capacity(int kind, int bn, int split) {
 
 // The form of least modelled time.  A CTA's time is its blocks (128 contraction elements) at
 // the rate measured for its tile, whole waves of tiles counted.  Measured on GB300 (forced
-// forms, 17 shapes), ns a block: 128 x 128 215, 128 x 256 405, pairs of 256 x 256 440; with
-// column scales, whose promotion takes twice the operations and reads every column's scale,
-// 340 / 650 / 650.  A split adds its exchange: barriers of the cluster, and the tile's rows
-// through its shared memory.
-Fp8Plan plan_fp8(int kind, int64_t gm, int64_t gn, int64_t nkb, int sm_count) {
+// forms, 34 shapes), ns a block: 128 x 128 215, 128 x 256 405, pairs of 256 x 256 440 while one
+// wave suffices; with more waves 255 / 425 / 420, as narrow tiles then wait for L2 and pairs,
+// which load least, do not (16384 x 12288 -> 4096: 785 / 586 / 558 us; 4031 x 4096 -> 4096: 61.5 /
+// 60.5 / 60.4).  With column scales, whose promotion takes twice the operations and reads every
+// column's scale, it is 350 / 690 / 655 for both.  A split adds its exchange: barriers of the
+// cluster, and the tile's rows through its shared memory.
+Fp8Plan plan_fp8(int kind, int64_t gm, int64_t gn, int64_t nkb, const DeviceContext& ctx) {
+  struct Rates {
+    double one_wave, more;
+  };
   const bool cols = kind == kFp8MM;
-  const double ns128 = cols ? 340.0 : 215.0, ns256 = cols ? 650.0 : 405.0, ns_pair = cols ? 650.0 : 440.0;
+  const int sm_count = ctx.sm_count;
+  const Rates r128 = cols ? Rates{350, 350} : Rates{215, 255}, r256 = cols ? Rates{690, 690} : Rates{405, 425},
+              r_pair = cols ? Rates{655, 655} : Rates{440, 420};
   Fp8Plan best = {128, kPlain, 1};
   double least = 1e30;
-  auto offer = [&](int bn, int form, int split, int64_t tiles, int64_t slots, double ns) {
-    double t = static_cast<double>(cdiv(tiles, slots) * cdiv(nkb, split)) * ns;
+  auto offer = [&](int bn, int form, int split, int64_t tiles, int64_t slots, const Rates& r) {
+    const int64_t waves = cdiv(tiles, slots);
+    double t = static_cast<double>(waves * cdiv(nkb, split)) * (waves == 1 ? r.one_wave : r.more);
     if (form == kSplit) t += 2300.0 + 200.0 * split + 12.0 * static_cast<double>(std::min<int64_t>(gm, 128)) * bn / 256;
     if (t < least) least = t, best = {bn, form, split};
   };
-  offer(256, kPair, 1, cdiv(gm, 256) * cdiv(gn, 256), sm_count / 2, ns_pair);
+  offer(256, kPair, 1, cdiv(gm, 256) * cdiv(gn, 256), sm_count / 2, r_pair);
   for (int bn = 256; bn >= 128; bn /= 2) {
     const int64_t tiles = cdiv(gm, 128) * cdiv(gn, bn);
-    const double ns = bn == 256 ? ns256 : ns128;
-    offer(bn, kPlain, 1, tiles, sm_count, ns);
+    const Rates& r = bn == 256 ? r256 : r128;
+    offer(bn, kPlain, 1, tiles, sm_count, r);
     for (int split = 2; split <= 8 && split <= nkb && tiles * split <= sm_count; ++split)
-      if (tiles <= cluster_capacity(kind, bn, split)) offer(bn, kSplit, split, tiles, tiles, ns);
+      if (tiles <= cluster_capacity(ctx.device, kind, bn, split)) offer(bn, kSplit, split, tiles, tiles, r);
   }
   return best;
 }
@@ -180,7 +190,8 @@ dp_status run_grouped(GroupedOp op, const void* a, int64_t lda, const void* b, i
     g.tiles_n = static_cast<int32_t>(cdiv(gn, bn));
     g.group_m = raster_rows(pair ? 256 : 128, gk * 2);
     tiles = tiles_m * g.tiles_n;
-    ok = encode_operand(&l.tmA, a, bf16, 2, T, gk, lda, 0, 0, 64, 128) &&
+    g.a_rows = rows_loaded(T);
+    ok = encode_operand(&l.tmA, a, bf16, 2, T, gk, lda, 0, 0, 64, static_cast<uint32_t>(g.a_rows)) &&
          (b_mn ? encode_operand(&l.tmB, b, bf16, 2, w_rows, w_cols, ldb, E, bsb, 64, 64)
                : encode_operand(&l.tmB, b, bf16, 2, w_rows, w_cols, ldb, E, bsb, 64, static_cast<uint32_t>(pair ? bn / 2 : bn)));
   }
@@ -228,7 +239,7 @@ dp_status run_fp8(GroupedOp op, const void* a, int64_t lda, int a_fmt, Scales sa
   std::memset(&l, 0, sizeof(l));
   PgArgs& g = l.args;
   const int kind = op == kFwd ? kFp8KK : op == kDgrad ? kFp8KM : kFp8MM;
-  const Fp8Plan plan = plan_fp8(kind, gm, gn, cdiv(gk, 128), ctx.sm_count);
+  const Fp8Plan plan = plan_fp8(kind, gm, gn, cdiv(gk, 128), ctx);
   const int bn = plan.bn, tm = plan.form == kPair ? 256 : 128;
   g.rows = static_cast<int32_t>(gm);
   g.gm = static_cast<int32_t>(gm);
@@ -241,6 +252,7 @@ dp_status run_fp8(GroupedOp op, const void* a, int64_t lda, int a_fmt, Scales sa
   g.tiles_m = static_cast<int32_t>(cdiv(gm, tm));
   g.tiles_n = static_cast<int32_t>(cdiv(gn, bn));
   g.split = plan.split;
+  g.a_rows = plan.form == kPair ? 128 : rows_loaded(gm);
   g.group_m = raster_rows(tm, gk);
   g.idesc = idesc_fp8_f32(tm, std::min(bn, 128), kind == kFp8MM, kind != kFp8KK, a_fmt == DP_FP8_E5M2, b_fmt == DP_FP8_E5M2);
   g.sa = sa.p;
@@ -255,7 +267,7 @@ dp_status run_fp8(GroupedOp op, const void* a, int64_t lda, int a_fmt, Scales sa
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const bool ok =
       (kind == kFp8MM ? encode_operand(&l.tmA, a, u8, 1, gk, gm, lda, 0, 0, 128, 128)
-                      : encode_operand(&l.tmA, a, u8, 1, gm, gk, lda, 0, 0, 128, 128)) &&
+                      : encode_operand(&l.tmA, a, u8, 1, gm, gk, lda, 0, 0, 128, static_cast<uint32_t>(g.a_rows))) &&
       (kind == kFp8KK ? encode_operand(&l.tmB, b, u8, 1, gn, gk, ldb, 0, 0, 128, static_cast<uint32_t>(plan.form == kPair ? bn / 2 : bn))
                       : encode_operand(&l.tmB, b, u8, 1, gk, gn, ldb, 0, 0, 128, 128));
   if (!ok) return DP_ERR_LAUNCH;

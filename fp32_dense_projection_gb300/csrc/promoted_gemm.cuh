@@ -62,6 +62,7 @@ struct PgArgs {
   int32_t out_f32;
   int32_t tiles_m, tiles_n;  // (row-grouped: tiles_m unused)
   int32_t group_m;           // raster: row tiles that share a column tile's operand in L2
+  int32_t a_rows;            // rows of A a load brings (K-major A; 128, or all rows where there are fewer)
   int32_t split;             // kSplit: CTAs that share a tile (2..8)
   uint32_t idesc;
   const float* sa;           // 8-bit products: scale of row m, block c at sa[m * sa_row + c * sa_blk]
@@ -508,7 +509,8 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
           };
           const int kx = (C::SPLIT ? t.kb0 + kb : kb) * C::BK;
           const int k0 = (C::K_GROUPS ? t.row0 : 0) + kx;
-          if (rank == 0) mbar_expect_tx(full_bar(stage), (PAIR ? 2 : 1) * (load_a ? C::A_BYTES : C::B_BYTES));
+          const int a_bytes = C::A_MN ? C::A_BYTES : args.a_rows * 128;
+          if (rank == 0) mbar_expect_tx(full_bar(stage), (PAIR ? 2 : 1) * (load_a ? a_bytes : C::B_BYTES));
           if (load_a) {
             const int m0 = t.tm * C::TM + static_cast<int>(rank) * C::BM;
             if (C::A_MN) {
