@@ -812,15 +812,14 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
         };
         if (C::COL_SCALES) {
           // Column scales: a thread takes pairs of columns of four rows (16x256b) instead of one
-          // row, so a warp reads a chunk's scales as 16 words of 8 bytes a thread and not as 32
-          // broadcasts of 16 (which took the SM ~1000 cycles of shared-memory bandwidth a chunk).
-#pragma unroll
-          for (int c = 0; c < C::HALF; c += 32) {
-            uint32_t v[2][16];
+          // row, so that a warp reads a chunk's scales as 16 words of 8 bytes a thread and not as 32
+          // broadcasts of 16.  The registers are filled in turn as below.
+          using Block = uint32_t[2][16];
+          auto load32 = [&](Block& v, int c) {
             tmem_ld_16x256b_x4(t_addr + c, v[0]);
             tmem_ld_16x256b_x4(t_addr + c + (16u << 16), v[1]);
-            tmem_wait_ld();
-            if (c + 32 == C::HALF) release();
+          };
+          auto add_cols32 = [&](Block& v, int c) {
             const uint32_t x = sc + (128 + tile_col(c) + 2 * (lane & 3)) * 4;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -832,6 +831,21 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
                 a0 = fma_f32x2(mul_f32x2(pack_u32x2(r[0], r[1]), col), srow[k], a0);
               }
             }
+          };
+          Block v0, v1;
+          load32(v0, 0);
+          load32(v1, 32);
+          tmem_wait_ld();
+          if (C::HALF == 64) release();
+          add_cols32(v0, 0);
+          if (C::HALF == 128) load32(v0, 64);
+          add_cols32(v1, 32);
+          if (C::HALF == 128) {
+            load32(v1, 96);
+            tmem_wait_ld();
+            release();
+            add_cols32(v0, 64);
+            add_cols32(v1, 96);
           }
         } else {
           uint32_t r0[32], r1[32];
