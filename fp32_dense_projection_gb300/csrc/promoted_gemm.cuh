@@ -113,6 +113,8 @@ struct PgCfg {
   // scale times that of the tile's first and second 128 columns (128 x 128 blocks of B), or
   // the scales of the rows and then of the BN columns.
   static constexpr bool COL_SCALES = KIND == kFp8MM;
+  // A promoting thread holds pairs of columns of four rows (16x256b) instead of one row.
+  static constexpr bool QUADS = COL_SCALES || K_GROUPS;
   static constexpr int SCALE_FLOATS = COL_SCALES ? 128 + BN : 256;
   static constexpr int SCALE_SLOTS = !FP8 ? 1 : NSUB == 2 ? 8 : 16;
   static constexpr int SCALE_BYTES = FP8 ? SCALE_SLOTS * SCALE_FLOATS * 4 : 0;
@@ -810,10 +812,10 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
               mbar_arrive(tempty_bar(buf));
           }
         };
-        if (C::COL_SCALES) {
-          // Column scales: a thread takes pairs of columns of four rows (16x256b) instead of one
-          // row, so that a warp reads a chunk's scales as 16 words of 8 bytes a thread and not as 32
-          // broadcasts of 16.  The registers are filled in turn as below.
+        if (C::QUADS) {
+          // A thread takes pairs of columns of four rows.  With column scales a warp then reads a
+          // chunk's as 16 words of 8 bytes a thread and not as 32 broadcasts of 16; without, the
+          // output goes straight from registers (below).  The registers are filled in turn.
           using Block = uint32_t[2][16];
           auto load32 = [&](Block& v, int c) {
             tmem_ld_16x256b_x4(t_addr + c, v[0]);
@@ -823,23 +825,24 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
             const uint32_t x = sc + (128 + tile_col(c) + 2 * (lane & 3)) * 4;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint64_t col = ld_shared_u64(x + 32 * i);
+              const uint64_t col = C::COL_SCALES ? ld_shared_u64(x + 32 * i) : 0;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 uint64_t& a0 = acc[c / 2 + 4 * i + k];
                 const uint32_t* r = &v[k >> 1][4 * i + 2 * (k & 1)];
-                a0 = fma_f32x2(mul_f32x2(pack_u32x2(r[0], r[1]), col), srow[k], a0);
+                const uint64_t p = pack_u32x2(r[0], r[1]);
+                a0 = C::COL_SCALES ? fma_f32x2(mul_f32x2(p, col), srow[k], a0) : add_f32x2(p, a0);
               }
             }
           };
           Block v0, v1;
           load32(v0, 0);
-          load32(v1, 32);
+          if (C::HALF >= 64) load32(v1, 32);
           tmem_wait_ld();
-          if (C::HALF == 64) release();
+          if (C::HALF <= 64) release();
           add_cols32(v0, 0);
           if (C::HALF == 128) load32(v0, 64);
-          add_cols32(v1, 32);
+          if (C::HALF >= 64) add_cols32(v1, 32);
           if (C::HALF == 128) {
             load32(v1, 96);
             tmem_wait_ld();
@@ -912,17 +915,24 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
       auto lo32 = [&](int j) { return static_cast<uint32_t>(acc[j]); };
       auto hi32 = [&](int j) { return static_cast<uint32_t>(acc[j] >> 32); };
       auto bf16x2 = [&](int j) { return pack_bf16x2(__uint_as_float(lo32(j)), __uint_as_float(hi32(j))); };
-      if (C::COL_SCALES) {
-        // (a thread's pairs go straight out: four lanes write 32 (FP32) or 16 consecutive bytes)
+      if (C::QUADS) {
+        // Straight from registers: neighbouring lanes swap a pair of columns, so that four lanes
+        // hold 16 consecutive columns of a row (64 bytes of FP32, 32 of BF16).
+        const bool odd = (lane & 1) != 0;
+        auto swap32 = [&](uint32_t a, uint32_t b) { return __shfl_xor_sync(0xffffffffu, odd ? a : b, 1); };
 #pragma unroll
-        for (int j = 0; j < C::HALF / 2; ++j) {
-          const int r = 8 * (j & 3) + lane / 4, col = n0 + tile_col(j / 16 * 32) + (j % 16) / 4 * 8 + 2 * (lane & 3);
-          if (r < rows_left && col < args.gn) {
-            char* p = out + (r * args.ldo + col) * esize;
-            if (args.out_f32)
-              *reinterpret_cast<uint64_t*>(p) = acc[j];
-            else
-              *reinterpret_cast<uint32_t*>(p) = bf16x2(j);
+        for (int j = 0; j < C::HALF / 2; j += j % 4 == 3 ? 5 : 1) {  // columns c..c+7, and c+8..c+15 at j + 4
+          const int r = 8 * (j & 3) + lane / 4;
+          const int col = n0 + tile_col(j / 16 * 32) + (j % 16) / 4 * 8 + 2 * (lane & 2) + (odd ? 8 : 0);
+          const bool in = r < rows_left && col < args.gn;
+          char* p = out + (r * args.ldo + col) * esize;
+          if (args.out_f32) {
+            const uint32_t x = swap32(lo32(j), lo32(j + 4)), y = swap32(hi32(j), hi32(j + 4));
+            const uint4 w = odd ? make_uint4(x, y, lo32(j + 4), hi32(j + 4)) : make_uint4(lo32(j), hi32(j), x, y);
+            if (in) *reinterpret_cast<uint4*>(p) = w;
+          } else {
+            const uint32_t a = bf16x2(j), b = bf16x2(j + 4), x = swap32(a, b);
+            if (in) *reinterpret_cast<uint2*>(p) = odd ? make_uint2(x, b) : make_uint2(a, x);
           }
         }
       } else if (args.out_f32) {
