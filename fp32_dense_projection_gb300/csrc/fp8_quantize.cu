@@ -5,13 +5,14 @@
 // weight gradient), or 128 x 128 (weights).  Row and column blocks together come from one
 // read of x.
 //
-// Bound: HBM bytes (2 or 4 read, 1 or 2 written per value).  One CTA of 16 warps takes a
-// 128 x 128 tile and keeps it in registers (BF16 pairs packed), so x is read once whatever the
-// blocks; a thread's loads are in flight together and several CTAs share an SM, so that one
-// tile's loads run beside another's stores.  What stands beside the bytes is instructions: the
-// first form (FP32 in registers, a division per lane and row) took 32 a value and 107 us for
-// 16384 x 4096 BF16, rows and columns.  A row's maximum is a shuffle reduction of two rows at a
-// time, a column's a maximum over the warps in shared memory.
+// Bound: HBM bytes (2 or 4 read, 1 or 2 written per value): 16384 x 4096 BF16, rows and columns,
+// takes 43 us or 6.2 TB/s, FP32 63 us or 6.4 TB/s.  One CTA takes a 128 x 128 tile and keeps it in
+// registers (BF16 pairs packed), so x is read once whatever the blocks; a thread's loads are in
+// flight together and several CTAs share an SM, so that one tile's loads run beside another's
+// stores.  What stands beside the bytes is instructions: the first form (FP32 in registers, a
+// division per lane and row) took 32 a value and 107 us for that BF16 tensor, this one 15.  A
+// row's maximum is a shuffle reduction of two rows at a time, a column's a maximum over the
+// warps in shared memory.
 //
 // Maxima are taken on the bits of |x| as integers (two BF16 at a time): that order puts NaN
 // above infinity, so a block with a NaN gets a NaN scale (and one with an infinity an
@@ -69,21 +70,27 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t m, uint32_t x) {
   return F32 ? max(m, x & 0x7FFFFFFFu) : __vmaxu2(m, x & 0x7FFF7FFFu);
 }
 
-constexpr int kWarps = 16;  // warps of a CTA, 8 rows each
+// Warps of a CTA: FP32 tiles take 16 warps of 8 rows and two CTAs an SM, BF16 tiles, half as many
+// bytes, 8 warps of 16 rows and four CTAs, so that the same bytes are in flight and fewer
+// warps wait at a tile's barriers (16384 x 4096 BF16, rows and columns: 50.8 us with 16 warps, 43.1
+// with 8; FP32: 63.1 with 16, 64.8 with 8).
+template <bool F32>
+constexpr int kWarps = F32 ? 16 : 8;
 
 // A thread holds 16 bytes (4 FP32 or 8 BF16 columns) of each of ITERS rows: a warp's load covers
 // one FP32 row or two BF16 rows of the tile.
 template <int MODE, bool F32, bool E5M2>
-__global__ void __launch_bounds__(kWarps * 32, 2) quantize_kernel(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(kWarps<F32> * 32, F32 ? 2 : 4) quantize_kernel(const __grid_constant__ QuantArgs a) {
   constexpr float kTop = E5M2 ? 57344.0f : 448.0f;
   constexpr bool COL = MODE == kCol || MODE == kBoth, ROW = MODE == kRow || MODE == kBoth;
-  constexpr int CPL = F32 ? 4 : 8, LPR = 128 / CPL, RPI = 32 / LPR, ITERS = 8 / RPI;
-  __shared__ __align__(16) uint32_t part[COL ? kWarps * RPI : 1][COL ? LPR * 4 : 32];
+  constexpr int CPL = F32 ? 4 : 8, LPR = 128 / CPL, RPI = 32 / LPR, WARPS = kWarps<F32>, ROWS = 128 / WARPS,
+                ITERS = ROWS / RPI;
+  __shared__ __align__(16) uint32_t part[COL ? WARPS * RPI : 1][COL ? LPR * 4 : 32];
   __shared__ __align__(16) float factors[COL ? 128 : 4];
   const int lane = static_cast<int>(threadIdx.x) & 31, warp = static_cast<int>(threadIdx.x) >> 5;
   const int cb = static_cast<int>(blockIdx.x) % a.blk_cols, rb = static_cast<int>(blockIdx.x) / a.blk_cols;
   const int tcol = lane % LPR * CPL, col = cb * 128 + tcol;
-  const int row0 = rb * 128 + warp * 8 + lane / LPR;  // this thread's rows: row0 + RPI * i
+  const int row0 = rb * 128 + warp * ROWS + lane / LPR;  // this thread's rows: row0 + RPI * i
   // (cols is a multiple of 16: a thread's columns exist together)
   const int rows = col < a.cols ? a.rows - row0 : 0;
   uint32_t v[ITERS][4];
@@ -167,7 +174,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quantize_kernel(const __grid_c
       const uint32_t w = __reduce_max_sync(0xffffffffu, m[0]);
       if (lane == 0) part[0][warp] = w;
       __syncthreads();
-      const float top = block_max(__reduce_max_sync(0xffffffffu, part[0][lane % kWarps])), f = __fdiv_rn(kTop, top);
+      const float top = block_max(__reduce_max_sync(0xffffffffu, part[0][lane % WARPS])), f = __fdiv_rn(kTop, top);
       if (threadIdx.x == 0) a.s[rb * a.s_row + cb * a.s_col] = __fdiv_rn(top, kTop);
       uint8_t* p = a.q + row0 * a.ldq + col;
 #pragma unroll
@@ -181,7 +188,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quantize_kernel(const __grid_c
         const int t = static_cast<int>(threadIdx.x);
         uint32_t w = 0;
 #pragma unroll
-        for (int k = 0; k < kWarps * RPI; ++k) w = max_bits<F32>(w, part[k][t]);
+        for (int k = 0; k < WARPS * RPI; ++k) w = max_bits<F32>(w, part[k][t]);
         constexpr int PER = CPL / 4;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
@@ -206,16 +213,16 @@ template <bool F32, bool E5M2>
 void launch_quantize(int mode, const QuantArgs& a, unsigned grid, cudaStream_t stream) {
   switch (mode) {
     case kRow:
-      quantize_kernel<kRow, F32, E5M2><<<grid, kWarps * 32, 0, stream>>>(a);
+      quantize_kernel<kRow, F32, E5M2><<<grid, kWarps<F32> * 32, 0, stream>>>(a);
       break;
     case kCol:
-      quantize_kernel<kCol, F32, E5M2><<<grid, kWarps * 32, 0, stream>>>(a);
+      quantize_kernel<kCol, F32, E5M2><<<grid, kWarps<F32> * 32, 0, stream>>>(a);
       break;
     case kBlock:
-      quantize_kernel<kBlock, F32, E5M2><<<grid, kWarps * 32, 0, stream>>>(a);
+      quantize_kernel<kBlock, F32, E5M2><<<grid, kWarps<F32> * 32, 0, stream>>>(a);
       break;
     default:
-      quantize_kernel<kBoth, F32, E5M2><<<grid, kWarps * 32, 0, stream>>>(a);
+      quantize_kernel<kBoth, F32, E5M2><<<grid, kWarps<F32> * 32, 0, stream>>>(a);
       break;
   }
 }
