@@ -24,8 +24,11 @@
 // and a block's maximum is a shuffle reduction over 16 lanes.  One CTA per chunk and not a
 // persistent grid: 1216 CTAs of which 912 are resident left a third of the second round idle
 // (134M elements, BF16 gradients and copies: 700 against 611 us with 32-bit, 495 against 415 us
-// with 8-bit moments).  The tensors' table travels
-// as a kernel parameter: no copy to the device, no state between calls.
+// with 8-bit moments).  With 8-bit moments a warp computes half its time, too long for its
+// loads alone to keep HBM busy, so each CTA also asks L2 for the chunk two per SM further:
+// 427 -> 372 us or 6.6 TB/s (one per SM 422, three 375, four 379, six 382).  32-bit moments, at 609
+// us or 7.0 TB/s without, lose by it (643 at six per SM).  The tensors' table travels as a kernel
+// parameter: no copy to the device, no state between calls.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -59,6 +62,7 @@ struct Table {
   Entry e[MAX];
   int64_t chunk0[MAX + 1];  // first chunk of each tensor
   int32_t count;
+  int32_t ahead;  // 8-bit moments: chunks from one to the one it prefetches
   float beta1, one_beta1, beta2, one_beta2, eps, keep, root_scale, lr;
   float grad_scale;
   const float* grad_scale_ptr;
@@ -149,10 +153,9 @@ __device__ __forceinline__ Pair operator*(Pair a, Pair b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a.v), "l"(b.v));
   return {d};
 }
+// (two instructions: a paired sum of a paired product may be fused with it, into one rounding)
 __device__ __forceinline__ Pair operator+(Pair a, Pair b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a.v), "l"(b.v));
-  return {d};
+  return pair(__fadd_rn(a.lo(), b.lo()), __fadd_rn(a.hi(), b.hi()));
 }
 __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
   uint64_t d;
@@ -215,6 +218,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// Bring `bytes` (a multiple of 16, as is the address) into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 template <int MAX, bool EIGHT>
 __global__ void __launch_bounds__(256, EIGHT ? 6 : 5) adamw_kernel(const __grid_constant__ Table<MAX> t) {
   const float gs = t.grad_scale_ptr ? t.grad_scale * __ldg(t.grad_scale_ptr) : t.grad_scale;
@@ -234,6 +242,14 @@ __global__ void __launch_bounds__(256, EIGHT ? 6 : 5) adamw_kernel(const __grid_
     const int n = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
     const bool fast = (e.flags & 4) != 0 && n == 8;
     const bool p16 = (e.flags & 1) != 0, g16 = (e.flags & 2) != 0;
+    if (EIGHT && threadIdx.x < 4 && (e.flags & 4) != 0 && c + t.ahead + 1 < t.chunk0[lo + 1]) {
+      // (a whole chunk of this tensor, of p, g, m or v)
+      const int w = static_cast<int>(threadIdx.x);
+      const int size = w == 0 ? (p16 ? 2 : 4) : w == 1 ? (g16 ? 2 : 4) : 1;
+      prefetch_l2(static_cast<const char*>(w == 0 ? e.p : w == 1 ? e.g : w == 2 ? e.m : e.v) +
+                      (c - t.chunk0[lo] + t.ahead) * kChunkElems * size,
+                  size * kChunkElems);
+    }
     float p[8], g[8], m[8], v[8];
     load8(e.p, at, p16, fast, n, p);
     load8(e.g, at, g16, fast, n, g);
@@ -325,6 +341,7 @@ cudaError_t launch_adamw(const dp_adamw_tensor* t, int64_t count, const dp_adamw
     tab.chunk0[n] = chunks;
     if (chunks == 0) continue;
     tab.count = n;
+    tab.ahead = 2 * sm_count;
     tab.beta1 = static_cast<float>(h.beta1);
     tab.one_beta1 = static_cast<float>(1.0 - h.beta1);
     tab.beta2 = static_cast<float>(h.beta2);

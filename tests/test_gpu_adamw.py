@@ -8,6 +8,7 @@ the FP32 arithmetic before it adds 1e-6 of the block's largest value, 448 scales
 """
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -177,3 +178,30 @@ def test_more_than_2_31_elements():
     opt = dp.AdamW([p], state_bits=8, lr=0.5, weight_decay=0.0)
     opt.step([g])
     assert bool((p[-200:] == -0.5).all()) and bool((p[-300:-200] == 0).all()) and bool((p[:1000] == 0).all())
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.3])
+def test_8_bit_state_is_the_fp32_formulas_bit_for_bit(scale):
+    """Every operation on the moments is rounded once: FP32 arithmetic elsewhere gives the same codes and scales."""
+    n = 1 << 20
+    p, g, m, v = make([(n,)], 6, torch.float32, torch.bfloat16)
+    (qm, sm), (qv, sv) = encode(m[0]), encode(v[0].sqrt())
+    f = np.float32
+    state = [x.float().cpu().numpy() for x in (qm, sm, qv, sv)]
+    opt = dp.AdamW(p, state_bits=8, exp_avg=[qm], exp_avg_scale=[sm], exp_avg_sq=[qv], exp_avg_sq_scale=[sv], **H)
+    grad = g[0].float().cpu().numpy() * f(scale)
+    (b1, b2), c1, c2 = H["betas"], f(1 - H["betas"][0]), f(1 - H["betas"][1])
+    for _ in range(2):
+        dm, dv = state[0].reshape(-1, 128) * state[1][:, None], state[2].reshape(-1, 128) * state[3][:, None]
+        x = grad.reshape(-1, 128)
+        nm = dm * f(b1) + x * c1
+        root = np.sqrt((dv * dv) * f(b2) + (x * x) * c2)
+        state = []
+        for y, low in ((nm, None), (root, f(2.0 ** -9))):
+            a = np.maximum(np.abs(y).max(1), f(1e-30))
+            z = y * ((f(1) / a) * f(448))[:, None]
+            z = z if low is None else np.where(y > 0, np.maximum(z, low), z)
+            state += [torch.from_numpy(z).to(torch.float8_e4m3fn).float().numpy().reshape(-1), a * (f(1) / f(448))]
+        opt.step(g, grad_scale=scale)
+        for got, want in zip((opt.exp_avg, opt.exp_avg_scale, opt.exp_avg_sq, opt.exp_avg_sq_scale), state):
+            assert np.array_equal(got[0].float().cpu().numpy().reshape(-1), want)
