@@ -17,6 +17,18 @@ _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+def load():
+    """Load the library: a module's first call (it fills the module's table of functions, at once)."""
+    from . import lib
+    lib()
+
+
+def check(code: int, what: str):
+    """Raise the status of a call that did not succeed."""
+    from . import _check
+    _check(code, what)
+
+
 def refuse_devices(name: str, tensors: dict):
     """Say which of the tensors is not on the first one's CUDA device (one of them is not)."""
     first = None

@@ -31,8 +31,8 @@ _fn = {}
 
 
 def _bind(L):
-    _fn["step"] = L.dp_adamw_step
     L.dp_adamw_step.argtypes = [c.P, c.I, c.S, ctypes.POINTER(_Hyper), c.P]
+    _fn["step"] = L.dp_adamw_step
 
 
 _data_ptr, _is_contiguous, _get_device = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
@@ -45,6 +45,10 @@ def _need(ok, what, kind=ValueError):
         raise kind(f"AdamW: {what}")
 
 
+def _scale_shape(shape):
+    return torch.Size((-(-shape.numel() // _BLOCK),))
+
+
 class AdamW:
     """AdamW with decoupled weight decay over a list of tensors.
 
@@ -52,7 +56,8 @@ class AdamW:
     codes with an fp32 scale per 128 consecutive elements: ``exp_avg`` holds m / scale,
     ``exp_avg_sq`` holds sqrt(v) / scale.  The moments are attributes (tuples of tensors) and
     may be passed in, with ``step`` the updates already done, to resume a run.  The updates
-    are made in place, outside autograd.
+    are made in place, outside autograd.  The lists of tensors are fixed at construction; the
+    tensors may get new memory between steps (``.data``), of their shape.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32, copies=None,
@@ -74,68 +79,66 @@ class AdamW:
         _need(copies is None or len(self.copies) == n, "copies must have one entry (a tensor or None) per parameter")
         self._table = np.zeros(n, _ENTRY)
         self._shapes = [p.shape for p in self.params]
-        self._pointers = None
-        self._check_params()
         kind = torch.float8_e4m3fn if state_bits == 8 else _F32
-        self.exp_avg = self._state("exp_avg", exp_avg, kind, False)
-        self.exp_avg_sq = self._state("exp_avg_sq", exp_avg_sq, kind, False)
+        self.exp_avg = self._state(exp_avg, kind, False)
+        self.exp_avg_sq = self._state(exp_avg_sq, kind, False)
         self.exp_avg_scale = self.exp_avg_sq_scale = None
         if state_bits == 8:
-            self.exp_avg_scale = self._state("exp_avg_scale", exp_avg_scale, _F32, True)
-            self.exp_avg_sq_scale = self._state("exp_avg_sq_scale", exp_avg_sq_scale, _F32, True)
+            self.exp_avg_scale = self._state(exp_avg_scale, _F32, True)
+            self.exp_avg_sq_scale = self._state(exp_avg_sq_scale, _F32, True)
         else:
             _need(exp_avg_scale is None and exp_avg_sq_scale is None, "scales belong to state_bits=8")
+        lists = (self.params, self.copies, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)
+        self._held = tuple(x for t in lists for x in t or () if x is not None)
+        self._enter()
 
     def _alike(self, what, t, shape, dtypes):
         _need(isinstance(t, torch.Tensor) and t.device == self.device, f"{what} must be on {self.device}")
         _need(t.dtype in dtypes, f"{what} must be {' or '.join(map(str, dtypes))}", TypeError)
         _need(t.shape == shape and t.is_contiguous(), f"{what} must be contiguous with shape {tuple(shape)}")
 
-    def _check_params(self):
-        """Check the parameters and copies and enter them in the table: at construction, and
-        again whenever one of them has moved (a module's .data may have been replaced)."""
-        for i, (p, shape) in enumerate(zip(self.params, self._shapes)):
-            self._alike(f"params[{i}]", p, shape, (_F32, _BF16))
-        for i, (x, shape) in enumerate(zip(self.copies or (), self._shapes)):
-            if x is not None:
-                self._alike(f"copies[{i}]", x, shape, (_BF16,))
-        t = self._table
-        t["numel"] = [p.numel() for p in self.params]
-        t["param"] = [p.data_ptr() for p in self.params]
-        t["param_bf16"] = [p.dtype is _BF16 for p in self.params]
-        t["copy"] = [0 if x is None else x.data_ptr() for x in self.copies or (None,) * len(self.params)]
+    def _where(self):
+        """Where the parameters, copies and moments are: a step enters them again when one has
+        moved (a module's .data may have been replaced)."""
+        return list(map(_data_ptr, self._held))
+
+    def _enter(self):
+        """Check the tensors and enter them in the table."""
+        kind = torch.float8_e4m3fn if self.state_bits == 8 else _F32
+        for what, tensors in (("param", self.params), ("copy", self.copies), ("exp_avg", self.exp_avg),
+                              ("exp_avg_sq", self.exp_avg_sq), ("exp_avg_scale", self.exp_avg_scale),
+                              ("exp_avg_sq_scale", self.exp_avg_sq_scale)):
+            if tensors is None:
+                continue
+            name = {"param": "params", "copy": "copies"}.get(what, what)
+            _need(len(tensors) == len(self._shapes), f"{name} must have one tensor per parameter")
+            dtypes = {"param": (_F32, _BF16), "copy": (_BF16,)}.get(what, (_F32,) if "scale" in what else (kind,))
+            for i, (x, shape) in enumerate(zip(tensors, self._shapes)):
+                if x is not None or what != "copy":
+                    self._alike(f"{name}[{i}]", x, _scale_shape(shape) if "scale" in what else shape, dtypes)
+            self._table[what] = [0 if x is None else x.data_ptr() for x in tensors]
+        self._table["numel"] = [p.numel() for p in self.params]
+        self._table["param_bf16"] = [p.dtype is _BF16 for p in self.params]
         self._pointers = self._where()
         self._grad_dtypes = None
 
-    def _where(self):
-        where = list(map(_data_ptr, self.params))
-        if self.copies is not None:
-            where += [0 if x is None else x.data_ptr() for x in self.copies]
-        return where
-
-    def _state(self, what, given, dtype, scales):
-        shapes = [torch.Size((-(-p.numel() // _BLOCK),)) if scales else p.shape for p in self.params]
+    def _state(self, given, dtype, scales):
         if given is None:
-            given = tuple(torch.zeros(s, dtype=dtype, device=self.device) for s in shapes)
-        given = tuple(given)
-        _need(len(given) == len(shapes), f"{what} must have one tensor per parameter")
-        for i, (t, s) in enumerate(zip(given, shapes)):
-            self._alike(f"{what}[{i}]", t, s, (dtype,))
-        self._table[what] = [t.data_ptr() for t in given]
-        return given
+            given = (torch.zeros(_scale_shape(p.shape) if scales else p.shape, dtype=dtype, device=self.device)
+                     for p in self.params)
+        return tuple(given)
 
     def step(self, grads, lr=None, grad_scale=1.0, stream=None):
         """One update.  lr overrides the constructor's for this step (a schedule); the
         gradients are multiplied by grad_scale, a number or a one-element fp32 CUDA tensor (a
         clipping coefficient computed on the device, read without synchronising)."""
-        from . import _check as status, lib
         grads = list(grads)
         _need(len(grads) == len(self.params), "grads must have one entry (a tensor or None) per parameter")
         if not grads:
             self.step_count += 1
             return
         if self._where() != self._pointers:
-            self._check_params()
+            self._enter()
         index = self.device.index
         some = [g for g in grads if g is not None]
         shapes = self._shapes if len(some) == len(grads) else [s for g, s in zip(grads, self._shapes) if g is not None]
@@ -163,9 +166,10 @@ class AdamW:
         used = () if stream is None else (*some, *self.params, *self.exp_avg, *self.exp_avg_sq, *(self.exp_avg_scale or ()),
                                           *(self.exp_avg_sq_scale or ()), *(x for x in self.copies or () if x is not None),
                                           *((grad_scale,) if isinstance(grad_scale, torch.Tensor) else ()))
-        lib()
+        if not _fn:
+            c.load()
         code = c.on_stream(index, stream, used,
                            lambda st: _fn["step"](t.ctypes.data, len(grads), self.state_bits, ctypes.byref(h), st))
         if code:
-            status(code, "dp_adamw_step")
+            c.check(code, "dp_adamw_step")
         self.step_count += 1

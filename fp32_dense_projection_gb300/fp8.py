@@ -24,17 +24,16 @@ _fn = {}
 
 def _bind(L):
     P, I, S = c.P, c.I, c.S
-    _fn["dp_fp8_quantize"] = L.dp_fp8_quantize
+    products = ("dp_gemm_fwd_fp8", "dp_gemm_dgrad_fp8", "dp_gemm_wgrad_fp8")
     L.dp_fp8_quantize.argtypes = [P, I, S, I, I, S, S, P, I, P, I, I, P, I, P, I, P]
-    for name in ("dp_gemm_fwd_fp8", "dp_gemm_dgrad_fp8", "dp_gemm_wgrad_fp8"):
-        _fn[name] = getattr(L, name)
-        _fn[name].argtypes = [P, I, S, P, I, I, P, I, S, P, I, I, P, I, I, I, I, S, P]
+    for name in products:
+        getattr(L, name).argtypes = [P, I, S, P, I, I, P, I, S, P, I, I, P, I, I, I, I, S, P]
+    _fn.update({name: getattr(L, name) for name in ("dp_fp8_quantize", *products)})
 
 
 def fp8_quantize(x, scaling="row", dtype=torch.float8_e4m3fn, stream=None):
     """Quantise x [T, C] (bf16 or fp32; C a multiple of 16) with a scale per 128 values:
     (q, scales), or (q_row, scales_row, q_col, scales_col) with scaling="both"."""
-    from . import _check as status, lib
     name = "fp8_quantize"
     mode, fmt = _SCALINGS.get(scaling), _FORMATS.get(dtype)
     if mode is None:
@@ -50,7 +49,8 @@ def fp8_quantize(x, scaling="row", dtype=torch.float8_e4m3fn, stream=None):
     ldx = c.ld(x, name, "x")
     T, C = x.shape
     tb, cb, device = -(-T // 128), -(-C // 128), x.device
-    lib()
+    if not _fn:
+        c.load()
 
     def work(st):
         q = s = qc = sc = None
@@ -70,7 +70,7 @@ def fp8_quantize(x, scaling="row", dtype=torch.float8_e4m3fn, stream=None):
                                       None if s is None else s.data_ptr(), s_row, s_col,
                                       None if qc is None else qc.data_ptr(), C, None if sc is None else sc.data_ptr(), C, st)
         if code:
-            status(code, name)
+            c.check(code, name)
         return (q, s, qc, sc) if mode == 3 else (qc, sc) if mode == 1 else (q, s)
 
     return c.on_stream(index, stream, (x,), work)
@@ -90,21 +90,21 @@ def _refuse(name, a, sa, a_shape, b, sb, b_shape):
 
 
 def _product(name, a, sa, a_shape, b, sb, b_shape, out, out_shape, out_dtype, T, N, K, stream):
-    from . import _check as status, lib
     index, fa, fb = a.get_device(), _FORMATS.get(a.dtype), _FORMATS.get(b.dtype)
     if (index < 0 or sa.get_device() != index or b.get_device() != index or sb.get_device() != index or fa is None or
             fb is None or sa.dtype is not c.F32 or sb.dtype is not c.F32 or sa.shape != a_shape or sb.shape != b_shape):
         _refuse(name, a, sa, a_shape, b, sb, b_shape)
     lda, ldb = c.ld(a, name, "the first operand"), c.ld(b, name, "the second operand")
     (ra, ca), (rb, cb) = sa.stride(), sb.stride()
-    lib()
+    if not _fn:
+        c.load()
 
     def work(st):
         y, code = c.output(out, out_shape, out_dtype, index, a.device, name)
         code = _fn[name](a.data_ptr(), lda, fa, sa.data_ptr(), ra, ca, b.data_ptr(), ldb, fb, sb.data_ptr(), rb, cb,
                          y.data_ptr(), c.ld(y, name, "out"), T, N, K, code, st)
         if code:
-            status(code, name)
+            c.check(code, name)
         return y
 
     return c.on_stream(index, stream, (a, sa, b, sb, out), work)

@@ -16,16 +16,16 @@ import torch
 from . import _call as c
 
 _BITS = {torch.int32: 32, torch.int64: 64}
+_LAYOUTS = {"nk": 0, "kn": 1}
 _fn = {}
 
 
 def _bind(L):
     P, I, S = c.P, c.I, c.S
     for name in ("dp_gemm_fwd_grouped", "dp_gemm_dgrad_grouped"):
-        _fn[name] = getattr(L, name)
-        _fn[name].argtypes = [P, I, P, I, I, S, P, S, P, I, I, I, I, I, S, P]
-    _fn["dp_gemm_wgrad_grouped"] = L.dp_gemm_wgrad_grouped
+        getattr(L, name).argtypes = [P, I, P, I, I, S, P, S, P, I, I, I, I, I, S, P]
     L.dp_gemm_wgrad_grouped.argtypes = [P, I, P, I, P, S, P, I, I, S, I, I, I, I, S, P]
+    _fn.update({name: getattr(L, name) for name in ("dp_gemm_fwd_grouped", "dp_gemm_dgrad_grouped", "dp_gemm_wgrad_grouped")})
 
 
 def _experts(w: torch.Tensor, name: str, what: str):
@@ -35,6 +35,13 @@ def _experts(w: torch.Tensor, name: str, what: str):
         raise ValueError(f"{name}: {what} must be [E, rows, columns] with unit column stride")
     ld = strides[1] if shape[1] > 1 else max(shape[2], 1)
     return ld, strides[0] if shape[0] > 1 else shape[1] * ld
+
+
+def _layout(weight_layout):
+    kn = _LAYOUTS.get(weight_layout)
+    if kn is None:
+        raise ValueError('weight_layout must be "nk" ([N, K] weights) or "kn" ([K, N])')
+    return kn
 
 
 def _check(name, a, b, b_name, offsets, E):
@@ -53,7 +60,6 @@ def _check(name, a, b, b_name, offsets, E):
 
 
 def _rows_by_experts(name, forward, a, W, offsets, out, out_dtype, weight_layout, stream):
-    from . import _check as status, _layout, lib
     kn = _layout(weight_layout)
     if a.dim() != 2 or W.dim() != 3:
         raise ValueError(f"{name}: rows must be 2-D and weights 3-D")
@@ -66,14 +72,15 @@ def _rows_by_experts(name, forward, a, W, offsets, out, out_dtype, weight_layout
     index, bits = _check(name, a, W, "weights", offsets, E)
     ldw, bsw = _experts(W, name, "weights")
     lda = c.ld(a, name, "rows")
-    lib()
+    if not _fn:
+        c.load()
 
     def work(st):
         y, code = c.output(out, (T, N if forward else K), out_dtype, index, a.device, name)
         code = _fn[name](a.data_ptr(), lda, W.data_ptr(), ldw, bsw, kn, offsets.data_ptr(), bits, y.data_ptr(),
                          c.ld(y, name, "out"), E, T, N, K, code, st)
         if code:
-            status(code, name)
+            c.check(code, name)
         return y
 
     return c.on_stream(index, stream, (a, W, offsets, out), work)
@@ -91,7 +98,6 @@ def dp_gemm_dgrad_grouped(dY, W, offsets, out=None, out_dtype=c.BF16, weight_lay
 
 def dp_gemm_wgrad_grouped(dY, X, offsets, out=None, out_dtype=c.BF16, weight_layout="nk", stream=None):
     """dW_e = sum over expert e's rows of dY[t]^T X[t]: dY [T,N]; X [T,K]; dW [E,N,K] ("nk") or [E,K,N] ("kn")."""
-    from . import _check as status, _layout, lib
     name = "dp_gemm_wgrad_grouped"
     kn = _layout(weight_layout)
     if dY.dim() != 2 or X.dim() != 2 or dY.shape[0] != X.shape[0]:
@@ -100,7 +106,8 @@ def dp_gemm_wgrad_grouped(dY, X, offsets, out=None, out_dtype=c.BF16, weight_lay
     E = offsets.numel() - 1
     index, bits = _check(name, dY, X, "X", offsets, max(E, 0))
     ldg, ldx = c.ld(dY, name, "dY"), c.ld(X, name, "X")
-    lib()
+    if not _fn:
+        c.load()
 
     def work(st):
         dW, code = c.output(out, (E, K, N) if kn else (E, N, K), out_dtype, index, dY.device, name)
@@ -108,7 +115,7 @@ def dp_gemm_wgrad_grouped(dY, X, offsets, out=None, out_dtype=c.BF16, weight_lay
         code = _fn[name](dY.data_ptr(), ldg, X.data_ptr(), ldx, offsets.data_ptr(), bits, dW.data_ptr(), ldw, bsw, kn, E, T,
                          N, K, code, st)
         if code:
-            status(code, name)
+            c.check(code, name)
         return dW
 
     return c.on_stream(index, stream, (dY, X, offsets, out), work)

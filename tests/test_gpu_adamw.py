@@ -205,3 +205,30 @@ def test_8_bit_state_is_the_fp32_formulas_bit_for_bit(scale):
         opt.step(g, grad_scale=scale)
         for got, want in zip((opt.exp_avg, opt.exp_avg_scale, opt.exp_avg_sq, opt.exp_avg_sq_scale), state):
             assert np.array_equal(got[0].float().cpu().numpy().reshape(-1), want)
+
+
+def test_tensors_that_move_between_steps():
+    """Parameters, copies and moments may get new memory; of another shape it is refused."""
+    (p,), (g,), _, _ = make([(64, 64)], 8, torch.float32, torch.bfloat16)
+    ref = p.clone()
+    copy = torch.empty_like(p, dtype=torch.bfloat16)
+    a, b = dp.AdamW([p], copies=[copy], **H), dp.AdamW([ref], **H)
+    a.step([g])
+    b.step([g])
+    moved = (p, copy, a.exp_avg[0], a.exp_avg_sq[0])
+    kept, old = [x.clone() for x in moved], [x.data for x in moved]
+    for x in moved:
+        x.data = x.clone()
+    a.step([g])
+    b.step([g])
+    assert torch.equal(p, ref) and torch.equal(copy, ref.bfloat16()) and torch.equal(a.exp_avg[0], b.exp_avg[0])
+    assert all(torch.equal(x, y) for x, y in zip(old, kept))
+    good = p.data
+    for bad in (good[:32].clone(), good.clone().t()):
+        p.data = bad
+        with pytest.raises(ValueError, match="params"):
+            a.step([g])
+    p.data = good
+    a.step([g])
+    b.step([g])
+    assert torch.equal(p, ref)
