@@ -12,8 +12,22 @@
 //   warps 4..11  promotion and epilogue: read a finished chunk's accumulator from TMEM,
 //                add it (scaled) to FP32 registers; after the last chunk, round once and
 //                store.  Warp w holds rows 32 (w % 4) .. + 32 and one half of the columns.
-// A chunk's accumulator is one of two TMEM buffers, so the promotion of one chunk runs
-// beside the MMAs of the next.
+// A chunk's accumulator is one of two TMEM buffers of the tile's width (8-bit tiles of 256
+// columns: two of four halves, each promoted by its own four warps), so the promotion of one
+// chunk runs beside the MMAs of the next.
+//
+// What bounds it, measured on GB300:
+//   grouped, few rows: the experts' weights from HBM (64 rows over 64 experts, 4096 -> 1024: 59-67 us,
+//     5.1-5.8 TB/s, by where the weights lie; 4031 rows over 32: 60 us);
+//   grouped, training: HBM and MMAs about equally (16384 rows over 64 experts, 4096 -> 2048: input
+//     gradient 250-275 us, 1.0-1.1 PFLOP/s beside 4.6-5.1 TB/s), the weight gradient its FP32 output
+//     (407-430 us, 5.5-5.8 TB/s; shared-memory bandwidth 79% busy with the operands);
+//   8-bit: the promotion.  A 128 x 256 block's MMAs take 512 cycles; reading its sums from TMEM (145
+//     cycles), adding them (256 at the FP32 pipe's rate) and the waits around them one after
+//     another 700-800, with column scales and their second multiplication 1200 (T = 16384,
+//     12288 -> 4096: 591-622 us, 2.7 PFLOP/s; weight gradient T = 16173, 1024 x 4096: 80 us).  Asking
+//     for the next chunk before adding this one took 4 to 7% off; more promoting warps, reading
+//     the next chunk's first columns early and spinning waits took nothing.
 //
 // Why promotion: (1) the scale of a 128-element block multiplies that block's sum only,
 // so it cannot be applied after the whole contraction; (2) the tensor core rounds every
@@ -759,15 +773,16 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
     // the tile is decoded again for the store.)
     uint32_t it = 0;  // chunks done by this CTA
     bool exchanged = false;
-    bool ok = true;
+    bool ok = true, ready = false;
     for (int u = unit0; u < units; u += step) {
       uint64_t acc[C::HALF / 2];  // pairs of columns
 #pragma unroll
       for (int j = 0; j < C::HALF / 2; ++j) acc[j] = 0;
       for (int left = (walk.at(u).nkb + CHUNK - 1) / CHUNK; left > 0; --left, ++it) {
-        const uint32_t buf = C::NSUB == 2 ? 2 * (it & 1u) + static_cast<uint32_t>(h) : it % C::NBUF;
-        const uint32_t parity = (it * C::NSUB / C::NBUF) & 1u;
-        if (!__all_sync(0xffffffffu, mbar_wait_soon<PAIR>(tfull_bar(buf), parity, args.wait_ns))) {
+        auto buffer = [&](uint32_t i) { return C::NSUB == 2 ? 2 * (i & 1u) + static_cast<uint32_t>(h) : i % C::NBUF; };
+        auto parity = [&](uint32_t i) { return (i * C::NSUB / C::NBUF) & 1u; };
+        const uint32_t buf = buffer(it);
+        if (!ready && !__all_sync(0xffffffffu, mbar_wait_soon<PAIR>(tfull_bar(buf), parity(it), args.wait_ns))) {
           if (lane == 0) atomicOr(args.fault, kFaultEpilogueWait);
           ok = false;
           break;
@@ -811,6 +826,9 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
             else
               mbar_arrive(tempty_bar(buf));
           }
+          // (whether the next chunk is there is asked here, beside the additions that follow)
+          const uint32_t next = tfull_bar(buffer(it + 1));
+          ready = __all_sync(0xffffffffu, PAIR ? mbar_peek_cluster(next, parity(it + 1)) : mbar_peek(next, parity(it + 1)));
         };
         if (C::QUADS) {
           // A thread takes pairs of columns of four rows.  With column scales a warp then reads a
