@@ -68,10 +68,10 @@ int cluster_capacity(int dev, int kind, int bn, int split) {
 // The form of least modelled time.  A CTA's time is its blocks (128 contraction elements) at
 // the rate measured for its tile, whole waves of tiles counted.  Measured on GB300 (forced
 // forms, 34 shapes), ns a block: 128 x 128 215, 128 x 256 405, pairs of 256 x 256 440 while one
-// wave suffices; with more waves 255 / 425 / 420, as narrow tiles then wait for L2 and pairs,
-// which load least, do not (16384 x 12288 -> 4096: 785 / 586 / 558 us; 4031 x 4096 -> 4096: 61.5 /
-// 60.5 / 60.4).  With column scales, whose promotion takes twice the operations and reads every
-// column's scale, it is 350 / 640 / 630 for both.  A split adds its exchange: barriers of the
+// wave suffices; with more waves 255 / 410 / 400, as narrow tiles then wait for L2 and pairs,
+// which load least, do not (16384 x 12288 -> 4096: 795 / 559 / 537 us; 4031 x 4096 -> 4096: 62.0 /
+// 57.5 / 57.8).  With column scales, whose promotion takes twice the operations and reads every
+// column's scale, it is 350 / 595 / 585 for both.  A split adds its exchange: barriers of the
 // cluster, and the tile's rows through its shared memory.
 Fp8Plan plan_fp8(int kind, int64_t gm, int64_t gn, int64_t nkb, const DeviceContext& ctx) {
   struct Rates {
@@ -79,8 +79,8 @@ Fp8Plan plan_fp8(int kind, int64_t gm, int64_t gn, int64_t nkb, const DeviceCont
   };
   const bool cols = kind == kFp8MM;
   const int sm_count = ctx.sm_count;
-  const Rates r128 = cols ? Rates{350, 350} : Rates{215, 255}, r256 = cols ? Rates{640, 640} : Rates{405, 425},
-              r_pair = cols ? Rates{630, 630} : Rates{440, 420};
+  const Rates r128 = cols ? Rates{350, 350} : Rates{215, 255}, r256 = cols ? Rates{595, 595} : Rates{405, 410},
+              r_pair = cols ? Rates{585, 585} : Rates{440, 400};
   Fp8Plan best = {128, kPlain, 1};
   double least = 1e30;
   auto offer = [&](int bn, int form, int split, int64_t tiles, int64_t slots, const Rates& r) {
