@@ -23,7 +23,7 @@
 // thread 8 consecutive ones: every load of the chunk is in flight before the first use,
 // and a block's maximum is a shuffle reduction over 16 lanes.  One CTA per chunk and not a
 // persistent grid: 1216 CTAs of which 912 are resident left a third of the second round idle
-// (134M elements, BF16 gradients and copies: 700 against 611 us with 32-bit, 495 against 415 us
+// (153M elements, BF16 gradients and copies: 700 against 611 us with 32-bit, 495 against 415 us
 // with 8-bit moments).  With 8-bit moments a warp computes half its time, too long for its
 // loads alone to keep HBM busy, so each CTA also asks L2 for the chunk two per SM further:
 // 427 -> 372 us or 6.6 TB/s (one per SM 422, three 375, four 379, six 382).  32-bit moments, at 609

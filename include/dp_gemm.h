@@ -288,7 +288,7 @@ dp_status router_wgrad_ex(const float* dY, int64_t ldg, const float* X, int64_t 
  * Experts without rows: dW_e = 0.
  * weight_kn: W_e and dW_e are [N][K] (0) or [K][N] (1) matrices, ldw apart by rows and bsw
  *   apart by experts (elements; 0 = packed).
- * FP32 accumulation in pieces of 2048 contraction elements that are added in FP32 with
+ * FP32 accumulation in pieces of 512 contraction elements that are added in FP32 with
  * round-to-nearest, whatever the group's size; every output is deterministic.  One launch,
  * no workspace.  At most 1024 experts. */
 dp_status dp_gemm_fwd_grouped(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t bsw, int weight_kn,

@@ -262,3 +262,22 @@ def test_output_beyond_32_bit_offsets():
         e = 0 if s.start < T // 2 else 1
         assert torch.equal(out[s], (c["X"][s].double() @ c["W"][e].double().T).to(torch.bfloat16))
     assert bool((out[T - 3:] == 0).all())
+
+
+@pytest.mark.parametrize("depth", [64, 512, 2048, 16384])
+def test_error_does_not_grow_with_the_contraction(depth):
+    """FP32 outputs: the tensor core's sums over 16384 elements are 1.9e-5 off, so over 512 elements
+    6e-7; up to 32 such sums added in FP32 give 2e-7 more."""
+    g = torch.Generator(device=DEV).manual_seed(depth)
+    X = torch.randn(96, depth, device=DEV, generator=g).bfloat16()
+    W = torch.randn(3, 128, depth, device=DEV, generator=g).bfloat16()
+    offsets = torch.tensor([0, 40, 40, 96], device=DEV, dtype=torch.int32)
+    D = torch.randn(depth, 96, device=DEV, generator=g).bfloat16()
+    Z = torch.randn(depth, 128, device=DEV, generator=g).bfloat16()
+
+    def error(got, want):
+        return float((got.double() - want).norm() / want.norm())
+    want = torch.cat([X[:40].double() @ W[0].double().T, X[40:].double() @ W[2].double().T])
+    assert error(dp.dp_gemm_fwd_grouped(X, W, offsets, out_dtype=torch.float32), want) < 8e-7
+    one = torch.tensor([0, depth], device=DEV, dtype=torch.int32)
+    assert error(dp.dp_gemm_wgrad_grouped(D, Z, one, out_dtype=torch.float32)[0], D.double().T @ Z.double()) < 8e-7
