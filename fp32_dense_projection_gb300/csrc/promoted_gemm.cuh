@@ -493,272 +493,273 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
 
   // (Narrower tiles need fewer registers than every thread has at launch.)
   if (warp < 4) {
-  if (BN == 256) regs_give<88>();
-  if (warp == 0 || warp == 2) {
-    // -------------------------------------------------------------- producers
-    if (lane == 0) {
-      const bool load_a = warp == 0;
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_phase = 0;
+    if (BN == 256) regs_give<88>();
+    if (warp == 0 || warp == 2) {
+      // -------------------------------------------------------------- producers
+      if (lane == 0) {
+        const bool load_a = warp == 0;
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, issued_phase = 0;
+        bool ok = true;
+        for (int u = unit0; ok && u < units; u += step) {
+          const PgTile t = walk.at(u);
+          for (int kb = 0; kb < t.nkb; ++kb) {
+            if (!mbar_wait<PAIR>(empty_bar(stage), phase ^ 1u, args.wait_ns)) {
+              atomicOr(args.fault, kFaultProducerWait);
+              ok = false;
+              break;
+            }
+            // (a pair's loads all complete on the leader's barrier)
+            const uint32_t fb = PAIR ? map_shared_rank(full_bar(stage), 0) : full_bar(stage);
+            const uint32_t sa = base + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+            auto load2 = [&](uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y) {
+              if (PAIR)
+                tma_load_2d_pair(dst, map, fb, x, y);
+              else
+                tma_load_2d(dst, map, fb, x, y);
+            };
+            auto load3 = [&](uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z) {
+              if (PAIR)
+                tma_load_3d_pair(dst, map, fb, x, y, z);
+              else
+                tma_load_3d(dst, map, fb, x, y, z);
+            };
+            const int kx = (C::SPLIT ? t.kb0 + kb : kb) * C::BK;
+            const int k0 = (C::K_GROUPS ? t.row0 : 0) + kx;
+            const int a_bytes = C::A_MN ? C::A_BYTES : args.a_rows * 128;
+            if (rank == 0) mbar_expect_tx(full_bar(stage), (PAIR ? 2 : 1) * (load_a ? a_bytes : C::B_BYTES));
+            if (load_a) {
+              const int m0 = t.tm * C::TM + static_cast<int>(rank) * C::BM;
+              if (C::A_MN) {
+#pragma unroll
+                for (int g = 0; g < C::BM / C::MN; ++g) load2(sa + g * (C::BK * 128), &tmA, m0 + g * C::MN, k0);
+              } else {
+                load2(sa, &tmA, kx, C::ROW_GROUPS ? t.row0 + static_cast<int>(rank) * C::BM : m0);
+              }
+            } else {
+              const int n0 = t.tn * BN + static_cast<int>(rank) * C::BNL;
+              if (C::B_MN) {
+#pragma unroll
+                for (int g = 0; g < C::BNL / C::MN; ++g) {
+                  if (C::ROW_GROUPS)
+                    load3(sb + g * (C::BK * 128), &tmB, n0 + g * C::MN, k0, t.e);
+                  else
+                    load2(sb + g * (C::BK * 128), &tmB, n0 + g * C::MN, k0);
+                }
+              } else if (C::ROW_GROUPS) {
+                load3(sb, &tmB, kx, n0, t.e);
+              } else {
+                load2(sb, &tmB, kx, n0);
+              }
+            }
+            issued |= 1u << stage;
+            issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        // every load has landed before the CTA may exit (a pair's: the MMAs that read it are done)
+        for (int s = 0; s < STAGES; ++s)
+          if ((issued >> s) & 1u)
+            if (!mbar_wait<PAIR>(PAIR ? empty_bar(s) : full_bar(s), (issued_phase >> s) & 1u, args.wait_ns))
+              atomicOr(args.fault, kFaultDrainWait);
+      }
+    } else if (warp == 1) {
+      if (rank == 0) {
+        // ------------------------------------------------------------- MMA issuer
+        // One elected thread walks the list (297 cycles a block with nothing to wait for, against
+        // 415 where the whole warp walks it, votes and elects for each block: a block's MMAs take
+        // 512).  Ragged contractions need the warp: its lanes zero the rows of a last block.
+        constexpr bool SOLO = !C::K_GROUPS;
+        if (!SOLO || elect_one()) {
+          auto all = [](bool in) { return SOLO ? in : __all_sync(0xffffffffu, in) != 0; };
+          auto one = []() { return SOLO || elect_one(); };
+          auto give_up = [&]() {
+            if (SOLO || lane == 0) atomicOr(args.fault, kFaultMmaWait);
+            return false;
+          };
+          int stage = 0, buf = 0;
+          uint32_t phase = 0, bphase = 0;
+          bool ok = true;
+          // descriptors of stage 0 and their step per slice: K-major 32 bytes along the swizzled row,
+          // MN-major SLICE rows of 128 bytes (see sdesc_sw128)
+          constexpr uint32_t A_STEP = C::A_MN ? C::SLICE * 8 : 2, B_STEP = C::B_MN ? C::SLICE * 8 : 2;
+          // B of the second 128-column MMA: 128 K-major rows further, or the next MN-major box.  A
+          // pair's MMA takes 64 of its columns from each CTA: 64 rows further, or 64 bytes along the
+          // rows of the one box (see tile_col for the columns this makes).
+          constexpr uint32_t SUB_STEP = !PAIR ? 128 * 128 / 16 : C::B_MN ? 64 / 16 : 64 * 128 / 16;
+          const uint64_t a_desc = sdesc_sw128(base, C::A_MN ? C::BK * 128 : 16, 1024);
+          const uint64_t b_desc = sdesc_sw128(base + C::A_BYTES, C::B_MN ? C::BK * 128 : 16, 1024);
+          const uint32_t a_lo = static_cast<uint32_t>(a_desc), a_hi = static_cast<uint32_t>(a_desc >> 32);
+          const uint32_t b_lo = static_cast<uint32_t>(b_desc), b_hi = static_cast<uint32_t>(b_desc >> 32);
+          for (int u = unit0; ok && u < units; u += step) {
+            const PgTile t = walk.at(u);
+            for (int c0 = 0; ok && c0 < t.nkb; c0 += CHUNK) {
+              const int c1 = min(c0 + CHUNK, t.nkb);
+              auto wait_empty = [&](int b) {
+                return all(mbar_wait_soon<PAIR>(tempty_bar(b), bphase ^ 1u, args.wait_ns)) || give_up();
+              };
+              if (!(ok = wait_empty(buf))) break;
+              for (int kb = c0; kb < c1; ++kb) {
+                if (!all(mbar_wait_soon<PAIR>(full_bar(stage), phase, args.wait_ns))) {
+                  ok = give_up();
+                  break;
+                }
+                int slices = C::BK / C::SLICE;
+                if (C::K_GROUPS) {
+                  // the last block's rows past the group's end belong to the next group: contract
+                  // whole slices only, and zero the rest of the last one in both operands (a
+                  // product with an infinity or NaN there would not vanish)
+                  const int valid = t.k_left - kb * C::BK;
+                  if (valid < C::BK) {
+                    slices = (valid + C::SLICE - 1) / C::SLICE;
+                    const int rows = slices * C::SLICE - valid;  // 0..15 rows of 128 bytes in each box
+                    constexpr int BOXES = (C::BM + BN) / C::MN;
+                    for (int i = lane; i < rows * 8 * BOXES; i += 32) {
+                      const int box = i / (rows * 8), j = i - box * (rows * 8);
+                      const int at = box * (C::BK * 128) + (valid + (j >> 3)) * 128 + (j & 7) * 16;
+                      st_shared_u4(base + stage * C::STAGE_BYTES + at, make_uint4(0, 0, 0, 0));
+                    }
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                  }
+                }
+#pragma unroll
+                for (int sub = 0; sub < C::NSUB; ++sub) {
+                  if (sub > 0 && !(ok = wait_empty(buf + sub))) break;
+                  tc_fence_after();
+                  if (one()) {
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((buf + sub) * C::SUB);
+                    const uint32_t at = static_cast<uint32_t>(stage) * (C::STAGE_BYTES >> 4);
+                    auto issue = [&](int kk) {
+                      mma_lo<C::FP8, PAIR>(d_tmem, a_lo + at + kk * A_STEP, a_hi, b_lo + at + sub * SUB_STEP + kk * B_STEP, b_hi,
+                                           args.idesc, (kb > c0 || kk > 0) ? 1u : 0u);
+                    };
+                    if (C::K_GROUPS && slices < C::BK / C::SLICE) {
+                      for (int kk = 0; kk < slices; ++kk) issue(kk);
+                    } else {
+#pragma unroll
+                      for (int kk = 0; kk < C::BK / C::SLICE; ++kk) issue(kk);
+                    }
+                    auto commit = [&](uint32_t bar) {  // (in both CTAs of a pair)
+                      if (PAIR)
+                        mma_commit_pair_multicast(bar, 0x3);
+                      else
+                        mma_commit(bar);
+                    };
+                    if (sub == C::NSUB - 1) commit(empty_bar(stage));
+                    if (kb + 1 == c1) commit(tfull_bar(buf + sub));
+                  }
+                  if (!SOLO) __syncwarp();
+                }
+                if (!ok) break;
+                if (++stage == STAGES) {
+                  stage = 0;
+                  phase ^= 1u;
+                }
+              }
+              if (!ok) break;
+              if ((buf += C::NSUB) == C::NBUF) {
+                buf = 0;
+                bphase ^= 1u;
+              }
+            }
+          }
+          // every MMA has finished before TMEM is freed (a commit covers the MMAs of the thread that
+          // issues it: the elected one is the same throughout)
+          if (one()) {
+            if (PAIR)
+              mma_commit_pair(drain_bar);
+            else
+              mma_commit(drain_bar);
+            if (!mbar_wait(drain_bar, 0, args.wait_ns)) atomicOr(args.fault, kFaultDrainWait);
+          }
+        }
+        __syncwarp();
+      }
+    } else if (C::FP8) {
+      // ------------------------------------------------------------------ scales
+      // A chunk's accumulator barriers take an arrival of this warp beside the MMAs' commit, so the
+      // epilogue waits once for the sums and their scales.  The arrival may be made once the
+      // barrier's phase before is over (the chunk NBUF / NSUB earlier); the loads run kScaleAhead
+      // chunks ahead of it, in registers.  A ring slot's last readers are done by then: they gave
+      // back the accumulator of a later chunk, which the MMAs of that earlier phase overwrote.
+      static_assert(!C::FP8 || C::SCALE_SLOTS > 2 * C::NBUF / C::NSUB, "scale ring");
+      constexpr int NB = C::COL_SCALES ? BN / 32 : 2, NV = 4 + NB;
+      float v[kScaleAhead][NV];
+      int lu = unit0, left = 0;  // tile of the next load, chunks left in it
+      const float* at[NV];
+      bool in[NV];
+      // (rows and columns past the edges have zero operands: their scale is zero)
+      auto load = [&](float (&x)[NV]) {
+        if (left == 0) {
+          if (lu >= units) return;
+          const PgTile t = walk.at(lu);
+          lu += step;
+          left = t.nkb;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int m = t.tm * C::TM + static_cast<int>(rank) * C::BM + 32 * j + lane;
+            in[j] = m < args.gm;
+            at[j] = args.sa + (in[j] ? m * args.sa_row + t.kb0 * args.sa_blk : 0);
+          }
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            const int n = t.tn * BN + (C::COL_SCALES ? 32 * j + lane : 128 * j);
+            in[4 + j] = n < args.gn;
+            at[4 + j] = args.sb + (in[4 + j] ? (C::COL_SCALES ? n : n / 128) * args.sb_row + t.kb0 * args.sb_blk : 0);
+          }
+        }
+        --left;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          x[j] = in[j] ? __ldg(at[j]) : 0.0f;
+          at[j] += j < 4 ? args.sa_blk : args.sb_blk;
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < kScaleAhead; ++i) load(v[i]);
+      // (every tile has the same number of blocks; a split launch gives each CTA one share)
+      const int nkb = C::SPLIT ? walk.at(unit0).nkb : (args.gk + C::BK - 1) / C::BK;
+      const int total = unit0 < units ? ((units - unit0 + step - 1) / step) * nkb : 0;
       bool ok = true;
-      for (int u = unit0; ok && u < units; u += step) {
-        const PgTile t = walk.at(u);
-        for (int kb = 0; kb < t.nkb; ++kb) {
-          if (!mbar_wait<PAIR>(empty_bar(stage), phase ^ 1u, args.wait_ns)) {
-            atomicOr(args.fault, kFaultProducerWait);
+      for (int i0 = 0; ok && i0 < total; i0 += kScaleAhead) {
+#pragma unroll
+        for (int k = 0; k < kScaleAhead; ++k) {
+          const int i = i0 + k;
+          if (i >= total) break;
+          const int b = i * C::NSUB % C::NBUF;
+          const uint32_t parity = ((i * C::NSUB / C::NBUF) & 1) ^ 1;
+          bool free = mbar_wait_soon<PAIR>(tfull_bar(b), parity, args.wait_ns);
+          if (C::NSUB == 2) free = free && mbar_wait_soon<PAIR>(tfull_bar(b + 1), parity, args.wait_ns);
+          if (!__all_sync(0xffffffffu, free)) {
+            if (lane == 0) atomicOr(args.fault, kFaultProducerWait);
             ok = false;
             break;
           }
-          // (a pair's loads all complete on the leader's barrier)
-          const uint32_t fb = PAIR ? map_shared_rank(full_bar(stage), 0) : full_bar(stage);
-          const uint32_t sa = base + stage * C::STAGE_BYTES, sb = sa + C::A_BYTES;
-          auto load2 = [&](uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y) {
-            if (PAIR)
-              tma_load_2d_pair(dst, map, fb, x, y);
-            else
-              tma_load_2d(dst, map, fb, x, y);
-          };
-          auto load3 = [&](uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z) {
-            if (PAIR)
-              tma_load_3d_pair(dst, map, fb, x, y, z);
-            else
-              tma_load_3d(dst, map, fb, x, y, z);
-          };
-          const int kx = (C::SPLIT ? t.kb0 + kb : kb) * C::BK;
-          const int k0 = (C::K_GROUPS ? t.row0 : 0) + kx;
-          const int a_bytes = C::A_MN ? C::A_BYTES : args.a_rows * 128;
-          if (rank == 0) mbar_expect_tx(full_bar(stage), (PAIR ? 2 : 1) * (load_a ? a_bytes : C::B_BYTES));
-          if (load_a) {
-            const int m0 = t.tm * C::TM + static_cast<int>(rank) * C::BM;
-            if (C::A_MN) {
+          const uint32_t dst = scbase + static_cast<uint32_t>(i % C::SCALE_SLOTS) * (C::SCALE_FLOATS * 4);
+          if (C::COL_SCALES) {
 #pragma unroll
-              for (int g = 0; g < C::BM / C::MN; ++g) load2(sa + g * (C::BK * 128), &tmA, m0 + g * C::MN, k0);
-            } else {
-              load2(sa, &tmA, kx, C::ROW_GROUPS ? t.row0 + static_cast<int>(rank) * C::BM : m0);
-            }
+            for (int j = 0; j < NV; ++j) st_shared_f32(dst + (32 * j + lane) * 4, v[k][j]);
           } else {
-            const int n0 = t.tn * BN + static_cast<int>(rank) * C::BNL;
-            if (C::B_MN) {
 #pragma unroll
-              for (int g = 0; g < C::BNL / C::MN; ++g) {
-                if (C::ROW_GROUPS)
-                  load3(sb + g * (C::BK * 128), &tmB, n0 + g * C::MN, k0, t.e);
-                else
-                  load2(sb + g * (C::BK * 128), &tmB, n0 + g * C::MN, k0);
-              }
-            } else if (C::ROW_GROUPS) {
-              load3(sb, &tmB, kx, n0, t.e);
-            } else {
-              load2(sb, &tmB, kx, n0);
-            }
+            for (int j = 0; j < 4; ++j) st_shared_f2(dst + (32 * j + lane) * 8, v[k][j] * v[k][4], v[k][j] * v[k][5]);
           }
-          issued |= 1u << stage;
-          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(tfull_bar(b));
+            if (C::NSUB == 2) mbar_arrive(tfull_bar(b + 1));
           }
-        }
-      }
-      // every load has landed before the CTA may exit (a pair's: the MMAs that read it are done)
-      for (int s = 0; s < STAGES; ++s)
-        if ((issued >> s) & 1u)
-          if (!mbar_wait<PAIR>(PAIR ? empty_bar(s) : full_bar(s), (issued_phase >> s) & 1u, args.wait_ns))
-            atomicOr(args.fault, kFaultDrainWait);
-    }
-  } else if (warp == 1) {
-    if (rank == 0) {
-    // ------------------------------------------------------------- MMA issuer
-    // One elected thread walks the list (297 cycles a block with nothing to wait for, against
-    // 415 where the whole warp walks it, votes and elects for each block: a block's MMAs take
-    // 512).  Ragged contractions need the warp: its lanes zero the rows of a last block.
-    constexpr bool SOLO = !C::K_GROUPS;
-    if (!SOLO || elect_one()) {
-    auto all = [](bool in) { return SOLO ? in : __all_sync(0xffffffffu, in) != 0; };
-    auto one = []() { return SOLO || elect_one(); };
-    auto give_up = [&]() {
-      if (SOLO || lane == 0) atomicOr(args.fault, kFaultMmaWait);
-      return false;
-    };
-    int stage = 0, buf = 0;
-    uint32_t phase = 0, bphase = 0;
-    bool ok = true;
-    // descriptors of stage 0 and their step per slice: K-major 32 bytes along the swizzled row,
-    // MN-major SLICE rows of 128 bytes (see sdesc_sw128)
-    constexpr uint32_t A_STEP = C::A_MN ? C::SLICE * 8 : 2, B_STEP = C::B_MN ? C::SLICE * 8 : 2;
-    // B of the second 128-column MMA: 128 K-major rows further, or the next MN-major box.  A
-    // pair's MMA takes 64 of its columns from each CTA: 64 rows further, or 64 bytes along the
-    // rows of the one box (see tile_col for the columns this makes).
-    constexpr uint32_t SUB_STEP = !PAIR ? 128 * 128 / 16 : C::B_MN ? 64 / 16 : 64 * 128 / 16;
-    const uint64_t a_desc = sdesc_sw128(base, C::A_MN ? C::BK * 128 : 16, 1024);
-    const uint64_t b_desc = sdesc_sw128(base + C::A_BYTES, C::B_MN ? C::BK * 128 : 16, 1024);
-    const uint32_t a_lo = static_cast<uint32_t>(a_desc), a_hi = static_cast<uint32_t>(a_desc >> 32);
-    const uint32_t b_lo = static_cast<uint32_t>(b_desc), b_hi = static_cast<uint32_t>(b_desc >> 32);
-    for (int u = unit0; ok && u < units; u += step) {
-      const PgTile t = walk.at(u);
-      for (int c0 = 0; ok && c0 < t.nkb; c0 += CHUNK) {
-        const int c1 = min(c0 + CHUNK, t.nkb);
-        auto wait_empty = [&](int b) {
-          return all(mbar_wait_soon<PAIR>(tempty_bar(b), bphase ^ 1u, args.wait_ns)) || give_up();
-        };
-        if (!(ok = wait_empty(buf))) break;
-        for (int kb = c0; kb < c1; ++kb) {
-          if (!all(mbar_wait_soon<PAIR>(full_bar(stage), phase, args.wait_ns))) {
-            ok = give_up();
-            break;
-          }
-          int slices = C::BK / C::SLICE;
-          if (C::K_GROUPS) {
-            // the last block's rows past the group's end belong to the next group: contract
-            // whole slices only, and zero the rest of the last one in both operands (a
-            // product with an infinity or NaN there would not vanish)
-            const int valid = t.k_left - kb * C::BK;
-            if (valid < C::BK) {
-              slices = (valid + C::SLICE - 1) / C::SLICE;
-              const int rows = slices * C::SLICE - valid;  // 0..15 rows of 128 bytes in each box
-              constexpr int BOXES = (C::BM + BN) / C::MN;
-              for (int i = lane; i < rows * 8 * BOXES; i += 32) {
-                const int box = i / (rows * 8), j = i - box * (rows * 8);
-                st_shared_u4(base + stage * C::STAGE_BYTES + box * (C::BK * 128) + (valid + (j >> 3)) * 128 + (j & 7) * 16, make_uint4(0, 0, 0, 0));
-              }
-              fence_proxy_async_shared();
-              __syncwarp();
-            }
-          }
-#pragma unroll
-          for (int sub = 0; sub < C::NSUB; ++sub) {
-            if (sub > 0 && !(ok = wait_empty(buf + sub))) break;
-            tc_fence_after();
-            if (one()) {
-              const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((buf + sub) * C::SUB);
-              const uint32_t at = static_cast<uint32_t>(stage) * (C::STAGE_BYTES >> 4);
-              auto issue = [&](int kk) {
-                mma_lo<C::FP8, PAIR>(d_tmem, a_lo + at + kk * A_STEP, a_hi, b_lo + at + sub * SUB_STEP + kk * B_STEP, b_hi,
-                                     args.idesc, (kb > c0 || kk > 0) ? 1u : 0u);
-              };
-              if (C::K_GROUPS && slices < C::BK / C::SLICE) {
-                for (int kk = 0; kk < slices; ++kk) issue(kk);
-              } else {
-#pragma unroll
-                for (int kk = 0; kk < C::BK / C::SLICE; ++kk) issue(kk);
-              }
-              auto commit = [&](uint32_t bar) {  // (in both CTAs of a pair)
-                if (PAIR)
-                  mma_commit_pair_multicast(bar, 0x3);
-                else
-                  mma_commit(bar);
-              };
-              if (sub == C::NSUB - 1) commit(empty_bar(stage));
-              if (kb + 1 == c1) commit(tfull_bar(buf + sub));
-            }
-            if (!SOLO) __syncwarp();
-          }
-          if (!ok) break;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        if (!ok) break;
-        if ((buf += C::NSUB) == C::NBUF) {
-          buf = 0;
-          bphase ^= 1u;
+          load(v[k]);
         }
       }
     }
-    // every MMA has finished before TMEM is freed (a commit covers the MMAs of the thread that
-    // issues it: the elected one is the same throughout)
-    if (one()) {
-      if (PAIR)
-        mma_commit_pair(drain_bar);
-      else
-        mma_commit(drain_bar);
-      if (!mbar_wait(drain_bar, 0, args.wait_ns)) atomicOr(args.fault, kFaultDrainWait);
+    if (C::SPLIT) {  // (the epilogue warps' exchange)
+      cluster_sync();
+      cluster_sync();
     }
-    }
-    __syncwarp();
-    }
-  } else if (C::FP8) {
-    // ------------------------------------------------------------------ scales
-    // A chunk's accumulator barriers take an arrival of this warp beside the MMAs' commit, so the
-    // epilogue waits once for the sums and their scales.  The arrival may be made once the
-    // barrier's phase before is over (the chunk NBUF / NSUB earlier); the loads run kScaleAhead
-    // chunks ahead of it, in registers.  A ring slot's last readers are done by then: they gave
-    // back the accumulator of a later chunk, which the MMAs of that earlier phase overwrote.
-    static_assert(!C::FP8 || C::SCALE_SLOTS > 2 * C::NBUF / C::NSUB, "scale ring");
-    constexpr int NB = C::COL_SCALES ? BN / 32 : 2, NV = 4 + NB;
-    float v[kScaleAhead][NV];
-    int lu = unit0, left = 0;  // tile of the next load, chunks left in it
-    const float* at[NV];
-    bool in[NV];
-    // (rows and columns past the edges have zero operands: their scale is zero)
-    auto load = [&](float (&x)[NV]) {
-      if (left == 0) {
-        if (lu >= units) return;
-        const PgTile t = walk.at(lu);
-        lu += step;
-        left = t.nkb;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int m = t.tm * C::TM + static_cast<int>(rank) * C::BM + 32 * j + lane;
-          in[j] = m < args.gm;
-          at[j] = args.sa + (in[j] ? m * args.sa_row + t.kb0 * args.sa_blk : 0);
-        }
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const int n = t.tn * BN + (C::COL_SCALES ? 32 * j + lane : 128 * j);
-          in[4 + j] = n < args.gn;
-          at[4 + j] = args.sb + (in[4 + j] ? (C::COL_SCALES ? n : n / 128) * args.sb_row + t.kb0 * args.sb_blk : 0);
-        }
-      }
-      --left;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        x[j] = in[j] ? __ldg(at[j]) : 0.0f;
-        at[j] += j < 4 ? args.sa_blk : args.sb_blk;
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < kScaleAhead; ++i) load(v[i]);
-    // (every tile has the same number of blocks; a split launch gives each CTA one share)
-    const int nkb = C::SPLIT ? walk.at(unit0).nkb : (args.gk + C::BK - 1) / C::BK;
-    const int total = unit0 < units ? ((units - unit0 + step - 1) / step) * nkb : 0;
-    bool ok = true;
-    for (int i0 = 0; ok && i0 < total; i0 += kScaleAhead) {
-#pragma unroll
-      for (int k = 0; k < kScaleAhead; ++k) {
-        const int i = i0 + k;
-        if (i >= total) break;
-        const int b = i * C::NSUB % C::NBUF;
-        const uint32_t parity = ((i * C::NSUB / C::NBUF) & 1) ^ 1;
-        bool free = mbar_wait_soon<PAIR>(tfull_bar(b), parity, args.wait_ns);
-        if (C::NSUB == 2) free = free && mbar_wait_soon<PAIR>(tfull_bar(b + 1), parity, args.wait_ns);
-        if (!__all_sync(0xffffffffu, free)) {
-          if (lane == 0) atomicOr(args.fault, kFaultProducerWait);
-          ok = false;
-          break;
-        }
-        const uint32_t dst = scbase + static_cast<uint32_t>(i % C::SCALE_SLOTS) * (C::SCALE_FLOATS * 4);
-        if (C::COL_SCALES) {
-#pragma unroll
-          for (int j = 0; j < NV; ++j) st_shared_f32(dst + (32 * j + lane) * 4, v[k][j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) st_shared_f2(dst + (32 * j + lane) * 8, v[k][j] * v[k][4], v[k][j] * v[k][5]);
-        }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(tfull_bar(b));
-          if (C::NSUB == 2) mbar_arrive(tfull_bar(b + 1));
-        }
-        load(v[k]);
-      }
-    }
-  }
-  if (C::SPLIT) {  // (the epilogue warps' exchange)
-    cluster_sync();
-    cluster_sync();
-  }
   } else {
     // -------------------------------------------------- promotion and epilogue
     if (BN == 256) regs_take<208>();
