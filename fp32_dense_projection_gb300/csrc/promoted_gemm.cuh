@@ -24,7 +24,7 @@
 //     (407-430 us, 5.5-5.8 TB/s; shared-memory bandwidth 79% busy with the operands);
 //   8-bit: the promotion.  A 128 x 256 block's MMAs take 512 cycles; reading its sums from TMEM (145
 //     cycles), adding them (256 at the FP32 pipe's rate) and the waits around them one after
-//     another 700-800, with column scales and their second multiplication 1200 (T = 16384,
+//     another about 690, with column scales and their second multiplication 1100 (T = 16384,
 //     12288 -> 4096: 591-622 us, 2.7 PFLOP/s; weight gradient T = 16173, 1024 x 4096: 80 us).  Asking
 //     for the next chunk before adding this one took 4 to 7% off; more promoting warps, reading
 //     the next chunk's first columns early and spinning waits took nothing.
@@ -189,6 +189,11 @@ struct PgTile {
   int nkb;     // contraction blocks
   int k_left;  // contraction elements
   int kb0;     // first contraction block (of this CTA's share)
+};
+
+template <int N>
+struct Int {
+  static constexpr int value = N;
 };
 
 template <int BN, int KIND, int FORM>
@@ -912,26 +917,15 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
         exchanged = true;
         break;
       }
-      // Store 32 rows x HALF columns through the warp's 2 KB block: 64-byte rows (32 BF16 or
-      // 16 FP32 columns), 16-byte chunks XOR-swizzled by row, read back so that four lanes
-      // write 64 consecutive bytes of a row.
+      // Store 32 rows x HALF columns through the warp's 2 KB block, a pass of 16 rows of 128 bytes
+      // (32 rows of 64 where HALF is 32 BF16 columns), 16-byte chunks XOR-swizzled by row, read
+      // back so that eight (four) lanes write consecutive bytes of a row.
       const int half_row = static_cast<int>(rank) * C::BM + q * 32;  // of the tile's rows
       const int rows_left = t.m_left - half_row;
       const int64_t row = (C::ROW_GROUPS ? static_cast<int64_t>(t.row0) : static_cast<int64_t>(t.tm) * C::TM) + half_row;
       const int esize = args.out_f32 ? 4 : 2;
       char* out = static_cast<char*>(args.out) +
                   ((C::K_GROUPS ? t.e * args.out_gstride : int64_t{0}) + row * args.ldo) * esize;
-      const int ch = lane & 3, r0 = lane >> 2;
-      auto flush = [&](int col0, int per_chunk) {
-        const int col = col0 + ch * per_chunk;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * i + r0;
-          const uint4 x = ld_shared_u4(ebuf + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
-          if (col < args.gn && r < rows_left)
-            *reinterpret_cast<uint4*>(out + (r * args.ldo + col) * esize) = x;
-        }
-      };
       auto lo32 = [&](int j) { return static_cast<uint32_t>(acc[j]); };
       auto hi32 = [&](int j) { return static_cast<uint32_t>(acc[j] >> 32); };
       auto bf16x2 = [&](int j) { return pack_bf16x2(__uint_as_float(lo32(j)), __uint_as_float(hi32(j))); };
@@ -955,28 +949,45 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
             if (in) *reinterpret_cast<uint2*>(p) = odd ? make_uint2(x, b) : make_uint2(a, x);
           }
         }
-      } else if (args.out_f32) {
-#pragma unroll
-        for (int c = 0; c < C::HALF; c += 16) {
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            st_shared_u4(ebuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4),
-                         make_uint4(lo32(c / 2 + 2 * j), hi32(c / 2 + 2 * j), lo32(c / 2 + 2 * j + 1), hi32(c / 2 + 2 * j + 1)));
-          __syncwarp();
-          flush(n0 + tile_col(c), 4);
-        }
       } else {
+        auto put = [&](auto chunks, int col0, int per_chunk, auto chunk) {
+          constexpr int CH = decltype(chunks)::value, ROWS = 128 / CH, SHIFT = CH == 8 ? 0 : 1;
+          const int ch = lane % CH, r0 = lane / CH, mine = lane % ROWS;
+          const int col = col0 + ch * per_chunk;
+          char* p = out + (r0 * args.ldo + col) * esize;
+          const int64_t down = 32 / CH * args.ldo * esize;
 #pragma unroll
-        for (int c = 0; c < C::HALF; c += 32) {
-          __syncwarp();
+          for (int pass = 0; pass < 32 / ROWS; ++pass) {
+            __syncwarp();
+            if (lane / ROWS == pass) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            st_shared_u4(ebuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4),
-                         make_uint4(bf16x2(c / 2 + 4 * j), bf16x2(c / 2 + 4 * j + 1), bf16x2(c / 2 + 4 * j + 2),
-                                    bf16x2(c / 2 + 4 * j + 3)));
-          __syncwarp();
-          flush(n0 + tile_col(c), 8);
+              for (int j = 0; j < CH; ++j)
+                st_shared_u4(ebuf + mine * (CH * 16) + ((j ^ ((mine >> SHIFT) & (CH - 1))) << 4), chunk(j));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i, p += down) {
+              const int r = 32 / CH * i + r0;
+              const uint4 x = ld_shared_u4(ebuf + r * (CH * 16) + ((ch ^ ((r >> SHIFT) & (CH - 1))) << 4));
+              if (col < args.gn && pass * ROWS + r < rows_left) *reinterpret_cast<uint4*>(p) = x;
+            }
+          }
+        };
+        if (args.out_f32) {
+#pragma unroll
+          for (int c = 0; c < C::HALF; c += 32)
+            put(Int<8>(), n0 + tile_col(c), 4, [&](int j) {
+              const int k = c / 2 + 2 * j;
+              return make_uint4(lo32(k), hi32(k), lo32(k + 1), hi32(k + 1));
+            });
+        } else {
+          constexpr int CH = C::HALF >= 64 ? 8 : 4;
+#pragma unroll
+          for (int c = 0; c < C::HALF; c += CH * 8)
+            put(Int<CH>(), n0 + tile_col(c), 8, [&](int j) {
+              const int k = c / 2 + 4 * j;
+              return make_uint4(bf16x2(k), bf16x2(k + 1), bf16x2(k + 2), bf16x2(k + 3));
+            });
         }
       }
     }
