@@ -40,9 +40,9 @@ def refuse_devices(name: str, tensors: dict):
             raise ValueError(f"{name}: {what} is on {t.device}, the first operand on {first}")
 
 
-def ld(t: torch.Tensor, name: str, what: str) -> int:
-    """Leading dimension of a 2-D view with unit column stride."""
-    strides, shape = t.stride(), t.shape
+def ld(t: torch.Tensor, name: str, what: str, shape=None) -> int:
+    """Leading dimension of a 2-D view (of that shape) with unit column stride."""
+    strides, shape = t.stride(), t.shape if shape is None else shape
     if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name}: {what} must be 2-D with unit column stride")
     return strides[0] if shape[0] > 1 else max(strides[0], shape[1])

@@ -89,12 +89,12 @@ def _refuse(name, a, sa, a_shape, b, sb, b_shape):
     raise AssertionError(name)
 
 
-def _product(name, a, sa, a_shape, b, sb, b_shape, out, out_shape, out_dtype, T, N, K, stream):
+def _product(name, a, a_shape, sa, sa_shape, b, b_shape, sb, sb_shape, out, out_shape, out_dtype, T, N, K, stream):
     index, fa, fb = a.get_device(), _FORMATS.get(a.dtype), _FORMATS.get(b.dtype)
     if (index < 0 or sa.get_device() != index or b.get_device() != index or sb.get_device() != index or fa is None or
-            fb is None or sa.dtype is not c.F32 or sb.dtype is not c.F32 or sa.shape != a_shape or sb.shape != b_shape):
-        _refuse(name, a, sa, a_shape, b, sb, b_shape)
-    lda, ldb = c.ld(a, name, "the first operand"), c.ld(b, name, "the second operand")
+            fb is None or sa.dtype is not c.F32 or sb.dtype is not c.F32 or sa.shape != sa_shape or sb.shape != sb_shape):
+        _refuse(name, a, sa, sa_shape, b, sb, sb_shape)
+    lda, ldb = c.ld(a, name, "the first operand", a_shape), c.ld(b, name, "the second operand", b_shape)
     (ra, ca), (rb, cb) = sa.stride(), sb.stride()
     if not _fn:
         c.load()
@@ -102,7 +102,7 @@ def _product(name, a, sa, a_shape, b, sb, b_shape, out, out_shape, out_dtype, T,
     def work(st):
         y, code = c.output(out, out_shape, out_dtype, index, a.device, name)
         code = _fn[name](a.data_ptr(), lda, fa, sa.data_ptr(), ra, ca, b.data_ptr(), ldb, fb, sb.data_ptr(), rb, cb,
-                         y.data_ptr(), c.ld(y, name, "out"), T, N, K, code, st)
+                         y.data_ptr(), c.ld(y, name, "out", out_shape), T, N, K, code, st)
         if code:
             c.check(code, name)
         return y
@@ -111,30 +111,34 @@ def _product(name, a, sa, a_shape, b, sb, b_shape, out, out_shape, out_dtype, T,
 
 
 def _shapes(name, a, b, dim_a, dim_b, what):
-    if a.dim() != 2 or b.dim() != 2 or a.shape[dim_a] != b.shape[dim_b]:
+    sa, sb = a.shape, b.shape
+    if len(sa) != 2 or len(sb) != 2 or sa[dim_a] != sb[dim_b]:
         raise ValueError(f"{name}: {what}")
-    return a.shape, b.shape
+    return sa, sb
 
 
 def dp_gemm_fwd_fp8(Xq, Xs, Wq, Ws, out=None, out_dtype=c.BF16, stream=None):
     """Y[T,N] = X W^T: Xq [T,K] with row scales Xs [T, ceil(K/128)], Wq [N,K] with Ws [ceil(N/128), ceil(K/128)]."""
     name = "dp_gemm_fwd_fp8"
-    (T, K), (N, _) = _shapes(name, Xq, Wq, 1, 1, "X[T,K] and W[N,K] must share K")
+    x, w = _shapes(name, Xq, Wq, 1, 1, "X[T,K] and W[N,K] must share K")
+    (T, K), N = x, w[0]
     kb = -(-K // 128)
-    return _product(name, Xq, Xs, (T, kb), Wq, Ws, (-(-N // 128), kb), out, (T, N), out_dtype, T, N, K, stream)
+    return _product(name, Xq, x, Xs, (T, kb), Wq, w, Ws, (-(-N // 128), kb), out, (T, N), out_dtype, T, N, K, stream)
 
 
 def dp_gemm_dgrad_fp8(dYq, dYs, Wq, Ws, out=None, out_dtype=c.BF16, stream=None):
     """dX[T,K] = dY W: dYq [T,N] with row scales dYs [T, ceil(N/128)], Wq and Ws as in the forward pass."""
     name = "dp_gemm_dgrad_fp8"
-    (T, N), (_, K) = _shapes(name, dYq, Wq, 1, 0, "dY[T,N] and W[N,K] must share N")
+    g, w = _shapes(name, dYq, Wq, 1, 0, "dY[T,N] and W[N,K] must share N")
+    (T, N), K = g, w[1]
     nb = -(-N // 128)
-    return _product(name, dYq, dYs, (T, nb), Wq, Ws, (nb, -(-K // 128)), out, (T, K), out_dtype, T, N, K, stream)
+    return _product(name, dYq, g, dYs, (T, nb), Wq, w, Ws, (nb, -(-K // 128)), out, (T, K), out_dtype, T, N, K, stream)
 
 
 def dp_gemm_wgrad_fp8(dYq, dYs, Xq, Xs, out=None, out_dtype=c.BF16, stream=None):
     """dW[N,K] = dY^T X: dYq [T,N] and Xq [T,K] with column scales dYs [ceil(T/128), N], Xs [ceil(T/128), K]."""
     name = "dp_gemm_wgrad_fp8"
-    (T, N), (_, K) = _shapes(name, dYq, Xq, 0, 0, "dY[T,N] and X[T,K] must share T")
+    g, x = _shapes(name, dYq, Xq, 0, 0, "dY[T,N] and X[T,K] must share T")
+    (T, N), K = g, x[1]
     tb = -(-T // 128)
-    return _product(name, dYq, dYs, (tb, N), Xq, Xs, (tb, K), out, (N, K), out_dtype, T, N, K, stream)
+    return _product(name, dYq, g, dYs, (tb, N), Xq, x, Xs, (tb, K), out, (N, K), out_dtype, T, N, K, stream)

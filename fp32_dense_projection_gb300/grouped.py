@@ -28,9 +28,9 @@ def _bind(L):
     _fn.update({name: getattr(L, name) for name in ("dp_gemm_fwd_grouped", "dp_gemm_dgrad_grouped", "dp_gemm_wgrad_grouped")})
 
 
-def _experts(w: torch.Tensor, name: str, what: str):
-    """(leading dimension, expert stride) of an [E, rows, columns] view."""
-    strides, shape = w.stride(), w.shape
+def _experts(w: torch.Tensor, name: str, what: str, shape):
+    """(leading dimension, expert stride) of an [E, rows, columns] view of that shape."""
+    strides = w.stride()
     if len(shape) != 3 or (strides[2] != 1 and shape[2] > 1):
         raise ValueError(f"{name}: {what} must be [E, rows, columns] with unit column stride")
     ld = strides[1] if shape[1] > 1 else max(shape[2], 1)
@@ -61,24 +61,26 @@ def _check(name, a, b, b_name, offsets, E):
 
 def _rows_by_experts(name, forward, a, W, offsets, out, out_dtype, weight_layout, stream):
     kn = _layout(weight_layout)
-    if a.dim() != 2 or W.dim() != 3:
+    rows, weights = a.shape, W.shape
+    if len(rows) != 2 or len(weights) != 3:
         raise ValueError(f"{name}: rows must be 2-D and weights 3-D")
-    T, width = a.shape
-    E, N, K = W.shape
+    T, width = rows
+    E, N, K = weights
     if kn:
         N, K = K, N
     if width != (K if forward else N):
         raise ValueError(f"{name}: the rows' length does not match the weights")
     index, bits = _check(name, a, W, "weights", offsets, E)
-    ldw, bsw = _experts(W, name, "weights")
-    lda = c.ld(a, name, "rows")
+    ldw, bsw = _experts(W, name, "weights", weights)
+    lda = c.ld(a, name, "rows", rows)
     if not _fn:
         c.load()
 
     def work(st):
-        y, code = c.output(out, (T, N if forward else K), out_dtype, index, a.device, name)
+        shape = (T, N if forward else K)
+        y, code = c.output(out, shape, out_dtype, index, a.device, name)
         code = _fn[name](a.data_ptr(), lda, W.data_ptr(), ldw, bsw, kn, offsets.data_ptr(), bits, y.data_ptr(),
-                         c.ld(y, name, "out"), E, T, N, K, code, st)
+                         c.ld(y, name, "out", shape), E, T, N, K, code, st)
         if code:
             c.check(code, name)
         return y
@@ -110,8 +112,9 @@ def dp_gemm_wgrad_grouped(dY, X, offsets, out=None, out_dtype=c.BF16, weight_lay
         c.load()
 
     def work(st):
-        dW, code = c.output(out, (E, K, N) if kn else (E, N, K), out_dtype, index, dY.device, name)
-        ldw, bsw = _experts(dW, name, "out")
+        shape = (E, K, N) if kn else (E, N, K)
+        dW, code = c.output(out, shape, out_dtype, index, dY.device, name)
+        ldw, bsw = _experts(dW, name, "out", shape)
         code = _fn[name](dY.data_ptr(), ldg, X.data_ptr(), ldx, offsets.data_ptr(), bits, dW.data_ptr(), ldw, bsw, kn, E, T,
                          N, K, code, st)
         if code:
