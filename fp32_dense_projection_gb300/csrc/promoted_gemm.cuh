@@ -899,8 +899,17 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
       const PgTile t = walk.at(us);
       const int n0 = t.tn * BN;
       if (C::SPLIT) {
-        // This rank's partial tile, [pair of columns][row], into the operand ring (whose loads and
-        // MMAs are done).
+        // This rank's partial tile, [pair of columns][row], into the operand ring.  Its loads and MMAs
+        // have to be done: where a block takes two MMAs, the warps of the first half have waited for
+        // the first one's commit only, so they wait for the last block's second one here.
+        if (C::NSUB == 2 && h == 0) {
+          const uint32_t last = it - 1;
+          if (!__all_sync(0xffffffffu, mbar_wait_soon<PAIR>(tfull_bar(2 * (last & 1u) + 1), (last * C::NSUB / C::NBUF) & 1u,
+                                                            args.wait_ns))) {
+            if (lane == 0) atomicOr(args.fault, kFaultEpilogueWait);
+            break;
+          }
+        }
         if (C::COL_SCALES) {
           const uint32_t at = base + static_cast<uint32_t>((h * (C::HALF / 2) + (lane & 3)) * C::BM + q * 32 + lane / 4) * 8;
 #pragma unroll
