@@ -22,6 +22,9 @@ struct DeviceContext {
 // The current device's context; initialises the device on its first call.
 dp_status device_context(DeviceContext* ctx);
 
+// A tuning override's value: `unset` if the variable is absent or the process has no DP_TUNING.
+int tuning_override(const char* name, int unset);
+
 bool is_aligned16(const void* p);
 
 // A row-major rows x cols operand with leading dimension *ld (0 = cols).

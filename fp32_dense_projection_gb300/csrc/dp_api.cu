@@ -819,6 +819,8 @@ dp_status device_context(DeviceContext* ctx) {
   return DP_OK;
 }
 
+int tuning_override(const char* name, int unset) { return env_int(name, unset); }
+
 bool is_aligned16(const void* p) { return aligned16(p); }
 
 dp_status check_operand(const void* p, int64_t rows, int64_t cols, int64_t* ld, int esize) {

@@ -50,7 +50,7 @@ dp_status zero_rows(void* out, int64_t rows, int64_t cols, int64_t ld, int esize
 // ------------------------------------------------ how an 8-bit product is launched
 
 struct Fp8Plan {
-  int bn, form, split;
+  int bn, form, split;  // bn 0: no form meets the overrides
 };
 
 // Clusters that run at one time, asked once per kernel, size and device.
@@ -72,7 +72,8 @@ int cluster_capacity(int dev, int kind, int bn, int split) {
 // which load least, do not (16384 x 12288 -> 4096: 795 / 559 / 537 us; 4031 x 4096 -> 4096: 62.0 /
 // 57.5 / 57.8).  With column scales, whose promotion takes twice the operations and reads every
 // column's scale, it is 350 / 595 / 585 for both.  A split adds its exchange: barriers of the
-// cluster, and the tile's rows through its shared memory.
+// cluster, and the tile's rows through its shared memory.  DP_FORCE_BN, DP_FORCE_PAIR and
+// DP_FORCE_SPLITS leave only the forms that they name (a split then need not run in one wave).
 Fp8Plan plan_fp8(int kind, int64_t gm, int64_t gn, int64_t nkb, const DeviceContext& ctx) {
   struct Rates {
     double one_wave, more;
@@ -81,9 +82,14 @@ Fp8Plan plan_fp8(int kind, int64_t gm, int64_t gn, int64_t nkb, const DeviceCont
   const int sm_count = ctx.sm_count;
   const Rates r128 = cols ? Rates{350, 350} : Rates{215, 255}, r256 = cols ? Rates{595, 595} : Rates{405, 410},
               r_pair = cols ? Rates{585, 585} : Rates{440, 400};
-  Fp8Plan best = {128, kPlain, 1};
+  const int want_bn = tuning_override("DP_FORCE_BN", 0), want_pair = tuning_override("DP_FORCE_PAIR", -1),
+            want_split = tuning_override("DP_FORCE_SPLITS", 0);
+  Fp8Plan best = {0, kPlain, 1};
   double least = 1e30;
   auto offer = [&](int bn, int form, int split, int64_t tiles, int64_t slots, const Rates& r) {
+    if ((want_bn > 0 && bn != want_bn) || (want_pair >= 0 && (form == kPair) != (want_pair != 0)) ||
+        (want_split > 0 && split != want_split))
+      return;
     const int64_t waves = cdiv(tiles, slots);
     double t = static_cast<double>(waves * cdiv(nkb, split)) * (waves == 1 ? r.one_wave : r.more);
     if (form == kSplit) t += 2300.0 + 200.0 * split + 12.0 * static_cast<double>(std::min<int64_t>(gm, 128)) * bn / 256;
@@ -94,8 +100,11 @@ Fp8Plan plan_fp8(int kind, int64_t gm, int64_t gn, int64_t nkb, const DeviceCont
     const int64_t tiles = cdiv(gm, 128) * cdiv(gn, bn);
     const Rates& r = bn == 256 ? r256 : r128;
     offer(bn, kPlain, 1, tiles, sm_count, r);
-    for (int split = 2; split <= 8 && split <= nkb && tiles * split <= sm_count; ++split)
-      if (tiles <= cluster_capacity(ctx.device, kind, bn, split)) offer(bn, kSplit, split, tiles, tiles, r);
+    for (int split = 2; split <= 8 && split <= nkb; ++split) {
+      if (want_split == 0 && tiles * split > sm_count) break;
+      const int64_t room = cluster_capacity(ctx.device, kind, bn, split);
+      if (want_split > 0 ? room > 0 : tiles <= room) offer(bn, kSplit, split, tiles, std::max<int64_t>(1, std::min(tiles, room)), r);
+    }
   }
   return best;
 }
@@ -240,6 +249,7 @@ dp_status run_fp8(GroupedOp op, const void* a, int64_t lda, int a_fmt, Scales sa
   PgArgs& g = l.args;
   const int kind = op == kFwd ? kFp8KK : op == kDgrad ? kFp8KM : kFp8MM;
   const Fp8Plan plan = plan_fp8(kind, gm, gn, cdiv(gk, 128), ctx);
+  if (plan.bn == 0) return DP_ERR_UNSUPPORTED;
   const int bn = plan.bn, tm = plan.form == kPair ? 256 : 128;
   g.rows = static_cast<int32_t>(gm);
   g.gm = static_cast<int32_t>(gm);
@@ -272,7 +282,7 @@ dp_status run_fp8(GroupedOp op, const void* a, int64_t lda, int a_fmt, Scales sa
                       : encode_operand(&l.tmB, b, u8, 1, gk, gn, ldb, 0, 0, 128, 128));
   if (!ok) return DP_ERR_LAUNCH;
   const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
-  if (tiles > kMaxInt) return DP_ERR_UNSUPPORTED;
+  if (tiles * plan.split > kMaxInt) return DP_ERR_UNSUPPORTED;
   l.grid = static_cast<int>(plan.form == kPair    ? 2 * std::min<int64_t>(ctx.sm_count / 2, tiles)
                             : plan.form == kSplit ? tiles * plan.split
                                                   : std::min<int64_t>(ctx.sm_count, tiles));

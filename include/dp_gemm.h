@@ -408,6 +408,9 @@ dp_status dp_adamw_step(const dp_adamw_tensor* tensors, int64_t count, int state
  * blocks per ring stage; BF16x3 plans keep 1), DP_FORCE_FFMA (0 / 1: the router's
  * BF16x3 or SIMT program), DP_FORCE_GROUP (raster group width in tiles) and
  * DP_FORCE_RASTER_M (1: groups of row tiles, 0: of column tiles).
+ * The 8-bit products read DP_FORCE_BN (128 / 256), DP_FORCE_PAIR and DP_FORCE_SPLITS (1: no
+ * split; 2 to 8: clusters of that many CTAs share a tile's contraction); a call that
+ * has no such form is refused with DP_ERR_UNSUPPORTED.
  * A forced plan is still deterministic and keeps the accumulation-length bound. */
 
 /* The plan the library uses for one call.  The planner is a pure function of

@@ -27,3 +27,48 @@ def exact(op, T, N, K, repeats=1):
                                       ("wgrad", 4500, 1024, 1536), ("wgrad", 5000, 2048, 768), ("wgrad", 4700, 1024, 1536)])
 def test_wide_tiles_split_over_clusters(op, T, N, K):
     exact(op, T, N, K, repeats=20)
+
+
+FORMS = {"128": dict(BN=128, PAIR=0, SPLITS=1), "256": dict(BN=256, PAIR=0, SPLITS=1), "pair": dict(BN=256, PAIR=1, SPLITS=1)}
+
+
+def force(monkeypatch, **form):
+    for k, v in form.items():
+        monkeypatch.setenv(f"DP_FORCE_{k}", str(v))
+
+
+def sizes(op, gm, gn, gk):
+    """(T, N, K) of a product of gm x gn outputs over gk contraction elements."""
+    return {"fwd": (gm, gn, gk), "dgrad": (gm, gk, gn), "wgrad": (gk, gm, gn)}[op]
+
+
+@pytest.mark.parametrize("form", sorted(FORMS))
+@pytest.mark.parametrize("op", ["fwd", "dgrad", "wgrad"])
+def test_every_tile(monkeypatch, op, form):
+    """One to nine blocks (the rings wrap), a partial last one, ragged tiles; then several tiles for each SM."""
+    force(monkeypatch, **FORMS[form])
+    for blocks in range(1, 10):
+        exact(op, *sizes(op, 208, 528, 128 * blocks - (16 if blocks % 2 else 0)))
+    exact(op, *sizes(op, 16, 144, 400))
+    exact(op, *sizes(op, 2608, 4112, 656))
+
+
+@pytest.mark.parametrize("split", range(2, 9))
+@pytest.mark.parametrize("bn", [128, 256])
+@pytest.mark.parametrize("op", ["fwd", "dgrad", "wgrad"])
+def test_every_split(monkeypatch, op, bn, split):
+    """Shares of one to six blocks (each residue of the ring's four stages), even and uneven ones."""
+    force(monkeypatch, BN=bn, PAIR=0, SPLITS=split)
+    for share in range(1, 7):
+        exact(op, *sizes(op, 208, 528, 128 * share * split - 48), repeats=3)
+        exact(op, *sizes(op, 80, 272, 128 * (share * split + 1)))
+    exact(op, *sizes(op, 1, 256, 128 * 3 * split) if op != "wgrad" else sizes(op, 16, 256, 128 * 3 * split))
+
+
+@pytest.mark.parametrize("form", [dict(BN=128, PAIR=1), dict(BN=64), dict(SPLITS=9), dict(PAIR=1, SPLITS=2), dict(BN=128, SPLITS=4)])
+def test_forms_that_do_not_exist_are_refused(monkeypatch, form):
+    (a, _), (b, _) = operands("fwd", 64, 256, 384, 1, ints=True)  # (three blocks: no split in four)
+    force(monkeypatch, **form)
+    with pytest.raises(dp.DPError) as e:
+        call("fwd", a, b)
+    assert e.value.status == 3
