@@ -41,11 +41,16 @@ def refuse_devices(name: str, tensors: dict):
 
 
 def ld(t: torch.Tensor, name: str, what: str, shape=None) -> int:
-    """Leading dimension of a 2-D view (of that shape) with unit column stride."""
+    """Leading dimension of a 2-D view (of that shape) with unit column stride.  Rows that share
+    their memory (an expanded row) are refused: to the library a stride of 0 means packed rows."""
     strides, shape = t.stride(), t.shape if shape is None else shape
     if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name}: {what} must be 2-D with unit column stride")
-    return strides[0] if shape[0] > 1 else max(strides[0], shape[1])
+    if shape[0] <= 1:
+        return max(strides[0], shape[1])
+    if strides[0] == 0:
+        raise ValueError(f"{name}: {what} must not be expanded over its rows (stride 0)")
+    return strides[0]
 
 
 def output(out, shape, dtype, index: int, device, name: str):

@@ -33,6 +33,8 @@ def _experts(w: torch.Tensor, name: str, what: str, shape):
     strides = w.stride()
     if len(shape) != 3 or (strides[2] != 1 and shape[2] > 1):
         raise ValueError(f"{name}: {what} must be [E, rows, columns] with unit column stride")
+    if (strides[1] == 0 and shape[1] > 1) or (strides[0] == 0 and shape[0] > 1):  # (0 means packed to the library)
+        raise ValueError(f"{name}: {what} must not be expanded over experts or rows (stride 0)")
     ld = strides[1] if shape[1] > 1 else max(shape[2], 1)
     return ld, strides[0] if shape[0] > 1 else shape[1] * ld
 
