@@ -242,6 +242,8 @@ def _ld(t: torch.Tensor) -> int:
         raise ValueError("operands must be 2-D with unit column stride")
     if t.size(0) <= 1:
         return max(t.stride(0), t.size(1))
+    if t.stride(0) == 0:  # (to the library a stride of 0 means packed rows)
+        raise ValueError("operands must not be expanded over their rows (stride 0)")
     return t.stride(0)
 
 
@@ -400,6 +402,8 @@ def _bview(t: torch.Tensor, name: str):
     """(leading dimension, batch stride) of a [B, rows, cols] view with unit column stride."""
     if t.dim() != 3 or (t.size(2) > 1 and t.stride(2) != 1):
         raise ValueError(f"{name}: operands must be [B, rows, cols] views with unit column stride")
+    if (t.size(1) > 1 and t.stride(1) == 0) or (t.size(0) > 1 and t.stride(0) == 0):  # (0 means packed to the library)
+        raise ValueError(f"{name}: operands must not be expanded over batch or rows (stride 0)")
     ld = t.stride(1) if t.size(1) > 1 else t.size(2)
     bs = t.stride(0) if t.size(0) > 1 else t.size(1) * ld
     return ld, bs

@@ -25,6 +25,31 @@ def test_marshalling_refuses_stride_0():
     assert grouped._experts(bf16(64, 8, 32).transpose(0, 1), "f", "w", (8, 64, 32)) == (8 * 32, 32)
 
 
+def test_dense_marshalling_refuses_stride_0():
+    with pytest.raises(ValueError, match="stride 0"):
+        dp._ld(bf16(1, 64).expand(128, 64))
+    for t in (bf16(64, 32).expand(8, 64, 32), bf16(8, 1, 32).expand(8, 64, 32)):
+        with pytest.raises(ValueError, match="stride 0"):
+            dp._bview(t, "f")
+    assert dp._ld(bf16(1, 64).expand(1, 64)) == 64 and dp._ld(bf16(5, 96)[:, :64]) == 96
+    assert dp._bview(bf16(64, 8, 32).transpose(0, 1), "f") == (8 * 32, 32) and dp._bview(bf16(1, 4, 32), "f") == (32, 128)
+
+
+@pytest.mark.gpu
+def test_dense_entry_points_refuse_stride_0():
+    x, row = bf16(128, 64, device="cuda"), bf16(1, 64, device="cuda").expand(128, 64)
+    b, one = bf16(4, 64, 64, device="cuda"), bf16(64, 64, device="cuda").expand(4, 64, 64)
+    f, frow = x.float(), row.float()[:1].expand(128, 64)
+    calls = [lambda: dp.dp_gemm_fwd(row, x), lambda: dp.dp_gemm_fwd(x, row), lambda: dp.dp_gemm_dgrad(row, x[:64]),
+             lambda: dp.dp_gemm_fwd(x, x[:64], out=row), lambda: dp.dp_gemm_wgrad(x, row), lambda: dp.dp_gemm_bwd(row, x, x[:64]),
+             lambda: dp.dp_gemm_wgrad_noalloc(row, x, x[:64]), lambda: dp.router_fwd(frow, f), lambda: dp.router_wgrad(f, frow),
+             lambda: dp.dp_gemm_fwd_batched(b, one), lambda: dp.dp_gemm_dgrad_batched(one, b),
+             lambda: dp.dp_gemm_wgrad_batched(b, b, out=one)]
+    for call in calls:
+        with pytest.raises(ValueError, match="stride 0"):
+            call()
+
+
 @pytest.mark.gpu
 def test_entry_points_refuse_stride_0():
     x, row = bf16(128, 64, device="cuda"), bf16(1, 64, device="cuda").expand(128, 64)
