@@ -54,7 +54,10 @@ class AdamW:
 
     state_bits=32 keeps both moments in fp32.  state_bits=8 keeps them as float8_e4m3fn
     codes with an fp32 scale per 128 consecutive elements: ``exp_avg`` holds m / scale,
-    ``exp_avg_sq`` holds sqrt(v) / scale.  The moments are attributes (tuples of tensors) and
+    ``exp_avg_sq`` holds sqrt(v) / scale.  Codes of moments with a long memory (sqrt(v) above
+    beta2 = 0.95, m above beta1 = 0.98) are rounded stochastically, by a hash of element and step (a
+    run repeats bit for bit): rounded to nearest they would not follow their small changes.
+    The moments are attributes (tuples of tensors) and
     may be passed in, with ``step`` the updates already done, to resume a run.  The updates
     are made in place, outside autograd.  The lists of tensors are fixed at construction; the
     tensors may get new memory between steps (``.data``), of their shape.

@@ -16,8 +16,22 @@
 // codes of m / s with s = max|m| / 448.  sqrt(v), not v, is held the same way: the root
 // halves the exponents' range, so E4M3's 2^17.8 covers v over 2^35; a v above zero never
 // becomes zero (the smallest code is kept), since a lost v would blow up m / sqrt(v).
-// A code's rounding is up to 1/16 of the value; a second moment that moves by less than
-// half a code relative to its block's maximum keeps its code.
+// A code's rounding is up to 1/16 of the value.  Rounding to nearest therefore drops every change
+// of less than half a code against the block's maximum, and a step at rate 1 - beta changes m by
+// that share of itself and sqrt(v) by half of it.  Where the rate is small the codes are rounded
+// stochastically instead: up with the probability of the distance from the code below, so that
+// the expected state follows the recurrence.  The 16 random bits an element are a hash of its index
+// in the tensor and of the step (the splitmix64 sequence of Steele, Lea and Flood), so that a
+// run repeats bit for bit, also after a resume.  Mean and standard deviation of sqrt(v) over its 32-bit
+// value, normal gradients, stationary and six time constants after a tenfold fall of half of them
+// (restated in numpy):
+//     beta2        0.9           0.95          0.98          0.99          0.999
+//     nearest      1.01 +- 0.07  1.06 +- 0.09  1.43 +- 0.25  1.31 +- 0.18  1.09 +- 0.22
+//                  1.02 +- 0.08  1.34 +- 0.42  6.2 +- 5.1    6.1 +- 4.9    4.6 +- 3.9
+//     stochastic   1.00 +- 0.09  1.00 +- 0.12  1.01 +- 0.15  1.01 +- 0.16  1.01 +- 0.16
+//                  1.01 +- 0.11  1.01 +- 0.14  1.02 +- 0.17  1.02 +- 0.18  1.02 +- 0.19
+// so it is used above beta2 = 0.95; below, nearest codes carry less noise.  Nearest codes of m
+// keep its mean within 3% up to beta1 = 0.98 (0.9: 0.6%; 0.99: 5%; 0.999: off by its own size).
 //
 // Bound: HBM bytes (14 to 34 per element).  A CTA takes one chunk of 2048 elements, a
 // thread 8 consecutive ones: every load of the chunk is in flight before the first use,
@@ -26,7 +40,8 @@
 // (153M elements, BF16 gradients and copies: 700 against 611 us with 32-bit, 495 against 415 us
 // with 8-bit moments).  With 8-bit moments a warp computes half its time, too long for its
 // loads alone to keep HBM busy, so each CTA also asks L2 for the chunk two per SM further:
-// 427 -> 372 us or 6.6 TB/s (one per SM 422, three 375, four 379, six 382).  32-bit moments, at 609
+// 427 -> 372 us or 6.6 TB/s (one per SM 422, three 375, four 379, six 382; with stochastic codes
+// of sqrt(v) 432, of m too 502: bound by instructions).  32-bit moments, at 609
 // us or 7.0 TB/s without, lose by it (643 at six per SM).  The tensors' table travels as a kernel
 // parameter: no copy to the device, no state between calls.
 #include <cuda_runtime.h>
@@ -34,6 +49,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "api_internal.h"
 #include "ptx.cuh"
@@ -44,6 +60,9 @@ namespace {
 constexpr int kBlockElems = 128;   // 8-bit moments: elements per scale
 constexpr int kChunkElems = 2048;  // elements per CTA step (256 threads x 8)
 constexpr float kTop = 448.0f, kTinyMax = 1e-30f, kSmallest = 0.001953125f;  // E4M3: largest, smallest > 0
+constexpr float kNormal = 0.015625f;                                            // E4M3: smallest normal
+constexpr double kNearestBeta1 = 0.98, kNearestBeta2 = 0.95;  // 8 bits: stochastic codes above
+constexpr uint64_t kGamma = 0x9E3779B97F4A7C15ull;            // step of the splitmix64 sequence
 
 struct Entry {
   void* p;
@@ -66,6 +85,8 @@ struct Table {
   float beta1, one_beta1, beta2, one_beta2, eps, keep, root_scale, lr;
   float grad_scale;
   const float* grad_scale_ptr;
+  uint64_t seed;             // of this step's random bits
+  int32_t dither_m, dither_v;  // 8-bit moments: stochastic codes of m, of v's root
 };
 
 __device__ __forceinline__ float bf16_at(uint32_t w, int half) {
@@ -187,6 +208,30 @@ __device__ __forceinline__ uint32_t encode4(const float* x) {
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
+// The output function of splitmix64.
+__host__ __device__ __forceinline__ uint64_t mix64(uint64_t z) {
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  return z ^ (z >> 31);
+}
+
+// |x| up to 448 rounded to E4M3's values by 16 random bits: the 20 bits below the third of the mantissa get
+// a uniform addend and are cut.  Values below the normal range have the spacing of the first
+// normal binade and are rounded there.
+__device__ __forceinline__ float stochastic(float x, uint32_t bits) {
+  const float shift = fabsf(x) < kNormal ? kNormal : 0.0f;
+  const uint32_t a = __float_as_uint(__fadd_rn(fabsf(x), shift));
+  return copysignf(__uint_as_float((a + (bits << 4) + 8u) & 0xFFF00000u) - shift, x);
+}
+__device__ __forceinline__ void stochastic8(float (&x)[8], uint64_t counter) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint64_t r = mix64(counter + h * kGamma);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[4 * h + j] = stochastic(x[4 * h + j], static_cast<uint32_t>(r >> (16 * j)) & 0xFFFFu);
+  }
+}
+
 // max(|a|, |b|, |c|); a NaN wins.
 __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   float d;
@@ -223,7 +268,7 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-template <int MAX, bool EIGHT>
+template <int MAX, bool EIGHT, bool DITHER>
 __global__ void __launch_bounds__(256, EIGHT ? 6 : 5) adamw_kernel(const __grid_constant__ Table<MAX> t) {
   const float gs = t.grad_scale_ptr ? t.grad_scale * __ldg(t.grad_scale_ptr) : t.grad_scale;
   const int64_t chunks = t.chunk0[t.count];
@@ -300,6 +345,11 @@ __global__ void __launch_bounds__(256, EIGHT ? 6 : 5) adamw_kernel(const __grid_
         root[j] = fmaxf(vv.lo(), fminf(floor.lo(), kSmallest));
         root[j + 1] = fmaxf(vv.hi(), fminf(floor.hi(), kSmallest));
       }
+      if (DITHER) {  // (a floor is a value of the grid's, which stays)
+        const uint64_t counter = t.seed + static_cast<uint64_t>(at >> 3) * (4 * kGamma);
+        if (t.dither_v) stochastic8(root, counter);
+        if (t.dither_m) stochastic8(m, counter + 2 * kGamma);
+      }
       store_codes(e.m, at, fast, n, make_uint2(encode4(m), encode4(m + 4)));
       store_codes(e.v, at, fast, n, make_uint2(encode4(root), encode4(root + 4)));
       if ((threadIdx.x & 15) == 0 && n > 0) {
@@ -313,7 +363,7 @@ __global__ void __launch_bounds__(256, EIGHT ? 6 : 5) adamw_kernel(const __grid_
   }
 }
 
-template <int MAX, bool EIGHT>
+template <int MAX, bool EIGHT, bool DITHER = false>
 cudaError_t launch_adamw(const dp_adamw_tensor* t, int64_t count, const dp_adamw_hyper& h, int sm_count,
                          cudaStream_t stream) {
   static_assert(sizeof(Table<MAX>) <= 32764, "kernel parameters");
@@ -352,8 +402,11 @@ cudaError_t launch_adamw(const dp_adamw_tensor* t, int64_t count, const dp_adamw
     tab.lr = static_cast<float>(h.lr / (1.0 - std::pow(h.beta1, static_cast<double>(h.step))));
     tab.grad_scale = static_cast<float>(h.grad_scale);
     tab.grad_scale_ptr = h.grad_scale_ptr;
+    tab.seed = mix64(static_cast<uint64_t>(h.step) * kGamma);
+    tab.dither_m = h.beta1 > kNearestBeta1;
+    tab.dither_v = h.beta2 > kNearestBeta2;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(chunks, 0x7FFFFFFF));
-    adamw_kernel<MAX, EIGHT><<<grid, 256, 0, stream>>>(tab);
+    adamw_kernel<MAX, EIGHT, DITHER><<<grid, 256, 0, stream>>>(tab);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }
@@ -392,12 +445,16 @@ extern "C" dp_status dp_adamw_step(const dp_adamw_tensor* tensors, int64_t count
   if (st != DP_OK) return st;
   cudaStream_t str = static_cast<cudaStream_t>(stream);
   // (a small table for few tensors: its launch carries 2 KB of parameters instead of 20)
+  auto launch = [&](auto eight, auto dither) {
+    return count <= 24 ? launch_adamw<24, decltype(eight)::value, decltype(dither)::value>(tensors, count, h, ctx.sm_count, str)
+                       : launch_adamw<256, decltype(eight)::value, decltype(dither)::value>(tensors, count, h, ctx.sm_count, str);
+  };
   cudaError_t e;
-  if (count <= 24)
-    e = state_bits == 8 ? launch_adamw<24, true>(tensors, count, h, ctx.sm_count, str)
-                        : launch_adamw<24, false>(tensors, count, h, ctx.sm_count, str);
+  if (state_bits == 32)
+    e = launch(std::false_type(), std::false_type());
+  else if (h.beta1 > kNearestBeta1 || h.beta2 > kNearestBeta2)
+    e = launch(std::true_type(), std::true_type());
   else
-    e = state_bits == 8 ? launch_adamw<256, true>(tensors, count, h, ctx.sm_count, str)
-                        : launch_adamw<256, false>(tensors, count, h, ctx.sm_count, str);
+    e = launch(std::true_type(), std::false_type());
   return e == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
 }

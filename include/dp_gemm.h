@@ -378,8 +378,12 @@ typedef struct dp_adamw_hyper {
  * in FP32: the moments' operations rounded one by one, the parameter's quotient to two units
  * in the last place; p is rounded once to its type.
  * state_bits = 8: m is held as E4M3 codes with a scale max|m| / 448 for each 128 consecutive
- * elements, and sqrt(v) likewise; a v above zero is never held as zero.  A non-finite
- * gradient makes its element (32 bits) or its 128 elements' state (8 bits) non-finite.
+ * elements, and sqrt(v) likewise; a v above zero is never held as zero.  Codes are rounded to
+ * nearest up to beta1 = 0.98 (m) and beta2 = 0.95 (sqrt(v)); above, where a step moves the moment by
+ * less than a nearest code would show, stochastically, by a hash of the element's index in its
+ * tensor and `step`: the same call gives the same bits.  sqrt(v) then follows its 32-bit value
+ * with a standard deviation of 12 to 20%.  A non-finite gradient makes its element (32 bits)
+ * or its 128 elements' state (8 bits) non-finite.
  * 16-byte aligned tensors are faster; any element alignment works.  One launch per 256
  * tensors, no workspace. */
 dp_status dp_adamw_step(const dp_adamw_tensor* tensors, int64_t count, int state_bits, const dp_adamw_hyper* hyper,
