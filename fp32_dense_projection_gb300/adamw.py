@@ -100,14 +100,17 @@ class AdamW:
         _need(t.dtype in dtypes, f"{what} must be {' or '.join(map(str, dtypes))}", TypeError)
         _need(t.shape == shape and t.is_contiguous(), f"{what} must be contiguous with shape {tuple(shape)}")
 
-    def _where(self):
-        """Where the parameters, copies and moments are: a step enters them again when one has
-        moved (a module's .data may have been replaced)."""
-        return list(map(_data_ptr, self._held))
+    def _changed(self):
+        """Whether a parameter, copy or moment is not what was entered: its .data may have been
+        replaced, also by another view or type at the same address."""
+        held = self._held
+        return (list(map(_data_ptr, held)) != self._pointers or list(map(_dtype, held)) != self._dtypes or
+                list(map(_shape, held)) != self._held_shapes or False in map(_is_contiguous, held))
 
     def _enter(self):
-        """Check the tensors and enter them in the table."""
+        """Check the tensors and then enter them in the table (all of them or, if one is refused, none)."""
         kind = torch.float8_e4m3fn if self.state_bits == 8 else _F32
+        columns = {}
         for what, tensors in (("param", self.params), ("copy", self.copies), ("exp_avg", self.exp_avg),
                               ("exp_avg_sq", self.exp_avg_sq), ("exp_avg_scale", self.exp_avg_scale),
                               ("exp_avg_sq_scale", self.exp_avg_sq_scale)):
@@ -119,10 +122,13 @@ class AdamW:
             for i, (x, shape) in enumerate(zip(tensors, self._shapes)):
                 if x is not None or what != "copy":
                     self._alike(f"{name}[{i}]", x, _scale_shape(shape) if "scale" in what else shape, dtypes)
-            self._table[what] = [0 if x is None else x.data_ptr() for x in tensors]
+            columns[what] = [0 if x is None else x.data_ptr() for x in tensors]
+        for what, column in columns.items():
+            self._table[what] = column
         self._table["numel"] = [p.numel() for p in self.params]
         self._table["param_bf16"] = [p.dtype is _BF16 for p in self.params]
-        self._pointers = self._where()
+        self._pointers, self._dtypes = list(map(_data_ptr, self._held)), list(map(_dtype, self._held))
+        self._held_shapes = list(map(_shape, self._held))
         self._grad_dtypes = None
 
     def _state(self, given, dtype, scales):
@@ -140,7 +146,7 @@ class AdamW:
         if not grads:
             self.step_count += 1
             return
-        if self._where() != self._pointers:
+        if self._changed():
             self._enter()
         index = self.device.index
         some = [g for g in grads if g is not None]

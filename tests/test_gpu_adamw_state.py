@@ -1,0 +1,79 @@
+"""AdamW's tensors between steps: what a replaced .data may be."""
+import pytest
+import torch
+
+import fp32_dense_projection_gb300 as dp
+from gpu_common import DEV
+
+pytestmark = pytest.mark.gpu
+
+
+def make(n=64, **kw):
+    p = torch.randn(n, n, device=DEV)
+    opt = dp.AdamW([p], copies=[torch.empty_like(p, dtype=torch.bfloat16)], **kw)
+    return p, opt, [torch.randn(n, n, device=DEV)]
+
+
+def bits(x):
+    return x.contiguous().view(torch.uint8)
+
+
+def refused(opt, g, match):
+    before = [x.clone() for x in opt.params + opt.exp_avg]
+    with pytest.raises((ValueError, TypeError), match=match):
+        opt.step(g)
+    assert all(torch.equal(bits(x), bits(y)) for x, y in zip(before, opt.params + opt.exp_avg))
+
+
+def test_another_view_at_the_same_address_is_refused():
+    p, opt, g = make()
+    opt.step(g)
+    good = p.data
+    for bad in (good.t(), good[:32], good.view(-1)[:64 * 32].view(32, 64), good.view(-1)):
+        assert bad.data_ptr() == good.data_ptr()
+        p.data = bad
+        refused(opt, g, "params")
+    p.data = good
+    for x in (opt.copies[0], opt.exp_avg[0], opt.exp_avg_sq[0]):
+        good = x.data
+        x.data = good.t()
+        refused(opt, g, "contiguous")
+        x.data = good
+    opt.step(g)
+
+
+def test_another_type_at_the_same_address_is_entered_or_refused():
+    """BF16 in the first half of the FP32 parameter's memory: the second half stays as it was."""
+    p, opt, g = make()
+    opt.step(g)
+    whole = p.data
+    half = whole.view(torch.bfloat16).view(-1)[:64 * 64].view(64, 64)
+    assert half.data_ptr() == whole.data_ptr()
+    rest = whole.view(-1)[64 * 32:].clone()
+    p.data = half
+    opt.step(g)
+    assert torch.equal(whole.view(-1)[64 * 32:], rest) and p.dtype == torch.bfloat16
+    assert torch.equal(bits(opt.copies[0]), bits(p))  # (bits: FP32 halves read as BF16 hold NaN)
+    m = opt.exp_avg[0].data
+    opt.exp_avg[0].data = m.view(torch.int32)
+    refused(opt, g, "exp_avg")
+    opt.exp_avg[0].data = m
+
+
+def test_a_refused_step_enters_nothing():
+    """The parameter moves and the moment becomes unfit: refused.  With the moment fit and the parameter back in its old
+    place, the step writes there and not to the place seen by the refused one."""
+    p, opt, g = make()
+    ref, twin, _ = make()
+    ref.copy_(p)
+    opt.step(g)
+    twin.step(g)
+    old, moved, m = p.data, p.data.clone(), opt.exp_avg_sq[0].data
+    p.data, opt.exp_avg_sq[0].data = moved, m[:32].clone()
+    seen = moved.clone()
+    with pytest.raises(ValueError, match="exp_avg_sq"):
+        opt.step(g)
+    p.data, opt.exp_avg_sq[0].data = old, m
+    opt.step(g)
+    twin.step(g)
+    assert torch.equal(moved, seen) and torch.equal(p, ref) and opt.step_count == 2
