@@ -35,6 +35,7 @@ def _bind(L):
     _fn["step"] = L.dp_adamw_step
 
 
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 _data_ptr, _is_contiguous, _get_device = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
 _shape, _dtype = attrgetter("shape"), attrgetter("dtype")
 _F32, _BF16 = torch.float32, torch.bfloat16
@@ -60,7 +61,8 @@ class AdamW:
     The moments are attributes (tuples of tensors) and
     may be passed in, with ``step`` the updates already done, to resume a run.  The updates
     are made in place, outside autograd.  The lists of tensors are fixed at construction; the
-    tensors may get new memory between steps (``.data``), of their shape.
+    tensors may get new memory between steps (``.data``), of their shape.  A step cannot be
+    captured into a CUDA graph: its count and rate are arguments of the launch.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32, copies=None,
@@ -177,8 +179,12 @@ class AdamW:
                                           *((grad_scale,) if isinstance(grad_scale, torch.Tensor) else ()))
         if not _fn:
             c.load()
-        code = c.on_stream(index, stream, used,
-                           lambda st: _fn["step"](t.ctypes.data, len(grads), self.state_bits, ctypes.byref(h), st))
+
+        def work(st):
+            if _capturing():  # (a replay would repeat this step's corrections and rate)
+                raise RuntimeError("AdamW.step: a step cannot be captured: its count and rate are arguments of its launch")
+            return _fn["step"](t.ctypes.data, len(grads), self.state_bits, ctypes.byref(h), st)
+        code = c.on_stream(index, stream, used, work)
         if code:
             c.check(code, "dp_adamw_step")
         self.step_count += 1

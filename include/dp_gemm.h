@@ -385,7 +385,8 @@ typedef struct dp_adamw_hyper {
  * with a standard deviation of 12 to 20%.  A non-finite gradient makes its element (32 bits)
  * or its 128 elements' state (8 bits) non-finite.
  * 16-byte aligned tensors are faster; any element alignment works.  One launch per 256
- * tensors, no workspace. */
+ * tensors, no workspace.  Rate, step and the table are arguments of the launch: a captured
+ * call repeats that one step, so a graph's replays do not continue it. */
 dp_status dp_adamw_step(const dp_adamw_tensor* tensors, int64_t count, int state_bits, const dp_adamw_hyper* hyper,
                         dp_stream stream);
 

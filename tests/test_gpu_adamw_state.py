@@ -77,3 +77,24 @@ def test_a_refused_step_enters_nothing():
     opt.step(g)
     twin.step(g)
     assert torch.equal(moved, seen) and torch.equal(p, ref) and opt.step_count == 2
+
+
+def test_capture_is_refused():
+    """A replay would repeat one step's bias corrections; the refusal leaves the count, and the stream usable."""
+    p, opt, g = make()
+    opt.step(g)
+    before = p.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        g[0].mul_(1.0)
+        with pytest.raises(RuntimeError, match="captured"):
+            opt.step(g)
+        with pytest.raises(RuntimeError, match="captured"):
+            opt.step(g, stream=side)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(p, before) and opt.step_count == 1
+    opt.step(g)
+    assert opt.step_count == 2 and not torch.equal(p, before)
