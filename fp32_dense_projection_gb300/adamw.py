@@ -4,7 +4,8 @@
   opt.step(grads, grad_scale=clip)
 
 params are dense fp32 or bf16 CUDA tensors, updated in place; grads fp32 or bf16, one per
-parameter (None: that parameter is left as it is).  copies are optional bf16 tensors that
+parameter (None: that parameter, its moments and its count of updates are left as they are).
+copies are optional bf16 tensors that
 receive the updated parameter: the working weights of the GEMMs beside fp32 master weights.
 """
 from __future__ import annotations
@@ -59,7 +60,9 @@ class AdamW:
     beta2 = 0.95, m above beta1 = 0.98) are rounded stochastically, by a hash of element and step (a
     run repeats bit for bit): rounded to nearest they would not follow their small changes.
     The moments are attributes (tuples of tensors) and
-    may be passed in, with ``step`` the updates already done, to resume a run.  The updates
+    may be passed in, with ``step`` the updates already done (a number, or one per parameter as in
+    ``steps``), to resume a run.  ``step_count`` counts the calls of ``step``; a parameter's bias
+    corrections go by the updates that it had.  The updates
     are made in place, outside autograd.  The lists of tensors are fixed at construction; the
     tensors may get new memory between steps (``.data``), of their shape.  A step cannot be
     captured into a CUDA graph: its count and rate are arguments of the launch.
@@ -70,10 +73,13 @@ class AdamW:
         _need(state_bits in (8, 32), "state_bits must be 8 or 32")
         _need(len(betas) == 2 and all(0.0 <= b < 1.0 for b in betas), "betas must lie in [0, 1)")
         _need(lr >= 0 and eps >= 0 and weight_decay >= 0, "lr, eps and weight_decay must not be negative")
-        _need(step >= 0, "step must not be negative")
         self.params = tuple(params)
+        steps = [int(x) for x in step] if isinstance(step, (list, tuple)) else [int(step)] * len(self.params)
+        _need(len(steps) == len(self.params), "step must be a number or have one entry per parameter")
+        _need(min(steps, default=0) >= 0, "step must not be negative")
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
-        self.state_bits, self.step_count = state_bits, int(step)
+        self.state_bits, self.step_count = state_bits, max(steps, default=0)
+        self._missed = [self.step_count - x for x in steps] if len(set(steps)) > 1 else None  # per parameter; None: none
         n = len(self.params)
         self.device = None
         for i, p in enumerate(self.params):
@@ -139,6 +145,11 @@ class AdamW:
                      for p in self.params)
         return tuple(given)
 
+    @property
+    def steps(self):
+        """Updates that each parameter had."""
+        return tuple(self.step_count - x for x in self._missed or [0] * len(self.params))
+
     def step(self, grads, lr=None, grad_scale=1.0, stream=None):
         """One update.  lr overrides the constructor's for this step (a schedule); the
         gradients are multiplied by grad_scale, a number or a one-element fp32 CUDA tensor (a
@@ -159,15 +170,14 @@ class AdamW:
             raise ValueError(f"AdamW.step: every gradient must be contiguous, float32 or bfloat16, on {self.device} and of its "
                              "parameter's shape")
         t = self._table
-        t["grad"] = list(map(_data_ptr, some)) if len(some) == len(grads) else [0 if g is None else g.data_ptr() for g in grads]
+        at = list(map(_data_ptr, some)) if len(some) == len(grads) else [0 if g is None else g.data_ptr() for g in grads]
         if len(some) != len(grads):
             t["grad_bf16"] = [g is not None and g.dtype is _BF16 for g in grads]
             self._grad_dtypes = None
         elif dtypes != self._grad_dtypes:
             t["grad_bf16"] = [d is _BF16 for d in dtypes]
             self._grad_dtypes = dtypes
-        h = _Hyper(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, 1.0, None,
-                   self.step_count + 1)
+        h = _Hyper(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, 1.0, None, 0)
         if isinstance(grad_scale, torch.Tensor):
             if grad_scale.numel() != 1 or grad_scale.dtype is not _F32 or grad_scale.get_device() != index:
                 raise ValueError("AdamW.step: a grad_scale tensor must hold one float32 on the parameters' device")
@@ -183,8 +193,17 @@ class AdamW:
         def work(st):
             if _capturing():  # (a replay would repeat this step's corrections and rate)
                 raise RuntimeError("AdamW.step: a step cannot be captured: its count and rate are arguments of its launch")
-            return _fn["step"](t.ctypes.data, len(grads), self.state_bits, ctypes.byref(h), st)
+            # one call for the parameters that have had the same number of updates
+            for missed in (0,) if self._missed is None else {x for x, a in zip(self._missed, at) if a}:
+                t["grad"] = at if self._missed is None else [a if x == missed else 0 for x, a in zip(self._missed, at)]
+                h.step = self.step_count + 1 - missed
+                code = _fn["step"](t.ctypes.data, len(grads), self.state_bits, ctypes.byref(h), st)
+                if code:
+                    return code
+            return 0
         code = c.on_stream(index, stream, used, work)
         if code:
             c.check(code, "dp_adamw_step")
         self.step_count += 1
+        if len(some) != len(grads):
+            self._missed = [x + (g is None) for x, g in zip(self._missed or [0] * len(grads), grads)]

@@ -369,7 +369,7 @@ typedef struct dp_adamw_hyper {
     double lr, beta1, beta2, eps, weight_decay;
     double grad_scale;            /* gradients are multiplied by this */
     const float* grad_scale_ptr;  /* and, if not null, by this DEVICE value */
-    int64_t step;                 /* 1 for the first update (bias corrections) */
+    int64_t step;                 /* 1 for the first update (bias corrections) of these tensors */
 } dp_adamw_hyper;
 
 /* One AdamW update of `count` dense tensors (the table is read on the host during the call):

@@ -98,3 +98,31 @@ def test_capture_is_refused():
     assert torch.equal(p, before) and opt.step_count == 1
     opt.step(g)
     assert opt.step_count == 2 and not torch.equal(p, before)
+
+
+@pytest.mark.parametrize("state_bits", [32, 8])
+def test_a_parameter_that_missed_steps_has_its_own_corrections(state_bits):
+    """Without a gradient a parameter makes no step: alone in an optimizer of its own, called only when it has a
+    gradient, it gets the same bits.  The same after a resume from ``steps``."""
+    kw = dict(lr=1e-2, betas=(0.9, 0.999), state_bits=state_bits)
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    start = [torch.randn(s, device=DEV, generator=gen) for s in (300, 2048, 77)]
+    has = [(1, 0, 1), (1, 1, 0), (0, 0, 0), (1, 1, 1), (0, 1, 1), (1, 1, 1)]
+    opt = dp.AdamW([x.clone() for x in start], **kw)
+    own = [dp.AdamW([x.clone()], **kw) for x in start]
+    for n, row in enumerate(has):
+        grads = [torch.randn(x.shape, device=DEV, generator=gen) for x in start]
+        opt.step([g if h else None for g, h in zip(grads, row)])
+        for o, g, h in zip(own, grads, row):
+            if h:
+                o.step([g])
+        if n == 3:
+            opt = dp.AdamW(opt.params, step=opt.steps, exp_avg=opt.exp_avg, exp_avg_sq=opt.exp_avg_sq, exp_avg_scale=opt.exp_avg_scale,
+                           exp_avg_sq_scale=opt.exp_avg_sq_scale, **kw)
+    assert opt.steps == (4, 4, 4) and tuple(o.step_count for o in own) == (4, 4, 4)
+    for i, o in enumerate(own):
+        assert torch.equal(opt.params[i], o.params[0]) and torch.equal(bits(opt.exp_avg_sq[i]), bits(o.exp_avg_sq[0]))
+    with pytest.raises(ValueError, match="per parameter"):
+        dp.AdamW(opt.params, step=(1, 2), **kw)
+    with pytest.raises(ValueError, match="negative"):
+        dp.AdamW(opt.params, step=(1, -2, 0), **kw)
