@@ -36,6 +36,7 @@ def _bind(L):
     _fn["step"] = L.dp_adamw_step
 
 
+_increment_version = torch.autograd.graph.increment_version
 _capturing = torch._C._cuda_isCurrentStreamCapturing
 _data_ptr, _is_contiguous, _get_device = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
 _shape, _dtype = attrgetter("shape"), attrgetter("dtype")
@@ -63,7 +64,8 @@ class AdamW:
     may be passed in, with ``step`` the updates already done (a number, or one per parameter as in
     ``steps``), to resume a run.  ``step_count`` counts the calls of ``step``; a parameter's bias
     corrections go by the updates that it had.  The updates
-    are made in place, outside autograd.  The lists of tensors are fixed at construction; the
+    are made in place, outside autograd; they raise the versions of parameters and copies, so that
+    a backward pass that has saved one of them refuses to use what it has become.  The lists of tensors are fixed at construction; the
     tensors may get new memory between steps (``.data``), of their shape.  A step cannot be
     captured into a CUDA graph: its count and rate are arguments of the launch.
     """
@@ -135,6 +137,10 @@ class AdamW:
             self._table[what] = column
         self._table["numel"] = [p.numel() for p in self.params]
         self._table["param_bf16"] = [p.dtype is _BF16 for p in self.params]
+        # (inference tensors have no version)
+        self._versioned = [tuple(x for x in (p, q) if x is not None and not x.is_inference())
+                           for p, q in zip(self.params, self.copies or [None] * len(self.params))]
+        self._all_versioned = tuple(x for group in self._versioned for x in group)
         self._pointers, self._dtypes = list(map(_data_ptr, self._held)), list(map(_dtype, self._held))
         self._held_shapes = list(map(_shape, self._held))
         self._grad_dtypes = None
@@ -205,5 +211,8 @@ class AdamW:
         if code:
             c.check(code, "dp_adamw_step")
         self.step_count += 1
-        if len(some) != len(grads):
+        if len(some) == len(grads):
+            _increment_version(self._all_versioned)
+        else:
+            _increment_version([x for group, g in zip(self._versioned, grads) if g is not None for x in group])
             self._missed = [x + (g is None) for x, g in zip(self._missed or [0] * len(grads), grads)]

@@ -126,3 +126,26 @@ def test_a_parameter_that_missed_steps_has_its_own_corrections(state_bits):
         dp.AdamW(opt.params, step=(1, 2), **kw)
     with pytest.raises(ValueError, match="negative"):
         dp.AdamW(opt.params, step=(1, -2, 0), **kw)
+
+
+def test_autograd_notices_the_update():
+    """A backward pass through a parameter or a copy saved before the step is refused, as for other in-place
+    updates; one through a tensor that the step left alone is not.  Inference tensors have no version and are updated too."""
+    p, opt, g = make()
+    q = torch.randn(8, device=DEV)
+    both = dp.AdamW([p, q])
+    for saved, step, changed in ((p, lambda: opt.step(g), True), (opt.copies[0], lambda: opt.step(g), True),
+                                 (p, lambda: both.step([g[0], None]), True), (q, lambda: both.step([g[0], None]), False)):
+        x = torch.ones_like(saved, requires_grad=True)
+        y = (x * saved).sum()
+        step()
+        if changed:
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                y.backward()
+        else:
+            y.backward()
+    with torch.inference_mode():
+        w = torch.ones(16, device=DEV)
+    before = w.clone()
+    dp.AdamW([w]).step([torch.ones(16, device=DEV)])
+    assert bool((w < before).all())
