@@ -1,4 +1,5 @@
 """AdamW's tensors between steps: what a replaced .data may be."""
+import numpy as np
 import pytest
 import torch
 
@@ -149,3 +150,32 @@ def test_autograd_notices_the_update():
     before = w.clone()
     dp.AdamW([w]).step([torch.ones(16, device=DEV)])
     assert bool((w < before).all())
+
+
+@pytest.mark.parametrize("beta2", [0.95, 0.999])
+def test_tiny_second_moments_beside_a_large_one(beta2):
+    """One large gradient in each block among ones 1e-7 to 1e-12 of it and zeros: what is above zero is held as the
+    smallest code at least, zeros as zero, bit for bit the FP32 formula's (nearest and stochastic codes agree there: the
+    smallest code is a value of the grid)."""
+    n, f, betas = 128 * 64, np.float32, (0.9, beta2)
+    rng = np.random.default_rng(7)
+    grad = (10.0 ** rng.uniform(-12, -7, n) * rng.choice([-1, 1], n)).astype(f)
+    grad[rng.random(n) < 0.2] = 0
+    grad[::128] = 1
+    opt = dp.AdamW([torch.zeros(n, device=DEV)], betas=betas, state_bits=8)
+    codes, scales = np.zeros(n, f), np.zeros(n // 128, f)
+    for t in range(2):
+        opt.step([torch.from_numpy(grad).to(DEV)])
+        x, old = grad.reshape(-1, 128), codes.reshape(-1, 128) * scales[:, None]
+        root = np.sqrt((old * old) * f(betas[1]) + (x * x) * f(1 - betas[1]))
+        a = np.maximum(root.max(1), f(1e-30))
+        y = root * ((f(1) / a) * f(448))[:, None]
+        held = np.where(y > 0, np.maximum(y, f(2.0 ** -9)), y)
+        # (at first they would round to zero; then they are the smallest code, decayed)
+        assert ((0 < y) & (y < 2.0 ** (-9 if t else -10))).sum() > n // 2
+        codes, scales = torch.from_numpy(held).to(torch.float8_e4m3fn).float().numpy().reshape(-1), a * (f(1) / f(448))
+        got = opt.exp_avg_sq[0].view(torch.uint8).cpu().numpy()
+        assert np.array_equal(opt.exp_avg_sq[0].float().cpu().numpy(), codes)
+        assert np.array_equal(opt.exp_avg_sq_scale[0].cpu().numpy(), scales)
+        assert (got[grad == 0] == 0).all() and (got[np.abs(grad) < 1e-6][grad[np.abs(grad) < 1e-6] != 0] == 1).all()
+        assert bool(torch.isfinite(opt.params[0]).all())
