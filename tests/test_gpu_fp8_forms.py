@@ -18,23 +18,31 @@ def exact(op, T, N, K, repeats=1):
     assert dp.device_error() == 0
 
 
-# 256-column tiles over clusters of three SMs: a rank passes its partial tile through the operand
-# ring, which the last block's second MMA may still read.  The blocks are 64 to 67 (33 to 40), so that a
-# rank's last block lies in each of the ring's four stages.
+def force(monkeypatch, **form):
+    for k, v in form.items():
+        monkeypatch.setenv(f"DP_FORCE_{k}", str(v))
+
+
+# 256-column tiles over clusters: a rank passes its partial tile through the operand ring, which the last
+# block's second MMA may still read.  The blocks are 64 to 67 (32 to 40) over three ranks, so that a rank's last block lies
+# in each of the ring's four stages.
 @pytest.mark.parametrize("op,T,N,K", [("fwd", 16, 12288, 8192), ("fwd", 100, 12288, 8320), ("fwd", 1, 12288, 8576),
                                       ("fwd", 128, 12288, 8704), ("dgrad", 16, 8192, 12288), ("dgrad", 77, 8448, 12288),
                                       ("dgrad", 3, 8576, 12288), ("wgrad", 4096, 1024, 1536), ("wgrad", 4200, 1024, 1536),
                                       ("wgrad", 4500, 1024, 1536), ("wgrad", 5000, 2048, 768), ("wgrad", 4700, 1024, 1536)])
-def test_wide_tiles_split_over_clusters(op, T, N, K):
+def test_wide_tiles_split_over_clusters(monkeypatch, op, T, N, K):
+    force(monkeypatch, BN=256, PAIR=0, SPLITS=3)
+    exact(op, T, N, K, repeats=20)
+
+
+@pytest.mark.parametrize("op,T,N,K", [("fwd", 16, 8192, 20608), ("fwd", 128, 8192, 28672), ("dgrad", 50, 20736, 8192),
+                                      ("wgrad", 8192, 512, 2560), ("wgrad", 16500, 1024, 1024)])
+def test_wide_tiles_split_as_planned(op, T, N, K):
+    """Sizes at which the planner takes that form by itself on 152 SMs."""
     exact(op, T, N, K, repeats=20)
 
 
 FORMS = {"128": dict(BN=128, PAIR=0, SPLITS=1), "256": dict(BN=256, PAIR=0, SPLITS=1), "pair": dict(BN=256, PAIR=1, SPLITS=1)}
-
-
-def force(monkeypatch, **form):
-    for k, v in form.items():
-        monkeypatch.setenv(f"DP_FORCE_{k}", str(v))
 
 
 def sizes(op, gm, gn, gk):
