@@ -336,7 +336,11 @@ dp_status dp_fp8_quantize(const void* x, int64_t ldx, int x_f32, int64_t rows, i
  *   weight gradient  dW = dY^T X  dY and X: column blocks (along T)
  * Scales lie at any non-negative strides: row blocks at s[t * row + block * blk], 128 x 128
  * blocks at s[row block * row + column block * col], column blocks at
- * s[block * blk + column * col].  N, K and leading dimensions multiples of 16.  T == 0 as
+ * s[block * blk + column * col].  A block's two scales meet in FP32: the products of row and
+ * 128 x 128 scales are rounded to FP32 before they multiply the block's sum, column scales
+ * multiply it one after the other.  Scales from 2^-60 to 2^60 lose nothing by that which an FP32
+ * output could hold; two scales whose product leaves FP32's range give zeros, infinities
+ * or NaN even where the sum times both would not.  N, K and leading dimensions multiples of 16.  T == 0 as
  * for the BF16 calls.  Deterministic; one launch, no workspace. */
 dp_status dp_gemm_fwd_fp8(const void* Xq, int64_t ldx, dp_fp8_format x_format, const float* Xs, int64_t xs_row,
                           int64_t xs_blk, const void* Wq, int64_t ldw, dp_fp8_format w_format, const float* Ws,

@@ -80,3 +80,14 @@ def test_forms_that_do_not_exist_are_refused(monkeypatch, form):
     with pytest.raises(dp.DPError) as e:
         call("fwd", a, b)
     assert e.value.status == 3
+
+
+@pytest.mark.parametrize("ea,eb", [(-60, -60), (60, -60), (-60, 60), (60, 50)])
+@pytest.mark.parametrize("op", ["fwd", "dgrad", "wgrad"])
+def test_scales_at_the_ends_of_their_range(op, ea, eb):
+    """Powers of two: exact in FP32 as long as no scale, product of scales or sum leaves its range."""
+    for T, N, K in ((130, 144, 272), (2400, 2064, 2064)):
+        (a, _), (b, _) = operands(op, T, N, K, 9, ints=True)
+        a, b = (a[0], torch.full_like(a[1], 2.0 ** ea)), (b[0], torch.full_like(b[1], 2.0 ** eb))
+        ref = product(op, a[0].double(), b[0].double()) * 2.0 ** (ea + eb)
+        assert torch.equal(call(op, a, b, out_dtype=torch.float32), ref.float())
