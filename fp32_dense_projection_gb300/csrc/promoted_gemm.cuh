@@ -1011,7 +1011,8 @@ __global__ void __launch_bounds__(PgCfg<BN, KIND, FORM>::THREADS, 1)
       for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (warp - 4); i < idle; i += static_cast<int64_t>(gridDim.x) * 8) {
         const int64_t r = i < lo ? i : hi + (i - lo);
         char* p = static_cast<char*>(args.out) + r * args.ldo * esize;
-        for (int b = lane * 16; b < args.gn * esize; b += 512) *reinterpret_cast<uint4*>(p + b) = make_uint4(0, 0, 0, 0);
+        const int64_t bytes = static_cast<int64_t>(args.gn) * esize;
+        for (int64_t b = lane * 16; b < bytes; b += 512) *reinterpret_cast<uint4*>(p + b) = make_uint4(0, 0, 0, 0);
       }
     }
   }

@@ -6,6 +6,8 @@ import numpy as np
 import pytest
 import torch
 
+import fp32_dense_projection_gb300 as dp
+from gpu_common import DEV
 from test_gpu_grouped import call, edges_of, reference, tensors
 
 pytestmark = pytest.mark.gpu
@@ -24,3 +26,16 @@ def test_real_values_within_the_summations_bound(op, T, E, N, K):
     tol = (4 * min(depth, 512) / 16 + depth / 512 + 2) * 2.0 ** -23 * mag
     assert bool(((call(op, c, out_dtype=torch.float32).double() - ref).abs() <= tol).all())
     assert bool(((call(op, c).double() - ref).abs() <= tol + 2.0 ** -8 * ref.abs()).all())
+
+
+def test_padding_rows_of_more_than_2_31_bytes_are_zero():
+    """An output row whose bytes pass 32 bits: the padding row is zeroed to its end, the expert's row is right at both ends."""
+    N, K = 2 ** 29 + 64, 8
+    W = torch.zeros(1, N, K, dtype=torch.bfloat16, device=DEV)
+    W[0, :64] = 2
+    W[0, -64:] = 3
+    X = torch.ones(2, K, dtype=torch.bfloat16, device=DEV)
+    out = torch.full((2, N), 5.0, device=DEV)
+    dp.dp_gemm_fwd_grouped(X, W, torch.tensor([0, 1], dtype=torch.int32, device=DEV), out=out)
+    assert bool((out[1] == 0).all())
+    assert bool((out[0, :64] == 16).all()) and bool((out[0, -64:] == 24).all()) and bool((out[0, 64:-64] == 0).all())
