@@ -133,6 +133,10 @@ class AdamW:
                 if x is not None or what != "copy":
                     self._alike(f"{name}[{i}]", x, _scale_shape(shape) if "scale" in what else shape, dtypes)
             columns[what] = [0 if x is None else x.data_ptr() for x in tensors]
+        # (blocks of one launch write each tensor without regard to the others)
+        spans = sorted((x.data_ptr(), x.nbytes) for x in self._held if x.numel())
+        for (a, size), (b, _) in zip(spans, spans[1:]):
+            _need(a + size <= b, "params, copies and moments must not share memory (a tied weight is one parameter)")
         for what, column in columns.items():
             self._table[what] = column
         self._table["numel"] = [p.numel() for p in self.params]

@@ -112,7 +112,7 @@ def test_runs_repeat_and_resume_bit_for_bit():
     for x in grads[:3]:
         b.step(x)
     more = [torch.zeros(1, device=DEV) for _ in range(30)]
-    c = dp.AdamW([*more, *b.params], step=3, exp_avg=[*(x.to(E4) for x in more), *b.exp_avg], exp_avg_scale=[*more, *b.exp_avg_scale],
+    c = dp.AdamW([*more, *b.params], step=3, exp_avg=[*(x.to(E4) for x in more), *b.exp_avg], exp_avg_scale=[*(x.clone() for x in more), *b.exp_avg_scale],
                  exp_avg_sq=[*(x.to(E4) for x in more), *b.exp_avg_sq], exp_avg_sq_scale=[*(x.clone() for x in more), *b.exp_avg_sq_scale], **kw)
     for x in grads[3:]:
         c.step([*(None for _ in more), *x])

@@ -179,3 +179,19 @@ def test_tiny_second_moments_beside_a_large_one(beta2):
         assert np.array_equal(opt.exp_avg_sq_scale[0].cpu().numpy(), scales)
         assert (got[grad == 0] == 0).all() and (got[np.abs(grad) < 1e-6][grad[np.abs(grad) < 1e-6] != 0] == 1).all()
         assert bool(torch.isfinite(opt.params[0]).all())
+
+
+def test_shared_memory_is_refused():
+    """The same or overlapping memory twice would be updated by blocks that run beside each other."""
+    w = torch.randn(4096, device=DEV)
+    h = torch.zeros(4096, dtype=torch.bfloat16, device=DEV)
+    m, v = torch.zeros_like(w), torch.zeros_like(w)
+    for kw in (dict(params=[w, w]), dict(params=[w, w.view(64, 64)]), dict(params=[w[:3000], w[2999:]]), dict(params=[h], copies=[h]),
+               dict(params=[w], exp_avg=[m], exp_avg_sq=[m]), dict(params=[w[:96], w[96:]], copies=[h[:96], h[90:4090]])):
+        with pytest.raises(ValueError, match="share memory"):
+            dp.AdamW(**kw)
+    opt = dp.AdamW([w[:96], w[96:], w[:0]], copies=[h[:96], h[96:], None])  # neighbours in one buffer
+    opt.step([torch.ones(96, device=DEV), torch.ones(4000, device=DEV), torch.ones(0, device=DEV)])
+    opt.params[0].data = w[1:97]
+    with pytest.raises(ValueError, match="share memory"):
+        opt.step([torch.ones(96, device=DEV), torch.ones(4000, device=DEV), torch.ones(0, device=DEV)])
