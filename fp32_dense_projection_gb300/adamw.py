@@ -133,8 +133,11 @@ class AdamW:
                 if x is not None or what != "copy":
                     self._alike(f"{name}[{i}]", x, _scale_shape(shape) if "scale" in what else shape, dtypes)
             columns[what] = [0 if x is None else x.data_ptr() for x in tensors]
-        # (blocks of one launch write each tensor without regard to the others)
-        spans = sorted((x.data_ptr(), x.nbytes) for x in self._held if x.numel())
+        # (blocks of one launch write each tensor without regard to the others; a BF16 parameter may be its own copy)
+        own = {id(q) for p, q in zip(self.params, self.copies or ()) if q is not None and q.data_ptr() == p.data_ptr() and
+               q.nbytes == p.nbytes}
+        spans = sorted((x.data_ptr(), x.nbytes) for i, x in enumerate(self._held)
+                       if x.numel() and (i < len(self.params) or id(x) not in own))
         for (a, size), (b, _) in zip(spans, spans[1:]):
             _need(a + size <= b, "params, copies and moments must not share memory (a tied weight is one parameter)")
         for what, column in columns.items():

@@ -8,9 +8,9 @@
 // fused multiply-add, and for 8-bit moments the IEEE square root and reciprocal): a code on the
 // edge between two values would else depend on how its FP32 value was computed, and a run
 // would not be reproducible elsewhere.  The parameter's quotient, which no state depends on, takes
-// the approximate instructions (two units in the last place of the update).  The parameter is
-// rounded once to its type, and its optional BF16 copy (the working weight of the GEMMs) from
-// the rounded parameter.
+// the approximate instructions: root (2^-23) and reciprocal (2^-23), the constants' and three other
+// roundings make up to 5.4e-7 of the update.  The parameter is rounded once to its type, and its
+// optional BF16 copy (the working weight of the GEMMs) from the rounded parameter.
 //
 // 8-bit moments: 128 consecutive elements of a tensor share a scale.  m is held as E4M3
 // codes of m / s with s = max|m| / 448.  sqrt(v), not v, is held the same way: the root
@@ -268,6 +268,7 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// (8-bit moments: six CTAs an SM leave 40 registers a thread, and two words of it are spilled.)
 template <int MAX, bool EIGHT, bool DITHER>
 __global__ void __launch_bounds__(256, EIGHT ? 6 : 5) adamw_kernel(const __grid_constant__ Table<MAX> t) {
   const float gs = t.grad_scale_ptr ? t.grad_scale * __ldg(t.grad_scale_ptr) : t.grad_scale;

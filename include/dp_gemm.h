@@ -290,7 +290,10 @@ dp_status router_wgrad_ex(const float* dY, int64_t ldg, const float* X, int64_t 
  *   apart by experts (elements; 0 = packed).
  * FP32 accumulation in pieces of 512 contraction elements that are added in FP32 with
  * round-to-nearest, whatever the group's size; every output is deterministic.  One launch,
- * no workspace.  At most 1024 experts. */
+ * no workspace.  At most 1024 experts.
+ * One SM (or a pair) contracts an output tile's whole length: a few experts with a few tiles
+ * leave SMs idle however long the contraction (one expert of 256 x 256, weight gradient: 8
+ * tiles); dp_gemm_wgrad shares a contraction among SMs. */
 dp_status dp_gemm_fwd_grouped(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t bsw, int weight_kn,
                               const void* offsets, int offset_bits, void* Y, int64_t ldy,
                               int64_t E, int64_t T, int64_t N, int64_t K, dp_out_dtype out, dp_stream stream);
@@ -379,8 +382,8 @@ typedef struct dp_adamw_hyper {
 /* One AdamW update of `count` dense tensors (the table is read on the host during the call):
  *   g' = g * scale;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
  *   p  = p (1 - lr wd) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * in FP32: the moments' operations rounded one by one, the parameter's quotient to two units
- * in the last place; p is rounded once to its type.
+ * in FP32: the moments' operations rounded one by one, the parameter's update to 6e-7 of
+ * itself; p is rounded once to its type.
  * state_bits = 8: m is held as E4M3 codes with a scale max|m| / 448 for each 128 consecutive
  * elements, and sqrt(v) likewise; a v above zero is never held as zero.  Codes are rounded to
  * nearest up to beta1 = 0.98 (m) and beta2 = 0.95 (sqrt(v)); above, where a step moves the moment by

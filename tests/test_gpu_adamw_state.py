@@ -186,10 +186,14 @@ def test_shared_memory_is_refused():
     w = torch.randn(4096, device=DEV)
     h = torch.zeros(4096, dtype=torch.bfloat16, device=DEV)
     m, v = torch.zeros_like(w), torch.zeros_like(w)
-    for kw in (dict(params=[w, w]), dict(params=[w, w.view(64, 64)]), dict(params=[w[:3000], w[2999:]]), dict(params=[h], copies=[h]),
-               dict(params=[w], exp_avg=[m], exp_avg_sq=[m]), dict(params=[w[:96], w[96:]], copies=[h[:96], h[90:4090]])):
+    for kw in (dict(params=[w, w]), dict(params=[w, w.view(64, 64)]), dict(params=[w[:3000], w[2999:]]), dict(params=[h[:64]], copies=[h[32:96]]),
+               dict(params=[w], exp_avg=[m], exp_avg_sq=[m]), dict(params=[h, w], copies=[None, h]), dict(params=[w[:96], w[96:]], copies=[h[:96], h[90:4090]])):
         with pytest.raises(ValueError, match="share memory"):
             dp.AdamW(**kw)
+    a, b = h.clone(), h.clone()  # a BF16 parameter may be its own copy
+    for opt in (dp.AdamW([a], copies=[a]), dp.AdamW([b])):
+        opt.step([w])
+    assert torch.equal(a, b) and bool((a != 0).any())
     opt = dp.AdamW([w[:96], w[96:], w[:0]], copies=[h[:96], h[96:], None])  # neighbours in one buffer
     opt.step([torch.ones(96, device=DEV), torch.ones(4000, device=DEV), torch.ones(0, device=DEV)])
     opt.params[0].data = w[1:97]
