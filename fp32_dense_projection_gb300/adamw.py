@@ -39,6 +39,7 @@ def _bind(L):
 _increment_version = torch.autograd.graph.increment_version
 _capturing = torch._C._cuda_isCurrentStreamCapturing
 _data_ptr, _is_contiguous, _get_device = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
+_numel = torch.Tensor.numel
 _shape, _dtype = attrgetter("shape"), attrgetter("dtype")
 _F32, _BF16 = torch.float32, torch.bfloat16
 
@@ -112,10 +113,11 @@ class AdamW:
 
     def _changed(self):
         """Whether a parameter, copy or moment is not what was entered: its .data may have been
-        replaced, also by another view or type at the same address."""
+        replaced, also by another view or type at the same address.  (As many elements of the same
+        type in one piece there are the same elements; a shape is four times as dear to read as their number.)"""
         held = self._held
         return (list(map(_data_ptr, held)) != self._pointers or list(map(_dtype, held)) != self._dtypes or
-                list(map(_shape, held)) != self._held_shapes or False in map(_is_contiguous, held))
+                list(map(_numel, held)) != self._numels or False in map(_is_contiguous, held))
 
     def _enter(self):
         """Check the tensors and then enter them in the table (all of them or, if one is refused, none)."""
@@ -149,7 +151,7 @@ class AdamW:
                            for p, q in zip(self.params, self.copies or [None] * len(self.params))]
         self._all_versioned = tuple(x for group in self._versioned for x in group)
         self._pointers, self._dtypes = list(map(_data_ptr, self._held)), list(map(_dtype, self._held))
-        self._held_shapes = list(map(_shape, self._held))
+        self._numels = list(map(_numel, self._held))
         self._grad_dtypes = None
 
     def _state(self, given, dtype, scales):
