@@ -94,17 +94,30 @@ class AdamW:
         self._table = np.zeros(n, _ENTRY)
         self._shapes = [p.shape for p in self.params]
         kind = torch.float8_e4m3fn if state_bits == 8 else _F32
-        self.exp_avg = self._state(exp_avg, kind, False)
-        self.exp_avg_sq = self._state(exp_avg_sq, kind, False)
-        self.exp_avg_scale = self.exp_avg_sq_scale = None
+        m = self._moments = {"exp_avg": self._state(exp_avg, kind, False), "exp_avg_sq": self._state(exp_avg_sq, kind, False),
+                             "exp_avg_scale": None, "exp_avg_sq_scale": None}
         if state_bits == 8:
-            self.exp_avg_scale = self._state(exp_avg_scale, _F32, True)
-            self.exp_avg_sq_scale = self._state(exp_avg_sq_scale, _F32, True)
+            m["exp_avg_scale"] = self._state(exp_avg_scale, _F32, True)
+            m["exp_avg_sq_scale"] = self._state(exp_avg_sq_scale, _F32, True)
         else:
             _need(exp_avg_scale is None and exp_avg_sq_scale is None, "scales belong to state_bits=8")
-        lists = (self.params, self.copies, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)
-        self._held = tuple(x for t in lists for x in t or () if x is not None)
+        self._held = tuple(x for t in (self.params, self.copies, *m.values()) for x in t or () if x is not None)
+        # tensors that someone else may hold: all, until then without the moments made here
+        given = any(x is not None for x in (exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale))
+        self._watched = self._held if given else self._held[:len(self._held) - sum(len(t) for t in m.values() if t is not None)]
         self._enter()
+
+    def _moment(name):
+        def get(self):
+            if self._watched is not self._held:
+                self._watched = self._held
+                self._note()
+            return self._moments[name]
+        return property(get)
+
+    exp_avg, exp_avg_sq = _moment("exp_avg"), _moment("exp_avg_sq")
+    exp_avg_scale, exp_avg_sq_scale = _moment("exp_avg_scale"), _moment("exp_avg_sq_scale")
+    del _moment
 
     def _alike(self, what, t, shape, dtypes):
         _need(isinstance(t, torch.Tensor) and t.device == self.device, f"{what} must be on {self.device}")
@@ -115,17 +128,20 @@ class AdamW:
         """Whether a parameter, copy or moment is not what was entered: its .data may have been
         replaced, also by another view or type at the same address.  (As many elements of the same
         type in one piece there are the same elements; a shape is four times as dear to read as their number.)"""
-        held = self._held
-        return (list(map(_data_ptr, held)) != self._pointers or list(map(_dtype, held)) != self._dtypes or
-                list(map(_numel, held)) != self._numels or False in map(_is_contiguous, held))
+        watched = self._watched
+        return (list(map(_data_ptr, self._held)) != self._pointers or list(map(_dtype, watched)) != self._dtypes or
+                list(map(_numel, watched)) != self._numels or False in map(_is_contiguous, watched))
+
+    def _note(self):
+        """What later steps compare with."""
+        self._pointers = list(map(_data_ptr, self._held))
+        self._dtypes, self._numels = list(map(_dtype, self._watched)), list(map(_numel, self._watched))
 
     def _enter(self):
         """Check the tensors and then enter them in the table (all of them or, if one is refused, none)."""
         kind = torch.float8_e4m3fn if self.state_bits == 8 else _F32
         columns = {}
-        for what, tensors in (("param", self.params), ("copy", self.copies), ("exp_avg", self.exp_avg),
-                              ("exp_avg_sq", self.exp_avg_sq), ("exp_avg_scale", self.exp_avg_scale),
-                              ("exp_avg_sq_scale", self.exp_avg_sq_scale)):
+        for what, tensors in {"param": self.params, "copy": self.copies, **self._moments}.items():
             if tensors is None:
                 continue
             name = {"param": "params", "copy": "copies"}.get(what, what)
@@ -150,9 +166,8 @@ class AdamW:
         self._versioned = [tuple(x for x in (p, q) if x is not None and not x.is_inference())
                            for p, q in zip(self.params, self.copies or [None] * len(self.params))]
         self._all_versioned = tuple(x for group in self._versioned for x in group)
-        self._pointers, self._dtypes = list(map(_data_ptr, self._held)), list(map(_dtype, self._held))
-        self._numels = list(map(_numel, self._held))
         self._grad_dtypes = None
+        self._note()
 
     def _state(self, given, dtype, scales):
         if given is None:
@@ -199,9 +214,7 @@ class AdamW:
             h.grad_scale_ptr = grad_scale.data_ptr()
         else:
             h.grad_scale = float(grad_scale)
-        used = () if stream is None else (*some, *self.params, *self.exp_avg, *self.exp_avg_sq, *(self.exp_avg_scale or ()),
-                                          *(self.exp_avg_sq_scale or ()), *(x for x in self.copies or () if x is not None),
-                                          *((grad_scale,) if isinstance(grad_scale, torch.Tensor) else ()))
+        used = () if stream is None else (*some, *self._held, *((grad_scale,) if isinstance(grad_scale, torch.Tensor) else ()))
         if not _fn:
             c.load()
 

@@ -199,3 +199,31 @@ def test_shared_memory_is_refused():
     opt.params[0].data = w[1:97]
     with pytest.raises(ValueError, match="share memory"):
         opt.step([torch.ones(96, device=DEV), torch.ones(4000, device=DEV), torch.ones(0, device=DEV)])
+
+
+@pytest.mark.parametrize("state_bits", [32, 8])
+def test_moments_that_were_looked_at_are_watched(state_bits):
+    """Moments made by the optimizer are its own until someone reads the attribute; what is then put in their place is
+    followed or refused.  The attributes cannot be set: the steps would not go by what was set."""
+    p, opt, g = make(state_bits=state_bits)
+    ref, twin, _ = make(state_bits=state_bits)
+    ref.copy_(p)
+    for _ in range(2):
+        opt.step(g)
+        twin.step(g)
+    names = ["exp_avg", "exp_avg_sq"] + ["exp_avg_scale", "exp_avg_sq_scale"] * (state_bits == 8)
+    for name in names:
+        with pytest.raises(AttributeError):
+            setattr(opt, name, getattr(opt, name))
+        x = getattr(opt, name)[0]
+        assert getattr(opt, name)[0] is x
+        good = x.data
+        x.data = good[:1]
+        refused(opt, g, name)
+        x.data, kept = good.clone(), good.clone()
+        g = [torch.randn_like(p)]
+        opt.step(g)
+        twin.step(g)
+        assert torch.equal(bits(good), bits(kept))
+        assert not torch.equal(bits(x), bits(good)) and torch.equal(bits(x), bits(getattr(twin, name)[0])) and torch.equal(p, ref)
+    assert (opt.exp_avg_scale is None) == (state_bits == 32)
