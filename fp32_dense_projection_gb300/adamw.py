@@ -59,16 +59,19 @@ class AdamW:
     state_bits=32 keeps both moments in fp32.  state_bits=8 keeps them as float8_e4m3fn
     codes with an fp32 scale per 128 consecutive elements: ``exp_avg`` holds m / scale,
     ``exp_avg_sq`` holds sqrt(v) / scale.  Codes of moments with a long memory (sqrt(v) above
-    beta2 = 0.95, m above beta1 = 0.98) are rounded stochastically, by a hash of element and step (a
-    run repeats bit for bit): rounded to nearest they would not follow their small changes.
-    The moments are attributes (tuples of tensors) and
-    may be passed in, with ``step`` the updates already done (a number, or one per parameter as in
-    ``steps``), to resume a run.  ``step_count`` counts the calls of ``step``; a parameter's bias
-    corrections go by the updates that it had.  The updates
-    are made in place, outside autograd; they raise the versions of parameters and copies, so that
-    a backward pass that has saved one of them refuses to use what it has become.  The lists of tensors are fixed at construction; the
-    tensors may get new memory between steps (``.data``), of their shape.  A step cannot be
-    captured into a CUDA graph: its count and rate are arguments of the launch.
+    beta2 = 0.95, m above beta1 = 0.98) are rounded stochastically, by a hash of element and
+    step (a run repeats bit for bit): rounded to nearest they would not follow small changes.
+
+    The moments are attributes (tuples of tensors) and may be passed in, with ``step`` the
+    updates already done (a number, or one per parameter as in ``steps``), to resume a run.
+    ``step_count`` counts the calls of ``step``; a parameter's bias corrections go by the
+    updates that it had.
+
+    The updates are made in place, outside autograd; they raise the versions of parameters
+    and copies, so that a backward pass that has saved one of them refuses to use what it has
+    become.  The lists of tensors are fixed at construction; the tensors may get new memory
+    between steps (``.data``), of their shape, but not share it.  A step cannot be captured
+    into a CUDA graph: its count and rate are arguments of the launch.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32, copies=None,
