@@ -23,6 +23,15 @@ first call raises.
   AdamW                    the weights' update over many tensors in one launch, moments in
                            32 or 8 bits
 
+  layer_norm_fwd / layer_norm_bwd
+                           layer norm over rows, with the gradients of weight and bias
+  route_topk / route_topk_bwd
+                           the router's choice of k experts with its gates, and its gradient
+  expert_sort / expert_gather / expert_combine / expert_combine_bwd
+                           tokens sorted by expert and back, weighted, with the gradients
+  int4_quantize / int4_dequantize / dp_gemm_fwd_int4 / dp_gemm_fwd_int4_grouped
+                           weights in 4 bits with a scale per group, products of few rows with them
+
 Outputs are bf16 (``out_dtype=torch.bfloat16``) or fp32 for the BF16 ops.  An
 ``out=`` tensor may be a column slice of a wider buffer (padded row stride).
 """
@@ -102,7 +111,7 @@ def lib():
         L.dp_gemm_bwd.argtypes = [P, I, P, I, P, I, P, I, S, P, I, S, I, I, I, S, P, Z, P]
         L.dp_plan_query_bwd.argtypes = [I, I, I, S, S, S, ctypes.POINTER(BwdPlanInfo)]
         L.dp_workspace_size_bwd.argtypes = [I, I, I, S, S, S, ctypes.POINTER(ctypes.c_size_t)]
-        for m in (grouped, fp8, adamw):
+        for m in (grouped, fp8, adamw, layer_norm, experts, int4):
             m._bind(L)
         L.dp_init.argtypes = [S]
         L.dp_device_error.argtypes = [S]
@@ -523,7 +532,11 @@ def dp_gemm_wgrad_noalloc(dY, X, out, out_dtype=None, deterministic=True, stream
     return out
 
 
-from . import adamw, fp8, grouped  # noqa: E402  (they use the definitions above)
+from . import adamw, experts, fp8, grouped, int4, layer_norm  # noqa: E402  (they use the definitions above)
 from .adamw import AdamW  # noqa: E402
+from .experts import (expert_combine, expert_combine_bwd, expert_gather, expert_sort, route_topk,  # noqa: E402
+                      route_topk_bwd)
 from .fp8 import dp_gemm_dgrad_fp8, dp_gemm_fwd_fp8, dp_gemm_wgrad_fp8, fp8_quantize  # noqa: E402
 from .grouped import dp_gemm_dgrad_grouped, dp_gemm_fwd_grouped, dp_gemm_wgrad_grouped  # noqa: E402
+from .int4 import dp_gemm_fwd_int4, dp_gemm_fwd_int4_grouped, int4_dequantize, int4_quantize  # noqa: E402
+from .layer_norm import layer_norm_bwd, layer_norm_fwd  # noqa: E402

@@ -36,4 +36,7 @@ dp_status check_operand(const void* p, int64_t rows, int64_t cols, int64_t* ld, 
 bool encode_operand(CUtensorMap* map, const void* ptr, CUtensorMapDataType type, int esize, int64_t rows, int64_t cols,
                     int64_t ld, int64_t batch, int64_t bstride, uint32_t box_cols, uint32_t box_rows);
 
+// Shared memory of the products with 4-bit weights (for the current device).
+cudaError_t set_attributes_int4();
+
 }  // namespace dp

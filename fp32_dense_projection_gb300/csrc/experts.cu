@@ -1,0 +1,414 @@
+// Tokens to their experts and back.  P = T k (token, choice) pairs, pair p = t k + j:
+//   sort     rows of the sorted buffer by expert, pairs of one expert in their order (stable):
+//            offsets [E + 1], row_of [P] (the row of a pair), order [P] (the pair of a row).  Pairs
+//            without an expert (choice outside [0, E)) follow the last group; their row r is
+//            held as ~r, below zero
+//   gather   rows[row_of[t, j]] = x[t]; rows of pairs without an expert are zero
+//   combine  out[t] = add[t] + sum_j gate[t, j] y[row_of[t, j]] over the pairs that have an expert
+//   and combine's gradient  dy[row_of[t, j]] = gate[t, j] dout[t],  dgate[t, j] = dout[t] . y[row_of[t, j]]
+// The gradient of gather is combine without gates.
+//
+// Bound: gather, combine and its gradient move rows and are bound by HBM: the threads of a token
+// go over its k rows together, so a token's own row is read or written once, and each sum is
+// taken by one thread in the order of j (no atomics).  The sort moves 12 bytes a pair and is
+// latency: a counting sort without atomics.  A warp counts its own run of pairs in its own
+// counters (lanes with one expert find each other by a match), counters are summed over the
+// warps, and each warp walks its run again with its running positions.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "api_internal.h"
+#include "row_ops.cuh"
+
+namespace dp {
+namespace {
+
+constexpr int64_t kMaxExpertCount = 1024;
+constexpr int64_t kMaxPairs = 0x7FFFFFFF - 256;
+constexpr uint32_t kAll = 0xffffffffu;
+
+// ------------------------------------------------------------------------ sort
+
+struct SortArgs {
+  const void* choice;
+  int wide;  // int64 choices
+  int32_t P, E;
+  int32_t per_block, per_warp;  // pairs, multiples of 32
+  int32_t* counts;              // [blocks][E + 1], more than one block
+  int32_t* offsets;
+  int32_t* row_of;
+  int32_t* order;
+};
+
+__device__ __forceinline__ int key_of(const SortArgs& a, int i) {
+  const int64_t e = a.wide ? static_cast<const int64_t*>(a.choice)[i] : static_cast<const int32_t*>(a.choice)[i];
+  return e >= 0 && e < a.E ? static_cast<int>(e) : a.E;
+}
+
+// The warp's own counts of the pairs in its run, in shared memory (zero before).
+__device__ __forceinline__ void count_run(const SortArgs& a, int begin, int end, int32_t* mine) {
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  for (int i = begin + lane; i - lane < end; i += 32) {
+    const int key = i < end ? key_of(a, i) : -1;
+    const uint32_t same = __match_any_sync(kAll, key);
+    if (key >= 0 && lane == __ffs(static_cast<int>(same)) - 1) mine[key] += __popc(same);
+    __syncwarp();
+  }
+}
+
+__global__ void __launch_bounds__(1024) sort_count_kernel(const __grid_constant__ SortArgs a) {
+  extern __shared__ int32_t warp_counts[];  // [warps][E + 1]
+  const int n = a.E + 1, warp = static_cast<int>(threadIdx.x) >> 5, warps = static_cast<int>(blockDim.x) >> 5;
+  for (int i = static_cast<int>(threadIdx.x); i < warps * n; i += static_cast<int>(blockDim.x)) warp_counts[i] = 0;
+  __syncthreads();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * a.per_block;
+  const int begin = static_cast<int>(min(static_cast<int64_t>(a.P), first + warp * a.per_warp));
+  const int end = static_cast<int>(min(static_cast<int64_t>(a.P), min(first + a.per_block, first + (warp + 1) * a.per_warp)));
+  count_run(a, begin, end, warp_counts + warp * n);
+  __syncthreads();
+  for (int e = static_cast<int>(threadIdx.x); e < n; e += static_cast<int>(blockDim.x)) {
+    int32_t s = 0;
+    for (int w = 0; w < warps; ++w) s += warp_counts[w * n + e];
+    a.counts[static_cast<int64_t>(blockIdx.x) * n + e] = s;
+  }
+}
+
+__global__ void __launch_bounds__(1024) sort_place_kernel(const __grid_constant__ SortArgs a) {
+  extern __shared__ int32_t warp_counts[];  // [warps][E + 1], then base [E + 1]
+  __shared__ int32_t scan[33];
+  const int n = a.E + 1, tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const int threads = static_cast<int>(blockDim.x), warps = threads >> 5;
+  int32_t* base = warp_counts + warps * n;
+  for (int i = tid; i < warps * n; i += threads) warp_counts[i] = 0;
+  __syncthreads();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * a.per_block;
+  const int begin = static_cast<int>(min(static_cast<int64_t>(a.P), first + warp * a.per_warp));
+  const int end = static_cast<int>(min(static_cast<int64_t>(a.P), min(first + a.per_block, first + (warp + 1) * a.per_warp)));
+  count_run(a, begin, end, warp_counts + warp * n);
+  __syncthreads();
+  // positions of the warps within their block, the pairs of each expert in all blocks and before this one
+  int32_t carry = 0;
+  for (int e0 = 0; e0 < n; e0 += threads) {
+    const int e = e0 + tid;
+    int32_t own = 0, total = 0, before = 0;
+    if (e < n) {
+      for (int w = 0; w < warps; ++w) {
+        const int32_t c = warp_counts[w * n + e];
+        warp_counts[w * n + e] = own;
+        own += c;
+      }
+      total = own;
+      if (gridDim.x > 1) {
+        total = 0;
+        for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+          if (b == static_cast<int>(blockIdx.x)) before = total;
+          total += a.counts[static_cast<int64_t>(b) * n + e];
+        }
+      }
+    }
+    int32_t incl = total;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(kAll, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int32_t lower = carry;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) lower += scan[w];
+      carry += scan[w];
+    }
+    if (e < n) {
+      const int32_t start = lower + incl - total;
+      base[e] = start + before;
+      if (blockIdx.x == 0) a.offsets[e] = start;
+    }
+    __syncthreads();
+  }
+  int32_t* mine = warp_counts + warp * n;
+  for (int i = begin + lane; i - lane < end; i += 32) {
+    const int key = i < end ? key_of(a, i) : -1;
+    const uint32_t same = __match_any_sync(kAll, key);
+    const int32_t at = key >= 0 ? base[key] + mine[key] + __popc(same & ((1u << lane) - 1)) : 0;
+    __syncwarp();
+    if (key >= 0) {
+      if (lane == __ffs(static_cast<int>(same)) - 1) mine[key] += __popc(same);
+      a.row_of[i] = key < a.E ? at : ~at;
+      a.order[at] = i;
+    }
+    __syncwarp();
+  }
+}
+
+struct SortShape {
+  int warps, blocks;
+  int32_t per_warp, per_block;
+  size_t smem;
+};
+
+constexpr int kSortBlocks = 128;
+
+SortShape sort_shape(int64_t P, int64_t E) {
+  SortShape s;
+  // (counters and positions: at most 46 KB)
+  s.warps = static_cast<int>(std::min<int64_t>(32, (46 << 8) / (E + 1) - 1));
+  const int64_t runs = (P + 31) / 32;  // 32 pairs each
+  s.blocks = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSortBlocks, runs / (s.warps * 4))));
+  const int64_t per = (runs + static_cast<int64_t>(s.blocks) * s.warps - 1) / (static_cast<int64_t>(s.blocks) * s.warps);
+  s.per_warp = static_cast<int32_t>(per * 32);
+  s.per_block = s.per_warp * s.warps;
+  s.smem = static_cast<size_t>(s.warps + 1) * (E + 1) * 4;
+  return s;
+}
+
+// ------------------------------------------------------------- gather, combine
+
+struct RowArgs {
+  const void* x;  // gather: x; combine: y; gradient: dout
+  int64_t ldx;
+  const void* y;  // gradient: y
+  int64_t ld_y;
+  const int32_t* row_of;
+  const float* gates;  // null: 1
+  const void* add;     // null: 0
+  int64_t ld_add;
+  void* out;  // gather: rows; combine: out; gradient: dy
+  int64_t ldo;
+  float* dgates;
+  int64_t T;
+  int32_t k, C, tpr, P;
+  uint32_t* fault;
+};
+
+// The row that a pair's entry names and whether the pair has an expert.  An entry that names no
+// row of the buffer is reported, and its pair left out.
+struct Place {
+  int32_t row;  // -1: none
+  bool live;
+};
+
+__device__ __forceinline__ Place place_of(const RowArgs& a, int64_t pair) {
+  const int32_t r = __ldg(a.row_of + pair), row = r < 0 ? ~r : r;
+  if (row < a.P) return {row, r >= 0};
+  atomicOr(a.fault, kFaultOffsets);
+  return {-1, false};
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ RowArgs a) {
+  const int sub = static_cast<int>(threadIdx.x) / a.tpr, lane = static_cast<int>(threadIdx.x) % a.tpr;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (256 / a.tpr) + sub;
+  if (t >= a.T) return;
+  for (int col = lane * 8; col < a.C; col += a.tpr * 8) {
+    const Raw8<F32> v = load_raw8<F32>(a.x, t * a.ldx + col);
+    for (int j = 0; j < a.k; ++j) {
+      const Place at = place_of(a, t * a.k + j);
+      if (at.row >= 0) store_raw8<F32>(a.out, at.row * a.ldo + col, at.live ? v : zero_raw8<F32>());
+    }
+  }
+}
+
+template <bool YF32, bool OF32>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ RowArgs a) {
+  const int sub = static_cast<int>(threadIdx.x) / a.tpr, lane = static_cast<int>(threadIdx.x) % a.tpr;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (256 / a.tpr) + sub;
+  if (t >= a.T) return;
+  for (int col = lane * 8; col < a.C; col += a.tpr * 8) {
+    float s[8];
+    if (a.add != nullptr) {
+      load8<OF32>(a.add, t * a.ld_add + col, s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = 0.0f;
+    }
+    for (int j = 0; j < a.k; ++j) {
+      const Place at = place_of(a, t * a.k + j);
+      if (!at.live) continue;
+      const float g = a.gates != nullptr ? __ldg(a.gates + t * a.k + j) : 1.0f;
+      float v[8];
+      load8<YF32>(a.x, at.row * a.ldx + col, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = fmaf(g, v[i], s[i]);
+    }
+    store8<OF32>(a.out, t * a.ldo + col, s);
+  }
+}
+
+template <bool DF32, bool YF32, bool OF32>
+__global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant__ RowArgs a) {
+  __shared__ float part[2][32][1];
+  const int sub = static_cast<int>(threadIdx.x) / a.tpr, lane = static_cast<int>(threadIdx.x) % a.tpr;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (256 / a.tpr) + sub;
+  const bool live = t < a.T;
+  GroupSum<1> sum(part, a.tpr);
+  for (int j = 0; j < a.k; ++j) {  // (every thread of the block: the sums meet in barriers)
+    const Place at = live ? place_of(a, t * a.k + j) : Place{-1, false};
+    const float g = at.live ? __ldg(a.gates + t * a.k + j) : 0.0f;
+    float dot[1] = {0.0f};
+    for (int col = lane * 8; at.row >= 0 && col < a.C; col += a.tpr * 8) {
+      float d[8], v[8];
+      if (at.live) {
+        load8<DF32>(a.x, t * a.ldx + col, d);
+        load8<YF32>(a.y, at.row * a.ld_y + col, v);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (at.live) dot[0] = fmaf(d[i], v[i], dot[0]);
+        d[i] = at.live ? d[i] * g : 0.0f;
+      }
+      store8<OF32>(a.out, at.row * a.ldo + col, d);
+    }
+    sum(dot);
+    if (live && lane == 0) a.dgates[t * a.k + j] = dot[0];
+  }
+}
+
+int threads_per_token(int64_t C) {
+  int tpr = 8;
+  while (tpr < 256 && tpr * 8 < C) tpr *= 2;
+  return tpr;
+}
+
+bool flag(int v) { return v == 0 || v == 1; }
+
+template <typename F>
+void by_bool(bool v, F f) {
+  v ? f(std::true_type()) : f(std::false_type());
+}
+
+dp_status check_pairs(const int32_t* row_of, int64_t T, int64_t k, int64_t C) {
+  if (T < 0 || k < 1 || C < 1) return DP_ERR_INVALID_ARG;
+  if (C % 8 != 0 || C > 0x7FFFFF00 || T > kMaxPairs || k > kMaxPairs || T * k > kMaxPairs) return DP_ERR_UNSUPPORTED;
+  if (T > 0 && row_of == nullptr) return DP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(row_of) & 3) != 0) return DP_ERR_ALIGNMENT;
+  return DP_OK;
+}
+
+RowArgs row_args(const int32_t* row_of, const float* gates, int64_t T, int64_t k, int64_t C, const DeviceContext& ctx) {
+  RowArgs a = {};
+  a.row_of = row_of, a.gates = gates, a.T = T, a.k = static_cast<int32_t>(k), a.C = static_cast<int32_t>(C);
+  a.tpr = threads_per_token(C), a.P = static_cast<int32_t>(T * k), a.fault = ctx.fault;
+  return a;
+}
+
+unsigned token_blocks(const RowArgs& a) { return static_cast<unsigned>((a.T + 256 / a.tpr - 1) / (256 / a.tpr)); }
+
+}  // namespace
+}  // namespace dp
+
+extern "C" dp_status dp_expert_sort_workspace_size(int64_t pairs, int64_t E, size_t* bytes) {
+  using namespace dp;
+  if (bytes == nullptr || pairs < 0 || E < 1) return DP_ERR_INVALID_ARG;
+  if (E > kMaxExpertCount || pairs > kMaxPairs) return DP_ERR_UNSUPPORTED;
+  const SortShape s = sort_shape(pairs, E);
+  *bytes = s.blocks > 1 ? static_cast<size_t>(s.blocks) * (E + 1) * 4 : 0;
+  return DP_OK;
+}
+
+extern "C" dp_status dp_expert_sort(const void* choice, int choice_bits, int64_t pairs, int64_t E, int32_t* offsets,
+                                    int32_t* row_of, int32_t* order, void* workspace, size_t workspace_bytes,
+                                    dp_stream stream) {
+  using namespace dp;
+  if ((choice_bits != 32 && choice_bits != 64) || pairs < 0 || E < 1 || offsets == nullptr) return DP_ERR_INVALID_ARG;
+  if (E > kMaxExpertCount || pairs > kMaxPairs) return DP_ERR_UNSUPPORTED;
+  if (pairs > 0 && (choice == nullptr || row_of == nullptr || order == nullptr)) return DP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(choice) & (choice_bits / 8 - 1)) != 0 ||
+      ((reinterpret_cast<uintptr_t>(offsets) | reinterpret_cast<uintptr_t>(row_of) | reinterpret_cast<uintptr_t>(order) |
+        reinterpret_cast<uintptr_t>(workspace)) & 3) != 0)
+    return DP_ERR_ALIGNMENT;
+  const SortShape s = sort_shape(pairs, E);
+  if (s.blocks > 1 && (workspace == nullptr || workspace_bytes < static_cast<size_t>(s.blocks) * (E + 1) * 4))
+    return DP_ERR_WORKSPACE;
+  DeviceContext ctx;
+  const dp_status st = device_context(&ctx);
+  if (st != DP_OK) return st;
+  cudaStream_t str = static_cast<cudaStream_t>(stream);
+  SortArgs a = {};
+  a.choice = choice, a.wide = choice_bits == 64, a.P = static_cast<int32_t>(pairs), a.E = static_cast<int32_t>(E);
+  a.per_block = s.per_block, a.per_warp = s.per_warp, a.counts = static_cast<int32_t*>(workspace);
+  a.offsets = offsets, a.row_of = row_of, a.order = order;
+  if (s.blocks > 1) {
+    sort_count_kernel<<<s.blocks, s.warps * 32, s.smem, str>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return DP_ERR_LAUNCH;
+  }
+  sort_place_kernel<<<s.blocks, s.warps * 32, s.smem, str>>>(a);
+  return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+}
+
+extern "C" dp_status dp_expert_gather(const void* x, int64_t ldx, int x_f32, const int32_t* row_of, void* rows, int64_t ldr,
+                                      int64_t T, int64_t k, int64_t C, dp_stream stream) {
+  using namespace dp;
+  if (!flag(x_f32)) return DP_ERR_INVALID_ARG;
+  dp_status st = check_pairs(row_of, T, k, C);
+  if (st == DP_OK) st = check_operand(x, T, C, &ldx, x_f32 ? 4 : 2);
+  if (st == DP_OK) st = check_operand(rows, T, C, &ldr, x_f32 ? 4 : 2);
+  if (st != DP_OK) return st;
+  DeviceContext ctx;
+  if ((st = device_context(&ctx)) != DP_OK) return st;
+  if (T == 0) return DP_OK;
+  RowArgs a = row_args(row_of, nullptr, T, k, C, ctx);
+  a.x = x, a.ldx = ldx, a.out = rows, a.ldo = ldr;
+  by_bool(x_f32, [&](auto f) {
+    gather_kernel<decltype(f)::value><<<token_blocks(a), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  });
+  return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+}
+
+extern "C" dp_status dp_expert_combine(const void* y, int64_t ldy, int y_f32, const int32_t* row_of, const float* gates,
+                                       const void* add, int64_t ld_add, void* out, int64_t ldo, dp_out_dtype out_dtype,
+                                       int64_t T, int64_t k, int64_t C, dp_stream stream) {
+  using namespace dp;
+  const int code = static_cast<int>(out_dtype);
+  if (!flag(y_f32) || !flag(code)) return DP_ERR_INVALID_ARG;
+  dp_status st = check_pairs(row_of, T, k, C);
+  if (st == DP_OK) st = check_operand(y, T, C, &ldy, y_f32 ? 4 : 2);
+  if (st == DP_OK) st = check_operand(out, T, C, &ldo, code ? 4 : 2);
+  if (st == DP_OK && add != nullptr) st = check_operand(add, T, C, &ld_add, code ? 4 : 2);
+  if (st != DP_OK) return st;
+  if ((reinterpret_cast<uintptr_t>(gates) & 3) != 0) return DP_ERR_ALIGNMENT;
+  DeviceContext ctx;
+  if ((st = device_context(&ctx)) != DP_OK) return st;
+  if (T == 0) return DP_OK;
+  RowArgs a = row_args(row_of, gates, T, k, C, ctx);
+  a.x = y, a.ldx = ldy, a.add = add, a.ld_add = ld_add, a.out = out, a.ldo = ldo;
+  by_bool(y_f32, [&](auto yf) {
+    by_bool(code, [&](auto of) {
+      combine_kernel<decltype(yf)::value, decltype(of)::value><<<token_blocks(a), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    });
+  });
+  return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+}
+
+extern "C" dp_status dp_expert_combine_bwd(const void* dout, int64_t ldd, int dout_f32, const void* y, int64_t ldy, int y_f32,
+                                           const int32_t* row_of, const float* gates, void* dy, int64_t ld_dy,
+                                           dp_out_dtype dy_dtype, float* dgates, int64_t T, int64_t k, int64_t C,
+                                           dp_stream stream) {
+  using namespace dp;
+  const int code = static_cast<int>(dy_dtype);
+  if (!flag(dout_f32) || !flag(y_f32) || !flag(code)) return DP_ERR_INVALID_ARG;
+  dp_status st = check_pairs(row_of, T, k, C);
+  if (st == DP_OK) st = check_operand(dout, T, C, &ldd, dout_f32 ? 4 : 2);
+  if (st == DP_OK) st = check_operand(y, T, C, &ldy, y_f32 ? 4 : 2);
+  if (st == DP_OK) st = check_operand(dy, T, C, &ld_dy, code ? 4 : 2);
+  if (st != DP_OK) return st;
+  if (T > 0 && (gates == nullptr || dgates == nullptr)) return DP_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(gates) | reinterpret_cast<uintptr_t>(dgates)) & 3) != 0) return DP_ERR_ALIGNMENT;
+  DeviceContext ctx;
+  if ((st = device_context(&ctx)) != DP_OK) return st;
+  if (T == 0) return DP_OK;
+  RowArgs a = row_args(row_of, gates, T, k, C, ctx);
+  a.x = dout, a.ldx = ldd, a.y = y, a.ld_y = ldy, a.out = dy, a.ldo = ld_dy, a.dgates = dgates;
+  by_bool(dout_f32, [&](auto df) {
+    by_bool(y_f32, [&](auto yf) {
+      by_bool(code, [&](auto of) {
+        combine_bwd_kernel<decltype(df)::value, decltype(yf)::value, decltype(of)::value>
+            <<<token_blocks(a), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+      });
+    });
+  });
+  return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+}

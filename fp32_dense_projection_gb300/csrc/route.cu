@@ -1,0 +1,238 @@
+// The router's choice: the k largest of each token's E logits (FP32) and their gates, and the
+// gradient of the gates with respect to the logits.
+//   chosen by value, the lowest index first among equals; a logit of -infinity is a closed expert:
+//   it is never chosen (choice -1, gate 0, where fewer than k are open)
+//   gate_j = exp(l_j - m) / sum exp(l - m), the sum over the chosen or over all experts
+// Gradient, with s = sum_j dg_j gate_j over the chosen:
+//   over the chosen:  dl_e = gate_e (dg_e - s), 0 for the others
+//   over all:         dl_e = p_e ([e chosen] dg_e - s)
+//
+// Bound: the logits' bytes; a few rows are latency.  One warp a token holds its logits in
+// registers, so they are read once; a choice is two warp-wide integer reductions (the largest key,
+// then the lowest index that has it).  Keys order floats as integers: -0 as +0, NaN above all.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "api_internal.h"
+
+namespace dp {
+namespace {
+
+constexpr int kMaxRouted = 1024, kMaxChosen = 32;
+constexpr int kWarps = 8;  // tokens a block has at a time
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct RouteArgs {
+  const float* logits;
+  int64_t ld;
+  int64_t T;
+  int32_t E, k, renormalize;
+  float* gates;
+  int32_t* choice;
+  const float* dgates;
+  float* dlogits;
+  int64_t ldd;
+};
+
+// An integer that orders as the float does; above 0 for every float.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) return 0xFFFFFFFFu;
+  const uint32_t b = __float_as_uint(x + 0.0f);  // (-0 becomes +0)
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ float key_value(uint32_t key) {
+  if (key == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+
+constexpr uint32_t kClosed = 0x007FFFFFu;  // order_key(-infinity)
+
+template <int VPL>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteArgs a) {
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const float* p = a.logits + t * a.ld;
+  uint32_t key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = e < a.E ? order_key(__ldg(p + e)) : 0;
+  }
+  uint32_t all = 0;  // the largest key of the row
+  float total = 0.0f;
+  if (!a.renormalize) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) all = max(all, key[i]);
+    all = __reduce_max_sync(kAll, all);
+    const float m = key_value(all);
+    if (all != kClosed) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (key[i] > kClosed) total += expf(key_value(key[i]) - m);
+      total = warp_sum(total);
+    }
+  }
+  uint32_t mine = 0;  // lane j: the j-th choice's key and index
+  int at = -1;
+  uint32_t first = 0;
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
+    best = __reduce_max_sync(kAll, best);
+    if (best <= kClosed) break;
+    uint32_t index = kAll;
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; --i)
+      if (key[i] == best) index = static_cast<uint32_t>(lane + 32 * i);
+    index = __reduce_min_sync(kAll, index);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (index == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
+    if (j == 0) first = best;
+    if (lane == j) mine = best, at = static_cast<int>(index);
+  }
+  float e = at >= 0 ? expf(key_value(mine) - key_value(first)) : 0.0f;
+  if (a.renormalize) total = warp_sum(e);
+  if (lane < a.k) {
+    a.gates[t * a.k + lane] = at >= 0 ? e / total : 0.0f;
+    a.choice[t * a.k + lane] = at;
+  }
+}
+
+template <int VPL>
+__global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_constant__ RouteArgs a) {
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  int at = -1;
+  float g = 0.0f, dg = 0.0f;
+  if (lane < a.k) {
+    at = a.choice[t * a.k + lane];
+    if (at < 0 || at >= a.E) at = -1;
+    if (at >= 0) g = a.gates[t * a.k + lane], dg = a.dgates[t * a.k + lane];
+  }
+  const float s = warp_sum(at >= 0 ? g * dg : 0.0f);
+  float d[VPL];
+  if (a.renormalize) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) d[i] = 0.0f;
+  } else {
+    const float* p = a.logits + t * a.ld;
+    float l[VPL], m = -INFINITY, total = 0.0f;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane + 32 * i;
+      l[i] = e < a.E ? __ldg(p + e) : -INFINITY;
+      nan = nan || l[i] != l[i];
+      m = fmaxf(m, l[i]);
+    }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, w));
+    if (__any_sync(kAll, nan)) m = __uint_as_float(0x7FC00000u);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      l[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - m);
+      total += l[i];
+    }
+    total = warp_sum(total);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) d[i] = l[i] == 0.0f ? 0.0f : -(l[i] / total) * s;
+  }
+  const float own = a.renormalize ? g * (dg - s) : g * dg;
+  for (int j = 0; j < a.k; ++j) {
+    const int e = __shfl_sync(kAll, at, j);
+    const float v = __shfl_sync(kAll, own, j);
+    if (e < 0) continue;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (e == lane + 32 * i) d[i] += v;
+  }
+  float* out = a.dlogits + t * a.ldd;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 32 * i;
+    if (e < a.E) out[e] = d[i];
+  }
+}
+
+template <typename F>
+void by_width(int64_t E, F f) {
+  if (E <= 64)
+    f(std::integral_constant<int, 2>());
+  else if (E <= 256)
+    f(std::integral_constant<int, 8>());
+  else if (E <= 512)
+    f(std::integral_constant<int, 16>());
+  else
+    f(std::integral_constant<int, 32>());
+}
+
+dp_status check_route(const float* logits, int64_t* ld, int64_t T, int64_t E, int64_t k, int renormalize) {
+  if (T < 0 || E < 1 || k < 1 || k > E || (renormalize != 0 && renormalize != 1)) return DP_ERR_INVALID_ARG;
+  if (E > kMaxRouted || k > kMaxChosen || T > 0x7FFFFFFF) return DP_ERR_UNSUPPORTED;
+  if (*ld == 0) *ld = E;
+  if (*ld < E || (T > 0 && logits == nullptr)) return DP_ERR_INVALID_ARG;
+  if (*ld > (int64_t{1} << 36)) return DP_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(logits) & 3) != 0) return DP_ERR_ALIGNMENT;
+  return DP_OK;
+}
+
+}  // namespace
+}  // namespace dp
+
+extern "C" dp_status dp_route_topk(const float* logits, int64_t ld, float* gates, int32_t* choice, int64_t T, int64_t E,
+                                   int64_t k, int renormalize, dp_stream stream) {
+  using namespace dp;
+  dp_status st = check_route(logits, &ld, T, E, k, renormalize);
+  if (st != DP_OK) return st;
+  if (T > 0 && (gates == nullptr || choice == nullptr)) return DP_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(gates) | reinterpret_cast<uintptr_t>(choice)) & 3) != 0) return DP_ERR_ALIGNMENT;
+  DeviceContext ctx;
+  if ((st = device_context(&ctx)) != DP_OK) return st;
+  if (T == 0) return DP_OK;
+  RouteArgs a = {};
+  a.logits = logits, a.ld = ld, a.T = T, a.E = static_cast<int32_t>(E), a.k = static_cast<int32_t>(k);
+  a.renormalize = renormalize, a.gates = gates, a.choice = choice;
+  const unsigned grid = static_cast<unsigned>((T + kWarps - 1) / kWarps);
+  by_width(E, [&](auto v) {
+    route_kernel<decltype(v)::value><<<grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  });
+  return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+}
+
+extern "C" dp_status dp_route_topk_bwd(const float* dgates, const float* logits, int64_t ld, const float* gates,
+                                       const int32_t* choice, float* dlogits, int64_t ldd, int64_t T, int64_t E, int64_t k,
+                                       int renormalize, dp_stream stream) {
+  using namespace dp;
+  // (over the chosen, the gates say all: the logits are not read and may be null)
+  dp_status st = check_route(renormalize ? dlogits : logits, &ld, T, E, k, renormalize);
+  if (st == DP_OK) st = check_route(dlogits, &ldd, T, E, k, renormalize);
+  if (st != DP_OK) return st;
+  if (T > 0 && (gates == nullptr || choice == nullptr || dgates == nullptr)) return DP_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(gates) | reinterpret_cast<uintptr_t>(choice) | reinterpret_cast<uintptr_t>(dgates)) & 3) != 0)
+    return DP_ERR_ALIGNMENT;
+  DeviceContext ctx;
+  if ((st = device_context(&ctx)) != DP_OK) return st;
+  if (T == 0) return DP_OK;
+  RouteArgs a = {};
+  a.logits = logits, a.ld = ld, a.T = T, a.E = static_cast<int32_t>(E), a.k = static_cast<int32_t>(k);
+  a.renormalize = renormalize, a.gates = const_cast<float*>(gates), a.choice = const_cast<int32_t*>(choice);
+  a.dgates = dgates, a.dlogits = dlogits, a.ldd = ldd;
+  const unsigned grid = static_cast<unsigned>((T + kWarps - 1) / kWarps);
+  by_width(E, [&](auto v) {
+    route_bwd_kernel<decltype(v)::value><<<grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  });
+  return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+}

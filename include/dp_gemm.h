@@ -397,6 +397,96 @@ typedef struct dp_adamw_hyper {
 dp_status dp_adamw_step(const dp_adamw_tensor* tensors, int64_t count, int state_bits, const dp_adamw_hyper* hyper,
                         dp_stream stream);
 
+/* ------------------------------------------------------------------- layer norm */
+/* Over each row of x [T][C] (BF16, or FP32 with x_f32):
+ *   mu = mean(x), rs = 1 / sqrt(mean((x - mu)^2) + eps), h = (x - mu) rs, y = h weight + bias
+ * weight, bias: [C], both FP32 (weight_f32) or both BF16; null: 1 and 0.  mean and rstd [T] receive mu
+ * and rs, which the backward pass reads.  FP32 arithmetic, y rounded once.
+ * Backward, with g = dy weight (dy BF16, or FP32 with dy_f32):
+ *   dx = rs (g - mean(g) - h mean(g h)),  dw = sum_t dy h,  db = sum_t dy   (dw, db FP32 [C])
+ * dw and db may both be null (then no workspace is needed either); T == 0 makes them zero.  Their
+ * sums are deterministic.  C a multiple of 8, at most 16384.  An infinity or a NaN in a row of x
+ * reaches that row's outputs, and dw and db, only.  Outputs must not overlap inputs. */
+dp_status dp_layer_norm_fwd(const void* x, int64_t ldx, int x_f32, const void* weight, const void* bias, int weight_f32,
+                            double eps, void* y, int64_t ldy, dp_out_dtype out, float* mean, float* rstd,
+                            int64_t T, int64_t C, dp_stream stream);
+dp_status dp_layer_norm_bwd(const void* dy, int64_t ldg, int dy_f32, const void* x, int64_t ldx, int x_f32,
+                            const float* mean, const float* rstd, const void* weight, int weight_f32, void* dx,
+                            int64_t ld_dx, dp_out_dtype out, float* dw, float* db, int64_t T, int64_t C,
+                            void* workspace, size_t workspace_bytes, dp_stream stream);
+/* Workspace of the backward pass (sm_count <= 0: the current device's). */
+dp_status dp_layer_norm_workspace_size(int64_t T, int64_t C, int sm_count, size_t* bytes);
+
+/* ---------------------------------------------------- the router's choice of experts */
+/* The k largest of each token's E logits (FP32, router_fwd's output), by value and then by the
+ * lowest index, and their gates (both [T][k]):
+ *   gate_j = exp(l_j - m) / sum exp(l - m)   over the k chosen (renormalize) or over all E
+ * A logit of -infinity is a closed expert: it is never chosen, and where fewer than k are open the
+ * rest of the row has choice -1 and gate 0.  A NaN counts as the largest value; a row with NaN or
+ * +infinity has NaN gates.  E at most 1024, k at most 32 (and E).
+ * Gradient of the logits [T][E] from that of the gates, with s = sum_j dgate_j gate_j:
+ *   over the chosen: gate_e (dgate_e - s), 0 elsewhere; over all: p_e ([e chosen] dgate_e - s)
+ * Choices outside [0, E) take no part, whatever their dgates.  logits are read only without
+ * renormalize and may be null with it. */
+dp_status dp_route_topk(const float* logits, int64_t ld, float* gates, int32_t* choice, int64_t T, int64_t E, int64_t k,
+                        int renormalize, dp_stream stream);
+dp_status dp_route_topk_bwd(const float* dgates, const float* logits, int64_t ld, const float* gates, const int32_t* choice,
+                            float* dlogits, int64_t ld_d, int64_t T, int64_t E, int64_t k, int renormalize, dp_stream stream);
+
+/* ------------------------------------------------ tokens to their experts and back */
+/* Pair p = t k + j is token t's j-th choice.  The sorted buffer has T k rows.
+ * Sort: offsets [E + 1] as the grouped products read them, row_of [pairs] the row of each pair,
+ *   order [pairs] the pair of each row; pairs of one expert keep their order.  Pairs whose choice
+ *   is outside [0, E) have no expert: they follow the last group (which the products leave out),
+ *   and their row r is held as ~r, below zero.  choice: int32 or int64 (choice_bits).  At most 1024
+ *   experts.
+ * Gather: rows[row_of[t][j]] = x[t], zeros for pairs without an expert.
+ * Combine: out[t] = add[t] + sum_j gate[t][j] y[row_of[t][j]] over the pairs that have an expert, in
+ *   FP32 in the order of j, rounded once.  gates [T][k] FP32 or null (1: the gradient of gather); add of
+ *   out's type, or null.
+ * Its gradient: dy[row_of[t][j]] = gate[t][j] dout[t] (zeros without an expert), dgates[t][j] =
+ *   dout[t] . y[row_of[t][j]] (0 without).
+ * An entry of row_of that names no row of the buffer is left out and reported as
+ * DP_ERR_INVALID_ARG by dp_device_error(); two pairs must not name one row.  C a multiple of 8.
+ * Outputs must not overlap inputs.  Deterministic. */
+dp_status dp_expert_sort(const void* choice, int choice_bits, int64_t pairs, int64_t E, int32_t* offsets, int32_t* row_of,
+                         int32_t* order, void* workspace, size_t workspace_bytes, dp_stream stream);
+dp_status dp_expert_sort_workspace_size(int64_t pairs, int64_t E, size_t* bytes);
+dp_status dp_expert_gather(const void* x, int64_t ldx, int x_f32, const int32_t* row_of, void* rows, int64_t ld_rows,
+                           int64_t T, int64_t k, int64_t C, dp_stream stream);
+dp_status dp_expert_combine(const void* y, int64_t ldy, int y_f32, const int32_t* row_of, const float* gates,
+                            const void* add, int64_t ld_add, void* out, int64_t ldo, dp_out_dtype out_dtype,
+                            int64_t T, int64_t k, int64_t C, dp_stream stream);
+dp_status dp_expert_combine_bwd(const void* dout, int64_t ldd, int dout_f32, const void* y, int64_t ldy, int y_f32,
+                                const int32_t* row_of, const float* gates, void* dy, int64_t ld_dy, dp_out_dtype dy_dtype,
+                                float* dgates, int64_t T, int64_t k, int64_t C, dp_stream stream);
+
+/* -------------------------------------------- 4-bit weights, a scale per group of a row */
+/* w[n][k] = (q - z) s for groups of 32, 64 or 128 elements along k (K a multiple of the group):
+ *   q  [rows][K / 2] bytes, two codes 0..15 each, the even k in the low half
+ *   s  [rows][K / group], FP32 (s_f32) or BF16
+ *   z  [rows][K / group] bytes (their low four bits), or null: 8
+ * all packed; experts follow one another as rows.
+ * Quantise (BF16, or FP32 with w_f32): without z, s = max(max|w| / 7, 1e-30); with z, over the range
+ *   [lo, hi] of the group and 0, s = max((hi - lo) / 15, 1e-30) and z = rn(-lo / s); s is rounded to its type
+ *   first, then q = min(max(rn(w / s) + z, 0), 15).  A group that holds a NaN gets a NaN scale.
+ * Dequantise: w = (q - z) s, rounded once.
+ * Products of few rows (decoding), X [T][K] BF16: Y[t][n] = sum_k X[t][k] w[n][k], the whole or by
+ *   expert with offsets as in dp_gemm_fwd_grouped (rows outside all groups are zero).  Each group's
+ *   sum meets its scale in FP32.  Right for any T and fast while the weights' bytes bound it (a few
+ *   dozen rows, or as many per expert); more rows want dp_int4_dequantize and dp_gemm_fwd.  N a
+ *   multiple of 8, K at most 32768.  Deterministic; one launch, no workspace. */
+dp_status dp_int4_quantize(const void* w, int64_t ldw, int w_f32, int64_t rows, int64_t K, int64_t group, void* q, void* s,
+                           int s_f32, void* z, dp_stream stream);
+dp_status dp_int4_dequantize(const void* q, const void* s, int s_f32, const void* z, int64_t rows, int64_t K, int64_t group,
+                             void* w, int64_t ldw, dp_out_dtype out, dp_stream stream);
+dp_status dp_gemm_fwd_int4(const void* X, int64_t ldx, const void* Wq, const void* Ws, int s_f32, const void* Wz,
+                           int64_t group, void* Y, int64_t ldy, int64_t T, int64_t N, int64_t K, dp_out_dtype out,
+                           dp_stream stream);
+dp_status dp_gemm_fwd_int4_grouped(const void* X, int64_t ldx, const void* Wq, const void* Ws, int s_f32, const void* Wz,
+                                   int64_t group, const void* offsets, int offset_bits, void* Y, int64_t ldy,
+                                   int64_t E, int64_t T, int64_t N, int64_t K, dp_out_dtype out, dp_stream stream);
+
 /* ------------------------------------------------------------ planning, misc */
 /* Tuning and test overrides.  They are read from the environment only in a
  * process that has DP_TUNING set when the library first plans a call; such a
@@ -523,7 +613,8 @@ dp_status dp_init(int device);
 
 /* Debug read-out: synchronise the current device and report whether any kernel
  * of this library gave up waiting (DP_ERR_TIMEOUT), or else was given group offsets
- * that decrease or leave [0, T] (DP_ERR_INVALID_ARG), since the last clear.
+ * that decrease or leave [0, T], or rows of pairs outside their buffer (DP_ERR_INVALID_ARG), since
+ * the last clear.
  * `clear` != 0 resets the flag.  Not for use inside stream capture. */
 dp_status dp_device_error(int clear);
 
