@@ -36,6 +36,11 @@ dp_status check_operand(const void* p, int64_t rows, int64_t cols, int64_t* ld, 
 bool encode_operand(CUtensorMap* map, const void* ptr, CUtensorMapDataType type, int esize, int64_t rows, int64_t cols,
                     int64_t ld, int64_t batch, int64_t bstride, uint32_t box_cols, uint32_t box_rows);
 
+// Tiled tensor map over rows of row_bytes bytes (packed; a multiple of 16), boxes of 128 bytes x box_rows with 128-byte
+// swizzle and zero fill outside; depth > 1 (rows of whole 128 bytes): of that many neighbouring 128-byte
+// pieces, [piece][row][128].
+bool encode_bytes(CUtensorMap* map, const void* ptr, int64_t rows, int64_t row_bytes, uint32_t box_rows, uint32_t depth);
+
 // Shared memory of the products with 4-bit weights (for the current device).
 cudaError_t set_attributes_int4();
 

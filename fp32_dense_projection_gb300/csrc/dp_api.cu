@@ -842,6 +842,19 @@ bool encode_operand(CUtensorMap* map, const void* ptr, CUtensorMapDataType type,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_bytes(CUtensorMap* map, const void* ptr, int64_t rows, int64_t row_bytes, uint32_t box_rows, uint32_t depth) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || (depth > 1 && row_bytes % 128 != 0)) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(depth > 1 ? 128 : row_bytes), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(row_bytes / 128)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), 128};
+  const cuuint32_t box[3] = {128, box_rows, depth};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, depth > 1 ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace dp
 
 // =================================================================== C ABI

@@ -4,18 +4,24 @@
 //
 // Products of few rows, plain or grouped by expert:  Y[t][n] = sum over groups of s sum x[t][k] (q - z)
 //
-// Bound: the codes' bytes from HBM.  A CTA takes R rows of weights (16, 32 or 64) and a slab of the
-// contraction, and asks for all of its codes at once with one bulk copy a row; several such CTAs
-// share an SM, so there is nothing to pipeline by hand.  The CTAs of the slabs of one tile are a
-// cluster and add their sums in rank order through shared memory.  A warp multiplies 16 rows of
-// weights (the MMA's 16 rows) with 8 tokens (its 8 columns):
-// - codes become BF16 by one OR (0x4300 | q is 128 + q) and one exact subtraction of 128 + z;
+// Bound: the codes' bytes from HBM, and beside them the instructions that unpack them.  A unit of work is
+// 16 rows of weights (the MMA's rows) times the tokens of their group (its 8 columns, once or twice).
+// One CTA an SM goes over a contiguous range of units, so the tokens stay in shared memory while the
+// codes stream past.  Teams of warps take the units in turn (four teams of four warps, or one of sixteen
+// where an SM has few units), each team through a ring of its own: a ring that they shared would be
+// read by one team or another, and a barrier's parity does not tell a round from the one after next.
+// A team's warps take blocks of 128 in turn and once a unit add their sums in order.  Four more
+// warps ask for the codes by TMA, as far ahead as the rings reach, and bring scales and zero points into
+// the form that the products read.  (A bulk copy for each row, 1 KB at a time, reached 3.1 TB/s without
+// any products behind it.)
+// - four bits at the low end of a BF16's mantissa, or the four above them, are the subnormal (or
+//   first normal) number q 2^-133 or q 2^-129: one AND and one exact fused multiply-add make
+//   (q - z) / 64 of two codes;
 // - the MMA's sums run over one group and meet the group's scale in FP32, so the product is as
-//   exact as with weights expanded in FP32.
-// The order of the contraction within a group is free as long as both operands agree: a thread takes
-// neighbouring codes, the words w of 8 codes, and reads pairs (i, i + 4) of a word with one mask;
-// x is laid out in shared memory in that order, so that a thread's operands of two MMAs are 16
-// neighbouring bytes.
+//   exact as with weights expanded in FP32 (sums below 2^-120 lose bits to the factor 64).
+// The order of the contraction within a group is free as long as both operands agree: the four threads
+// of a row take one word of 8 codes each, and each reads pairs (i, i + 4) of its word with one mask;
+// x is laid out in shared memory in the pairs' order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,21 +37,31 @@ namespace {
 
 constexpr int kMaxInt4Experts = 1024;
 constexpr int64_t kMaxInt4K = 32768;
-constexpr int kThreads = 256, kWarpCount = kThreads / 32;
-constexpr int kMaxSlabs = 8;  // CTAs of a cluster
+constexpr int kUserWarps = 16, kHelpers = 4;  // the warps that multiply, and those that load for them
+constexpr int kUsers = kUserWarps * 32, kThreads = kUsers + kHelpers * 32, kWarps = kThreads / 32;
+constexpr int kAhead = 3;    // stages whose scales are on their way
+constexpr int kRows = 16;    // of weights in a unit
+constexpr int kPiece = 256;  // contraction elements in 128 bytes of codes, the width of a swizzled row
+constexpr int kPieceBytes = kRows * 128;
+constexpr int kRedStride = kRows + 4;
+constexpr int kMostStages = 8;  // of a ring
+// Contraction elements of a stage: one or two blocks of 128 a warp (one with groups of 32, whose scales are many).
+constexpr int least_chunk(int teams) { return kUserWarps / teams * 128; }
+constexpr int most_chunk(int teams, int G) { return teams == 1 || G == 32 ? least_chunk(teams) : 2 * least_chunk(teams); }
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct ProductArgs {
   const void* x;
   int64_t ldx;
-  const uint8_t* q;  // [E][N][K / 2]
   const void* s;     // [E][N][K / G]
   const uint8_t* z;  // the same shape, or null
   int s_f32;
+  int pieces;  // 1: the codes' map is [rows][K / 2], 128 bytes wide boxes; else [pieces][rows][128] with a stage a box
   const void* offsets;  // null: one group of all T rows
   int offsets64;
   int32_t E, T, N, K;
-  int32_t R, slab, slabs, x_rows;  // rows of weights, contraction elements and CTAs a tile; rows of x in shared memory
+  int32_t x_rows, chunk, stages;  // tokens a pass; contraction elements of a stage, stages of a ring
+  int32_t tiles;                  // ceil(N / 16)
   void* out;
   int64_t ldo;
   int out_f32;
@@ -53,32 +69,24 @@ struct ProductArgs {
   uint64_t wait_ns;
 };
 
-// Shared memory of a CTA.
+// Shared memory of a CTA, from a multiple of 1024 on: codes of all rings' stages ([piece][16 rows][128
+// bytes], swizzled by TMA, so that a piece's 16 bytes of 8 rows lie in different banks), their scales, x, sums, table.
 struct Layout {
-  int32_t code_stride, x_stride, groups;
-  int32_t x, scale, zero, red, red_stride, bytes;  // (codes at 0)
+  int32_t code_bytes, meta, meta_bytes;  // of a stage
+  int32_t x_stride, x, red, table, bytes;
 };
 
-__host__ __device__ inline Layout layout_of(int G, int R, int slab, int x_rows, int tokens) {
+__host__ __device__ inline Layout layout_of(int G, int K, int teams, int chunk, int stages, int x_rows, int tokens, int experts) {
   Layout l;
-  // bytes of a row, padded so that the rows that a warp reads at a time lie in different banks: a
-  // thread reads G / 8 bytes, the four threads of a row G / 2
-  l.code_stride = (slab / 2 + 127) / 128 * 128 + G / 2;
-  l.x_stride = slab * 2 + 64;
-  l.groups = slab / G;
-  l.red_stride = R + 4;
-  l.x = R * l.code_stride;
-  l.scale = l.x + x_rows * l.x_stride;
-  l.zero = l.scale + R * l.groups * 4;
-  l.red = (l.zero + R * l.groups * 2 + 15) / 16 * 16;
-  l.bytes = l.red + kWarpCount / (R / 16) * tokens * l.red_stride * 4;
+  l.code_bytes = chunk / kPiece * kPieceBytes;
+  l.meta_bytes = chunk / G * (kRows + 1) * 8;
+  l.x_stride = (K + 127) / 128 * 256 + 64;  // (what a warp reads of two rows at a time lies in different banks)
+  l.meta = teams * stages * l.code_bytes;
+  l.x = (l.meta + teams * stages * l.meta_bytes + 15) / 16 * 16;
+  l.red = l.x + x_rows * l.x_stride;
+  l.table = l.red + kUserWarps * tokens * kRedStride * 4;
+  l.bytes = l.table + (experts > 0 ? (experts + 1) * 8 + experts * 2 : 0);
   return l;
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(bar)
-               : "memory");
 }
 
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -88,63 +96,141 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Codes i and i + 4 of a word of 8, less their zero point (`zero`: twice 128 + z in BF16; exact).
-__device__ __forceinline__ uint32_t code_pair(uint32_t word, int i, uint32_t zero) {
-  const uint32_t v = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&zero));
-  return *reinterpret_cast<const uint32_t*>(&d);
+__device__ __forceinline__ void mma_16x8x16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                                 uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// Where the 8 elements of chunk c (0..15) of a block of 128 lie in shared memory: the chunk that
-// thread t of a row's four needs for its word j is at 4 j + t.
-template <int G>
-__device__ __forceinline__ int chunk_place(int c) {
-  if (G == 128) return (c & 3) * 4 + (c >> 2);
-  if (G == 64) return ((c >> 3) * 2 + (c & 1)) * 4 + ((c >> 1) & 3);
-  return c;
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
 
-__device__ __forceinline__ float ld_float_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+// (q - z) / 64 for the codes i and i + 4 of a word of 8, as pairs p[i] (`zero`: twice -z / 64 in BF16).
+__device__ __forceinline__ void code_pairs(uint32_t word, uint32_t zero, uint32_t (&p)[4]) {
+  constexpr uint32_t kLow = 0x7F007F00u, kHigh = 0x7D007D00u;  // 2^127, 2^123
+  const uint32_t upper = word >> 8;
+  p[0] = fma_bf16x2(word & 0x000F000Fu, kLow, zero);
+  p[1] = fma_bf16x2(word & 0x00F000F0u, kHigh, zero);
+  p[2] = fma_bf16x2(upper & 0x000F000Fu, kLow, zero);
+  p[3] = fma_bf16x2(upper & 0x00F000F0u, kHigh, zero);
 }
 
-// The group's rows [lo, hi): offsets clamped to [0, T] and to the running maximum; all threads
-// call it.  What had to be clamped is reported by the CTAs of the first tile.
-__device__ __forceinline__ void group_rows(const ProductArgs& a, int e, int32_t& lo, int32_t& hi, int32_t& first, int32_t& last) {
-  __shared__ int32_t most[3][kWarpCount];
+// The groups' table: start[i], offset i clamped to [0, T] and to the running maximum; list, the experts
+// that have rows; passes[i], the passes over tokens of those before the i-th (and of all, behind
+// the last).  What had to be clamped is reported.  All threads call it.  Returns all passes.
+struct Table {
+  int32_t *start, *passes;
+  uint16_t* list;
+  int live;
+};
+
+__device__ __forceinline__ int build_table(const ProductArgs& a, Table& tab) {
+  __shared__ int32_t most[kWarps], rows[kWarps], count[kWarps];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  auto at = [&](int i) {
-    return a.offsets64 ? static_cast<const int64_t*>(a.offsets)[i] : static_cast<int64_t>(static_cast<const int32_t*>(a.offsets)[i]);
-  };
-  int32_t m[3] = {0, 0, 0};  // maxima over offsets up to e, up to e + 1, all
   bool bad = false;
-  int64_t before = 0;
-  for (int i = tid; i <= a.E; i += kThreads) {
-    const int64_t raw = at(i);
-    if (i > 0) before = at(i - 1);
-    bad = bad || raw < 0 || raw > a.T || (i > 0 && raw < before);
-    const int32_t v = static_cast<int32_t>(raw < 0 ? 0 : raw > a.T ? a.T : raw);
-    m[2] = max(m[2], v);
-    if (i <= e + 1) m[1] = max(m[1], v);
-    if (i <= e) m[0] = max(m[0], v);
+  int32_t carry = 0;
+  for (int i0 = 0; i0 <= a.E; i0 += kThreads) {
+    const int i = i0 + tid;
+    int32_t v = 0;
+    if (i <= a.E) {
+      const int64_t raw = a.offsets64 ? static_cast<const int64_t*>(a.offsets)[i] : static_cast<const int32_t*>(a.offsets)[i];
+      v = static_cast<int32_t>(raw < 0 ? 0 : raw > a.T ? a.T : raw);
+      bad = bad || raw != v;
+    }
+    int32_t top = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(kAll, top, d);
+      if (lane >= d) top = max(top, o);
+    }
+    if (lane == 31) most[warp] = top;
+    __syncthreads();
+    top = max(top, carry);
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) top = max(top, most[w]);
+      carry = max(carry, most[w]);
+    }
+    if (i <= a.E) {
+      bad = bad || v < top;
+      tab.start[i] = top;
+    }
+    __syncthreads();
   }
+  if (bad && blockIdx.x == 0) atomicOr(a.fault, kFaultOffsets);
+  int live = 0, total = 0;
+  for (int e0 = 0; e0 < a.E; e0 += kThreads) {
+    const int e = e0 + tid, n = e < a.E ? tab.start[e + 1] - tab.start[e] : 0;
+    const int own = (n + a.x_rows - 1) / a.x_rows;
+    const uint32_t mask = __ballot_sync(kAll, n > 0);
+    int incl = own;
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    m[i] = __reduce_max_sync(kAll, m[i]);
-    if (lane == 0) most[i][warp] = m[i];
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kAll, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) rows[warp] = __popc(mask), count[warp] = incl;
+    __syncthreads();
+    int at = live + __popc(mask & ((1u << lane) - 1)), before = total + incl - own;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += rows[w], before += count[w];
+      live += rows[w], total += count[w];
+    }
+    if (n > 0) tab.list[at] = static_cast<uint16_t>(e), tab.passes[at] = before;
+    __syncthreads();
   }
-  if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.fault, kFaultOffsets);
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 3; ++i)
-#pragma unroll
-    for (int w = 0; w < kWarpCount; ++w) m[i] = max(m[i], most[i][w]);
-  lo = m[0], hi = m[1], last = m[2];
-  const int64_t raw = at(0);
-  first = static_cast<int32_t>(raw < 0 ? 0 : raw > a.T ? a.T : raw);
+  if (tid == 0) tab.passes[live] = total;
+  tab.live = live;
+  return total;
 }
+
+// A CTA's range of units: passes (one over the tokens of an expert, x_rows at a time) and, of each, tiles.
+struct Pass {
+  int index, tile, end;        // the pass; its tiles in the range
+  int last_index, last_end;    // the range's last pass, and where in it the range ends
+  int at, e, tok, count;       // the expert's place in the list, the expert, the pass's first token and their number
+
+  __device__ __forceinline__ void enter(const ProductArgs& a, const Table& tab) {
+    end = index == last_index ? last_end : a.tiles;
+    int from = 0, hi = a.T, done = index;
+    e = 0;
+    if (a.offsets != nullptr) {
+      e = tab.list[at];
+      from = tab.start[e], hi = tab.start[e + 1];
+      done = index - tab.passes[at];
+    }
+    tok = from + done * a.x_rows;
+    count = min(a.x_rows, hi - tok);
+  }
+  __device__ __forceinline__ Pass(const ProductArgs& a, const Table& tab, int64_t from, int64_t to) {
+    index = static_cast<int>(from / a.tiles), tile = static_cast<int>(from % a.tiles);
+    last_index = static_cast<int>((to - 1) / a.tiles), last_end = static_cast<int>((to - 1) % a.tiles) + 1;
+    at = 0;
+    if (a.offsets != nullptr)
+      for (int step = 512; step > 0; step >>= 1)  // (at most 1024 experts)
+        if (at + step < tab.live && tab.passes[at + step] <= index) at += step;
+    enter(a, tab);
+  }
+  __device__ __forceinline__ bool done() const { return index > last_index; }
+  __device__ __forceinline__ void next(const ProductArgs& a, const Table& tab) {
+    tile = 0;
+    if (++index > last_index) return;
+    if (a.offsets != nullptr && index == tab.passes[at + 1]) ++at;
+    enter(a, tab);
+  }
+};
+
+// A place in a ring: stage and parity.
+struct Place {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void advance(int stages) {
+    if (++slot == stages) slot = 0, parity ^= 1;
+  }
+};
 
 __device__ __forceinline__ void store_out(const ProductArgs& a, int32_t t, int32_t n, float v) {
   const int64_t i = t * a.ldo + n;
@@ -154,172 +240,252 @@ __device__ __forceinline__ void store_out(const ProductArgs& a, int32_t t, int32
     static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16_rn(v);
 }
 
-template <int G, int NT>
-__global__ void __launch_bounds__(kThreads) int4_product_kernel(const __grid_constant__ ProductArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t barrier;
-  constexpr int TT = 8 * NT, GROUPS = 128 / G, STEPS = G / 32;
-  const Layout l = layout_of(G, a.R, a.slab, a.x_rows, TT);
+template <int G, int NT, int TEAMS>
+__global__ void __launch_bounds__(kThreads, 1)
+    int4_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ CUtensorMap codes_map) {
+  extern __shared__ __align__(1024) uint8_t raw_smem[];
+  uint8_t* smem = raw_smem + (0u - smem_addr(raw_smem)) % 1024;
+  __shared__ __align__(8) uint64_t barriers[2][TEAMS * kMostStages];
+  constexpr int WAYS = kUserWarps / TEAMS, TEAM = WAYS * 32, HELPERS = kHelpers / TEAMS;  // warps and threads of a team, helpers of a ring
+  constexpr int TT = 8 * NT, GROUPS = 128 / G, STEPS = G / 32, CHUNK = most_chunk(TEAMS, G);
+  const Layout l = layout_of(G, a.K, TEAMS, a.chunk, a.stages, a.x_rows, TT, a.offsets != nullptr ? a.E : 0);
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  const int rank = static_cast<int>(blockIdx.x), n0 = static_cast<int>(blockIdx.y) * a.R, e = static_cast<int>(blockIdx.z);
-  const int rows = min(a.R, a.N - n0), k0 = rank * a.slab, length = min(a.slab, a.K - k0);
-  int32_t lo = 0, hi = a.T;
-  if (a.offsets != nullptr) {
-    int32_t first, last;
-    group_rows(a, e, lo, hi, first, last);
-    if (rank == 0) {  // rows of no group are zero
-      auto zero = [&](int32_t from, int32_t to) {
-        const int64_t count = static_cast<int64_t>(to - from) * rows;
-        for (int64_t i = tid; i < count; i += kThreads)
-          store_out(a, from + static_cast<int32_t>(i / rows), n0 + static_cast<int32_t>(i % rows), 0.0f);
-      };
-      if (e == 0) zero(0, first);
-      if (e == a.E - 1) zero(last, a.T);
-    }
-  }
-  if (lo >= hi) return;  // (the whole cluster)
-  const uint32_t bar = smem_addr(&barrier), base = smem_addr(smem);
-  if (tid == 0) {
-    mbar_init(bar, 1);
+  // ring r's stage i is number r * stages + i
+  const uint32_t full = smem_addr(barriers[0]), empty = smem_addr(barriers[1]);
+  if (tid < TEAMS * a.stages) {
+    mbar_init(full + 8 * tid, 1 + HELPERS);  // the codes (bytes), and each helper's scales
+    mbar_init(empty + 8 * tid, WAYS);        // the team's warps
     fence_mbar_init();
   }
+  if (tid == kUsers) tma_prefetch_map(&codes_map);
+  Table tab;
+  tab.start = reinterpret_cast<int32_t*>(smem + l.table), tab.passes = tab.start + a.E + 1;
+  tab.list = reinterpret_cast<uint16_t*>(tab.passes + a.E + 1), tab.live = 0;
+  int passes = (a.T + a.x_rows - 1) / a.x_rows;
+  if (a.offsets != nullptr) {
+    passes = build_table(a, tab);
+    // rows of no group are zero
+    auto zero = [&](int32_t from, int32_t to) {
+      const int64_t count = static_cast<int64_t>(to - from) * a.N;
+      for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + tid; i < count; i += static_cast<int64_t>(gridDim.x) * kThreads)
+        store_out(a, from + static_cast<int32_t>(i / a.N), static_cast<int32_t>(i % a.N), 0.0f);
+    };
+    zero(0, tab.start[0]);
+    zero(tab.start[a.E], a.T);
+  }
+  const int64_t units = static_cast<int64_t>(passes) * a.tiles;
+  const int64_t from = units * blockIdx.x / gridDim.x, to = units * (blockIdx.x + 1) / gridDim.x;
   __syncthreads();
-  const int64_t row0 = static_cast<int64_t>(e) * a.N + n0;
-  if (warp == 0) {
-    if (lane == 0) mbar_expect_tx(bar, static_cast<uint32_t>(rows) * (length / 2));
-    __syncwarp();
-    for (int r = lane; r < rows; r += 32)
-      bulk_load(base + r * l.code_stride, a.q + (row0 + r) * (a.K / 2) + k0 / 2, length / 2, bar);
-  }
-  float* scale = reinterpret_cast<float*>(smem + l.scale);
-  uint16_t* zero = reinterpret_cast<uint16_t*>(smem + l.zero);
-  {
-    const int groups = a.K / G, g0 = k0 / G;
-    for (int i = tid; i < a.R * l.groups; i += kThreads) {
-      const int r = i / l.groups, g = g0 + i % l.groups;
-      float s = 0.0f;
-      uint32_t z = 8;
-      if (r < rows && g < groups) {
-        const int64_t at = (row0 + r) * groups + g;
-        s = a.s_f32 ? __ldg(static_cast<const float*>(a.s) + at)
-                    : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(a.s) + at)) << 16);
-        if (a.z != nullptr) z = __ldg(a.z + at) & 15u;
+  if (from >= to) return;
+  Pass pass(a, tab, from, to);
+  // A wait that runs out is recorded; the warp then waits no more, and a helper stops.
+  bool dead = false;
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    const bool ok = dead || mbar_wait_idle(bar, parity, a.wait_ns);
+    if (__all_sync(kAll, ok)) return;
+    dead = true;
+    atomicOr(a.fault, kFaultProducerWait);
+  };
+  Place at;
+  int phase = 0;  // units of the passes before, modulo the teams
+
+  if (warp >= kUserWarps) {
+    // --------------------------------------------------- codes, scales and zero points of a ring
+    // Scales are [group][row] (scale, twice -z / 64), some rows a helper; their loads are some stages ahead.
+    // (Helpers that took stages by turns could be two rounds from a barrier.)
+    constexpr int ROWS = kRows / HELPERS, PER = CHUNK / G * ROWS / 32;
+    const int team = (warp - kUserWarps) / HELPERS, helper = (warp - kUserWarps) % HELPERS;
+    const int groups = a.K / G, in_stage = a.chunk / G;  // (a power of two)
+    const int shift = 31 - __clz(in_stage);
+    uint32_t held_s[kAhead][PER], held_z[kAhead][PER];
+    int held_row[kAhead], held_k0[kAhead];
+    int k0 = 0, pending = 0, tile = 0;
+    auto settle = [&]() {  // the ring's next unit, from this pass on
+      while (!pass.done() && tile >= pass.end) {
+        phase = (phase + pass.end - pass.tile) % TEAMS;
+        pass.next(a, tab);
+        tile = pass.tile + (team - phase + TEAMS) % TEAMS;
       }
-      scale[i % l.groups * a.R + r] = s;  // [group][row]: the rows that a warp reads at a time lie side by side
-      zero[i % l.groups * a.R + r] = static_cast<uint16_t>(0x4300u | z);
-    }
-  }
-  const int tiles = a.R / 16, ways = kWarpCount / tiles;  // the warps' 16-row tiles, and how many share a tile's slab
-  const int tile = warp % tiles, way = warp / tiles, g = lane >> 2, t = lane & 3;
-  const int blocks = (length + 127) / 128;
-  float* red = reinterpret_cast<float*>(smem + l.red);
-  bool loaded = false;
-  for (int32_t tok = lo; tok < hi; tok += TT) {
-    const int count = min(TT, hi - tok);
-    // x, in the order of the codes' pairs; zeros behind the contraction's end
-    for (int i = tid; i < count * (blocks * 16); i += kThreads) {
-      const int r = i / (blocks * 16), c = i % (blocks * 16);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (c * 8 < length)
-        v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + (tok + r) * a.ldx + k0 + c * 8));
-      uint4 p;
-      p.x = __byte_perm(v.x, v.z, 0x5410);
-      p.y = __byte_perm(v.x, v.z, 0x7632);
-      p.z = __byte_perm(v.y, v.w, 0x5410);
-      p.w = __byte_perm(v.y, v.w, 0x7632);
-      *reinterpret_cast<uint4*>(smem + l.x + r * l.x_stride + (c >> 4) * 256 + chunk_place<G>(c & 15) * 16) = p;
-    }
-    if (!loaded) {
-      loaded = true;
-      if (!mbar_wait(bar, 0, a.wait_ns)) {
-        atomicOr(a.fault, kFaultProducerWait);
-        mbar_wait(bar, 0, a.wait_ns);
-      }
-    }
-    __syncthreads();
-    float acc[NT][4];
+    };
+    auto fetch = [&](uint32_t (&hs)[PER], uint32_t (&hz)[PER], int& row, int& from_k) {  // the next stage's, if there is one
+      if (pass.done()) return;
+      const int n0 = tile * kRows + helper * ROWS;
+      row = pass.e * a.N + tile * kRows, from_k = k0;
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-    const uint8_t* codes = smem + (tile * 16 + g) * l.code_stride + t * (G / 8);
-    const uint8_t* xs = smem + l.x + g * l.x_stride + t * 16;
-    for (int blk = way; blk < blocks; blk += ways) {
-#pragma unroll
-      for (int grp = 0; grp < GROUPS; ++grp) {
-        const int gi = blk * GROUPS + grp;
-        uint32_t wa[STEPS], wb[STEPS];
-        const uint8_t* p = codes + gi * (G / 2);
-#pragma unroll
-        for (int j = 0; j < STEPS; ++j) {
-          wa[j] = reinterpret_cast<const uint32_t*>(p)[j];
-          wb[j] = reinterpret_cast<const uint32_t*>(p + 8 * l.code_stride)[j];
+      for (int i = 0; i < PER; ++i) {
+        const int r = (i * 32 + lane) >> shift, gi = k0 / G + ((i * 32 + lane) & (in_stage - 1));
+        hs[i] = 0, hz[i] = 8;
+        if (r < ROWS && n0 + r < a.N && gi < groups) {
+          const int64_t p = static_cast<int64_t>(pass.e * a.N + n0 + r) * groups + gi;
+          // (as they come: a shift here would wait for them)
+          hs[i] = a.s_f32 ? __ldg(static_cast<const uint32_t*>(a.s) + p) : __ldg(static_cast<const uint16_t*>(a.s) + p);
+          if (a.z != nullptr) hz[i] = __ldg(a.z + p);
         }
-        const int at = gi * a.R + tile * 16 + g;
-        const uint32_t za = zero[at] * 0x10001u, zb = zero[at + 8] * 0x10001u;
-        const float fa = scale[at], fb = scale[at + 8];
-        float c[NT][4];
+      }
+      ++pending;
+      k0 += a.chunk;
+      if (k0 >= a.K) {
+        k0 = 0;
+        tile += TEAMS;
+        settle();
+      }
+    };
+    auto load_codes = [&](int stage, int row, int from_k) {  // (a box may reach into the next expert's rows: they are not used)
+      if (helper != 0) return;
+      const uint32_t bar = full + 8 * stage, dst = smem_addr(smem) + stage * l.code_bytes;
+      if (lane == 0) mbar_expect_tx(bar, l.code_bytes);
+      __syncwarp();
+      if (a.pieces == 1) {
+        if (lane < a.chunk / kPiece) tma_load_2d(dst + lane * kPieceBytes, &codes_map, bar, from_k / 2 + lane * 128, row);
+      } else if (lane == 0) {
+        tma_load_3d(dst, &codes_map, bar, 0, row, from_k / kPiece);
+      }
+    };
+    tile = pass.tile + team;
+    settle();
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+    for (int d = 0; d < kAhead; ++d) fetch(held_s[d], held_z[d], held_row[d], held_k0[d]);
+    // the first stages' codes do not wait for scales
+    int early = min(pending, min(a.stages, kAhead));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
+    for (int d = 0; d < kAhead; ++d)
+      if (d < early) load_codes(team * a.stages + d, held_row[d], held_k0[d]);
+    while (pending > 0 && !dead) {
 #pragma unroll
-        for (int j = 0; j < STEPS; ++j) {
-          uint4 x[NT];
+      for (int d = 0; d < kAhead; ++d) {
+        if (pending == 0 || dead) break;
+        const int stage = team * a.stages + at.slot;
+        wait(empty + 8 * stage, at.parity ^ 1);
+        if (dead) break;
+        if (early > 0)
+          --early;
+        else
+          load_codes(stage, held_row[d], held_k0[d]);
+        uint2* meta = reinterpret_cast<uint2*>(smem + l.meta + stage * l.meta_bytes) + helper * ROWS;
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-            x[i] = i * 8 + g < count ? *reinterpret_cast<const uint4*>(xs + i * 8 * l.x_stride + blk * 256 + (grp * STEPS + j) * 64)
-                                     : make_uint4(0, 0, 0, 0);
-          const uint32_t a0 = code_pair(wa[j], 0, za), a1 = code_pair(wb[j], 0, zb), a2 = code_pair(wa[j], 1, za),
-                         a3 = code_pair(wb[j], 1, zb);
-          const uint32_t a4 = code_pair(wa[j], 2, za), a5 = code_pair(wb[j], 2, zb), a6 = code_pair(wa[j], 3, za),
-                         a7 = code_pair(wb[j], 3, zb);
+        for (int i = 0; i < PER; ++i) {
+          const int r = (i * 32 + lane) >> shift, gi = (i * 32 + lane) & (in_stage - 1);
+          if (r < ROWS)
+            meta[gi * (kRows + 1) + r] = make_uint2(held_s[d][i] << (a.s_f32 ? 0 : 16),
+                                                    fma_bf16x2((held_z[d][i] & 15u) * 0x10001u, 0xFF00FF00u, 0));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + 8 * stage);
+        at.advance(a.stages);
+        --pending;
+        fetch(held_s[d], held_z[d], held_row[d], held_k0[d]);
+      }
+    }
+    // (a CTA does not end before its copies: without a fault the team has waited for them all)
+    for (int i = 0; dead && i < a.stages; ++i)  // stages before this place were filled in its round, the others in the one before
+      mbar_wait(full + 8 * (team * a.stages + i), i < at.slot ? at.parity : at.parity ^ 1, a.wait_ns);
+    return;
+  }
+  // ------------------------------------------------------------------ products
+  const int team = warp / WAYS, way = warp % WAYS, g = lane >> 2, t = lane & 3;
+  float* red = reinterpret_cast<float*>(smem + l.red) + team * (WAYS * TT * kRedStride);
+  // where in a swizzled piece this thread's words of row g lie (its blocks are all a piece's first or second half)
+  int32_t word[4];
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            mma_16x8x16(c[i], a0, a1, a2, a3, x[i].x, x[i].y);
-            mma_16x8x16(c[i], a4, a5, a6, a7, x[i].z, x[i].w);
+  for (int j = 0; j < 4; ++j) word[j] = way / 2 * kPieceBytes + g * 128 + (((way % 2 * 4 + j) ^ g) << 4) + t * 4;
+  for (; !pass.done(); phase = (phase + pass.end - pass.tile) % TEAMS, pass.next(a, tab)) {
+    const int count = pass.count;
+    int32_t x_row[NT];  // this thread's rows of x (columns behind the last token: its row again, their sums are not used)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) x_row[i] = l.x + min(i * 8 + g, count - 1) * l.x_stride + t * 16 + way * 256;
+    // the pass's tokens, in the order of the codes' pairs; zeros behind the contraction's end
+    named_sync(1, kUsers);
+    for (int c = tid; c < (a.K + 127) / 128 * 16; c += kUsers) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + pass.tok * a.ldx) + c;
+      for (int r0 = 0; r0 < count; r0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          v[r] = r0 + r < count && c * 8 < a.K ? __ldg(src + (r0 + r) * (a.ldx / 8)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r0 + r < count)
+            *reinterpret_cast<uint4*>(smem + l.x + (r0 + r) * l.x_stride + c * 16) =
+                make_uint4(__byte_perm(v[r].x, v[r].z, 0x5410), __byte_perm(v[r].x, v[r].z, 0x7632),
+                           __byte_perm(v[r].y, v[r].w, 0x5410), __byte_perm(v[r].y, v[r].w, 0x7632));
+      }
+    }
+    named_sync(1, kUsers);
+    for (int tile = pass.tile + (team - phase + TEAMS) % TEAMS; tile < pass.end; tile += TEAMS) {
+      float acc[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+      uint32_t xs = 0;
+      for (int k0 = 0; k0 < a.K; k0 += a.chunk) {
+        const int stage = team * a.stages + at.slot;
+        wait(full + 8 * stage, at.parity);
+        const uint2* meta = reinterpret_cast<const uint2*>(smem + l.meta + stage * l.meta_bytes) + way * (GROUPS * (kRows + 1)) + g;
+        const uint8_t* codes = smem + stage * l.code_bytes;
+        const int left = min(a.chunk, a.K - k0);
+        for (int k = way * 128; k < left; k += WAYS * 128) {
+          uint32_t wa[4], wb[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            wa[j] = *reinterpret_cast<const uint32_t*>(codes + word[j]);
+            wb[j] = *reinterpret_cast<const uint32_t*>(codes + word[j] + 8 * 128);
           }
-        }
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          acc[i][0] = fmaf(c[i][0], fa, acc[i][0]);
-          acc[i][1] = fmaf(c[i][1], fa, acc[i][1]);
-          acc[i][2] = fmaf(c[i][2], fb, acc[i][2]);
-          acc[i][3] = fmaf(c[i][3], fb, acc[i][3]);
-        }
-      }
-    }
+          for (int grp = 0; grp < GROUPS; ++grp) {
+            const uint2 ma = meta[grp * (kRows + 1)], mb = meta[grp * (kRows + 1) + 8];
+            float c[NT][4];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      float* d = red + (way * TT + i * 8 + 2 * t) * l.red_stride + tile * 16 + g;
-      d[0] = acc[i][0];
-      d[l.red_stride] = acc[i][1];
-      d[8] = acc[i][2];
-      d[l.red_stride + 8] = acc[i][3];
-    }
-    __syncthreads();
-    // the ways in order; then, where the contraction has more slabs, the cluster's ranks in order
-    for (int i = tid; i < count * a.R; i += kThreads) {
-      const int r = i / a.R, n = i % a.R;
-      float s = red[r * l.red_stride + n];
-      for (int w = 1; w < ways; ++w) s += red[(w * TT + r) * l.red_stride + n];
-      if (a.slabs > 1)
-        red[r * l.red_stride + n] = s;
-      else if (n < rows)
-        store_out(a, tok + r, n0 + n, s);
-    }
-    if (a.slabs > 1) {
-      cluster_sync();
-      const uint32_t mine = smem_addr(red);
-      for (int i = rank * kThreads + tid; i < count * a.R; i += a.slabs * kThreads) {
-        const int r = i / a.R, n = i % a.R;
-        float s = 0.0f;
-        for (int w = 0; w < a.slabs; ++w) s += ld_float_cluster(map_shared_rank(mine + (r * l.red_stride + n) * 4, w));
-        if (n < rows) store_out(a, tok + r, n0 + n, s);
+            for (int j = grp * STEPS; j < (grp + 1) * STEPS; ++j) {
+              uint32_t pa[4], pb[4];
+              code_pairs(wa[j], ma.y, pa);
+              code_pairs(wb[j], mb.y, pb);
+#pragma unroll
+              for (int i = 0; i < NT; ++i) {
+                const uint4 x = *reinterpret_cast<const uint4*>(smem + (x_row[i] + xs) + j * 64);
+                if (j == grp * STEPS)
+                  mma_16x8x16_zero(c[i], pa[0], pb[0], pa[1], pb[1], x.x, x.y);
+                else
+                  mma_16x8x16(c[i], pa[0], pb[0], pa[1], pb[1], x.x, x.y);
+                mma_16x8x16(c[i], pa[2], pb[2], pa[3], pb[3], x.z, x.w);
+              }
+            }
+            const float fa = __uint_as_float(ma.x), fb = __uint_as_float(mb.x);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              acc[i][0] = fmaf(c[i][0], fa, acc[i][0]);
+              acc[i][1] = fmaf(c[i][1], fa, acc[i][1]);
+              acc[i][2] = fmaf(c[i][2], fb, acc[i][2]);
+              acc[i][3] = fmaf(c[i][3], fb, acc[i][3]);
+            }
+          }
+          codes += WAYS / 2 * kPieceBytes;
+          meta += WAYS * GROUPS * (kRows + 1);
+          xs += WAYS * 256;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + 8 * stage);
+        at.advance(a.stages);
       }
-      cluster_sync();
-    } else {
-      __syncthreads();
+      named_sync(2 + team, TEAM);  // (the sums of the team's last unit have been read)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        float* d = red + (way * TT + i * 8 + 2 * t) * kRedStride + g;
+        d[0] = acc[i][0];
+        d[kRedStride] = acc[i][1];
+        d[8] = acc[i][2];
+        d[kRedStride + 8] = acc[i][3];
+      }
+      named_sync(2 + team, TEAM);
+      // the warps' sums in order
+      const int n0 = tile * kRows;
+      for (int i = tid % TEAM; i < count * kRows; i += TEAM) {
+        const int r = i / kRows, n = i % kRows;
+        float s = red[r * kRedStride + n];
+#pragma unroll
+        for (int w = 1; w < WAYS; ++w) s += red[(w * TT + r) * kRedStride + n];
+        if (n0 + n < a.N) store_out(a, pass.tok + r, n0 + n, s * 64.0f);
+      }
     }
   }
 }
@@ -423,38 +589,40 @@ void by_group(int64_t G, F f) {
 }
 
 template <typename F>
-void by_tokens(int nt, F f) {
+void by_form(int nt, int teams, F f) {
   if (nt == 1)
-    f(std::integral_constant<int, 1>());
-  else if (nt == 2)
-    f(std::integral_constant<int, 2>());
+    teams == 1 ? f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>())
+               : f(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
   else
-    f(std::integral_constant<int, 4>());
+    teams == 1 ? f(std::integral_constant<int, 2>(), std::integral_constant<int, 1>())
+               : f(std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
 }
 
-constexpr int kMaxShared = 227 * 1024 - 1024;
+constexpr int kMaxShared = 225 * 1024;
 
 struct Int4Plan {
-  int nt, R, slab, slabs, x_rows, bytes;
+  int nt, teams, x_rows, chunk, stages, bytes, grid;
 };
 
-// How a product is cut: tokens a pass, rows of weights and contraction elements a CTA.
-Int4Plan plan_int4(int64_t E, int64_t T, int64_t N, int64_t K, int64_t G, bool grouped) {
+// Tokens a pass: as many as shared memory holds beside two stages a ring, at most two MMAs' (16).
+Int4Plan plan_int4(int64_t E, int64_t T, int64_t N, int64_t K, int64_t G, bool grouped, int sm_count) {
   Int4Plan p;
-  const int64_t tokens = grouped ? (T + E - 1) / E : T;
-  p.nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
-  p.R = 16;
-  int64_t slabs = std::min<int64_t>(kMaxSlabs, (K + 2047) / 2048);
-  for (;;) {
-    p.slab = static_cast<int>(((K + slabs - 1) / slabs + 127) / 128 * 128);
-    p.slabs = static_cast<int>((K + p.slab - 1) / p.slab);
-    p.x_rows = static_cast<int>(std::min<int64_t>(T, 8 * p.nt));
-    p.bytes = layout_of(static_cast<int>(G), p.R, p.slab, p.x_rows, 8 * p.nt).bytes;
-    if (p.bytes <= kMaxShared) return p;
-    if (slabs < kMaxSlabs)
-      ++slabs;
-    else
-      p.nt /= 2;
+  const int64_t tokens = grouped ? (T + E - 1) / E : T, units = (N + kRows - 1) / kRows * (grouped ? std::min(E, T) : 1);
+  const int want = tuning_override("DP_FORCE_INT4_TOKENS", 0), want_teams = tuning_override("DP_FORCE_INT4_TEAMS", 0);
+  const int experts = grouped ? static_cast<int>(E) : 0, g = static_cast<int>(G), k = static_cast<int>(K);
+  p.teams = want_teams == 1 || want_teams == 4 ? want_teams : units < 12 * sm_count ? 1 : 4;
+  p.x_rows = static_cast<int>(std::min<int64_t>(T, want > 0 && want <= 16 ? want : tokens <= 4 && grouped ? 8 : 16));
+  for (;; p.x_rows = (p.x_rows + 1) / 2) {
+    p.nt = p.x_rows <= 8 ? 1 : 2;
+    for (p.chunk = most_chunk(p.teams, g); p.chunk >= least_chunk(p.teams); p.chunk /= 2) {
+      const Layout none = layout_of(g, k, p.teams, p.chunk, 0, p.x_rows, 8 * p.nt, experts);
+      p.stages = std::min(kMostStages, (kMaxShared - 1024 - none.bytes) / (p.teams * (none.code_bytes + none.meta_bytes)));
+      if (p.stages >= (p.chunk > least_chunk(p.teams) ? 3 : 2)) {
+        p.bytes = layout_of(g, k, p.teams, p.chunk, p.stages, p.x_rows, 8 * p.nt, experts).bytes + 1024;
+        p.grid = static_cast<int>(std::min<int64_t>(units * ((T + p.x_rows - 1) / p.x_rows), sm_count));
+        return p;
+      }
+    }
   }
 }
 
@@ -487,30 +655,22 @@ dp_status run_product(const void* x, int64_t ldx, const void* q, const void* s, 
     const size_t size = out_f32 ? 4 : 2;
     return cudaMemset2DAsync(out, ldo * size, 0, N * size, T, str) == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
   }
-  const Int4Plan p = plan_int4(E, T, N, K, G, offsets != nullptr);
+  const Int4Plan p = plan_int4(E, T, N, K, G, offsets != nullptr, ctx.sm_count);
   ProductArgs a = {};
-  a.x = x, a.ldx = ldx, a.q = static_cast<const uint8_t*>(q), a.s = s, a.z = static_cast<const uint8_t*>(z), a.s_f32 = s_f32;
+  a.x = x, a.ldx = ldx, a.s = s, a.z = static_cast<const uint8_t*>(z), a.s_f32 = s_f32;
   a.offsets = offsets, a.offsets64 = offset_bits == 64;
   a.E = static_cast<int32_t>(E), a.T = static_cast<int32_t>(T), a.N = static_cast<int32_t>(N), a.K = static_cast<int32_t>(K);
-  a.R = p.R, a.slab = p.slab, a.slabs = p.slabs, a.x_rows = p.x_rows;
+  a.x_rows = p.x_rows, a.chunk = p.chunk, a.stages = p.stages, a.tiles = static_cast<int32_t>((N + kRows - 1) / kRows);
   a.out = out, a.ldo = ldo, a.out_f32 = out_f32, a.fault = ctx.fault, a.wait_ns = kWaitLimitNs;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.slabs, static_cast<unsigned>((N + p.R - 1) / p.R), static_cast<unsigned>(E));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = p.bytes;
-  cfg.stream = str;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.slabs, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t err = cudaSuccess;
+  a.pieces = K % kPiece == 0 ? p.chunk / kPiece : 1;
+  CUtensorMap map;
+  if (!encode_bytes(&map, q, E * N, K / 2, kRows, a.pieces)) return DP_ERR_LAUNCH;
   by_group(G, [&](auto g) {
-    by_tokens(p.nt, [&](auto nt) {
-      err = cudaLaunchKernelEx(&cfg, int4_product_kernel<decltype(g)::value, decltype(nt)::value>, a);
+    by_form(p.nt, p.teams, [&](auto nt, auto teams) {
+      int4_product_kernel<decltype(g)::value, decltype(nt)::value, decltype(teams)::value><<<p.grid, kThreads, p.bytes, str>>>(a, map);
     });
   });
-  return err == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+  return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -519,10 +679,10 @@ cudaError_t set_attributes_int4() {
   cudaError_t e = cudaSuccess;
   for (int G = 32; G <= 128; G *= 2)
     by_group(G, [&](auto g) {
-      for (int n = 1; n <= 4; n *= 2)
-        by_tokens(n, [&](auto nt) {
+      for (int form = 0; form < 4; ++form)
+        by_form(1 + form % 2, form / 2 ? 4 : 1, [&](auto nt, auto teams) {
           if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(int4_product_kernel<decltype(g)::value, decltype(nt)::value>,
+            e = cudaFuncSetAttribute(int4_product_kernel<decltype(g)::value, decltype(nt)::value, decltype(teams)::value>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
         });
     });

@@ -115,6 +115,27 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
   }
 }
 
+// The same for a thread with nothing else to do: it sleeps up to 20 us at a time until the phase
+// completes, so that its polling takes no issue slots from the warps that it waits for.
+__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  auto test = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+  };
+  if (test()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!test())
+    if (globaltimer_ns() - t0 > limit_ns) return false;
+  return true;
+}
+
 // The same with a non-suspending test first: ~20 cycles where the phase has completed, against
 // ~50 for a satisfied try_wait (measured on GB300).
 template <bool CLUSTER = false>

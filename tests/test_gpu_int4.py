@@ -185,6 +185,31 @@ def test_grouped(groups, group):
     assert dp.device_error() == 0
 
 
+@pytest.mark.parametrize("teams", ["1", "4"])
+@pytest.mark.parametrize("tokens", ["1", "3", "8", "16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_forms(teams, tokens, group, monkeypatch):
+    """Each cut of the work over warps and passes, where a CTA's range holds several experts, passes and odd tiles."""
+    monkeypatch.setenv("DP_FORCE_INT4_TEAMS", teams)
+    monkeypatch.setenv("DP_FORCE_INT4_TOKENS", tokens)
+    counts = [3, 0, 21, 1, 16, 17, 0, 8, 9, 33, 2, 2]
+    edges = [2]
+    for n in counts:
+        edges.append(edges[-1] + n)
+    E, T = len(counts), edges[-1] + 5
+    for N, K in ((1000, 384), (424, 4096), (2056, 2304), (264, 5120)):
+        q, s, z = problem(E, N, K, group, True, BF16, N, True)
+        X = rows(T, K, 3, True)
+        ref = torch.zeros(T, N, dtype=torch.float64, device=DEV)
+        for e in range(E):
+            ref[edges[e]:edges[e + 1]] = X[edges[e]:edges[e + 1]].double() @ expand(q[e], s[e], z[e], group).T
+        got = dp.dp_gemm_fwd_int4_grouped(X, q, s, torch.tensor(edges, dtype=torch.int32, device=DEV), zeros=z, out_dtype=F32)
+        assert torch.equal(got, ref.float())
+        got = dp.dp_gemm_fwd_int4(X[:37], q[0], s[0], zeros=z[0], out_dtype=F32)
+        assert torch.equal(got, (X[:37].double() @ expand(q[0], s[0], z[0], group).T).float())
+    assert dp.device_error() == 0
+
+
 def test_bad_offsets_are_clamped_and_reported():
     E, T, N, K = 6, 40, 32, 128
     q, s, z = problem(E, N, K, 32, True, BF16, 1, True)
