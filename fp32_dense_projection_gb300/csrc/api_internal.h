@@ -41,7 +41,9 @@ bool encode_operand(CUtensorMap* map, const void* ptr, CUtensorMapDataType type,
 // pieces, [piece][row][128].
 bool encode_bytes(CUtensorMap* map, const void* ptr, int64_t rows, int64_t row_bytes, uint32_t box_rows, uint32_t depth);
 
-// Shared memory of the products with 4-bit weights (for the current device).
+// Shared memory of the products with 4-bit weights, of layer norm and of the sort by expert (for the current device).
 cudaError_t set_attributes_int4();
+cudaError_t set_attributes_layer_norm();
+cudaError_t set_attributes_experts();
 
 }  // namespace dp

@@ -65,6 +65,8 @@ dp_status init_device(int dev, DeviceState** out) {
       if (e == cudaSuccess) e = set_attributes_grouped();
       if (e == cudaSuccess) e = set_attributes_fp8();
       if (e == cudaSuccess) e = set_attributes_int4();
+      if (e == cudaSuccess) e = set_attributes_layer_norm();
+      if (e == cudaSuccess) e = set_attributes_experts();
       if (e == cudaSuccess) e = cudaGetSymbolAddress(&fault, g_fault_word);
       if (cur != dev) cudaSetDevice(cur);
       if (e != cudaSuccess) return DP_ERR_LAUNCH;

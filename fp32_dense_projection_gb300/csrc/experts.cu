@@ -13,7 +13,8 @@
 // taken by one thread in the order of j (no atomics).  The sort moves 12 bytes a pair and is
 // latency: a counting sort without atomics.  A warp counts its own run of pairs in its own
 // counters (lanes with one expert find each other by a match), counters are summed over the
-// warps, and each warp walks its run again with its running positions.
+// warps, and each warp walks its run again with its running positions; up to 2^18 pairs in one
+// launch of a cluster.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -144,16 +145,121 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const __grid_constant_
   }
 }
 
+// The same in one launch, for pairs that one cluster can go through: the blocks read each other's
+// counts from their shared memory.  (16384 pairs over 64 experts: 22 us in two launches of four blocks.)
+__global__ void __launch_bounds__(1024) sort_cluster_kernel(const __grid_constant__ SortArgs a) {
+  extern __shared__ int32_t warp_counts[];  // [warps][E + 1], then the block's totals [E + 1] and base [E + 1]
+  __shared__ int32_t scan[32];
+  constexpr int HELD = 4;  // runs of 32 pairs whose keys stay in registers
+  const int n = a.E + 1, tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const int threads = static_cast<int>(blockDim.x), warps = threads >> 5;
+  const int rank = static_cast<int>(blockIdx.x), ranks = static_cast<int>(gridDim.x);
+  int32_t* const totals = warp_counts + warps * n;
+  int32_t* const base = totals + n;
+  const int begin = static_cast<int>(min(static_cast<int64_t>(a.P), static_cast<int64_t>(rank) * a.per_block + warp * a.per_warp));
+  const int end = static_cast<int>(min(static_cast<int64_t>(a.P), static_cast<int64_t>(begin) + a.per_warp));
+  int held[HELD];
+#pragma unroll
+  for (int r = 0; r < HELD; ++r) held[r] = begin + r * 32 + lane < end ? key_of(a, begin + r * 32 + lane) : -1;
+  for (int i = tid; i < warps * n; i += threads) warp_counts[i] = 0;
+  __syncthreads();
+  int32_t* const mine = warp_counts + warp * n;
+  auto walk = [&](auto step) {  // the warp's runs in order: first pair of the run, this lane's key (-1: none)
+#pragma unroll
+    for (int r = 0; r < HELD; ++r)
+      if (begin + r * 32 < end) step(begin + r * 32, held[r]);
+    for (int i = begin + HELD * 32; i < end; i += 32) step(i, i + lane < end ? key_of(a, i + lane) : -1);
+  };
+  walk([&](int, int key) {
+    const uint32_t same = __match_any_sync(kAll, key);
+    if (key >= 0 && lane == __ffs(static_cast<int>(same)) - 1) mine[key] += __popc(same);
+    __syncwarp();
+  });
+  __syncthreads();
+  for (int e = tid; e < n; e += threads) {  // positions of the warps within their block
+    int32_t own = 0;
+#pragma unroll 8
+    for (int w = 0; w < warps; ++w) {
+      const int32_t c = warp_counts[w * n + e];
+      warp_counts[w * n + e] = own;
+      own += c;
+    }
+    totals[e] = own;
+  }
+  if (ranks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  int32_t carry = 0;
+  for (int e0 = 0; e0 < n; e0 += threads) {
+    const int e = e0 + tid;
+    int32_t total = 0, before = 0;
+    if (e < n) {
+      const uint32_t at = smem_addr(totals + e);
+      for (int r = 0; r < ranks; ++r) {
+        int32_t c = totals[e];
+        if (r != rank) asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(map_shared_rank(at, r)) : "memory");
+        if (r < rank) before += c;
+        total += c;
+      }
+    }
+    int32_t incl = total;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(kAll, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int32_t lower = carry;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) lower += scan[w];
+      carry += scan[w];
+    }
+    if (e < n) {
+      const int32_t start = lower + incl - total;
+      base[e] = start + before;
+      if (rank == 0) a.offsets[e] = start;
+    }
+    __syncthreads();
+  }
+  walk([&](int first, int key) {
+    const uint32_t same = __match_any_sync(kAll, key);
+    const int32_t at = key >= 0 ? base[key] + mine[key] + __popc(same & ((1u << lane) - 1)) : 0;
+    __syncwarp();
+    if (key >= 0) {
+      if (lane == __ffs(static_cast<int>(same)) - 1) mine[key] += __popc(same);
+      a.row_of[first + lane] = key < a.E ? at : ~at;
+      a.order[at] = first + lane;
+    }
+    __syncwarp();
+  });
+  if (ranks > 1) cluster_sync();  // (no block ends while others read its totals)
+}
+
 struct SortShape {
+  int ranks;  // of the cluster that sorts alone (0: two launches)
   int warps, blocks;
   int32_t per_warp, per_block;
   size_t smem;
 };
 
 constexpr int kSortBlocks = 128;
+constexpr int64_t kClusterPairs = 1 << 18;  // 32 runs a warp; from there on two launches of many blocks are as fast
 
 SortShape sort_shape(int64_t P, int64_t E) {
-  SortShape s;
+  SortShape s = {};
+  const int want = tuning_override("DP_FORCE_SORT_CLUSTER", -1);
+  if (want < 0 ? P <= kClusterPairs : want != 0) {
+    const int64_t all = (P + 31) / 32;
+    s.ranks = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, (all + 127) / 128)));
+    s.warps = all <= 16 ? 8 : 32;
+    s.per_warp = static_cast<int32_t>((all + s.ranks * s.warps - 1) / (s.ranks * s.warps) * 32);
+    s.per_block = s.per_warp * s.warps;
+    s.blocks = 1;  // (no workspace)
+    s.smem = static_cast<size_t>(s.warps + 2) * (E + 1) * 4;
+    return s;
+  }
   // (counters and positions: at most 46 KB)
   s.warps = static_cast<int>(std::min<int64_t>(32, (46 << 8) / (E + 1) - 1));
   const int64_t runs = (P + 31) / 32;  // 32 pairs each
@@ -212,6 +318,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ Row
   }
 }
 
+constexpr int kBatch = 4;  // rows of a token whose loads are in flight together
+
 template <bool YF32, bool OF32>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ RowArgs a) {
   const int sub = static_cast<int>(threadIdx.x) / a.tpr, lane = static_cast<int>(threadIdx.x) % a.tpr;
@@ -225,14 +333,25 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ro
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] = 0.0f;
     }
-    for (int j = 0; j < a.k; ++j) {
-      const Place at = place_of(a, t * a.k + j);
-      if (!at.live) continue;
-      const float g = a.gates != nullptr ? __ldg(a.gates + t * a.k + j) : 1.0f;
-      float v[8];
-      load8<YF32>(a.x, at.row * a.ldx + col, v);
+    for (int j0 = 0; j0 < a.k; j0 += kBatch) {
+      Raw8<YF32> v[kBatch];
+      float g[kBatch];
+      bool live[kBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = fmaf(g, v[i], s[i]);
+      for (int j = 0; j < kBatch; ++j) {
+        const Place at = j0 + j < a.k ? place_of(a, t * a.k + j0 + j) : Place{-1, false};
+        live[j] = at.live, g[j] = 1.0f;
+        v[j] = at.live ? load_raw8<YF32>(a.x, at.row * a.ldx + col) : zero_raw8<YF32>();
+        if (at.live && a.gates != nullptr) g[j] = __ldg(a.gates + t * a.k + j0 + j);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (!live[j]) continue;
+        float x[8];
+        unpack8<YF32>(v[j], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = fmaf(g[j], x[i], s[i]);
+      }
     }
     store8<OF32>(a.out, t * a.ldo + col, s);
   }
@@ -240,30 +359,43 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ro
 
 template <bool DF32, bool YF32, bool OF32>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant__ RowArgs a) {
-  __shared__ float part[2][32][1];
+  __shared__ float part[2][32][kBatch];
   const int sub = static_cast<int>(threadIdx.x) / a.tpr, lane = static_cast<int>(threadIdx.x) % a.tpr;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (256 / a.tpr) + sub;
-  const bool live = t < a.T;
-  GroupSum<1> sum(part, a.tpr);
-  for (int j = 0; j < a.k; ++j) {  // (every thread of the block: the sums meet in barriers)
-    const Place at = live ? place_of(a, t * a.k + j) : Place{-1, false};
-    const float g = at.live ? __ldg(a.gates + t * a.k + j) : 0.0f;
-    float dot[1] = {0.0f};
-    for (int col = lane * 8; at.row >= 0 && col < a.C; col += a.tpr * 8) {
-      float d[8], v[8];
-      if (at.live) {
-        load8<DF32>(a.x, t * a.ldx + col, d);
-        load8<YF32>(a.y, at.row * a.ld_y + col, v);
-      }
+  GroupSum<kBatch> sum(part, a.tpr);
+  for (int j0 = 0; j0 < a.k; j0 += kBatch) {  // (every thread of the block: the sums meet in barriers)
+    Place at[kBatch];
+    float g[kBatch], dot[kBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (at.live) dot[0] = fmaf(d[i], v[i], dot[0]);
-        d[i] = at.live ? d[i] * g : 0.0f;
+    for (int j = 0; j < kBatch; ++j) {
+      at[j] = t < a.T && j0 + j < a.k ? place_of(a, t * a.k + j0 + j) : Place{-1, false};
+      g[j] = at[j].live ? __ldg(a.gates + t * a.k + j0 + j) : 0.0f;
+      dot[j] = 0.0f;
+    }
+    for (int col = lane * 8; t < a.T && col < a.C; col += a.tpr * 8) {
+      Raw8<YF32> v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        v[j] = at[j].live ? load_raw8<YF32>(a.y, at[j].row * a.ld_y + col) : zero_raw8<YF32>();
+      float d[8];
+      load8<DF32>(a.x, t * a.ldx + col, d);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (at[j].row < 0) continue;
+        float x[8];
+        unpack8<YF32>(v[j], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (at[j].live) dot[j] = fmaf(d[i], x[i], dot[j]);
+          x[i] = at[j].live ? d[i] * g[j] : 0.0f;
+        }
+        store8<OF32>(a.out, at[j].row * a.ldo + col, x);
       }
-      store8<OF32>(a.out, at.row * a.ldo + col, d);
     }
     sum(dot);
-    if (live && lane == 0) a.dgates[t * a.k + j] = dot[0];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (t < a.T && lane == 0 && j0 + j < a.k) a.dgates[t * a.k + j0 + j] = dot[j];
   }
 }
 
@@ -298,6 +430,12 @@ RowArgs row_args(const int32_t* row_of, const float* gates, int64_t T, int64_t k
 unsigned token_blocks(const RowArgs& a) { return static_cast<unsigned>((a.T + 256 / a.tpr - 1) / (256 / a.tpr)); }
 
 }  // namespace
+
+cudaError_t set_attributes_experts() {
+  return cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>((32 + 2) * (kMaxExpertCount + 1) * 4));
+}
+
 }  // namespace dp
 
 extern "C" dp_status dp_expert_sort_workspace_size(int64_t pairs, int64_t E, size_t* bytes) {
@@ -331,6 +469,19 @@ extern "C" dp_status dp_expert_sort(const void* choice, int choice_bits, int64_t
   a.choice = choice, a.wide = choice_bits == 64, a.P = static_cast<int32_t>(pairs), a.E = static_cast<int32_t>(E);
   a.per_block = s.per_block, a.per_warp = s.per_warp, a.counts = static_cast<int32_t*>(workspace);
   a.offsets = offsets, a.row_of = row_of, a.order = order;
+  if (s.ranks > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(s.ranks));
+    cfg.blockDim = dim3(static_cast<unsigned>(s.warps * 32));
+    cfg.dynamicSmemBytes = s.smem;
+    cfg.stream = str;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(s.ranks), attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = s.ranks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, sort_cluster_kernel, a) == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+  }
   if (s.blocks > 1) {
     sort_count_kernel<<<s.blocks, s.warps * 32, s.smem, str>>>(a);
     if (cudaGetLastError() != cudaSuccess) return DP_ERR_LAUNCH;

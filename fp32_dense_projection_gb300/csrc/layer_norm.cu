@@ -4,11 +4,14 @@
 //   dx = rs (g - mean(g) - h mean(g h)),   dw = sum_t dy h,   db = sum_t dy
 //
 // Bound: HBM bytes (x read, y written; backward x and dy read, dx written).  A row's elements stay
-// in the registers of the threads that share it, so each is read once; the variance is the mean
-// of squared distances from the row's own mean, not a difference of two large sums.  dw and db are
-// summed in FP32 registers over the rows that a block visits, in row order; each block writes its
-// sums to the workspace, and a second launch adds them in block order: no atomics, the same bits
-// every time.
+// in the registers of the threads that share it, so each is read once; the variance is the mean of
+// squared distances from the row's own mean, not a difference of two large sums.  A thread's own
+// pieces of the next rows are on their way into shared memory meanwhile (asynchronous copies that
+// nobody else waits for); one row ahead in registers reached 3.6 TB/s in the backward pass.  Arithmetic
+// is packed, two FP32 values an instruction; weight and bias lie in shared memory in FP32.  dw and db
+// are summed in FP32 (registers; shared memory for rows of more than 8192 columns) over the rows that
+// a block visits, in row order; each block writes its sums to the workspace, and a second launch
+// adds them in block order: no atomics, the same bits every time.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -34,8 +37,10 @@ struct NormArgs {
   float inv_c;
   void* y;  // forward: y; backward: dx
   int64_t ldy;
+  int y_f32;
   float* mean;
   float* rstd;
+  int few;  // a block has one row (or one for each group of threads): weight and bias come straight from memory
   const void* dy;
   int64_t ldg;
   float* partial;  // [blocks][2][C]: each block's sums for dw and db (null: no weight)
@@ -52,53 +57,96 @@ __device__ __forceinline__ void load_param(const void* p, int f32, int at, float
   }
 }
 
-template <bool XF32, bool YF32, int CH, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float part[2][32][1];
-  const int t = static_cast<int>(threadIdx.x) % a.tpr, sub = static_cast<int>(threadIdx.x) / a.tpr;
-  const int rows = static_cast<int>(blockDim.x) / a.tpr;
-  GroupSum<1> sum(part, a.tpr);
-  float w[CH][8], b[CH][8];
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int col = (t + i * a.tpr) * 8;
-    if (col < a.C) {
-      load_param(a.w, a.w_f32, col, 1.0f, w[i]);
-      load_param(a.b, a.w_f32, col, 0.0f, b[i]);
-    }
+__device__ __forceinline__ void store_row8(const NormArgs& a, int64_t at, const Two (&v)[4]) {
+  if (a.y_f32)
+    store8<true>(a.y, at, v);
+  else
+    store8<false>(a.y, at, v);
+}
+
+// A vector over the columns in FP32, each thread's own pieces: [piece][half][thread of the row].
+__device__ __forceinline__ void keep_param(float4* kept, const NormArgs& a, const void* p, float other) {
+  for (int c = static_cast<int>(threadIdx.x); c < a.C / 8; c += static_cast<int>(blockDim.x)) {
+    float v[8];
+    load_param(p, a.w_f32, c * 8, other, v);
+    float4* at = kept + c / a.tpr * 2 * a.tpr + c % a.tpr;
+    at[0] = make_float4(v[0], v[1], v[2], v[3]);
+    at[a.tpr] = make_float4(v[4], v[5], v[6], v[7]);
   }
+}
+
+__device__ __forceinline__ void take_param(const float4* kept, int tpr, int t, int i, Two (&v)[4]) {
+  const float4 p = kept[2 * i * tpr + t], q = kept[(2 * i + 1) * tpr + t];
+  v[0] = two(p.x, p.y), v[1] = two(p.z, p.w), v[2] = two(q.x, q.y), v[3] = two(q.z, q.w);
+}
+
+__device__ __forceinline__ void read_param(const void* p, int f32, int col, float other, Two (&w)[4]) {
+  float v[8];
+  load_param(p, f32, col, other, v);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = two(v[2 * j], v[2 * j + 1]);
+}
+
+// Rows ahead: as many as shared memory holds beside the blocks that share an SM.
+constexpr int fwd_depth(int threads, bool f32) { return threads == 1024 && f32 ? 1 : 2; }
+constexpr int bwd_depth(int threads, bool x_f32, bool g_f32) { return threads == 1024 ? 1 : x_f32 && g_f32 ? 2 : 3; }
+
+template <bool XF32, int CH, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? (XF32 ? 3 : 4) : THREADS == 512 && !XF32 ? 2 : 1)
+    norm_fwd_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int DEPTH = fwd_depth(THREADS, XF32);
+  __shared__ float part[2][32][1];
+  extern __shared__ float4 shared[];  // rows ahead, weight and bias (rows of more than 8192 columns: weight only)
+  const int t = static_cast<int>(threadIdx.x) % a.tpr, sub = static_cast<int>(threadIdx.x) / a.tpr;
+  const int rows = THREADS / a.tpr;
+  GroupSum<1> sum(part, a.tpr);
+  Ahead<XF32, CH, DEPTH, THREADS> ahead(shared, a.tpr);
+  float4* const w_kept = shared + ahead.BYTES / 16;
+  float4* const b_kept = w_kept + 2 * CH * a.tpr;
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
-  Raw8<XF32> next[CH];
-  auto fetch = [&](int64_t row) {
+  auto fetch = [&](int slot, int64_t row) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int col = (t + i * a.tpr) * 8;
-      next[i] = row < a.T && col < a.C ? load_raw8<XF32>(a.x, row * a.ldx + col) : zero_raw8<XF32>();
-    }
+    for (int i = 0; i < CH; ++i) ahead.load(slot, i, a.x, row * a.ldx, a.tpr, t, a.C, row < a.T);
+    copies_commit();
   };
-  fetch(static_cast<int64_t>(blockIdx.x) * rows + sub);
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * rows; base < a.T; base += step) {
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) fetch(d, first + sub + d * step);
+  if (!a.few) {
+    keep_param(w_kept, a, a.w, 1.0f);
+    if (THREADS <= 512) keep_param(b_kept, a, a.b, 0.0f);
+    __syncthreads();
+  }
+  int slot = 0;
+  for (int64_t base = first; base < a.T; base += step) {
     const int64_t row = base + sub;
-    float x[CH][8], s[1] = {0.0f};
+    Two x[CH][4], s2 = twice(0.0f);
+    copies_wait<DEPTH - 1>();
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      unpack8<XF32>(next[i], x[i]);
+      unpack8<XF32>(ahead.take(slot, i), x[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] += x[i][j];
+      for (int j = 0; j < 4; ++j) s2 = s2 + x[i][j];
     }
-    fetch(row + step);
+    float s[1] = {lo(s2) + hi(s2)};
+    __syncwarp();
+    fetch(slot, row + DEPTH * step);
+    slot = slot + 1 == DEPTH ? 0 : slot + 1;
     sum(s);
     const float mean = s[0] * a.inv_c;
-    float q[1] = {0.0f};
+    Two q2 = twice(0.0f);
+    const Two minus = twice(-mean);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if ((t + i * a.tpr) * 8 >= a.C) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[i][j] -= mean;
-        q[0] = fmaf(x[i][j], x[i][j], q[0]);
+      for (int j = 0; j < 4; ++j) {
+        x[i][j] = x[i][j] + minus;
+        q2 = fma2(x[i][j], x[i][j], q2);
       }
     }
+    float q[1] = {lo(q2) + hi(q2)};
     sum(q);
     const float rstd = 1.0f / sqrtf(fmaf(q[0], a.inv_c, a.eps));
     if (row >= a.T) continue;
@@ -106,109 +154,218 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const __grid_constant
       a.mean[row] = mean;
       a.rstd[row] = rstd;
     }
+    const Two scale = twice(rstd);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int col = (t + i * a.tpr) * 8;
       if (col >= a.C) continue;
+      Two w[4], b[4];
+      if (a.few)
+        read_param(a.w, a.w_f32, col, 1.0f, w);
+      else
+        take_param(w_kept, a.tpr, t, i, w);
+      if (a.few || THREADS > 512)
+        read_param(a.b, a.w_f32, col, 0.0f, b);
+      else
+        take_param(b_kept, a.tpr, t, i, b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = fmaf(x[i][j] * rstd, w[i][j], b[i][j]);
-      store8<YF32>(a.y, row * a.ldy + col, x[i]);
+      for (int j = 0; j < 4; ++j) x[i][j] = fma2(x[i][j] * scale, w[j], b[j]);
+      store_row8(a, row * a.ldy + col, x[i]);
     }
   }
 }
 
-template <bool XF32, bool GF32, bool DF32, int CH, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+template <bool XF32, bool GF32, int CH, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+  constexpr bool HELD = THREADS == 1024;  // dw and db in shared memory, [piece][half][thread] each
+  constexpr int DEPTH = bwd_depth(THREADS, XF32, GF32);
   __shared__ float part[2][32][2];
-  extern __shared__ float shared_sums[];  // [2][C], where a block has more than one row at a time
+  extern __shared__ float4 shared[];  // rows ahead (x, then dy), then the weight or the HELD sums
   const int t = static_cast<int>(threadIdx.x) % a.tpr, sub = static_cast<int>(threadIdx.x) / a.tpr;
-  const int rows = static_cast<int>(blockDim.x) / a.tpr;
+  const int rows = THREADS / a.tpr;
+  pdl_launch_dependents();  // (the sums' kernel may take its place; it waits for this one)
   GroupSum<2> sum(part, a.tpr);
-  float dw[CH][8], db[CH][8], w[CH][8];
+  Ahead<XF32, CH, DEPTH, THREADS> ahead_x(shared, a.tpr);
+  Ahead<GF32, CH, DEPTH, THREADS> ahead_g(shared + ahead_x.BYTES / 16, a.tpr);
+  float4* const kept = shared + (HELD ? 0 : (ahead_x.BYTES + ahead_g.BYTES) / 16);
+  Raw8<XF32> next_x[HELD ? CH : 1];  // (HELD: the next row in registers instead)
+  Raw8<GF32> next_g[HELD ? CH : 1];
+  Two dw[HELD ? 1 : CH][4], db[HELD ? 1 : CH][4];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int col = (t + i * a.tpr) * 8;
-    if (col < a.C) load_param(a.w, a.w_f32, col, 1.0f, w[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) {
+      if (!HELD)
+        dw[i][j] = db[i][j] = twice(0.0f);
+      else if ((t + i * a.tpr) * 8 < a.C)
+        kept[(i * 4 + j) * THREADS + t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * rows; base < a.T; base += step) {
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  auto fetch_stats = [&](int64_t row) {
+    if (row < a.T) next_mean = __ldg(a.mean + row), next_rstd = __ldg(a.rstd + row);
+  };
+  auto fetch = [&](int slot, int64_t row) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int col = (t + i * a.tpr) * 8;
+      const bool inside = row < a.T && col < a.C;
+      if (HELD) {
+        next_x[HELD ? i : 0] = inside ? load_raw8<XF32>(a.x, row * a.ldx + col) : zero_raw8<XF32>();
+        next_g[HELD ? i : 0] = inside ? load_raw8<GF32>(a.dy, row * a.ldg + col) : zero_raw8<GF32>();
+      } else {
+        ahead_x.load(slot, i, a.x, row * a.ldx, a.tpr, t, a.C, row < a.T);
+        ahead_g.load(slot, i, a.dy, row * a.ldg, a.tpr, t, a.C, row < a.T);
+      }
+    }
+    if (!HELD) copies_commit();
+  };
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) fetch(d, first + sub + d * step);
+  fetch_stats(first + sub);
+  if (!HELD && !a.few) {
+    keep_param(kept, a, a.w, 1.0f);
+    __syncthreads();
+  }
+  int slot = 0;
+  for (int64_t base = first; base < a.T; base += step) {
     const int64_t row = base + sub;
     const bool live = row < a.T;
-    const float mean = live ? a.mean[row] : 0.0f, rstd = live ? a.rstd[row] : 0.0f;
-    float h[CH][8], g[CH][8], s[2] = {0.0f, 0.0f};
+    const float mean = next_mean, rstd = next_rstd;
+    fetch_stats(row + step);
+    Two h[CH][4], g[CH][4], s0 = twice(0.0f), s1 = twice(0.0f);
+    if (!HELD) {
+      copies_wait<DEPTH - 1>();
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      unpack8<XF32>(HELD ? next_x[HELD ? i : 0] : ahead_x.take(slot, i), h[i]);
+      unpack8<GF32>(HELD ? next_g[HELD ? i : 0] : ahead_g.take(slot, i), g[i]);
+    }
+    if (HELD) fetch(0, row + step);
+    const Two minus = twice(-mean), scale = twice(rstd);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int col = (t + i * a.tpr) * 8;
       if (!live || col >= a.C) continue;
-      load8<XF32>(a.x, row * a.ldx + col, h[i]);
-      load8<GF32>(a.dy, row * a.ldg + col, g[i]);
+      Two w[4];
+      if (HELD || a.few)
+        read_param(a.w, a.w_f32, col, 1.0f, w);
+      else
+        take_param(kept, a.tpr, t, i, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        h[i][j] = (h[i][j] - mean) * rstd;
-        dw[i][j] = fmaf(g[i][j], h[i][j], dw[i][j]);
-        db[i][j] += g[i][j];
-        g[i][j] *= w[i][j];
-        s[0] += g[i][j];
-        s[1] = fmaf(g[i][j], h[i][j], s[1]);
+      for (int j = 0; j < 4; ++j) h[i][j] = (h[i][j] + minus) * scale;
+      if (!HELD) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          dw[HELD ? 0 : i][j] = fma2(g[i][j], h[i][j], dw[HELD ? 0 : i][j]);
+          db[HELD ? 0 : i][j] = db[HELD ? 0 : i][j] + g[i][j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // (dw, db of two columns)
+          float4* p = kept + (i * 4 + j) * THREADS + t;
+          const float4 v = *p;
+          const Two vw = fma2(g[i][j], h[i][j], two(v.x, v.y)), vb = two(v.z, v.w) + g[i][j];
+          *p = make_float4(lo(vw), hi(vw), lo(vb), hi(vb));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        g[i][j] = g[i][j] * w[j];
+        s0 = s0 + g[i][j];
+        s1 = fma2(g[i][j], h[i][j], s1);
       }
     }
+    if (!HELD) {
+      __syncwarp();
+      fetch(slot, row + DEPTH * step);
+      slot = slot + 1 == DEPTH ? 0 : slot + 1;
+    }
+    float s[2] = {lo(s0) + hi(s0), lo(s1) + hi(s1)};
     sum(s);
     if (!live) continue;
-    const float m0 = s[0] * a.inv_c, m1 = s[1] * a.inv_c;
+    const Two c0 = twice(-s[0] * a.inv_c * rstd), c1 = twice(-s[1] * a.inv_c * rstd);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int col = (t + i * a.tpr) * 8;
       if (col >= a.C) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[i][j] = (g[i][j] - m0 - h[i][j] * m1) * rstd;
-      store8<DF32>(a.y, row * a.ldy + col, g[i]);
+      for (int j = 0; j < 4; ++j) g[i][j] = fma2(g[i][j], scale, fma2(h[i][j], c1, c0));
+      store_row8(a, row * a.ldy + col, g[i]);
     }
   }
   if (a.partial == nullptr) return;
   float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.C;
-  // the rows that the block had at a time are added in their order
+  if (HELD) {  // (one row at a time, each thread its own columns)
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int col = (t + i * a.tpr) * 8;
+      if (col >= a.C) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 v = kept[(i * 4 + j) * THREADS + t];
+        *reinterpret_cast<float2*>(out + col + 2 * j) = make_float2(v.x, v.y);
+        *reinterpret_cast<float2*>(out + a.C + col + 2 * j) = make_float2(v.z, v.w);
+      }
+    }
+    return;
+  }
+  // the rows that the block had at a time are added in their order (the rows ahead have been used up)
+  copies_wait<0>();
+  __syncthreads();
+  float* const held = reinterpret_cast<float*>(shared);
   for (int r = 0; r < rows; ++r) {
     if (sub == r) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
+      for (int i = 0; i < (HELD ? 1 : CH); ++i) {
         const int col = (t + i * a.tpr) * 8;
         if (col >= a.C) continue;
         if (r > 0) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dw[i][j] += shared_sums[col + j], db[i][j] += shared_sums[a.C + col + j];
+          for (int j = 0; j < 4; ++j) {
+            dw[i][j] = dw[i][j] + two(held[col + 2 * j], held[col + 2 * j + 1]);
+            db[i][j] = db[i][j] + two(held[a.C + col + 2 * j], held[a.C + col + 2 * j + 1]);
+          }
         }
-        if (r == rows - 1) {
-          store8<true>(out, col, dw[i]);
-          store8<true>(out, a.C + col, db[i]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) shared_sums[col + j] = dw[i][j], shared_sums[a.C + col + j] = db[i][j];
-        }
+        float* const to = r == rows - 1 ? out : held;
+        store8<true>(to, col, dw[i]);
+        store8<true>(to, a.C + col, db[i]);
       }
     }
     if (r < rows - 1) __syncthreads();
   }
 }
 
-// dw and db: the blocks' sums in block order (8 runs of blocks, then the runs).
-__global__ void __launch_bounds__(256) norm_sum_kernel(const float* partial, int blocks, int C, float* dw, float* db) {
-  __shared__ float runs[8][32];
+// dw and db: the blocks' sums in block order (32 runs of blocks, then the runs).  Few loads a thread, all in
+// flight: with 8 runs this took 10 us for 304 blocks of 4096 columns.
+__global__ void __launch_bounds__(1024) norm_sum_kernel(const float* partial, int blocks, int C, float* dw, float* db) {
+  __shared__ float runs[32][33];
   const int lane = static_cast<int>(threadIdx.x) & 31, run = static_cast<int>(threadIdx.x) >> 5;
   const int col = static_cast<int>(blockIdx.x) * 32 + lane;  // of 2 C
-  const int per = (blocks + 7) / 8;
+  const int per = (blocks + 31) / 32, end = min(blocks, (run + 1) * per);
+  pdl_wait();
   float s = 0.0f;
-  if (col < 2 * C)
-    for (int k = run * per; k < blocks && k < (run + 1) * per; ++k) s += partial[static_cast<int64_t>(k) * 2 * C + col];
+  if (col < 2 * C) {
+    const float* p = partial + static_cast<int64_t>(run * per) * 2 * C + col;
+#pragma unroll 10
+    for (int k = run * per; k < end; ++k, p += 2 * C) s += __ldcg(p);
+  }
   runs[run][lane] = s;
   __syncthreads();
-  if (run != 0 || col >= 2 * C) return;
-  for (int k = 1; k < 8; ++k) s += runs[k][lane];
-  if (col < C)
-    dw[col] = s;
+  // warp r adds the runs of column r: lanes meet pairwise
+  s = runs[lane][run];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  const int mine = static_cast<int>(blockIdx.x) * 32 + run;
+  if (lane != 0 || mine >= 2 * C) return;
+  if (mine < C)
+    dw[mine] = s;
   else
-    db[col - C] = s;
+    db[mine - C] = s;
 }
 
 // Threads per row: a power of two that leaves a thread at most two pieces of eight columns.
@@ -234,11 +391,35 @@ Shape shape_of(int64_t T, int64_t C, int sm_count, int per_sm) {
   return s;
 }
 
-constexpr int kFwdPerSm = 4, kBwdPerSm = 2;  // blocks of 256 threads an SM
+constexpr int kBwdPerSm = 2;  // blocks of 256 threads an SM
+
+int fwd_per_sm(int x_f32) { return x_f32 ? 3 : 4; }
 
 template <typename F>
 void by_bool(bool v, F f) {
   v ? f(std::true_type()) : f(std::false_type());
+}
+
+template <typename F>
+void by_shape(const Shape& s, F f) {
+  if (s.threads == 1024)
+    f(std::integral_constant<int, 2>(), std::integral_constant<int, 1024>());
+  else if (s.threads == 512)
+    f(std::integral_constant<int, 2>(), std::integral_constant<int, 512>());
+  else if (s.pieces == 2)
+    f(std::integral_constant<int, 2>(), std::integral_constant<int, 256>());
+  else
+    f(std::integral_constant<int, 1>(), std::integral_constant<int, 256>());
+}
+
+// Shared memory of the backward pass: rows ahead and the weight, or the sums of 1024 threads.  (A block's sums of several
+// rows at a time, at most 2048 columns, take the place of the rows ahead.)
+template <bool X, bool G, int CH, int N>
+size_t bwd_smem(int tpr) {
+  if (N == 1024) return static_cast<size_t>(CH) * 4 * N * 16;
+  constexpr int DEPTH = bwd_depth(N, X, G), AHEAD = Ahead<X, CH, DEPTH, N>::BYTES + Ahead<G, CH, DEPTH, N>::BYTES;
+  static_assert(N == 1024 || AHEAD >= CH * 8 * 128 * 8, "the sums of a row of 128 threads");
+  return AHEAD + static_cast<size_t>(tpr) * CH * 32;
 }
 
 dp_status check_vector(const void* p) { return is_aligned16(p) ? DP_OK : DP_ERR_ALIGNMENT; }
@@ -254,6 +435,31 @@ int64_t bwd_bytes(int64_t T, int64_t C, int sm_count) { return shape_of(T, C, sm
 bool flag(int v) { return v == 0 || v == 1; }
 
 }  // namespace
+
+cudaError_t set_attributes_layer_norm() {
+  cudaError_t e = cudaSuccess;
+  const int threads[] = {256, 256, 512, 1024};
+  for (int i = 0; i < 16; ++i) {
+    Shape s = {};
+    s.threads = threads[i / 4], s.pieces = i / 4 == 0 ? 1 : 2;
+    by_bool(i & 1, [&](auto xf) {
+      by_bool(i & 2, [&](auto gf) {
+        by_shape(s, [&](auto pieces, auto n) {
+          constexpr bool X = decltype(xf)::value, G = decltype(gf)::value;
+          constexpr int CH = decltype(pieces)::value, N = decltype(n)::value;
+          if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(norm_fwd_kernel<X, CH, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Ahead<X, CH, fwd_depth(N, X), N>::BYTES + N * CH * (N == 1024 ? 32 : 64));
+          if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(norm_bwd_kernel<X, G, CH, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(bwd_smem<X, G, CH, N>(N)));
+        });
+      });
+    });
+  }
+  return e;
+}
+
 }  // namespace dp
 
 extern "C" dp_status dp_layer_norm_workspace_size(int64_t T, int64_t C, int sm_count, size_t* bytes) {
@@ -287,22 +493,21 @@ extern "C" dp_status dp_layer_norm_fwd(const void* x, int64_t ldx, int x_f32, co
   DeviceContext ctx;
   if ((st = device_context(&ctx)) != DP_OK) return st;
   if (T == 0) return DP_OK;
-  const Shape s = shape_of(T, C, ctx.sm_count, kFwdPerSm);
+  const Shape s = shape_of(T, C, ctx.sm_count, fwd_per_sm(x_f32));
   NormArgs a = {};
   a.x = x, a.ldx = ldx, a.w = weight, a.b = bias, a.w_f32 = weight_f32, a.eps = static_cast<float>(eps);
   a.T = T, a.C = static_cast<int32_t>(C), a.tpr = s.tpr, a.inv_c = 1.0f / static_cast<float>(C);
   a.y = y, a.ldy = ldy, a.mean = mean, a.rstd = rstd;
+  a.few = T <= s.blocks * s.rows;
+  a.y_f32 = code;
   const unsigned grid = static_cast<unsigned>(s.blocks);
   cudaStream_t str = static_cast<cudaStream_t>(stream);
   by_bool(x_f32, [&](auto xf) {
-    by_bool(code, [&](auto yf) {
-      constexpr bool X = decltype(xf)::value, Y = decltype(yf)::value;
-      if (s.threads > 256)
-        norm_fwd_kernel<X, Y, 2, 1024><<<grid, s.threads, 0, str>>>(a);
-      else if (s.pieces == 2)
-        norm_fwd_kernel<X, Y, 2, 256><<<grid, s.threads, 0, str>>>(a);
-      else
-        norm_fwd_kernel<X, Y, 1, 256><<<grid, s.threads, 0, str>>>(a);
+    by_shape(s, [&](auto pieces, auto threads) {
+      constexpr bool X = decltype(xf)::value;
+      constexpr int CH = decltype(pieces)::value, N = decltype(threads)::value;
+      const size_t smem = Ahead<X, CH, fwd_depth(N, X), N>::BYTES + static_cast<size_t>(s.tpr) * CH * (N == 1024 ? 32 : 64);
+      norm_fwd_kernel<X, CH, N><<<grid, N, smem, str>>>(a);
     });
   });
   return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
@@ -343,25 +548,31 @@ extern "C" dp_status dp_layer_norm_bwd(const void* dy, int64_t ldg, int dy_f32, 
   a.x = x, a.ldx = ldx, a.w = weight, a.w_f32 = weight_f32;
   a.T = T, a.C = static_cast<int32_t>(C), a.tpr = s.tpr, a.inv_c = 1.0f / static_cast<float>(C);
   a.y = dx, a.ldy = ld_dx, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
+  a.few = T <= s.blocks * s.rows;
   a.dy = dy, a.ldg = ldg, a.partial = dw ? static_cast<float*>(workspace) : nullptr;
+  a.y_f32 = code;
   const unsigned grid = static_cast<unsigned>(s.blocks);
-  const size_t smem = s.rows > 1 && dw ? static_cast<size_t>(C) * 8 : 0;  // (at most 2048 columns: 16 KB)
   by_bool(x_f32, [&](auto xf) {
     by_bool(dy_f32, [&](auto gf) {
-      by_bool(code, [&](auto df) {
-        constexpr bool X = decltype(xf)::value, G = decltype(gf)::value, D = decltype(df)::value;
-        if (s.threads > 256)
-          norm_bwd_kernel<X, G, D, 2, 1024><<<grid, s.threads, smem, str>>>(a);
-        else if (s.pieces == 2)
-          norm_bwd_kernel<X, G, D, 2, 256><<<grid, s.threads, smem, str>>>(a);
-        else
-          norm_bwd_kernel<X, G, D, 1, 256><<<grid, s.threads, smem, str>>>(a);
+      by_shape(s, [&](auto pieces, auto threads) {
+        constexpr bool X = decltype(xf)::value, G = decltype(gf)::value;
+        constexpr int CH = decltype(pieces)::value, N = decltype(threads)::value;
+        norm_bwd_kernel<X, G, CH, N><<<grid, N, bwd_smem<X, G, CH, N>(s.tpr), str>>>(a);
       });
     });
   });
   if (cudaGetLastError() != cudaSuccess) return DP_ERR_LAUNCH;
   if (dw == nullptr) return DP_OK;
-  norm_sum_kernel<<<static_cast<unsigned>((2 * C + 31) / 32), 256, 0, str>>>(a.partial, static_cast<int>(s.blocks),
-                                                                             static_cast<int>(C), dw, db);
-  return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((2 * C + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = str;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_sum_kernel, static_cast<const float*>(a.partial), static_cast<int>(s.blocks),
+                                           static_cast<int>(C), dw, db);
+  return e == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
 }

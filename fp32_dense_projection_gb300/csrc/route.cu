@@ -38,9 +38,9 @@ struct RouteArgs {
 
 // An integer that orders as the float does; above 0 for every float.
 __device__ __forceinline__ uint32_t order_key(float x) {
-  if (x != x) return 0xFFFFFFFFu;
   const uint32_t b = __float_as_uint(x + 0.0f);  // (-0 becomes +0)
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  const uint32_t key = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+  return x != x ? 0xFFFFFFFFu : key;
 }
 
 __device__ __forceinline__ float key_value(uint32_t key) {
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     if (all != kClosed) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (key[i] > kClosed) total += expf(key_value(key[i]) - m);
+        if (key[i] > kClosed) total += __expf(key_value(key[i]) - m);
       total = warp_sum(total);
     }
   }
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     if (j == 0) first = best;
     if (lane == j) mine = best, at = static_cast<int>(index);
   }
-  float e = at >= 0 ? expf(key_value(mine) - key_value(first)) : 0.0f;
+  float e = at >= 0 ? __expf(key_value(mine) - key_value(first)) : 0.0f;
   if (a.renormalize) total = warp_sum(e);
   if (lane < a.k) {
     a.gates[t * a.k + lane] = at >= 0 ? e / total : 0.0f;
@@ -143,28 +143,37 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
     if (__any_sync(kAll, nan)) m = __uint_as_float(0x7FC00000u);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      l[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - m);
+      l[i] = l[i] == -INFINITY ? 0.0f : __expf(l[i] - m);
       total += l[i];
     }
     total = warp_sum(total);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) d[i] = l[i] == 0.0f ? 0.0f : -(l[i] / total) * s;
   }
-  const float own = a.renormalize ? g * (dg - s) : g * dg;
-  for (int j = 0; j < a.k; ++j) {
-    const int e = __shfl_sync(kAll, at, j);
-    const float v = __shfl_sync(kAll, own, j);
-    if (e < 0) continue;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (e == lane + 32 * i) d[i] += v;
-  }
   float* out = a.dlogits + t * a.ldd;
+  const float own = a.renormalize ? g * (dg - s) : g * dg;
+  // choices that differ, as route_kernel makes them, are put into the row by the lanes that have them;
+  // others are added up in their order
+  const uint32_t alike = __match_any_sync(kAll, at >= 0 ? at : -1 - lane);  // (all lanes: not behind a condition)
+  const bool repeated = __any_sync(kAll, __popc(alike) > 1);
+  if (repeated) {
+    for (int j = 0; j < a.k; ++j) {
+      const int e = __shfl_sync(kAll, at, j);
+      const float v = __shfl_sync(kAll, own, j);
+      if (e < 0) continue;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (e == lane + 32 * i) d[i] += v;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = lane + 32 * i;
     if (e < a.E) out[e] = d[i];
   }
+  __syncwarp();
+  // (gate_e is p_e: what stands there is -p_e s)
+  if (!repeated && at >= 0) out[at] = g * (dg - s);
 }
 
 template <typename F>

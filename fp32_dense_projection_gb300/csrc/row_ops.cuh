@@ -71,6 +71,94 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&x)[
   }
 }
 
+// Two FP32 values in one register pair, and the packed operations on them (each rounded as two
+// ordinary ones).
+struct Two {
+  uint64_t v;
+};
+__device__ __forceinline__ Two two(float lo, float hi) {
+  return {(static_cast<uint64_t>(__float_as_uint(hi)) << 32) | __float_as_uint(lo)};
+}
+__device__ __forceinline__ Two twice(float x) { return two(x, x); }
+__device__ __forceinline__ float lo(Two a) { return __uint_as_float(static_cast<uint32_t>(a.v)); }
+__device__ __forceinline__ float hi(Two a) { return __uint_as_float(static_cast<uint32_t>(a.v >> 32)); }
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  Two d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  Two d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+
+template <bool F32>
+__device__ __forceinline__ void unpack8(const Raw8<F32>& r, Two (&x)[4]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    x[i] = F32 ? two(__uint_as_float(w[F32 ? 2 * i : 0]), __uint_as_float(w[F32 ? 2 * i + 1 : 0]))
+               : two(__uint_as_float(w[F32 ? 0 : i] << 16), __uint_as_float(w[F32 ? 0 : i] & 0xFFFF0000u));
+}
+
+template <bool F32>
+__device__ __forceinline__ void store8(void* base, int64_t at, const Two (&x)[4]) {
+  const float v[8] = {lo(x[0]), hi(x[0]), lo(x[1]), hi(x[1]), lo(x[2]), hi(x[2]), lo(x[3]), hi(x[3])};
+  store8<F32>(base, at, v);
+}
+
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool inside) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(inside ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// Eight elements each of CH pieces of a thread's rows, DEPTH rows ahead, in shared memory that only
+// its warp touches (so nobody waits at a barrier for them): [row][piece][16 bytes].  A piece's column is
+// 8 t + 8 i threads-per-row.  FP32 pieces are 32 bytes: a warp's (or a shorter row's) threads copy the
+// 16-byte units in their order, half of them at a time, so that each request is whole sectors
+// (each thread its own 32 bytes asked twice for every sector: 3.9 TB/s in the forward pass of 1024
+// columns), and their places are exchanged within every second eight, so that threads read
+// their own two from different banks.
+template <bool F32, int CH, int DEPTH, int THREADS>
+struct Ahead {
+  static constexpr int UNITS = F32 ? 2 : 1, BYTES = DEPTH * CH * UNITS * THREADS * 16;
+  uint4* base;
+  int width, m;  // threads that share a row, up to a warp; this one's place among them
+
+  __device__ __forceinline__ Ahead(float4* at, int tpr)
+      : base(reinterpret_cast<uint4*>(at)), width(tpr < 32 ? tpr : 32), m(static_cast<int>(threadIdx.x) & (width - 1)) {
+    base += (static_cast<int>(threadIdx.x) - m) * UNITS;
+  }
+  static __device__ __forceinline__ int place(int u) { return F32 ? (u & ~7) | ((u ^ (u >> 3)) & 7) : u; }
+  // Ask for piece i of a row of x that begins at `row` (elements; rows outside are zeros); t: this thread's place in its row.
+  __device__ __forceinline__ void load(int slot, int i, const void* x, int64_t row, int tpr, int t, int cols, bool inside) const {
+#pragma unroll
+    for (int h = 0; h < UNITS; ++h) {
+      const int u = h * width + m, col = i * tpr * 8 + (F32 ? (t - m) * 8 + u * 4 : t * 8);
+      const bool in = inside && col < cols;
+      copy16_async(smem_addr(base + (slot * CH + i) * UNITS * THREADS + place(u)),
+                   static_cast<const char*>(x) + (in ? (row + col) * (F32 ? 4 : 2) : 0), in);
+    }
+  }
+  // (behind copies_wait and __syncwarp)
+  __device__ __forceinline__ Raw8<F32> take(int slot, int i) const {
+    Raw8<F32> r;
+#pragma unroll
+    for (int h = 0; h < UNITS; ++h) r.v[h] = base[(slot * CH + i) * UNITS * THREADS + place(UNITS * m + h)];
+    return r;
+  }
+};
+
 // Sums of N values over groups of `tpr` consecutive threads (a power of two; the block's threads
 // are a multiple of it and all call this).  Groups of more than a warp meet in `part`
 // [2][32][N], used by turns: one barrier a sum.

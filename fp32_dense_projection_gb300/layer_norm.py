@@ -64,12 +64,11 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=c.BF
 
     def work(st):
         y, code = c.output(out, shape, out_dtype, index, x.device, name)
-        stats = torch.empty((2, T), dtype=c.F32, device=x.device)
-        mean, rstd = stats[0], stats[1]
-        at = stats.data_ptr()
+        mean = torch.empty((T,), dtype=c.F32, device=x.device)
+        rstd = torch.empty((T,), dtype=c.F32, device=x.device)
         code = _fn["dp_layer_norm_fwd"](x.data_ptr(), ldx, f32, None if weight is None else weight.data_ptr(),
                                         None if bias is None else bias.data_ptr(), w32, eps, y.data_ptr(),
-                                        c.ld(y, name, "out", shape), code, at, at + 4 * T, T, C, st)
+                                        c.ld(y, name, "out", shape), code, mean.data_ptr(), rstd.data_ptr(), T, C, st)
         if code:
             c.check(code, name)
         return y, mean, rstd

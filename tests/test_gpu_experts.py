@@ -227,6 +227,17 @@ def test_sort_one_sided(pairs):
         check_sort(torch.where(at % 2 == 0, E, at % E).int(), E)
 
 
+@pytest.mark.parametrize("cluster", ["0", "1"])
+@pytest.mark.parametrize("pairs", [1, 500, 4096, 70001, 262144, 500000])
+def test_sort_forms(pairs, cluster, monkeypatch):
+    """One launch of a cluster, and two launches."""
+    monkeypatch.setenv("DP_FORCE_SORT_CLUSTER", cluster)
+    for E in (1, 64, 257, 1024):
+        choice = torch.randint(-1, E, (pairs,), device=DEV, generator=gen(E), dtype=torch.int32)
+        check_sort(choice, E)
+        check_sort(torch.sort(choice, descending=True).values.long(), E)
+
+
 def test_sort_feeds_the_grouped_products():
     """The offsets are the grouped products', whose padding the pairs without an expert are."""
     E, T, k, C = 16, 500, 2, 64

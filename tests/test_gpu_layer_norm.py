@@ -7,7 +7,7 @@ products a few u each).  Outputs in BF16 add half a step, 2^-8 |y|.
 Backward, from the FP32 mean and rs: h and g h carry 3 to 5 u, the two means 28 u and theirs, the last operations
 4 u:  |dx| within 48 u rs (|g| + mean|g| + |h| mean|g h|).
 dw, db: a block adds its rows one after the other (at most T / blocks each), then the rows that it has at a time
-(at most 64), then the blocks in 8 runs: within (T / 152 + 64 + 80 + 8) u of the sum of magnitudes.
+(at most 64), then the at most 304 blocks in runs of up to 80: within (T / 152 + 64 + 80 + 8) u of the sum of magnitudes.
 """
 import pytest
 import torch
