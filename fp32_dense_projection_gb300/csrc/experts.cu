@@ -38,6 +38,7 @@ struct SortArgs {
   int wide;  // int64 choices
   int32_t P, E;
   int32_t per_block, per_warp;  // pairs, multiples of 32
+  int32_t bits;                 // of the keys 0 .. E
   int32_t* counts;              // [blocks][E + 1], more than one block
   int32_t* offsets;
   int32_t* row_of;
@@ -49,12 +50,24 @@ __device__ __forceinline__ int key_of(const SortArgs& a, int i) {
   return e >= 0 && e < a.E ? static_cast<int>(e) : a.E;
 }
 
+// The lanes whose keys (below 2^bits; -1: none) are this lane's.  A vote for each bit: the hardware's match takes longer the
+// more keys differ.
+__device__ __forceinline__ uint32_t same_keys(int key, int bits) {
+  uint32_t same = __ballot_sync(kAll, key >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const bool set = (key >> b) & 1;
+    const uint32_t m = __ballot_sync(kAll, set);
+    same &= set ? m : ~m;
+  }
+  return same;
+}
+
 // The warp's own counts of the pairs in its run, in shared memory (zero before).
 __device__ __forceinline__ void count_run(const SortArgs& a, int begin, int end, int32_t* mine) {
   const int lane = static_cast<int>(threadIdx.x) & 31;
   for (int i = begin + lane; i - lane < end; i += 32) {
     const int key = i < end ? key_of(a, i) : -1;
-    const uint32_t same = __match_any_sync(kAll, key);
+    const uint32_t same = same_keys(key, a.bits);
     if (key >= 0 && lane == __ffs(static_cast<int>(same)) - 1) mine[key] += __popc(same);
     __syncwarp();
   }
@@ -133,7 +146,7 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const __grid_constant_
   int32_t* mine = warp_counts + warp * n;
   for (int i = begin + lane; i - lane < end; i += 32) {
     const int key = i < end ? key_of(a, i) : -1;
-    const uint32_t same = __match_any_sync(kAll, key);
+    const uint32_t same = same_keys(key, a.bits);
     const int32_t at = key >= 0 ? base[key] + mine[key] + __popc(same & ((1u << lane) - 1)) : 0;
     __syncwarp();
     if (key >= 0) {
@@ -146,7 +159,8 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const __grid_constant_
 }
 
 // The same in one launch, for pairs that one cluster can go through: the blocks read each other's
-// counts from their shared memory.  (16384 pairs over 64 experts: 22 us in two launches of four blocks.)
+// counts from their shared memory.  (16384 pairs over 64 experts: 22 us in two launches of
+// four blocks.)
 __global__ void __launch_bounds__(1024) sort_cluster_kernel(const __grid_constant__ SortArgs a) {
   extern __shared__ int32_t warp_counts[];  // [warps][E + 1], then the block's totals [E + 1] and base [E + 1]
   __shared__ int32_t scan[32];
@@ -154,37 +168,45 @@ __global__ void __launch_bounds__(1024) sort_cluster_kernel(const __grid_constan
   const int n = a.E + 1, tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int threads = static_cast<int>(blockDim.x), warps = threads >> 5;
   const int rank = static_cast<int>(blockIdx.x), ranks = static_cast<int>(gridDim.x);
-  int32_t* const totals = warp_counts + warps * n;
+  const int stride = n | 1;  // (counters of one expert lie in different banks)
+  int32_t* const totals = warp_counts + warps * stride;
   int32_t* const base = totals + n;
   const int begin = static_cast<int>(min(static_cast<int64_t>(a.P), static_cast<int64_t>(rank) * a.per_block + warp * a.per_warp));
   const int end = static_cast<int>(min(static_cast<int64_t>(a.P), static_cast<int64_t>(begin) + a.per_warp));
   int held[HELD];
 #pragma unroll
   for (int r = 0; r < HELD; ++r) held[r] = begin + r * 32 + lane < end ? key_of(a, begin + r * 32 + lane) : -1;
-  for (int i = tid; i < warps * n; i += threads) warp_counts[i] = 0;
+  for (int i = tid; i < warps * stride; i += threads) warp_counts[i] = 0;
+  uint32_t held_same[HELD];
+#pragma unroll
+  for (int r = 0; r < HELD; ++r)
+    if (begin + r * 32 < end) held_same[r] = same_keys(held[r], a.bits);
   __syncthreads();
-  int32_t* const mine = warp_counts + warp * n;
-  auto walk = [&](auto step) {  // the warp's runs in order: first pair of the run, this lane's key (-1: none)
+  int32_t* const mine = warp_counts + warp * stride;
+  auto walk = [&](auto step) {  // the warp's runs in order: first pair of the run, this lane's key (-1: none) and the lanes that share it
 #pragma unroll
     for (int r = 0; r < HELD; ++r)
-      if (begin + r * 32 < end) step(begin + r * 32, held[r]);
-    for (int i = begin + HELD * 32; i < end; i += 32) step(i, i + lane < end ? key_of(a, i + lane) : -1);
+      if (begin + r * 32 < end) step(begin + r * 32, held[r], held_same[r]);
+    for (int i = begin + HELD * 32; i < end; i += 32) {
+      const int key = i + lane < end ? key_of(a, i + lane) : -1;
+      step(i, key, same_keys(key, a.bits));
+    }
   };
-  walk([&](int, int key) {
-    const uint32_t same = __match_any_sync(kAll, key);
+  walk([&](int, int key, uint32_t same) {
     if (key >= 0 && lane == __ffs(static_cast<int>(same)) - 1) mine[key] += __popc(same);
     __syncwarp();
   });
   __syncthreads();
-  for (int e = tid; e < n; e += threads) {  // positions of the warps within their block
-    int32_t own = 0;
-#pragma unroll 8
-    for (int w = 0; w < warps; ++w) {
-      const int32_t c = warp_counts[w * n + e];
-      warp_counts[w * n + e] = own;
-      own += c;
+  for (int e = warp; e < n; e += warps) {  // positions of the warps within their block: lane w has warp w's count
+    const int32_t own = lane < warps ? warp_counts[lane * stride + e] : 0;
+    int32_t incl = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(kAll, incl, d);
+      if (lane >= d) incl += o;
     }
-    totals[e] = own;
+    if (lane < warps) warp_counts[lane * stride + e] = incl - own;
+    if (lane == 31) totals[e] = incl;
   }
   if (ranks > 1)
     cluster_sync();
@@ -211,11 +233,15 @@ __global__ void __launch_bounds__(1024) sort_cluster_kernel(const __grid_constan
     }
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    int32_t lower = carry;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) lower += scan[w];
-      carry += scan[w];
+    int32_t sums = lane < warps ? scan[lane] : 0;  // of the warps up to this lane's
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(kAll, sums, d);
+      if (lane >= d) sums += o;
     }
+    const int32_t up_to = __shfl_sync(kAll, sums, warp > 0 ? warp - 1 : 0);
+    const int32_t lower = carry + (warp > 0 ? up_to : 0);
+    carry += __shfl_sync(kAll, sums, 31);
     if (e < n) {
       const int32_t start = lower + incl - total;
       base[e] = start + before;
@@ -223,8 +249,7 @@ __global__ void __launch_bounds__(1024) sort_cluster_kernel(const __grid_constan
     }
     __syncthreads();
   }
-  walk([&](int first, int key) {
-    const uint32_t same = __match_any_sync(kAll, key);
+  walk([&](int first, int key, uint32_t same) {
     const int32_t at = key >= 0 ? base[key] + mine[key] + __popc(same & ((1u << lane) - 1)) : 0;
     __syncwarp();
     if (key >= 0) {
@@ -257,7 +282,7 @@ SortShape sort_shape(int64_t P, int64_t E) {
     s.per_warp = static_cast<int32_t>((all + s.ranks * s.warps - 1) / (s.ranks * s.warps) * 32);
     s.per_block = s.per_warp * s.warps;
     s.blocks = 1;  // (no workspace)
-    s.smem = static_cast<size_t>(s.warps + 2) * (E + 1) * 4;
+    s.smem = (static_cast<size_t>(s.warps) * ((E + 1) | 1) + 2 * (E + 1)) * 4;
     return s;
   }
   // (counters and positions: at most 46 KB)
@@ -433,7 +458,7 @@ unsigned token_blocks(const RowArgs& a) { return static_cast<unsigned>((a.T + 25
 
 cudaError_t set_attributes_experts() {
   return cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>((32 + 2) * (kMaxExpertCount + 1) * 4));
+                              static_cast<int>((32 + 2) * (kMaxExpertCount + 2) * 4));
 }
 
 }  // namespace dp
@@ -467,6 +492,7 @@ extern "C" dp_status dp_expert_sort(const void* choice, int choice_bits, int64_t
   cudaStream_t str = static_cast<cudaStream_t>(stream);
   SortArgs a = {};
   a.choice = choice, a.wide = choice_bits == 64, a.P = static_cast<int32_t>(pairs), a.E = static_cast<int32_t>(E);
+  while ((1 << a.bits) <= a.E) ++a.bits;
   a.per_block = s.per_block, a.per_warp = s.per_warp, a.counts = static_cast<int32_t*>(workspace);
   a.offsets = offsets, a.row_of = row_of, a.order = order;
   if (s.ranks > 0) {

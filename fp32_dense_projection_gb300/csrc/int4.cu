@@ -572,17 +572,27 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const __grid_constan
     row[k] = r, at[k] = i - r * a.per_row;
     raw[k] = i < a.pieces ? load_raw8<WF32>(a.w, row[k] * a.ldw + at[k] * 8) : zero_raw8<WF32>();
   }
+  // (a row is whole groups: the threads of a group are in range together)
+  // Of a group's first four threads (and every four after them), each divides for one of the pieces.
+  static_assert(kPerThread == 4, "pieces are shared among four threads");
+  float its_hi = 0.0f, its_minus_lo = 0.0f;
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
-    // (a row is whole groups: the threads of a group are in range together)
     float hi, minus_lo;
     group_range<WF32>(raw[k], width, hi, minus_lo);
-    float s = a.z != nullptr ? __fdiv_rn(hi + minus_lo, 15.0f) : __fdiv_rn(max_nan(hi, minus_lo), 7.0f);
-    s = max_nan(s, kTinyScale);
-    if (!a.s_f32) s = __bfloat162float(__float2bfloat16_rn(s));
-    float z = 8.0f;
-    if (a.z != nullptr) z = fminf(fmaxf(rintf(__fdiv_rn(minus_lo, s)), 0.0f), 15.0f);
-    const Two inverse = twice(__frcp_rn(s)), round = twice(kRound), unround = twice(-kRound), zero = twice(z);
+    if ((threadIdx.x & 3) == k) its_hi = hi, its_minus_lo = minus_lo;
+  }
+  float its_s = a.z != nullptr ? __fdiv_rn(its_hi + its_minus_lo, 15.0f) : __fdiv_rn(max_nan(its_hi, its_minus_lo), 7.0f);
+  its_s = max_nan(its_s, kTinyScale);
+  if (!a.s_f32) its_s = __bfloat162float(__float2bfloat16_rn(its_s));
+  float its_z = 8.0f;
+  if (a.z != nullptr) its_z = fminf(fmaxf(rintf(__fdiv_rn(its_minus_lo, its_s)), 0.0f), 15.0f);
+  const float its_inverse = __frcp_rn(its_s);
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const int from = static_cast<int>(threadIdx.x & 28) + k;
+    const float s = __shfl_sync(kAll, its_s, from), z = __shfl_sync(kAll, its_z, from);
+    const Two inverse = twice(__shfl_sync(kAll, its_inverse, from)), round = twice(kRound), unround = twice(-kRound), zero = twice(z);
     Two w[4];
     unpack8<WF32>(raw[k], w);
     float far = 0.0f, low = 0.0f, high = 0.0f;  // the farthest a quotient is from its integer; codes 0 to 3 and 4 to 7 as one number

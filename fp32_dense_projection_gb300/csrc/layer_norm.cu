@@ -40,7 +40,7 @@ struct NormArgs {
   int y_f32;
   float* mean;
   float* rstd;
-  int few;  // a block has one row (or one for each group of threads): weight and bias come straight from memory
+  int few;  // (forward) a block has one row, or one for each group of threads: weight and bias come straight from memory
   const void* dy;
   int64_t ldg;
   float* partial;  // [blocks][2][C]: each block's sums for dw and db (null: no weight)
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (XF32 ? 3 : 4) : THR
     const int64_t row = base + sub;
     Two x[CH][4], s2 = twice(0.0f);
     copies_wait<DEPTH - 1>();
-    __syncwarp();
+    if (XF32) __syncwarp();
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       unpack8<XF32>(ahead.take(slot, i), x[i]);
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (XF32 ? 3 : 4) : THR
       for (int j = 0; j < 4; ++j) s2 = s2 + x[i][j];
     }
     float s[1] = {lo(s2) + hi(s2)};
-    __syncwarp();
+    if (XF32) __syncwarp();
     fetch(slot, row + DEPTH * step);
     slot = slot + 1 == DEPTH ? 0 : slot + 1;
     sum(s);
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_bwd_kern
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) fetch(d, first + sub + d * step);
   fetch_stats(first + sub);
-  if (!HELD && !a.few) {
+  if (!HELD) {
     keep_param(kept, a, a.w, 1.0f);
     __syncthreads();
   }
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_bwd_kern
     Two h[CH][4], g[CH][4], s0 = twice(0.0f), s1 = twice(0.0f);
     if (!HELD) {
       copies_wait<DEPTH - 1>();
-      __syncwarp();
+      if (XF32 || GF32) __syncwarp();
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_bwd_kern
       const int col = (t + i * a.tpr) * 8;
       if (!live || col >= a.C) continue;
       Two w[4];
-      if (HELD || a.few)
+      if (HELD)
         read_param(a.w, a.w_f32, col, 1.0f, w);
       else
         take_param(kept, a.tpr, t, i, w);
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_bwd_kern
       }
     }
     if (!HELD) {
-      __syncwarp();
+      if (XF32 || GF32) __syncwarp();
       fetch(slot, row + DEPTH * step);
       slot = slot + 1 == DEPTH ? 0 : slot + 1;
     }
@@ -548,7 +548,6 @@ extern "C" dp_status dp_layer_norm_bwd(const void* dy, int64_t ldg, int dy_f32, 
   a.x = x, a.ldx = ldx, a.w = weight, a.w_f32 = weight_f32;
   a.T = T, a.C = static_cast<int32_t>(C), a.tpr = s.tpr, a.inv_c = 1.0f / static_cast<float>(C);
   a.y = dx, a.ldy = ld_dx, a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
-  a.few = T <= s.blocks * s.rows;
   a.dy = dy, a.ldg = ldg, a.partial = dw ? static_cast<float*>(workspace) : nullptr;
   a.y_f32 = code;
   const unsigned grid = static_cast<unsigned>(s.blocks);

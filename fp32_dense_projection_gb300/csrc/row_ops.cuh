@@ -150,7 +150,7 @@ struct Ahead {
                    static_cast<const char*>(x) + (in ? (row + col) * (F32 ? 4 : 2) : 0), in);
     }
   }
-  // (behind copies_wait and __syncwarp)
+  // (behind copies_wait and, FP32, __syncwarp)
   __device__ __forceinline__ Raw8<F32> take(int slot, int i) const {
     Raw8<F32> r;
 #pragma unroll
