@@ -277,7 +277,7 @@ SortShape sort_shape(int64_t P, int64_t E) {
   const int want = tuning_override("DP_FORCE_SORT_CLUSTER", -1);
   if (want < 0 ? P <= kClusterPairs : want != 0) {
     const int64_t all = (P + 31) / 32;
-    s.ranks = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, (all + 127) / 128)));
+    s.ranks = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, (all + 63) / 64)));
     s.warps = all <= 16 ? 8 : 32;
     s.per_warp = static_cast<int32_t>((all + s.ranks * s.warps - 1) / (s.ranks * s.warps) * 32);
     s.per_block = s.per_warp * s.warps;

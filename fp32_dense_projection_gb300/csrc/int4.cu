@@ -599,7 +599,8 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const __grid_constan
     auto codes = [&](int j, Two quotient) {
       const Two n = (quotient + round) + unround, off = fma2(n, twice(-1.0f), quotient), c = n + zero;
       far = fmaxf(far, fmaxf(fabsf(lo(off)), fabsf(dp::hi(off))));
-      const float c0 = fminf(fmaxf(lo(c), 0.0f), 15.0f), c1 = fminf(fmaxf(dp::hi(c), 0.0f), 15.0f);  // (NaN: 0)
+      // (at least 0: rn(-lo / s) = -rn(lo / s); above 15 only where both ends of a range are rounded up)
+      const float c0 = a.z != nullptr ? fminf(lo(c), 15.0f) : lo(c), c1 = a.z != nullptr ? fminf(dp::hi(c), 15.0f) : dp::hi(c);
       float& sum = j < 2 ? low : high;
       const float weight = j % 2 ? 256.0f : 1.0f;
       sum = fmaf(c1, 16.0f * weight, fmaf(c0, weight, sum));

@@ -8,8 +8,8 @@
 //   over all:         dl_e = p_e ([e chosen] dg_e - s)
 //
 // Bound: the logits' bytes; a few rows are latency.  One warp a token holds its logits in
-// registers, so they are read once; a choice is two warp-wide integer reductions (the largest key,
-// then the lowest index that has it).  Keys order floats as integers: -0 as +0, NaN above all.
+// registers, so they are read once; a choice is a warp-wide maximum of integers and the votes for it,
+// register by register, up to the first that has it.  Keys order floats as integers: -0 as +0, NaN above all.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -91,16 +91,19 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
     best = __reduce_max_sync(kAll, best);
     if (best <= kClosed) break;
-    uint32_t index = kAll;
+    // the lowest index that has it, which is taken out: indexes go up by lanes, then by registers
+    int index = -1;
 #pragma unroll
-    for (int i = VPL - 1; i >= 0; --i)
-      if (key[i] == best) index = static_cast<uint32_t>(lane + 32 * i);
-    index = __reduce_min_sync(kAll, index);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (index == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
+    for (int i = 0; i < VPL; ++i) {
+      if (index >= 0) continue;
+      const uint32_t have = __ballot_sync(kAll, key[i] == best);
+      if (have == 0) continue;
+      const int owner = __ffs(static_cast<int>(have)) - 1;
+      index = owner + 32 * i;
+      if (lane == owner) key[i] = 0;
+    }
     if (j == 0) first = best;
-    if (lane == j) mine = best, at = static_cast<int>(index);
+    if (lane == j) mine = best, at = index;
   }
   float e = at >= 0 ? __expf(key_value(mine) - key_value(first)) : 0.0f;
   if (a.renormalize) total = warp_sum(e);

@@ -159,9 +159,9 @@ struct Ahead {
   }
 };
 
-// Sums of N values over groups of `tpr` consecutive threads (a power of two; the block's threads
-// are a multiple of it and all call this).  Groups of more than a warp meet in `part`
-// [2][32][N], used by turns: one barrier a sum.
+// Sums of N values over groups of `tpr` consecutive threads (a power of two; all threads of a group call
+// this).  Groups of more than a warp meet in `part`
+// [2][32][N], used by turns, and at a barrier of their own: one a sum, and groups do not wait for others.
 template <int N>
 struct GroupSum {
   float (*part)[32][N];
@@ -179,7 +179,7 @@ struct GroupSum {
 #pragma unroll
       for (int i = 0; i < N; ++i) part[turn][warp][i] = v[i];
     }
-    __syncthreads();
+    named_sync(1 + static_cast<uint32_t>(threadIdx.x) / static_cast<uint32_t>(tpr), static_cast<uint32_t>(tpr));
     const int warps = tpr >> 5, from = warp / warps * warps + lane % warps;
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = part[turn][from][i];
