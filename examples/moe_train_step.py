@@ -3,10 +3,10 @@
     python examples/moe_train_step.py [--steps 30]
 
 The layer:  logits = router(x)                      FP32 router GEMM (BF16x3)
-            each token goes to its top-k experts    rows sorted by expert, offsets on the device
-            h_e = x W1_e^T, relu(h)^2, y_e = h W2_e^T    products grouped by expert
+            each token goes to its top-k experts    route_topk, expert_sort: offsets on the device
+            h_e = x W1_e^T, relu(h)^2, y_e = h W2_e^T    expert_gather, products grouped by expert
             shared expert z = x V^T                 8-bit product, scales per 128 values
-            out = z + sum_k gate_k y_k
+            out = z + sum_k gate_k y_k              expert_combine
 Loss: mean squared distance to a target.  The backward pass takes the grouped and 8-bit
 gradients (dgrad and wgrad) and the router's; AdamW then updates FP32 master weights, with
 8-bit moments, and writes the BF16 copies that the next step's products read.  No step
@@ -40,23 +40,17 @@ class MoELayer:
                             copies=[None, self.w1_16, self.w2_16, self.shared_16])
 
     def route(self, x):
-        """Each token's experts and gates, and the (token, choice) pairs sorted by expert."""
+        """Each token's experts, its logits and gates, the row of each (token, choice) pair sorted by expert, and the
+        groups' offsets."""
         logits = dp.router_fwd(x.float(), self.router)
-        top, choice = logits.topk(self.top_k, dim=1)
-        gates = top.softmax(1)
-        order = choice.flatten().argsort(stable=True)
-        counts = torch.zeros(self.experts, dtype=torch.int32, device=x.device)
-        counts.scatter_add_(0, choice.flatten(), torch.ones_like(order, dtype=torch.int32))
-        offsets = torch.zeros(self.experts + 1, dtype=torch.int32, device=x.device)
-        offsets[1:] = counts.cumsum(0)
-        return choice, gates, order, offsets
+        gates, choice = dp.route_topk(logits, self.top_k)
+        offsets, row_of, _ = dp.expert_sort(choice, self.experts)
+        return choice.long(), (logits, gates), row_of, offsets
 
     def forward_backward(self, x, target):
         """(loss, gradients in the order of ``masters``)."""
-        T = x.shape[0]
-        choice, gates, order, offsets = self.route(x)
-        token = order // self.top_k
-        rows = x[token]                                            # sorted by expert
+        choice, (logits, gates), row_of, offsets = self.route(x)
+        rows = dp.expert_gather(x, row_of)                         # sorted by expert
 
         h = dp.dp_gemm_fwd_grouped(rows, self.w1_16, offsets)
         r = h.float().relu()
@@ -66,8 +60,7 @@ class MoELayer:
         xq, xs, xq_col, xs_col = dp.fp8_quantize(x, "both")       # forward and weight gradient, one read
         vq, vs = dp.fp8_quantize(self.shared_16, "block")
         out = dp.dp_gemm_fwd_fp8(xq, xs, vq, vs, out_dtype=torch.float32)
-        gate = gates.flatten()[order]
-        out.index_add_(0, token, y * gate[:, None])
+        out = dp.expert_combine(y, row_of, gates, add=out, out_dtype=torch.float32)
 
         err = out - target
         loss = err.square().mean()
@@ -79,20 +72,16 @@ class MoELayer:
         dx = dp.dp_gemm_dgrad_fp8(dq, ds, vq, vs, out_dtype=torch.float32)
 
         # experts
-        d_rows = d_out[token]
-        d_gate = (d_rows * y).sum(1)
-        d_y = (d_rows * gate[:, None]).bfloat16()
+        d_y, d_gates = dp.expert_combine_bwd(d_out, y, row_of, gates)
         d_w2 = dp.dp_gemm_wgrad_grouped(d_y, a, offsets, out_dtype=torch.float32)
         d_a = dp.dp_gemm_dgrad_grouped(d_y, self.w2_16, offsets, out_dtype=torch.float32)
         d_h = (d_a * 2.0 * r).bfloat16()
         d_w1 = dp.dp_gemm_wgrad_grouped(d_h, rows, offsets, out_dtype=torch.float32)
-        dx.index_add_(0, token, dp.dp_gemm_dgrad_grouped(d_h, self.w1_16, offsets, out_dtype=torch.float32))
+        d_rows = dp.dp_gemm_dgrad_grouped(d_h, self.w1_16, offsets, out_dtype=torch.float32)
+        dx = dp.expert_combine(d_rows, row_of, add=dx, out_dtype=torch.float32)
 
         # router: the softmax of the chosen logits
-        d_g = torch.empty_like(gates)
-        d_g.view(-1)[order] = d_gate
-        d_top = gates * (d_g - (d_g * gates).sum(1, keepdim=True))
-        d_logits = torch.zeros(T, self.experts, device=x.device).scatter_(1, choice, d_top)
+        d_logits = dp.route_topk_bwd(d_gates, logits, gates, choice.int())
         d_router = dp.router_wgrad(d_logits, x.float())
         dx += dp.router_dgrad(d_logits, self.router)
         return loss, [d_router, d_w1, d_w2, d_shared], dx
