@@ -70,6 +70,16 @@ def output(out, shape, dtype, index: int, device, name: str):
     return out, code
 
 
+def output_rows(out, shape, dtype, index: int, device, name: str, what: str = "out"):
+    """The given 2-D output, checked, or a new one; its type's code; its leading dimension."""
+    if out is None:
+        code = OUT_CODES.get(dtype)
+        if code is not None:
+            return torch.empty(shape, dtype=dtype, device=device), code, shape[1]
+    y, code = output(out, shape, dtype, index, device, name)
+    return y, code, ld(y, name, what, shape)
+
+
 def on_stream(index: int, stream, tensors, work):
     """work(raw stream) with the device current and, if one is given, on that stream: memory
     that the call allocates belongs to it, and its operands' memory is not handed out again

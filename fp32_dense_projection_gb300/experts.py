@@ -23,6 +23,7 @@ from . import _call as c
 _I32 = torch.int32
 _BITS = {torch.int32: 32, torch.int64: 64}
 _ROW_TYPES = {c.BF16: 0, c.F32: 1}
+_NO_WORKSPACE = 4  # DP_ERR_WORKSPACE
 _fn = {}
 
 
@@ -105,9 +106,9 @@ def route_topk_bwd(d_gates, logits, gates, choice, renormalize=True, out=None, s
         c.load()
 
     def work(st):
-        d, _ = c.output(out, shape, c.F32, index, logits.device, name)
+        d, _, ldd = c.output_rows(out, shape, c.F32, index, logits.device, name)
         code = _fn["dp_route_topk_bwd"](d_gates.data_ptr(), logits.data_ptr(), ld, gates.data_ptr(), choice.data_ptr(), d.data_ptr(),
-                                        c.ld(d, name, "out", shape), T, E, k, bool(renormalize), st)
+                                        ldd, T, E, k, bool(renormalize), st)
         if code:
             c.check(code, name)
         return d
@@ -138,19 +139,15 @@ def expert_sort(choice, E, workspace=None, stream=None):
         offsets = torch.empty((E + 1 if E > 0 else 1,), dtype=_I32, device=device)
         row_of = torch.empty(choice.shape, dtype=_I32, device=device)
         order = torch.empty((pairs,), dtype=_I32, device=device)
-        buf, size = workspace, 0
-        if buf is None:
+        buf, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+        args = (choice.data_ptr(), bits, pairs, E, offsets.data_ptr(), row_of.data_ptr(), order.data_ptr())
+        code = _fn["dp_expert_sort"](*args, buf, size, st)
+        if code == _NO_WORKSPACE and workspace is None:  # (very many pairs: nothing has been launched)
             n = ctypes.c_size_t(0)
             code = _fn["dp_expert_sort_workspace_size"](pairs, E, ctypes.byref(n))
-            if code:
-                c.check(code, name)
-            size = n.value
-            if size:
-                buf = torch.empty((size,), dtype=torch.uint8, device=device)
-        else:
-            size = buf.nbytes
-        code = _fn["dp_expert_sort"](choice.data_ptr(), bits, pairs, E, offsets.data_ptr(), row_of.data_ptr(), order.data_ptr(),
-                                     None if buf is None else buf.data_ptr(), size, st)
+            if not code:
+                buf = torch.empty((n.value,), dtype=torch.uint8, device=device)
+                code = _fn["dp_expert_sort"](*args, buf.data_ptr(), n.value, st)
         if code:
             c.check(code, name)
         return offsets, row_of, order
@@ -191,9 +188,8 @@ def expert_gather(x, row_of, out=None, stream=None):
 
     def work(st):
         shape = (T * k, C)
-        rows, _ = c.output(out, shape, x.dtype, index, x.device, name)
-        code = _fn["dp_expert_gather"](x.data_ptr(), ldx, f32, row_of.data_ptr(), rows.data_ptr(), c.ld(rows, name, "out", shape),
-                                       T, k, C, st)
+        rows, _, ldr = c.output_rows(out, shape, x.dtype, index, x.device, name)
+        code = _fn["dp_expert_gather"](x.data_ptr(), ldx, f32, row_of.data_ptr(), rows.data_ptr(), ldr, T, k, C, st)
         if code:
             c.check(code, name)
         return rows
@@ -227,10 +223,9 @@ def expert_combine(y, row_of, gates=None, add=None, out=None, out_dtype=c.BF16, 
         c.load()
 
     def work(st):
-        o, code = c.output(out, shape, out_dtype, index, y.device, name)
+        o, code, ldo = c.output_rows(out, shape, out_dtype, index, y.device, name)
         code = _fn["dp_expert_combine"](y.data_ptr(), ldy, f32, row_of.data_ptr(), None if gates is None else gates.data_ptr(),
-                                        None if add is None else add.data_ptr(), lda, o.data_ptr(), c.ld(o, name, "out", shape), code,
-                                        T, k, C, st)
+                                        None if add is None else add.data_ptr(), lda, o.data_ptr(), ldo, code, T, k, C, st)
         if code:
             c.check(code, name)
         return o
@@ -256,10 +251,10 @@ def expert_combine_bwd(d_out, y, row_of, gates, d_y=None, dy_dtype=c.BF16, strea
         c.load()
 
     def work(st):
-        d, code = c.output(d_y, shape, dy_dtype, index, y.device, name)
+        d, code, ld_dy = c.output_rows(d_y, shape, dy_dtype, index, y.device, name, "d_y")
         d_gates = torch.empty((T, k), dtype=c.F32, device=y.device)
         code = _fn["dp_expert_combine_bwd"](d_out.data_ptr(), ldd, d32, y.data_ptr(), ldy, y32, row_of.data_ptr(), gates.data_ptr(),
-                                            d.data_ptr(), c.ld(d, name, "d_y", shape), code, d_gates.data_ptr(), T, k, C, st)
+                                            d.data_ptr(), ld_dy, code, d_gates.data_ptr(), T, k, C, st)
         if code:
             c.check(code, name)
         return d, d_gates

@@ -135,9 +135,9 @@ def dp_gemm_fwd_int4(X, q, s, zeros=None, out=None, out_dtype=c.BF16, stream=Non
         c.load()
 
     def work(st):
-        y, code = c.output(out, (T, N), out_dtype, index, X.device, name)
+        y, code, ldy = c.output_rows(out, (T, N), out_dtype, index, X.device, name)
         code = _fn[name](X.data_ptr(), ldx, q.data_ptr(), s.data_ptr(), f32, None if zeros is None else zeros.data_ptr(), group,
-                         y.data_ptr(), c.ld(y, name, "out", (T, N)), T, N, K, code, st)
+                         y.data_ptr(), ldy, T, N, K, code, st)
         if code:
             c.check(code, name)
         return y
@@ -165,9 +165,9 @@ def dp_gemm_fwd_int4_grouped(X, q, s, offsets, zeros=None, out=None, out_dtype=c
         c.load()
 
     def work(st):
-        y, code = c.output(out, (T, N), out_dtype, index, X.device, name)
+        y, code, ldy = c.output_rows(out, (T, N), out_dtype, index, X.device, name)
         code = _fn[name](X.data_ptr(), ldx, q.data_ptr(), s.data_ptr(), f32, None if zeros is None else zeros.data_ptr(), group,
-                         offsets.data_ptr(), bits, y.data_ptr(), c.ld(y, name, "out", (T, N)), E, T, N, K, code, st)
+                         offsets.data_ptr(), bits, y.data_ptr(), ldy, E, T, N, K, code, st)
         if code:
             c.check(code, name)
         return y

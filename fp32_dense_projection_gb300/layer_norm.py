@@ -63,17 +63,34 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=c.BF
         c.load()
 
     def work(st):
-        y, code = c.output(out, shape, out_dtype, index, x.device, name)
+        y, code, ldy = c.output_rows(out, shape, out_dtype, index, x.device, name)
         mean = torch.empty((T,), dtype=c.F32, device=x.device)
         rstd = torch.empty((T,), dtype=c.F32, device=x.device)
         code = _fn["dp_layer_norm_fwd"](x.data_ptr(), ldx, f32, None if weight is None else weight.data_ptr(),
-                                        None if bias is None else bias.data_ptr(), w32, eps, y.data_ptr(),
-                                        c.ld(y, name, "out", shape), code, mean.data_ptr(), rstd.data_ptr(), T, C, st)
+                                        None if bias is None else bias.data_ptr(), w32, eps, y.data_ptr(), ldy,
+                                        code, mean.data_ptr(), rstd.data_ptr(), T, C, st)
         if code:
             c.check(code, name)
         return y, mean, rstd
 
     return c.on_stream(index, stream, (x, weight, bias, out), work)
+
+
+_last_size = (None, 0)  # the last call's sizes and what they need
+
+
+def _workspace_size(index, T, C):
+    """Of the current device (asked again only where the sizes change)."""
+    global _last_size
+    key, size = _last_size
+    if key != (index, T, C):
+        n = ctypes.c_size_t(0)
+        status = _fn["dp_layer_norm_workspace_size"](T, C, 0, ctypes.byref(n))
+        if status:
+            c.check(status, "layer_norm_bwd")
+        size = n.value
+        _last_size = (index, T, C), size
+    return size
 
 
 def layer_norm_bwd(dY, x, mean, rstd, weight=None, dX=None, dx_dtype=c.BF16, workspace=None, stream=None):
@@ -99,24 +116,20 @@ def layer_norm_bwd(dY, x, mean, rstd, weight=None, dX=None, dx_dtype=c.BF16, wor
         c.load()
 
     def work(st):
-        d, code = c.output(dX, shape, dx_dtype, index, dY.device, name)
+        d, code, ld_dx = c.output_rows(dX, shape, dx_dtype, index, dY.device, name, "dX")
         dW = dB = buf = None
         size = 0
         if weight is not None:
             dW = torch.empty((C,), dtype=c.F32, device=dY.device)
             dB = torch.empty((C,), dtype=c.F32, device=dY.device)
             if workspace is None:
-                n = ctypes.c_size_t(0)
-                status = _fn["dp_layer_norm_workspace_size"](T, C, 0, ctypes.byref(n))
-                if status:
-                    c.check(status, name)
-                size = n.value
+                size = _workspace_size(index, T, C)
                 buf = torch.empty((size,), dtype=torch.uint8, device=dY.device)
             else:
                 buf, size = workspace, workspace.nbytes
         status = _fn["dp_layer_norm_bwd"](dY.data_ptr(), ldg, g32, x.data_ptr(), ldx, x32, mean.data_ptr(), rstd.data_ptr(),
                                           None if weight is None else weight.data_ptr(), weight is not None and weight.dtype is c.F32,
-                                          d.data_ptr(), c.ld(d, name, "dX", shape), code, None if dW is None else dW.data_ptr(),
+                                          d.data_ptr(), ld_dx, code, None if dW is None else dW.data_ptr(),
                                           None if dB is None else dB.data_ptr(), T, C, None if buf is None else buf.data_ptr(), size, st)
         if status:
             c.check(status, name)
