@@ -343,10 +343,13 @@ __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ Row
   }
 }
 
-constexpr int kBatch = 4;  // rows of a token whose loads are in flight together
+constexpr int kBatch = 4;  // rows of a token whose loads are in flight together (combine: 2 where there are no more)
 
-template <bool YF32, bool OF32>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ RowArgs a) {
+// (With loads for no more rows than there are: 8192 tokens of 2 rows of 4096 in BF16 36.5 us, 38.8 with room for four;
+// 16384 of one row of 1024 16.4, 19.2.  BF16 rows, five blocks an SM: 2048 tokens of 8 rows of 4096 26.3 us, 4096 of 3 rows
+// 26.3; with six 27.6 and 25.4; with the four that 50 registers leave 28.4 and 26.  FP32 rows need their registers: 27 us, 40 with 40.)
+template <bool YF32, bool OF32, int BATCH>
+__global__ void __launch_bounds__(256, YF32 ? 4 : 5) combine_kernel(const __grid_constant__ RowArgs a) {
   const int sub = static_cast<int>(threadIdx.x) / a.tpr, lane = static_cast<int>(threadIdx.x) % a.tpr;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (256 / a.tpr) + sub;
   if (t >= a.T) return;
@@ -358,19 +361,19 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ro
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] = 0.0f;
     }
-    for (int j0 = 0; j0 < a.k; j0 += kBatch) {
-      Raw8<YF32> v[kBatch];
-      float g[kBatch];
-      bool live[kBatch];
+    for (int j0 = 0; j0 < a.k; j0 += BATCH) {
+      Raw8<YF32> v[BATCH];
+      float g[BATCH];
+      bool live[BATCH];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
+      for (int j = 0; j < BATCH; ++j) {
         const Place at = j0 + j < a.k ? place_of(a, t * a.k + j0 + j) : Place{-1, false};
         live[j] = at.live, g[j] = 1.0f;
         v[j] = at.live ? load_raw8<YF32>(a.x, at.row * a.ldx + col) : zero_raw8<YF32>();
         if (at.live && a.gates != nullptr) g[j] = __ldg(a.gates + t * a.k + j0 + j);
       }
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
+      for (int j = 0; j < BATCH; ++j) {
         if (!live[j]) continue;
         float x[8];
         unpack8<YF32>(v[j], x);
@@ -554,7 +557,11 @@ extern "C" dp_status dp_expert_combine(const void* y, int64_t ldy, int y_f32, co
   a.x = y, a.ldx = ldy, a.add = add, a.ld_add = ld_add, a.out = out, a.ldo = ldo;
   by_bool(y_f32, [&](auto yf) {
     by_bool(code, [&](auto of) {
-      combine_kernel<decltype(yf)::value, decltype(of)::value><<<token_blocks(a), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+      constexpr bool Y = decltype(yf)::value, O = decltype(of)::value;
+      if (k <= 2)
+        combine_kernel<Y, O, 2><<<token_blocks(a), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+      else
+        combine_kernel<Y, O, kBatch><<<token_blocks(a), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
     });
   });
   return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;

@@ -555,7 +555,8 @@ __device__ __forceinline__ void group_range(const Raw8<F32>& raw, int width, flo
 // A thread takes 8 neighbouring values, the G / 8 threads of a group share their range.  The rounded
 // quotient rn(w / s) is that of w times 1 / s except next to a border between two codes, where
 // the division is done.  Bound: HBM bytes, and beside them instructions; 12288 x 4096 BF16 with zero points
-// took 100 us with a division for every value, 78 with it at the borders only, and so with packed arithmetic.
+// took 100 us with a division for every value, 78 with it at the borders only, 51 with one thread of four dividing
+// for a group, and NEW with addresses counted in 32 bits.
 template <bool WF32>
 __global__ void __launch_bounds__(256) int4_quantize_kernel(const __grid_constant__ CodeArgs a) {
   constexpr float kRound = 12582912.0f;  // 1.5 2^23: adding it leaves the nearest integer, to even between two
@@ -563,14 +564,10 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const __grid_constan
   const int width = 1 << a.group_shift;
   const uint32_t first = blockIdx.x * (256u * kPerThread) + threadIdx.x;
   Raw8<WF32> raw[kPerThread];
-  int64_t row[kPerThread];
-  uint32_t at[kPerThread];
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
-    const uint32_t i = first + k * 256;
-    const uint32_t r = (__umulhi(i, a.mul) + i) >> a.shift;
-    row[k] = r, at[k] = i - r * a.per_row;
-    raw[k] = i < a.pieces ? load_raw8<WF32>(a.w, row[k] * a.ldw + at[k] * 8) : zero_raw8<WF32>();
+    const uint32_t i = first + k * 256, r = (__umulhi(i, a.mul) + i) >> a.shift;
+    raw[k] = i < a.pieces ? load_raw8<WF32>(a.w, r * a.ldw + (i - r * a.per_row) * 8) : zero_raw8<WF32>();
   }
   // (a row is whole groups: the threads of a group are in range together)
   // Of a group's first four threads (and every four after them), each divides for one of the pieces.
@@ -613,11 +610,11 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const __grid_constan
 #pragma unroll
       for (int j = 0; j < 4; ++j) codes(j, two(__fdiv_rn(lo(w[j]), s), __fdiv_rn(dp::hi(w[j]), s)));
     }
-    if (first + k * 256 >= a.pieces) continue;
-    *reinterpret_cast<uint32_t*>(a.q + (row[k] * a.per_row + at[k]) * 4) =
-        __byte_perm(__float_as_uint(low + kInteger), __float_as_uint(high + kInteger), 0x5410);
+    const uint32_t i = first + k * 256;
+    if (i >= a.pieces) continue;
+    reinterpret_cast<uint32_t*>(a.q)[i] = __byte_perm(__float_as_uint(low + kInteger), __float_as_uint(high + kInteger), 0x5410);
     if ((threadIdx.x & (width - 1)) == 0) {
-      const int64_t g = row[k] * (a.per_row >> a.group_shift) + (at[k] >> a.group_shift);
+      const uint32_t g = i >> a.group_shift;  // (rows are whole groups, and packed)
       if (a.s_f32)
         static_cast<float*>(a.s)[g] = s;
       else
