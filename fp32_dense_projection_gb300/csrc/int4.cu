@@ -556,7 +556,7 @@ __device__ __forceinline__ void group_range(const Raw8<F32>& raw, int width, flo
 // quotient rn(w / s) is that of w times 1 / s except next to a border between two codes, where
 // the division is done.  Bound: HBM bytes, and beside them instructions; 12288 x 4096 BF16 with zero points
 // took 100 us with a division for every value, 78 with it at the borders only, 51 with one thread of four dividing
-// for a group, and NEW with addresses counted in 32 bits.
+// for a group, and 46 with addresses counted in 32 bits.
 template <bool WF32>
 __global__ void __launch_bounds__(256) int4_quantize_kernel(const __grid_constant__ CodeArgs a) {
   constexpr float kRound = 12582912.0f;  // 1.5 2^23: adding it leaves the nearest integer, to even between two

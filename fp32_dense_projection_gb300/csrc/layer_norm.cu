@@ -3,15 +3,24 @@
 // and its backward pass, with g = dy w:
 //   dx = rs (g - mean(g) - h mean(g h)),   dw = sum_t dy h,   db = sum_t dy
 //
-// Bound: HBM bytes (x read, y written; backward x and dy read, dx written).  A row's elements stay
-// in the registers of the threads that share it, so each is read once; the variance is the mean of
-// squared distances from the row's own mean, not a difference of two large sums.  A thread's own
+// Bound: HBM bytes (x read, y written; backward x and dy read, dx written), and beside them the instructions
+// of a row's sums, which a row's every warp spends.  Each row is read from memory once; the variance is the
+// mean of squared distances from the row's own mean, not a difference of two large sums.  A thread's own
 // pieces of the next rows are on their way into shared memory meanwhile (asynchronous copies that
 // nobody else waits for); one row ahead in registers reached 3.6 TB/s in the backward pass.  Arithmetic
 // is packed, two FP32 values an instruction; weight and bias lie in shared memory in FP32.  dw and db
-// are summed in FP32 (registers; shared memory for rows of more than 8192 columns) over the rows that
-// a block visits, in row order; each block writes its sums to the workspace, and a second launch
-// adds them in block order: no atomics, the same bits every time.
+// are summed in FP32 registers over the rows that a block visits, in row order; each block writes its sums
+// to the workspace, and a second launch adds them in block order: no atomics, the same bits every time.
+// The shape depends on C and the types alone, so that a row's result does not depend on how many there are.
+//
+// Four pieces of eight columns a thread halve the warps of a row against two (with 96 MB of x in BF16, us):
+//   forward, BF16     256 columns 34 / 45, 1024  40 / 48, 4096  46 / 55, 5120 55 / 74: always four;
+//   forward, FP32     256         26 / 28, 1024  31 / 32, 4096  36 / 36, 5120 34 / 57: four above 4096 (two leave
+//                     shorter tails of few rows: 16173 x 1024 forward and backward 58, 60 with four);
+//   backward, BF16    1024        59 / 56, 4096  60 / 59, 5120 67 / 75, 8192 68 / 66: four above 4096;
+//   backward, FP32 x  1024        47 / 38, 4096  48 / 41, 5120 55 / 49, 8192 58 / 46: two up to 8192.
+// Above 8192 columns four it is (one thread of 512 has no more than four): 16384 in BF16 76 us, 135 with 1024 threads
+// that held dw and db in shared memory.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -87,21 +96,25 @@ __device__ __forceinline__ void read_param(const void* p, int f32, int col, floa
   for (int j = 0; j < 4; ++j) w[j] = two(v[2 * j], v[2 * j + 1]);
 }
 
-// Rows ahead: as many as shared memory holds beside the blocks that share an SM.
-constexpr int fwd_depth(int threads, bool f32) { return threads == 1024 && f32 ? 1 : 2; }
-constexpr int bwd_depth(int threads, bool x_f32, bool g_f32) { return threads == 1024 ? 1 : x_f32 && g_f32 ? 2 : 3; }
+// Rows in shared memory: as many as it holds beside the blocks that share an SM.
+constexpr int fwd_depth(int threads, int pieces, bool f32) { return threads == 512 && pieces == 4 && f32 ? 1 : 2; }
+constexpr int bwd_depth(int pieces, bool x_f32, bool g_f32) {
+  return pieces == 4 ? (x_f32 || g_f32 ? 1 : 2) : x_f32 && g_f32 ? 2 : 3;
+}
+constexpr int fwd_per_sm(int threads) { return threads == 256 ? 3 : 1; }
+constexpr int bwd_per_sm(int threads) { return threads == 256 ? 2 : 1; }
 
 template <bool XF32, int CH, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? (XF32 ? 3 : 4) : THREADS == 512 && !XF32 ? 2 : 1)
+__global__ void __launch_bounds__(THREADS, fwd_per_sm(THREADS))
     norm_fwd_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int DEPTH = fwd_depth(THREADS, XF32);
+  constexpr int DEPTH = fwd_depth(THREADS, CH, XF32);
   __shared__ float part[2][32][1];
-  extern __shared__ float4 shared[];  // rows ahead, weight and bias (rows of more than 8192 columns: weight only)
+  extern __shared__ float4 shared[];  // rows ahead, weight and bias
   const int t = static_cast<int>(threadIdx.x) % a.tpr, sub = static_cast<int>(threadIdx.x) / a.tpr;
-  const int rows = THREADS / a.tpr;
+  const int rows = static_cast<int>(blockDim.x) / a.tpr;
   GroupSum<1> sum(part, a.tpr);
-  Ahead<XF32, CH, DEPTH, THREADS> ahead(shared, a.tpr);
-  float4* const w_kept = shared + ahead.BYTES / 16;
+  Ahead<XF32, CH> ahead(shared, a.tpr);
+  float4* const w_kept = shared + DEPTH * CH * ahead.UNITS * blockDim.x;
   float4* const b_kept = w_kept + 2 * CH * a.tpr;
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   auto fetch = [&](int slot, int64_t row) {
@@ -114,7 +127,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (XF32 ? 3 : 4) : THR
   for (int d = 0; d < DEPTH; ++d) fetch(d, first + sub + d * step);
   if (!a.few) {
     keep_param(w_kept, a, a.w, 1.0f);
-    if (THREADS <= 512) keep_param(b_kept, a, a.b, 0.0f);
+    keep_param(b_kept, a, a.b, 0.0f);
     __syncthreads();
   }
   int slot = 0;
@@ -148,7 +161,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (XF32 ? 3 : 4) : THR
     }
     float q[1] = {lo(q2) + hi(q2)};
     sum(q);
-    const float rstd = 1.0f / sqrtf(fmaf(q[0], a.inv_c, a.eps));
+    const float rstd = __frsqrt_rn(fmaf(q[0], a.inv_c, a.eps));
     if (row >= a.T) continue;
     if (t == 0) {
       a.mean[row] = mean;
@@ -160,14 +173,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (XF32 ? 3 : 4) : THR
       const int col = (t + i * a.tpr) * 8;
       if (col >= a.C) continue;
       Two w[4], b[4];
-      if (a.few)
+      if (a.few) {
         read_param(a.w, a.w_f32, col, 1.0f, w);
-      else
-        take_param(w_kept, a.tpr, t, i, w);
-      if (a.few || THREADS > 512)
         read_param(a.b, a.w_f32, col, 0.0f, b);
-      else
+      } else {
+        take_param(w_kept, a.tpr, t, i, w);
         take_param(b_kept, a.tpr, t, i, b);
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[i][j] = fma2(x[i][j] * scale, w[j], b[j]);
       store_row8(a, row * a.ldy + col, x[i]);
@@ -175,145 +187,110 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (XF32 ? 3 : 4) : THR
   }
 }
 
+// Four pieces a thread leave no registers for the row: it is read from shared memory again for dx.
 template <bool XF32, bool GF32, int CH, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
-  constexpr bool HELD = THREADS == 1024;  // dw and db in shared memory, [piece][half][thread] each
-  constexpr int DEPTH = bwd_depth(THREADS, XF32, GF32);
+__global__ void __launch_bounds__(THREADS, bwd_per_sm(THREADS)) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+  constexpr bool TWICE = CH == 4;
+  constexpr int DEPTH = bwd_depth(CH, XF32, GF32);
   __shared__ float part[2][32][2];
-  extern __shared__ float4 shared[];  // rows ahead (x, then dy), then the weight or the HELD sums
+  extern __shared__ float4 shared[];  // rows ahead (x, then dy), the weight
   const int t = static_cast<int>(threadIdx.x) % a.tpr, sub = static_cast<int>(threadIdx.x) / a.tpr;
-  const int rows = THREADS / a.tpr;
+  const int rows = static_cast<int>(blockDim.x) / a.tpr;
   pdl_launch_dependents();  // (the sums' kernel may take its place; it waits for this one)
   GroupSum<2> sum(part, a.tpr);
-  Ahead<XF32, CH, DEPTH, THREADS> ahead_x(shared, a.tpr);
-  Ahead<GF32, CH, DEPTH, THREADS> ahead_g(shared + ahead_x.BYTES / 16, a.tpr);
-  float4* const kept = shared + (HELD ? 0 : (ahead_x.BYTES + ahead_g.BYTES) / 16);
-  Raw8<XF32> next_x[HELD ? CH : 1];  // (HELD: the next row in registers instead)
-  Raw8<GF32> next_g[HELD ? CH : 1];
-  Two dw[HELD ? 1 : CH][4], db[HELD ? 1 : CH][4];
+  Ahead<XF32, CH> ahead_x(shared, a.tpr);
+  Ahead<GF32, CH> ahead_g(shared + DEPTH * CH * ahead_x.UNITS * blockDim.x, a.tpr);
+  float4* const kept = shared + DEPTH * CH * (ahead_x.UNITS + ahead_g.UNITS) * blockDim.x;
+  Two dw[CH][4], db[CH][4];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (!HELD)
-        dw[i][j] = db[i][j] = twice(0.0f);
-      else if ((t + i * a.tpr) * 8 < a.C)
-        kept[(i * 4 + j) * THREADS + t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
+    for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = twice(0.0f);
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   float next_mean = 0.0f, next_rstd = 0.0f;
   auto fetch_stats = [&](int64_t row) {
     if (row < a.T) next_mean = __ldg(a.mean + row), next_rstd = __ldg(a.rstd + row);
   };
+  auto fetch_piece = [&](int slot, int i, int64_t row) {
+    ahead_x.load(slot, i, a.x, row * a.ldx, a.tpr, t, a.C, row < a.T);
+    ahead_g.load(slot, i, a.dy, row * a.ldg, a.tpr, t, a.C, row < a.T);
+  };
   auto fetch = [&](int slot, int64_t row) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int col = (t + i * a.tpr) * 8;
-      const bool inside = row < a.T && col < a.C;
-      if (HELD) {
-        next_x[HELD ? i : 0] = inside ? load_raw8<XF32>(a.x, row * a.ldx + col) : zero_raw8<XF32>();
-        next_g[HELD ? i : 0] = inside ? load_raw8<GF32>(a.dy, row * a.ldg + col) : zero_raw8<GF32>();
-      } else {
-        ahead_x.load(slot, i, a.x, row * a.ldx, a.tpr, t, a.C, row < a.T);
-        ahead_g.load(slot, i, a.dy, row * a.ldg, a.tpr, t, a.C, row < a.T);
-      }
-    }
-    if (!HELD) copies_commit();
+    for (int i = 0; i < CH; ++i) fetch_piece(slot, i, row);
+    copies_commit();
   };
   const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) fetch(d, first + sub + d * step);
   fetch_stats(first + sub);
-  if (!HELD) {
-    keep_param(kept, a, a.w, 1.0f);
-    __syncthreads();
-  }
+  keep_param(kept, a, a.w, 1.0f);
+  __syncthreads();
   int slot = 0;
   for (int64_t base = first; base < a.T; base += step) {
     const int64_t row = base + sub;
     const bool live = row < a.T;
     const float mean = next_mean, rstd = next_rstd;
     fetch_stats(row + step);
-    Two h[CH][4], g[CH][4], s0 = twice(0.0f), s1 = twice(0.0f);
-    if (!HELD) {
-      copies_wait<DEPTH - 1>();
-      if (XF32 || GF32) __syncwarp();
-    }
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      unpack8<XF32>(HELD ? next_x[HELD ? i : 0] : ahead_x.take(slot, i), h[i]);
-      unpack8<GF32>(HELD ? next_g[HELD ? i : 0] : ahead_g.take(slot, i), g[i]);
-    }
-    if (HELD) fetch(0, row + step);
+    Two h[TWICE ? 1 : CH][4], g[TWICE ? 1 : CH][4], s0 = twice(0.0f), s1 = twice(0.0f);
     const Two minus = twice(-mean), scale = twice(rstd);
+    copies_wait<DEPTH - 1>();
+    if (XF32 || GF32) __syncwarp();
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int col = (t + i * a.tpr) * 8;
-      if (!live || col >= a.C) continue;
+      Two(&hx)[4] = h[TWICE ? 0 : i], (&gi)[4] = g[TWICE ? 0 : i];
+      unpack8<XF32>(ahead_x.take(slot, i), hx);
+      unpack8<GF32>(ahead_g.take(slot, i), gi);
+      if (!live || (t + i * a.tpr) * 8 >= a.C) continue;
       Two w[4];
-      if (HELD)
-        read_param(a.w, a.w_f32, col, 1.0f, w);
-      else
-        take_param(kept, a.tpr, t, i, w);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[i][j] = (h[i][j] + minus) * scale;
-      if (!HELD) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          dw[HELD ? 0 : i][j] = fma2(g[i][j], h[i][j], dw[HELD ? 0 : i][j]);
-          db[HELD ? 0 : i][j] = db[HELD ? 0 : i][j] + g[i][j];
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // (dw, db of two columns)
-          float4* p = kept + (i * 4 + j) * THREADS + t;
-          const float4 v = *p;
-          const Two vw = fma2(g[i][j], h[i][j], two(v.x, v.y)), vb = two(v.z, v.w) + g[i][j];
-          *p = make_float4(lo(vw), hi(vw), lo(vb), hi(vb));
-        }
-      }
+      take_param(kept, a.tpr, t, i, w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        g[i][j] = g[i][j] * w[j];
-        s0 = s0 + g[i][j];
-        s1 = fma2(g[i][j], h[i][j], s1);
+        hx[j] = (hx[j] + minus) * scale;
+        dw[i][j] = fma2(gi[j], hx[j], dw[i][j]);
+        db[i][j] = db[i][j] + gi[j];
+        gi[j] = gi[j] * w[j];
+        s0 = s0 + gi[j];
+        s1 = fma2(gi[j], hx[j], s1);
       }
     }
-    if (!HELD) {
+    if (!TWICE) {
       if (XF32 || GF32) __syncwarp();
       fetch(slot, row + DEPTH * step);
       slot = slot + 1 == DEPTH ? 0 : slot + 1;
     }
     float s[2] = {lo(s0) + hi(s0), lo(s1) + hi(s1)};
     sum(s);
-    if (!live) continue;
-    const Two c0 = twice(-s[0] * a.inv_c * rstd), c1 = twice(-s[1] * a.inv_c * rstd);
+    const Two c0 = twice(-s[0] * a.inv_c * rstd), c1 = twice(-s[1] * a.inv_c * rstd * (TWICE ? rstd : 1.0f));
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int col = (t + i * a.tpr) * 8;
-      if (col >= a.C) continue;
+      Two(&hx)[4] = h[TWICE ? 0 : i], (&gi)[4] = g[TWICE ? 0 : i];
+      if (TWICE) {
+        unpack8<XF32>(ahead_x.take(slot, i), hx);
+        unpack8<GF32>(ahead_g.take(slot, i), gi);
+        if (XF32 || GF32) __syncwarp();
+        fetch_piece(slot, i, row + DEPTH * step);
+      }
+      if (!live || col >= a.C) continue;
+      if (TWICE) {
+        Two w[4];
+        take_param(kept, a.tpr, t, i, w);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) g[i][j] = fma2(g[i][j], scale, fma2(h[i][j], c1, c0));
-      store_row8(a, row * a.ldy + col, g[i]);
+        for (int j = 0; j < 4; ++j) hx[j] = hx[j] + minus, gi[j] = gi[j] * w[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) gi[j] = fma2(gi[j], scale, fma2(hx[j], c1, c0));
+      store_row8(a, row * a.ldy + col, gi);
+    }
+    if (TWICE) {
+      copies_commit();
+      slot = slot + 1 == DEPTH ? 0 : slot + 1;
     }
   }
   if (a.partial == nullptr) return;
   float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.C;
-  if (HELD) {  // (one row at a time, each thread its own columns)
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int col = (t + i * a.tpr) * 8;
-      if (col >= a.C) continue;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 v = kept[(i * 4 + j) * THREADS + t];
-        *reinterpret_cast<float2*>(out + col + 2 * j) = make_float2(v.x, v.y);
-        *reinterpret_cast<float2*>(out + a.C + col + 2 * j) = make_float2(v.z, v.w);
-      }
-    }
-    return;
-  }
   // the rows that the block had at a time are added in their order (the rows ahead have been used up)
   copies_wait<0>();
   __syncthreads();
@@ -321,7 +298,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_bwd_kern
   for (int r = 0; r < rows; ++r) {
     if (sub == r) {
 #pragma unroll
-      for (int i = 0; i < (HELD ? 1 : CH); ++i) {
+      for (int i = 0; i < CH; ++i) {
         const int col = (t + i * a.tpr) * 8;
         if (col >= a.C) continue;
         if (r > 0) {
@@ -368,32 +345,54 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(const float* partial, in
     db[mine - C] = s;
 }
 
-// Threads per row: a power of two that leaves a thread at most two pieces of eight columns.
-int threads_per_row(int64_t C) {
-  int tpr = 4;
-  while (tpr * 16 < C) tpr *= 2;
-  return tpr;
-}
-
 struct Shape {
-  int tpr, threads, rows, pieces;
+  int pieces, threads;  // of eight columns a thread; the most threads of a block
+  int tpr, rows, block;
+  size_t smem;
   int64_t blocks;
 };
 
-Shape shape_of(int64_t T, int64_t C, int sm_count, int per_sm) {
-  Shape s;
-  s.tpr = threads_per_row(C);
-  s.threads = std::max(256, s.tpr);
-  s.rows = s.threads / s.tpr;
-  s.pieces = C > 8 * s.tpr ? 2 : 1;
-  const int64_t most = static_cast<int64_t>(sm_count) * std::max(1, per_sm * 256 / s.threads);
-  s.blocks = std::min(most, (T + s.rows - 1) / s.rows);
+// Threads per row: a power of two up to a warp, or whole warps.
+Shape shape_of(int64_t C, int pieces, int threads) {
+  Shape s = {pieces, threads};
+  const int n = static_cast<int>((C / 8 + pieces - 1) / pieces);
+  s.tpr = 4;
+  while (s.tpr < 32 && s.tpr < n) s.tpr *= 2;
+  if (n > 32) s.tpr = (n + 31) / 32 * 32;
+  s.rows = threads / s.tpr;
+  s.block = s.rows * s.tpr;
   return s;
 }
 
-constexpr int kBwdPerSm = 2;  // blocks of 256 threads an SM
+constexpr int kMaxShared = 226 * 1024;
 
-int fwd_per_sm(int x_f32) { return x_f32 ? 3 : 4; }
+void set_blocks(Shape* s, int64_t T, int sm_count, int per_sm, size_t smem) {
+  s->smem = smem;
+  int most = per_sm * s->threads / s->block;
+  if (smem > 0) most = std::min(most, static_cast<int>(228 * 1024 / (smem + 1536)));
+  s->blocks = std::min((T + s->rows - 1) / s->rows, static_cast<int64_t>(sm_count) * std::max(1, most));
+}
+
+Shape fwd_shape(int64_t T, int64_t C, bool x_f32, int sm_count, bool* few) {
+  auto with = [&](int pieces) {
+    Shape s = shape_of(C, pieces, C > 4096 ? 512 : 256);
+    const int units = fwd_depth(s.threads, pieces, x_f32) * pieces * (x_f32 ? 2 : 1);
+    set_blocks(&s, T, sm_count, fwd_per_sm(s.threads), static_cast<size_t>(units) * s.block * 16 + static_cast<size_t>(s.tpr) * pieces * 64);
+    *few = T <= s.blocks * s.rows;
+    return s;
+  };
+  return with(!x_f32 || C > 4096 ? 4 : 2);
+}
+
+Shape bwd_base(int64_t C, bool f32) { return shape_of(C, C > (f32 ? 8192 : 4096) ? 4 : 2, C > 4096 ? 512 : 256); }
+
+Shape bwd_shape(int64_t T, int64_t C, bool x_f32, bool g_f32, int sm_count) {
+  Shape s = bwd_base(C, x_f32 || g_f32);
+  const int units = bwd_depth(s.pieces, x_f32, g_f32) * s.pieces * ((x_f32 ? 2 : 1) + (g_f32 ? 2 : 1));
+  // (a block's sums of several rows at a time take the place of the rows ahead: 64 bytes a thread and piece, of two threads or more)
+  set_blocks(&s, T, sm_count, bwd_per_sm(s.threads), static_cast<size_t>(units) * s.block * 16 + static_cast<size_t>(s.tpr) * s.pieces * 32);
+  return s;
+}
 
 template <typename F>
 void by_bool(bool v, F f) {
@@ -402,24 +401,11 @@ void by_bool(bool v, F f) {
 
 template <typename F>
 void by_shape(const Shape& s, F f) {
-  if (s.threads == 1024)
-    f(std::integral_constant<int, 2>(), std::integral_constant<int, 1024>());
-  else if (s.threads == 512)
-    f(std::integral_constant<int, 2>(), std::integral_constant<int, 512>());
-  else if (s.pieces == 2)
-    f(std::integral_constant<int, 2>(), std::integral_constant<int, 256>());
-  else
-    f(std::integral_constant<int, 1>(), std::integral_constant<int, 256>());
-}
-
-// Shared memory of the backward pass: rows ahead and the weight, or the sums of 1024 threads.  (A block's sums of several
-// rows at a time, at most 2048 columns, take the place of the rows ahead.)
-template <bool X, bool G, int CH, int N>
-size_t bwd_smem(int tpr) {
-  if (N == 1024) return static_cast<size_t>(CH) * 4 * N * 16;
-  constexpr int DEPTH = bwd_depth(N, X, G), AHEAD = Ahead<X, CH, DEPTH, N>::BYTES + Ahead<G, CH, DEPTH, N>::BYTES;
-  static_assert(N == 1024 || AHEAD >= CH * 8 * 128 * 8, "the sums of a row of 128 threads");
-  return AHEAD + static_cast<size_t>(tpr) * CH * 32;
+  by_bool(s.pieces == 4, [&](auto four) {
+    by_bool(s.threads == 512, [&](auto large) {
+      f(std::integral_constant<int, decltype(four)::value ? 4 : 2>(), std::integral_constant<int, decltype(large)::value ? 512 : 256>());
+    });
+  });
 }
 
 dp_status check_vector(const void* p) { return is_aligned16(p) ? DP_OK : DP_ERR_ALIGNMENT; }
@@ -430,7 +416,16 @@ dp_status check_norm(int64_t T, int64_t C) {
   return DP_OK;
 }
 
-int64_t bwd_bytes(int64_t T, int64_t C, int sm_count) { return shape_of(T, C, sm_count, kBwdPerSm).blocks * 2 * C * 4; }
+// (for any types: as many blocks as registers allow)
+int64_t bwd_bytes(int64_t T, int64_t C, int sm_count) {
+  int64_t blocks = 0;
+  for (bool f32 : {false, true}) {
+    Shape s = bwd_base(C, f32);
+    set_blocks(&s, T, sm_count, bwd_per_sm(s.threads), 0);
+    blocks = std::max(blocks, s.blocks);
+  }
+  return blocks * 2 * C * 4;
+}
 
 bool flag(int v) { return v == 0 || v == 1; }
 
@@ -438,22 +433,19 @@ bool flag(int v) { return v == 0 || v == 1; }
 
 cudaError_t set_attributes_layer_norm() {
   cudaError_t e = cudaSuccess;
-  const int threads[] = {256, 256, 512, 1024};
-  for (int i = 0; i < 16; ++i) {
+  auto set = [&](const void* kernel) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+  };
+  for (int i = 0; i < 8; ++i) {
     Shape s = {};
-    s.threads = threads[i / 4], s.pieces = i / 4 == 0 ? 1 : 2;
+    s.pieces = i & 2 ? 4 : 2, s.threads = i & 4 ? 512 : 256;
     by_bool(i & 1, [&](auto xf) {
-      by_bool(i & 2, [&](auto gf) {
-        by_shape(s, [&](auto pieces, auto n) {
-          constexpr bool X = decltype(xf)::value, G = decltype(gf)::value;
-          constexpr int CH = decltype(pieces)::value, N = decltype(n)::value;
-          if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(norm_fwd_kernel<X, CH, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     Ahead<X, CH, fwd_depth(N, X), N>::BYTES + N * CH * (N == 1024 ? 32 : 64));
-          if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(norm_bwd_kernel<X, G, CH, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(bwd_smem<X, G, CH, N>(N)));
-        });
+      by_shape(s, [&](auto pieces, auto threads) {
+        constexpr bool X = decltype(xf)::value;
+        constexpr int CH = decltype(pieces)::value, N = decltype(threads)::value;
+        set(reinterpret_cast<const void*>(&norm_fwd_kernel<X, CH, N>));
+        set(reinterpret_cast<const void*>(&norm_bwd_kernel<X, false, CH, N>));
+        set(reinterpret_cast<const void*>(&norm_bwd_kernel<X, true, CH, N>));
       });
     });
   }
@@ -493,12 +485,13 @@ extern "C" dp_status dp_layer_norm_fwd(const void* x, int64_t ldx, int x_f32, co
   DeviceContext ctx;
   if ((st = device_context(&ctx)) != DP_OK) return st;
   if (T == 0) return DP_OK;
-  const Shape s = shape_of(T, C, ctx.sm_count, fwd_per_sm(x_f32));
+  bool few = false;
+  const Shape s = fwd_shape(T, C, x_f32, ctx.sm_count, &few);
   NormArgs a = {};
   a.x = x, a.ldx = ldx, a.w = weight, a.b = bias, a.w_f32 = weight_f32, a.eps = static_cast<float>(eps);
   a.T = T, a.C = static_cast<int32_t>(C), a.tpr = s.tpr, a.inv_c = 1.0f / static_cast<float>(C);
   a.y = y, a.ldy = ldy, a.mean = mean, a.rstd = rstd;
-  a.few = T <= s.blocks * s.rows;
+  a.few = few;
   a.y_f32 = code;
   const unsigned grid = static_cast<unsigned>(s.blocks);
   cudaStream_t str = static_cast<cudaStream_t>(stream);
@@ -506,8 +499,7 @@ extern "C" dp_status dp_layer_norm_fwd(const void* x, int64_t ldx, int x_f32, co
     by_shape(s, [&](auto pieces, auto threads) {
       constexpr bool X = decltype(xf)::value;
       constexpr int CH = decltype(pieces)::value, N = decltype(threads)::value;
-      const size_t smem = Ahead<X, CH, fwd_depth(N, X), N>::BYTES + static_cast<size_t>(s.tpr) * CH * (N == 1024 ? 32 : 64);
-      norm_fwd_kernel<X, CH, N><<<grid, N, smem, str>>>(a);
+      norm_fwd_kernel<X, CH, N><<<grid, s.block, s.smem, str>>>(a);
     });
   });
   return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
@@ -539,7 +531,7 @@ extern "C" dp_status dp_layer_norm_bwd(const void* dy, int64_t ldg, int dy_f32, 
     const bool ok = cudaMemsetAsync(dw, 0, C * 4, str) == cudaSuccess && cudaMemsetAsync(db, 0, C * 4, str) == cudaSuccess;
     return ok ? DP_OK : DP_ERR_LAUNCH;
   }
-  const Shape s = shape_of(T, C, ctx.sm_count, kBwdPerSm);
+  const Shape s = bwd_shape(T, C, x_f32, dy_f32, ctx.sm_count);
   if (dw != nullptr) {
     if (workspace == nullptr || workspace_bytes < static_cast<size_t>(bwd_bytes(T, C, ctx.sm_count))) return DP_ERR_WORKSPACE;
     if (!is_aligned16(workspace)) return DP_ERR_ALIGNMENT;
@@ -556,7 +548,7 @@ extern "C" dp_status dp_layer_norm_bwd(const void* dy, int64_t ldg, int dy_f32, 
       by_shape(s, [&](auto pieces, auto threads) {
         constexpr bool X = decltype(xf)::value, G = decltype(gf)::value;
         constexpr int CH = decltype(pieces)::value, N = decltype(threads)::value;
-        norm_bwd_kernel<X, G, CH, N><<<grid, N, bwd_smem<X, G, CH, N>(s.tpr), str>>>(a);
+        norm_bwd_kernel<X, G, CH, N><<<grid, s.block, s.smem, str>>>(a);
       });
     });
   });

@@ -123,20 +123,20 @@ __device__ __forceinline__ void copies_wait() {
 }
 
 // Eight elements each of CH pieces of a thread's rows, DEPTH rows ahead, in shared memory that only
-// its warp touches (so nobody waits at a barrier for them): [row][piece][16 bytes].  A piece's column is
+// its warp touches (so nobody waits at a barrier for them): [row][piece][unit][16 bytes of `stride` threads].  A piece's column is
 // 8 t + 8 i threads-per-row.  FP32 pieces are 32 bytes: a warp's (or a shorter row's) threads copy the
 // 16-byte units in their order, half of them at a time, so that each request is whole sectors
 // (each thread its own 32 bytes asked twice for every sector: 3.9 TB/s in the forward pass of 1024
 // columns), and their places are exchanged within every second eight, so that threads read
 // their own two from different banks.
-template <bool F32, int CH, int DEPTH, int THREADS>
+template <bool F32, int CH>
 struct Ahead {
-  static constexpr int UNITS = F32 ? 2 : 1, BYTES = DEPTH * CH * UNITS * THREADS * 16;
+  static constexpr int UNITS = F32 ? 2 : 1;
   uint4* base;
-  int width, m;  // threads that share a row, up to a warp; this one's place among them
+  int stride, width, m;  // threads that share a row, up to a warp; this one's place among them
 
   __device__ __forceinline__ Ahead(float4* at, int tpr)
-      : base(reinterpret_cast<uint4*>(at)), width(tpr < 32 ? tpr : 32), m(static_cast<int>(threadIdx.x) & (width - 1)) {
+      : base(reinterpret_cast<uint4*>(at)), stride(static_cast<int>(blockDim.x)), width(tpr < 32 ? tpr : 32), m(static_cast<int>(threadIdx.x) & (width - 1)) {
     base += (static_cast<int>(threadIdx.x) - m) * UNITS;
   }
   static __device__ __forceinline__ int place(int u) { return F32 ? (u & ~7) | ((u ^ (u >> 3)) & 7) : u; }
@@ -146,7 +146,7 @@ struct Ahead {
     for (int h = 0; h < UNITS; ++h) {
       const int u = h * width + m, col = i * tpr * 8 + (F32 ? (t - m) * 8 + u * 4 : t * 8);
       const bool in = inside && col < cols;
-      copy16_async(smem_addr(base + (slot * CH + i) * UNITS * THREADS + place(u)),
+      copy16_async(smem_addr(base + (slot * CH + i) * UNITS * stride + place(u)),
                    static_cast<const char*>(x) + (in ? (row + col) * (F32 ? 4 : 2) : 0), in);
     }
   }
@@ -154,36 +154,45 @@ struct Ahead {
   __device__ __forceinline__ Raw8<F32> take(int slot, int i) const {
     Raw8<F32> r;
 #pragma unroll
-    for (int h = 0; h < UNITS; ++h) r.v[h] = base[(slot * CH + i) * UNITS * THREADS + place(UNITS * m + h)];
+    for (int h = 0; h < UNITS; ++h) r.v[h] = base[(slot * CH + i) * UNITS * stride + place(UNITS * m + h)];
     return r;
   }
 };
 
-// Sums of N values over groups of `tpr` consecutive threads (a power of two; all threads of a group call
-// this).  Groups of more than a warp meet in `part`
+// Sums of N values over groups of `tpr` consecutive threads (a power of two, or whole warps; all threads of a
+// group call this).  Groups of more than a warp meet in `part`
 // [2][32][N], used by turns, and at a barrier of their own: one a sum, and groups do not wait for others.
 template <int N>
 struct GroupSum {
   float (*part)[32][N];
-  int tpr, turn = 0;
-  __device__ __forceinline__ GroupSum(float (*p)[32][N], int threads_per_row) : part(p), tpr(threads_per_row) {}
+  int tpr, warps, from, turn = 0;  // from: the warp whose sum this lane takes, or -1
+  uint32_t barrier;
+  __device__ __forceinline__ GroupSum(float (*p)[32][N], int threads_per_row) : part(p), tpr(threads_per_row), warps(tpr >> 5) {
+    const int group = static_cast<int>(threadIdx.x) / tpr;
+    int span = 1;
+    while (span < warps) span *= 2;
+    from = static_cast<int>(threadIdx.x) & (span - 1);
+    from = from < warps ? group * warps + from : -1;
+    barrier = 1 + group;
+  }
   __device__ __forceinline__ void operator()(float (&v)[N]) {
-    const int lane = static_cast<int>(threadIdx.x) & 31, warp = static_cast<int>(threadIdx.x) >> 5;
-    const int width = tpr < 32 ? tpr : 32;
-    for (int d = 1; d < width; d <<= 1) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      if (d >= tpr) break;
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
     }
     if (tpr <= 32) return;
-    if (lane == 0) {
+    if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) part[turn][warp][i] = v[i];
+      for (int i = 0; i < N; ++i) part[turn][threadIdx.x >> 5][i] = v[i];
     }
-    named_sync(1 + static_cast<uint32_t>(threadIdx.x) / static_cast<uint32_t>(tpr), static_cast<uint32_t>(tpr));
-    const int warps = tpr >> 5, from = warp / warps * warps + lane % warps;
+    named_sync(barrier, static_cast<uint32_t>(tpr));
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = part[turn][from][i];
-    for (int d = 1; d < warps; d <<= 1) {
+    for (int i = 0; i < N; ++i) v[i] = from < 0 ? 0.0f : part[turn][from][i];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      if (d >= warps) break;
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
     }

@@ -95,6 +95,19 @@ def test_forward_and_backward(T, C, xt, wt, out):
     assert dp.device_error() == 0
 
 
+# Rows enough that blocks go round their shared memory several times, in each form: threads of a row a power of two or whole
+# warps, one row or several a block.
+@pytest.mark.parametrize("T,C", [(20000, 72), (9000, 200), (5000, 776), (3001, 1544), (2003, 2560), (1300, 4160), (1200, 5120), (1000, 6152), (901, 8192),
+                                 (700, 8200), (703, 10240), (500, 16384)])
+@pytest.mark.parametrize("xt,gt", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)])
+def test_many_rows(T, C, xt, gt):
+    x = rows(T, C, xt, T + C, shift=0.5)
+    w, b = rows(1, C, F32, 1)[0] + 1, rows(1, C, BF16, 2)[0].float()
+    _, mean, rstd = check_fwd(x, w, b, BF16)
+    check_bwd(rows(T, C, gt, 3 * T + C), x, w, mean, rstd, F32)
+    assert dp.device_error() == 0
+
+
 @pytest.mark.parametrize("T,C", [(5, 64), (200, 1000), (50, 4096), (3, 16384)])
 def test_without_weight_or_bias(T, C):
     x, dy = rows(T, C, BF16, 1, shift=1.0), rows(T, C, BF16, 2)
