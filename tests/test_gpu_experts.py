@@ -101,6 +101,17 @@ def test_route_equal_logits(renormalize):
     assert choice.tolist() == [list(range(6))] * 4
 
 
+@pytest.mark.parametrize("values", [1, 2, 5, 40])
+@pytest.mark.parametrize("E,k", [(40, 3), (64, 16), (128, 8), (250, 2), (256, 16), (256, 17), (500, 12), (1000, 16), (1000, 32)])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_route_few_values(values, E, k, renormalize):
+    """Logits of few values, a third of them closed: more candidates above the bound than lanes, or just as many."""
+    l = torch.randint(0, values, (300, E), device=DEV, generator=gen(E + k)).float() / 4
+    l[:, ::3] = -INF
+    l[7, 5:] = -INF
+    check_route(l, k, renormalize)
+
+
 @pytest.mark.parametrize("renormalize", [True, False])
 def test_route_closed_experts(renormalize):
     """Rows with some, all but one, and all experts closed; the smallest finite logits are open."""
