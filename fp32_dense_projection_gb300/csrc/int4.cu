@@ -523,8 +523,8 @@ __device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
 }
 
 // The largest value and the largest negated one of a group of threads' pieces, and 0.
-template <bool F32>
-__device__ __forceinline__ void group_range(const Raw8<F32>& raw, int width, float& hi, float& minus_lo) {
+template <bool F32, int WIDTH>
+__device__ __forceinline__ void group_range(const Raw8<F32>& raw, float& hi, float& minus_lo) {
   const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
   if (F32) {
     hi = minus_lo = 0.0f;
@@ -534,7 +534,8 @@ __device__ __forceinline__ void group_range(const Raw8<F32>& raw, int width, flo
       hi = max_nan(hi, x);
       minus_lo = max_nan(minus_lo, -x);
     }
-    for (int d = 1; d < width; d <<= 1) {
+#pragma unroll
+    for (int d = 1; d < WIDTH; d <<= 1) {
       hi = max_nan(hi, __shfl_xor_sync(kAll, hi, d));
       minus_lo = max_nan(minus_lo, __shfl_xor_sync(kAll, minus_lo, d));
     }
@@ -546,7 +547,8 @@ __device__ __forceinline__ void group_range(const Raw8<F32>& raw, int width, flo
       down = max_nan2(down, w[j] ^ 0x80008000u);
     }
     uint32_t both = max_nan2(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));
-    for (int d = 1; d < width; d <<= 1) both = max_nan2(both, __shfl_xor_sync(kAll, both, d));
+#pragma unroll
+    for (int d = 1; d < WIDTH; d <<= 1) both = max_nan2(both, __shfl_xor_sync(kAll, both, d));
     hi = __uint_as_float(both << 16);
     minus_lo = __uint_as_float(both & 0xFFFF0000u);
   }
@@ -554,14 +556,14 @@ __device__ __forceinline__ void group_range(const Raw8<F32>& raw, int width, flo
 
 // A thread takes 8 neighbouring values, the G / 8 threads of a group share their range.  The rounded
 // quotient rn(w / s) is that of w times 1 / s except next to a border between two codes, where
-// the division is done.  Bound: HBM bytes, and beside them instructions; 12288 x 4096 BF16 with zero points
-// took 100 us with a division for every value, 78 with it at the borders only, 51 with one thread of four dividing
-// for a group, and 46 with addresses counted in 32 bits.
-template <bool WF32>
+// the division is done.  Bound: HBM bytes for FP32 (12288 x 4096 with zero points, groups of 128: 38 us, 6.0 TB/s),
+// instructions for BF16: 100 us with a division for every value, 78 with it at the borders only, 51 with one
+// thread of four dividing for a group, 46 with addresses counted in 32 bits, 38 with the zero point in the product's
+// addition, codes held to 15 where they can pass it only, and groups' widths known to the compiler.
+template <bool WF32, int WIDTH>
 __global__ void __launch_bounds__(256) int4_quantize_kernel(const __grid_constant__ CodeArgs a) {
   constexpr float kRound = 12582912.0f;  // 1.5 2^23: adding it leaves the nearest integer, to even between two
   constexpr float kInteger = 8388608.0f;  // 2^23: an integer's bits
-  const int width = 1 << a.group_shift;
   const uint32_t first = blockIdx.x * (256u * kPerThread) + threadIdx.x;
   Raw8<WF32> raw[kPerThread];
 #pragma unroll
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const __grid_constan
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
     float hi, minus_lo;
-    group_range<WF32>(raw[k], width, hi, minus_lo);
+    group_range<WF32, WIDTH>(raw[k], hi, minus_lo);
     if ((threadIdx.x & 3) == k) its_hi = hi, its_minus_lo = minus_lo;
   }
   float its_s = a.z != nullptr ? __fdiv_rn(its_hi + its_minus_lo, 15.0f) : __fdiv_rn(max_nan(its_hi, its_minus_lo), 7.0f);
@@ -584,36 +586,40 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const __grid_constan
   if (!a.s_f32) its_s = __bfloat162float(__float2bfloat16_rn(its_s));
   float its_z = 8.0f;
   if (a.z != nullptr) its_z = fminf(fmaxf(rintf(__fdiv_rn(its_minus_lo, its_s)), 0.0f), 15.0f);
-  const float its_inverse = __frcp_rn(its_s);
+  // No reciprocal where it might not be normal, or where both ends of a range may be rounded up and a code pass 15.
+  const float its_inverse = its_s < 1e37f && fmaf(its_hi, __frcp_rn(its_s), its_z) < 15.49f ? __frcp_rn(its_s) : __uint_as_float(0x7FC00000u);
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
     const int from = static_cast<int>(threadIdx.x & 28) + k;
-    const float s = __shfl_sync(kAll, its_s, from), z = __shfl_sync(kAll, its_z, from);
-    const Two inverse = twice(__shfl_sync(kAll, its_inverse, from)), round = twice(kRound), unround = twice(-kRound), zero = twice(z);
+    const float s = __shfl_sync(kAll, its_s, from), z = __shfl_sync(kAll, its_z, from), inverse = __shfl_sync(kAll, its_inverse, from);
     Two w[4];
     unpack8<WF32>(raw[k], w);
     float far = 0.0f, low = 0.0f, high = 0.0f;  // the farthest a quotient is from its integer; codes 0 to 3 and 4 to 7 as one number
-    auto codes = [&](int j, Two quotient) {
-      const Two n = (quotient + round) + unround, off = fma2(n, twice(-1.0f), quotient), c = n + zero;
-      far = fmaxf(far, fmaxf(fabsf(lo(off)), fabsf(dp::hi(off))));
-      // (at least 0: rn(-lo / s) = -rn(lo / s); above 15 only where both ends of a range are rounded up)
-      const float c0 = a.z != nullptr ? fminf(lo(c), 15.0f) : lo(c), c1 = a.z != nullptr ? fminf(dp::hi(c), 15.0f) : dp::hi(c);
+    auto add = [&](int j, float c0, float c1) {
       float& sum = j < 2 ? low : high;
       const float weight = j % 2 ? 256.0f : 1.0f;
       sum = fmaf(c1, 16.0f * weight, fmaf(c0, weight, sum));
     };
 #pragma unroll
-    for (int j = 0; j < 4; ++j) codes(j, w[j] * inverse);
-    // w (1 / s) is within 2^-22 of w / s, so within 4e-6 for quotients up to 15 (1 / s is normal below 1e37)
-    if (far > 0.49999f || !(s < 1e37f)) {
+    for (int j = 0; j < 4; ++j) {
+      const Two v = fma2(w[j], twice(inverse), twice(z)), c = (v + twice(kRound)) + twice(-kRound), off = fma2(c, twice(-1.0f), v);
+      far = fmaxf(far, fmaxf(fabsf(lo(off)), fabsf(dp::hi(off))));
+      add(j, lo(c), dp::hi(c));
+    }
+    // w (1 / s) + z is within 15 2^-22 + 2^-20 of w / s + z: another integer only next to a border between two
+    if (!(far <= 0.49999f) || inverse != inverse) {
       low = high = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) codes(j, two(__fdiv_rn(lo(w[j]), s), __fdiv_rn(dp::hi(w[j]), s)));
+      for (int j = 0; j < 4; ++j) {
+        const Two n = (two(__fdiv_rn(lo(w[j]), s), __fdiv_rn(dp::hi(w[j]), s)) + twice(kRound)) + twice(-kRound), c = n + twice(z);
+        // (at least 0: rn(-lo / s) = -rn(lo / s))
+        add(j, fminf(lo(c), 15.0f), fminf(dp::hi(c), 15.0f));
+      }
     }
     const uint32_t i = first + k * 256;
     if (i >= a.pieces) continue;
     reinterpret_cast<uint32_t*>(a.q)[i] = __byte_perm(__float_as_uint(low + kInteger), __float_as_uint(high + kInteger), 0x5410);
-    if ((threadIdx.x & (width - 1)) == 0) {
+    if ((threadIdx.x & (WIDTH - 1)) == 0) {
       const uint32_t g = i >> a.group_shift;  // (rows are whole groups, and packed)
       if (a.s_f32)
         static_cast<float*>(a.s)[g] = s;
@@ -813,10 +819,13 @@ extern "C" dp_status dp_int4_quantize(const void* w, int64_t ldw, int w_f32, int
   a.w = w, a.ldw = ldw, a.q = static_cast<uint8_t*>(q), a.s = s, a.z = static_cast<uint8_t*>(z), a.s_f32 = s_f32;
   a.K = static_cast<int32_t>(K), a.G = static_cast<int32_t>(group);
   return run_codes(a, rows, w_f32 ? 4 : 2, s_f32 ? 4 : 2, [&](const CodeArgs& part, unsigned grid) {
-    if (w_f32)
-      int4_quantize_kernel<true><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(part);
-    else
-      int4_quantize_kernel<false><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(part);
+    by_group(group, [&](auto g) {
+      constexpr int WIDTH = decltype(g)::value / 8;
+      if (w_f32)
+        int4_quantize_kernel<true, WIDTH><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(part);
+      else
+        int4_quantize_kernel<false, WIDTH><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(part);
+    });
   });
 }
 
