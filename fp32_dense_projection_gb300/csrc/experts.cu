@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const __grid_constant_
 }
 
 // The same in one launch, for pairs that one cluster can go through: the blocks read each other's
-// counts from their shared memory.  (16384 pairs over 64 experts: 22 us in two launches of
-// four blocks.)
+// counts from their shared memory.  Latency: 16384 pairs over 64 experts 8 us (22 in two launches of
+// four blocks; 11 with keys that meet by the hardware's match), 64 pairs 3 us.
 __global__ void __launch_bounds__(1024) sort_cluster_kernel(const __grid_constant__ SortArgs a) {
   extern __shared__ int32_t warp_counts[];  // [warps][E + 1], then the block's totals [E + 1] and base [E + 1]
   __shared__ int32_t scan[32];
@@ -329,6 +329,7 @@ __device__ __forceinline__ Place place_of(const RowArgs& a, int64_t pair) {
   return {-1, false};
 }
 
+// 2048 tokens to 8 rows each of 4096 in BF16: 22 us, 6.8 TB/s.
 template <bool F32>
 __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ RowArgs a) {
   const int sub = static_cast<int>(threadIdx.x) / a.tpr, lane = static_cast<int>(threadIdx.x) % a.tpr;
@@ -385,6 +386,8 @@ __global__ void __launch_bounds__(256, YF32 ? 4 : 5) combine_kernel(const __grid
   }
 }
 
+// dy goes out as y comes in, kBatch rows at a time, and the rows' dots meet together: 2048 tokens of 8 rows of 4096 in
+// BF16 45 us, 6.3 TB/s (62 with a row at a time; with combine before it batches of 2, 4, 8 rows took 84, 80, 88).
 template <bool DF32, bool YF32, bool OF32>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant__ RowArgs a) {
   __shared__ float part[2][32][kBatch];
