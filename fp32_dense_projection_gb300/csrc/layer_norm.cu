@@ -14,13 +14,13 @@
 // The shape depends on C and the types alone, so that a row's result does not depend on how many there are.
 //
 // Four pieces of eight columns a thread halve the warps of a row against two (with 96 MB of x in BF16, us):
-//   forward, BF16     256 columns 34 / 45, 1024  40 / 48, 4096  46 / 55, 5120 55 / 74: always four;
+//   forward, BF16     256 columns 34 / 45, 1024  39 / 48, 4096  46 / 55, 5120 53 / 74: always four;
 //   forward, FP32     256         26 / 28, 1024  31 / 32, 4096  36 / 36, 5120 34 / 57: four above 4096 (two leave
-//                     shorter tails of few rows: 16173 x 1024 forward and backward 58, 60 with four);
-//   backward, BF16    1024        59 / 56, 4096  60 / 59, 5120 67 / 75, 8192 68 / 66: four above 4096;
+//                     shorter tails of few rows: 16173 x 1024 forward and backward 57, 60 with four);
+//   backward, BF16    1024        59 / 56, 4096  60 / 57, 5120 67 / 75, 8192 67 / 66: four above 4096;
 //   backward, FP32 x  1024        47 / 38, 4096  48 / 41, 5120 55 / 49, 8192 58 / 46: two up to 8192.
-// Above 8192 columns four it is (one thread of 512 has no more than four): 16384 in BF16 76 us, 135 with 1024 threads
-// that held dw and db in shared memory.
+// Above 8192 columns four it is (one thread of 512 has no more than four): 16384 in BF16 75 us, 135 with 1024 threads
+// that held dw and db in shared memory.  16384 x 4096 in BF16 backward: 72.7 us, 5.5 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -97,32 +97,36 @@ __device__ __forceinline__ void read_param(const void* p, int f32, int col, floa
 }
 
 // Rows in shared memory: as many as it holds beside the blocks that share an SM.
-constexpr int fwd_depth(int threads, int pieces, bool f32) { return threads == 512 && pieces == 4 && f32 ? 1 : 2; }
+constexpr int fwd_depth(int threads, bool f32) { return threads == 512 && f32 ? 1 : 2; }
 constexpr int bwd_depth(int pieces, bool x_f32, bool g_f32) {
   return pieces == 4 ? (x_f32 || g_f32 ? 1 : 2) : x_f32 && g_f32 ? 2 : 3;
 }
+constexpr int fwd_pieces(bool x_f32, int threads) { return x_f32 && threads == 256 ? 2 : 4; }
+// Threads from piece to piece in shared memory (0: the block's): a constant where a block has the SM to itself and many
+// pieces (16384 columns backward, BF16 rows and FP32 gradients: 96 us, 114 with the block's).
+constexpr int ring_stride(int pieces, int threads) { return pieces == 4 && threads == 512 ? threads : 0; }
 constexpr int fwd_per_sm(int threads) { return threads == 256 ? 3 : 1; }
 constexpr int bwd_per_sm(int threads) { return threads == 256 ? 2 : 1; }
 
 template <bool XF32, int CH, int THREADS>
 __global__ void __launch_bounds__(THREADS, fwd_per_sm(THREADS))
     norm_fwd_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int DEPTH = fwd_depth(THREADS, CH, XF32);
+  constexpr int DEPTH = fwd_depth(THREADS, XF32);
   __shared__ float part[2][32][1];
   extern __shared__ float4 shared[];  // rows ahead, weight and bias
   const int t = static_cast<int>(threadIdx.x) % a.tpr, sub = static_cast<int>(threadIdx.x) / a.tpr;
   const int rows = static_cast<int>(blockDim.x) / a.tpr;
   GroupSum<1> sum(part, a.tpr);
-  Ahead<XF32, CH> ahead(shared, a.tpr);
-  float4* const w_kept = shared + DEPTH * CH * ahead.UNITS * blockDim.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows, first = static_cast<int64_t>(blockIdx.x) * rows;
+  Ahead<XF32, CH, DEPTH, ring_stride(CH, THREADS)> ahead(shared, a.tpr, t, a.x, a.ldx, first + sub, step, a.C);
+  float4* const w_kept = shared + ahead.units();
   float4* const b_kept = w_kept + 2 * CH * a.tpr;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   auto fetch = [&](int slot, int64_t row) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) ahead.load(slot, i, a.x, row * a.ldx, a.tpr, t, a.C, row < a.T);
+    for (int i = 0; i < CH; ++i) ahead.load(slot, i, row < a.T);
+    ahead.advance();
     copies_commit();
   };
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) fetch(d, first + sub + d * step);
   if (!a.few) {
@@ -198,30 +202,34 @@ __global__ void __launch_bounds__(THREADS, bwd_per_sm(THREADS)) norm_bwd_kernel(
   const int rows = static_cast<int>(blockDim.x) / a.tpr;
   pdl_launch_dependents();  // (the sums' kernel may take its place; it waits for this one)
   GroupSum<2> sum(part, a.tpr);
-  Ahead<XF32, CH> ahead_x(shared, a.tpr);
-  Ahead<GF32, CH> ahead_g(shared + DEPTH * CH * ahead_x.UNITS * blockDim.x, a.tpr);
-  float4* const kept = shared + DEPTH * CH * (ahead_x.UNITS + ahead_g.UNITS) * blockDim.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows, first = static_cast<int64_t>(blockIdx.x) * rows;
+  Ahead<XF32, CH, DEPTH, ring_stride(CH, THREADS)> ahead_x(shared, a.tpr, t, a.x, a.ldx, first + sub, step, a.C);
+  Ahead<GF32, CH, DEPTH, ring_stride(CH, THREADS)> ahead_g(shared + ahead_x.units(), a.tpr, t, a.dy, a.ldg, first + sub, step, a.C);
+  float4* const kept = shared + ahead_x.units() + ahead_g.units();
   Two dw[CH][4], db[CH][4];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = twice(0.0f);
   }
-  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   float next_mean = 0.0f, next_rstd = 0.0f;
   auto fetch_stats = [&](int64_t row) {
     if (row < a.T) next_mean = __ldg(a.mean + row), next_rstd = __ldg(a.rstd + row);
   };
   auto fetch_piece = [&](int slot, int i, int64_t row) {
-    ahead_x.load(slot, i, a.x, row * a.ldx, a.tpr, t, a.C, row < a.T);
-    ahead_g.load(slot, i, a.dy, row * a.ldg, a.tpr, t, a.C, row < a.T);
+    ahead_x.load(slot, i, row < a.T);
+    ahead_g.load(slot, i, row < a.T);
+  };
+  auto fetched = [&] {
+    ahead_x.advance();
+    ahead_g.advance();
+    copies_commit();
   };
   auto fetch = [&](int slot, int64_t row) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) fetch_piece(slot, i, row);
-    copies_commit();
+    fetched();
   };
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) fetch(d, first + sub + d * step);
   fetch_stats(first + sub);
@@ -285,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, bwd_per_sm(THREADS)) norm_bwd_kernel(
       store_row8(a, row * a.ldy + col, gi);
     }
     if (TWICE) {
-      copies_commit();
+      fetched();
       slot = slot + 1 == DEPTH ? 0 : slot + 1;
     }
   }
@@ -373,24 +381,23 @@ void set_blocks(Shape* s, int64_t T, int sm_count, int per_sm, size_t smem) {
   s->blocks = std::min((T + s->rows - 1) / s->rows, static_cast<int64_t>(sm_count) * std::max(1, most));
 }
 
-Shape fwd_shape(int64_t T, int64_t C, bool x_f32, int sm_count, bool* few) {
-  auto with = [&](int pieces) {
-    Shape s = shape_of(C, pieces, C > 4096 ? 512 : 256);
-    const int units = fwd_depth(s.threads, pieces, x_f32) * pieces * (x_f32 ? 2 : 1);
-    set_blocks(&s, T, sm_count, fwd_per_sm(s.threads), static_cast<size_t>(units) * s.block * 16 + static_cast<size_t>(s.tpr) * pieces * 64);
-    *few = T <= s.blocks * s.rows;
-    return s;
-  };
-  return with(!x_f32 || C > 4096 ? 4 : 2);
+int threads_of(int64_t C) { return C > 4096 ? 512 : 256; }
+
+Shape fwd_shape(int64_t T, int64_t C, bool x_f32, int sm_count) {
+  const int threads = threads_of(C), pieces = fwd_pieces(x_f32, threads);
+  Shape s = shape_of(C, pieces, threads);
+  const int units = fwd_depth(threads, x_f32) * pieces * (x_f32 ? 2 : 1);
+  set_blocks(&s, T, sm_count, fwd_per_sm(threads), static_cast<size_t>(units) * std::max(s.block, ring_stride(pieces, threads)) * 16 + static_cast<size_t>(s.tpr) * pieces * 64);
+  return s;
 }
 
-Shape bwd_base(int64_t C, bool f32) { return shape_of(C, C > (f32 ? 8192 : 4096) ? 4 : 2, C > 4096 ? 512 : 256); }
+Shape bwd_base(int64_t C, bool f32) { return shape_of(C, C > (f32 ? 8192 : 4096) ? 4 : 2, threads_of(C)); }
 
 Shape bwd_shape(int64_t T, int64_t C, bool x_f32, bool g_f32, int sm_count) {
   Shape s = bwd_base(C, x_f32 || g_f32);
   const int units = bwd_depth(s.pieces, x_f32, g_f32) * s.pieces * ((x_f32 ? 2 : 1) + (g_f32 ? 2 : 1));
   // (a block's sums of several rows at a time take the place of the rows ahead: 64 bytes a thread and piece, of two threads or more)
-  set_blocks(&s, T, sm_count, bwd_per_sm(s.threads), static_cast<size_t>(units) * s.block * 16 + static_cast<size_t>(s.tpr) * s.pieces * 32);
+  set_blocks(&s, T, sm_count, bwd_per_sm(s.threads), static_cast<size_t>(units) * std::max(s.block, ring_stride(s.pieces, s.threads)) * 16 + static_cast<size_t>(s.tpr) * s.pieces * 32);
   return s;
 }
 
@@ -399,13 +406,25 @@ void by_bool(bool v, F f) {
   v ? f(std::true_type()) : f(std::false_type());
 }
 
+// (pieces, threads) of the forward pass
 template <typename F>
-void by_shape(const Shape& s, F f) {
-  by_bool(s.pieces == 4, [&](auto four) {
-    by_bool(s.threads == 512, [&](auto large) {
-      f(std::integral_constant<int, decltype(four)::value ? 4 : 2>(), std::integral_constant<int, decltype(large)::value ? 512 : 256>());
+void by_fwd_shape(int threads, bool x_f32, F f) {
+  by_bool(x_f32, [&](auto xf) {
+    by_bool(threads == 512, [&](auto large) {
+      constexpr bool X = decltype(xf)::value, LARGE = decltype(large)::value;
+      f(xf, std::integral_constant<int, fwd_pieces(X, LARGE ? 512 : 256)>(), std::integral_constant<int, LARGE ? 512 : 256>());
     });
   });
+}
+
+template <typename F>
+void by_bwd_shape(const Shape& s, F f) {
+  if (s.threads == 256)
+    f(std::integral_constant<int, 2>(), std::integral_constant<int, 256>());
+  else if (s.pieces == 2)
+    f(std::integral_constant<int, 2>(), std::integral_constant<int, 512>());
+  else
+    f(std::integral_constant<int, 4>(), std::integral_constant<int, 512>());
 }
 
 dp_status check_vector(const void* p) { return is_aligned16(p) ? DP_OK : DP_ERR_ALIGNMENT; }
@@ -436,16 +455,19 @@ cudaError_t set_attributes_layer_norm() {
   auto set = [&](const void* kernel) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
   };
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i)
+    by_fwd_shape(i & 2 ? 512 : 256, i & 1, [&](auto xf, auto pieces, auto threads) {
+      set(reinterpret_cast<const void*>(&norm_fwd_kernel<decltype(xf)::value, decltype(pieces)::value, decltype(threads)::value>));
+    });
+  for (int i = 0; i < 12; ++i) {
     Shape s = {};
-    s.pieces = i & 2 ? 4 : 2, s.threads = i & 4 ? 512 : 256;
+    s.pieces = i / 4 == 2 ? 4 : 2, s.threads = i / 4 == 0 ? 256 : 512;
     by_bool(i & 1, [&](auto xf) {
-      by_shape(s, [&](auto pieces, auto threads) {
-        constexpr bool X = decltype(xf)::value;
-        constexpr int CH = decltype(pieces)::value, N = decltype(threads)::value;
-        set(reinterpret_cast<const void*>(&norm_fwd_kernel<X, CH, N>));
-        set(reinterpret_cast<const void*>(&norm_bwd_kernel<X, false, CH, N>));
-        set(reinterpret_cast<const void*>(&norm_bwd_kernel<X, true, CH, N>));
+      by_bool(i & 2, [&](auto gf) {
+        by_bwd_shape(s, [&](auto pieces, auto threads) {
+          constexpr bool X = decltype(xf)::value, G = decltype(gf)::value;
+          set(reinterpret_cast<const void*>(&norm_bwd_kernel<X, G, decltype(pieces)::value, decltype(threads)::value>));
+        });
       });
     });
   }
@@ -485,22 +507,17 @@ extern "C" dp_status dp_layer_norm_fwd(const void* x, int64_t ldx, int x_f32, co
   DeviceContext ctx;
   if ((st = device_context(&ctx)) != DP_OK) return st;
   if (T == 0) return DP_OK;
-  bool few = false;
-  const Shape s = fwd_shape(T, C, x_f32, ctx.sm_count, &few);
+  const Shape s = fwd_shape(T, C, x_f32, ctx.sm_count);
   NormArgs a = {};
   a.x = x, a.ldx = ldx, a.w = weight, a.b = bias, a.w_f32 = weight_f32, a.eps = static_cast<float>(eps);
   a.T = T, a.C = static_cast<int32_t>(C), a.tpr = s.tpr, a.inv_c = 1.0f / static_cast<float>(C);
   a.y = y, a.ldy = ldy, a.mean = mean, a.rstd = rstd;
-  a.few = few;
+  a.few = T <= s.blocks * s.rows;
   a.y_f32 = code;
   const unsigned grid = static_cast<unsigned>(s.blocks);
   cudaStream_t str = static_cast<cudaStream_t>(stream);
-  by_bool(x_f32, [&](auto xf) {
-    by_shape(s, [&](auto pieces, auto threads) {
-      constexpr bool X = decltype(xf)::value;
-      constexpr int CH = decltype(pieces)::value, N = decltype(threads)::value;
-      norm_fwd_kernel<X, CH, N><<<grid, s.block, s.smem, str>>>(a);
-    });
+  by_fwd_shape(s.threads, x_f32, [&](auto xf, auto pieces, auto threads) {
+    norm_fwd_kernel<decltype(xf)::value, decltype(pieces)::value, decltype(threads)::value><<<grid, s.block, s.smem, str>>>(a);
   });
   return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
 }
@@ -545,7 +562,7 @@ extern "C" dp_status dp_layer_norm_bwd(const void* dy, int64_t ldg, int dy_f32, 
   const unsigned grid = static_cast<unsigned>(s.blocks);
   by_bool(x_f32, [&](auto xf) {
     by_bool(dy_f32, [&](auto gf) {
-      by_shape(s, [&](auto pieces, auto threads) {
+      by_bwd_shape(s, [&](auto pieces, auto threads) {
         constexpr bool X = decltype(xf)::value, G = decltype(gf)::value;
         constexpr int CH = decltype(pieces)::value, N = decltype(threads)::value;
         norm_bwd_kernel<X, G, CH, N><<<grid, s.block, s.smem, str>>>(a);

@@ -113,8 +113,8 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const Two (&x)[4]
   store8<F32>(base, at, v);
 }
 
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool inside) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(inside ? 16 : 0) : "memory");
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
@@ -129,32 +129,54 @@ __device__ __forceinline__ void copies_wait() {
 // (each thread its own 32 bytes asked twice for every sector: 3.9 TB/s in the forward pass of 1024
 // columns), and their places are exchanged within every second eight, so that threads read
 // their own two from different banks.
-template <bool F32, int CH>
+// (STRIDE: threads, 0 for the block's own: blocks of fewer than the most then leave room for others on their SM.)
+template <bool F32, int CH, int DEPTH, int STRIDE>
 struct Ahead {
   static constexpr int UNITS = F32 ? 2 : 1;
   uint4* base;
-  int stride, width, m;  // threads that share a row, up to a warp; this one's place among them
+  int stride;
+  const char* next;  // this thread's first 16 bytes of the row to ask for next
+  int64_t step;
+  uint32_t inside = 0;      // which of its units are inside the row
+  int width, m, piece_bytes;  // threads that share a row, up to a warp; this one's place among them; from piece to piece
 
-  __device__ __forceinline__ Ahead(float4* at, int tpr)
-      : base(reinterpret_cast<uint4*>(at)), stride(static_cast<int>(blockDim.x)), width(tpr < 32 ? tpr : 32), m(static_cast<int>(threadIdx.x) & (width - 1)) {
+  // Rows of `cols` columns of x from `row` on, `rows` apart; t: this thread's place in its row.  What lies behind the columns is zero.
+  __device__ __forceinline__ Ahead(float4* at, int tpr, int t, const void* x, int64_t ld, int64_t row, int64_t rows, int cols)
+      : base(reinterpret_cast<uint4*>(at)), stride(STRIDE > 0 ? STRIDE : static_cast<int>(blockDim.x)), width(tpr < 32 ? tpr : 32), m(static_cast<int>(threadIdx.x) & (width - 1)) {
+    constexpr int SIZE = F32 ? 4 : 2;
     base += (static_cast<int>(threadIdx.x) - m) * UNITS;
-  }
-  static __device__ __forceinline__ int place(int u) { return F32 ? (u & ~7) | ((u ^ (u >> 3)) & 7) : u; }
-  // Ask for piece i of a row of x that begins at `row` (elements; rows outside are zeros); t: this thread's place in its row.
-  __device__ __forceinline__ void load(int slot, int i, const void* x, int64_t row, int tpr, int t, int cols, bool inside) const {
+    const int first = F32 ? (t - m) * 8 + m * 4 : t * 8;
+    next = static_cast<const char*>(x) + (row * ld + first) * SIZE;
+    step = rows * ld * SIZE;
+    piece_bytes = tpr * 8 * SIZE;
 #pragma unroll
-    for (int h = 0; h < UNITS; ++h) {
-      const int u = h * width + m, col = i * tpr * 8 + (F32 ? (t - m) * 8 + u * 4 : t * 8);
-      const bool in = inside && col < cols;
-      copy16_async(smem_addr(base + (slot * CH + i) * UNITS * stride + place(u)),
-                   static_cast<const char*>(x) + (in ? (row + col) * (F32 ? 4 : 2) : 0), in);
-    }
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int h = 0; h < UNITS; ++h) {
+        if (first + i * tpr * 8 + h * width * 4 < cols) {
+          inside |= 1u << (i * UNITS + h);
+        } else {
+#pragma unroll
+          for (int slot = 0; slot < DEPTH; ++slot) *unit(slot, i, h * width + m) = make_uint4(0, 0, 0, 0);
+        }
+      }
   }
+  __device__ __forceinline__ int units() const { return DEPTH * CH * UNITS * stride; }
+  __device__ __forceinline__ uint4* unit(int slot, int i, int u) const {
+    return base + (slot * CH + i) * UNITS * stride + (F32 ? (u & ~7) | ((u ^ (u >> 3)) & 7) : u);
+  }
+  // Ask for piece i of the next row, if there is one.
+  __device__ __forceinline__ void load(int slot, int i, bool row) const {
+#pragma unroll
+    for (int h = 0; h < UNITS; ++h)
+      if (row && (inside >> (i * UNITS + h) & 1)) copy16_async(smem_addr(unit(slot, i, h * width + m)), next + (i * piece_bytes + h * width * 16));
+  }
+  __device__ __forceinline__ void advance() { next += step; }
   // (behind copies_wait and, FP32, __syncwarp)
   __device__ __forceinline__ Raw8<F32> take(int slot, int i) const {
     Raw8<F32> r;
 #pragma unroll
-    for (int h = 0; h < UNITS; ++h) r.v[h] = base[(slot * CH + i) * UNITS * stride + place(UNITS * m + h)];
+    for (int h = 0; h < UNITS; ++h) r.v[h] = *unit(slot, i, UNITS * m + h);
     return r;
   }
 };
