@@ -46,4 +46,18 @@ cudaError_t set_attributes_int4();
 cudaError_t set_attributes_layer_norm();
 cudaError_t set_attributes_experts();
 
+// A launch that may begin while the grid before it on the stream ends (the kernel waits for it by itself).
+template <typename... P, typename... A>
+dp_status launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, dp_stream stream, A&&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid), cfg.blockDim = dim3(block), cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream), cfg.attrs = attr, cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...) == cudaSuccess) return DP_OK;
+  cudaGetLastError();  // (reported here: not once more by the next call that asks)
+  return DP_ERR_LAUNCH;
+}
+
 }  // namespace dp

@@ -150,6 +150,13 @@ __device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity, ui
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Both, for kernels that read and write nothing before the grid before them is done: only then may the next
+// one begin (so whatever comes before this grid is done when that one does).
+__device__ __forceinline__ void pdl_begin() {
+  pdl_wait();
+  pdl_launch_dependents();
+}
+
 // True in one lane of a converged warp.  Code under it that issues tcgen05 instructions or
 // TMA copies keeps its operands in uniform registers, which a branch on the lane index does not.
 __device__ __forceinline__ bool elect_one() {

@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "api_internal.h"
+#include "ptx.cuh"
 
 namespace dp {
 namespace {
@@ -67,11 +68,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
   __shared__ uint2 found[kWarps][32];  // candidates: key, index
   const int lane = static_cast<int>(threadIdx.x) & 31, warp = static_cast<int>(threadIdx.x) >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  pdl_begin();
   if (t >= a.T) return;
   const float* p = a.logits + t * a.ld;
   float x[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) x[i] = lane + 32 * i < a.E ? __ldg(p + lane + 32 * i) : -INFINITY;
+  for (int i = 0; i < VPL; ++i) x[i] = lane + 32 * i < a.E ? p[lane + 32 * i] : -INFINITY;
   uint32_t key[VPL], most = 0;  // this lane's largest
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -146,6 +148,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
   __shared__ uint8_t holder[kWarps][VPL * 32];  // of an expert: a lane that has it
   const int lane = static_cast<int>(threadIdx.x) & 31, warp = static_cast<int>(threadIdx.x) >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  pdl_begin();
   if (t >= a.T) return;
   int at = -1;
   float g = 0.0f, dg = 0.0f;
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = lane + 32 * i;
-      l[i] = e < a.E ? __ldg(p + e) : -INFINITY;
+      l[i] = e < a.E ? p[e] : -INFINITY;
       nan = nan || l[i] != l[i];
       m = fmaxf(m, l[i]);
     }
@@ -251,9 +254,9 @@ extern "C" dp_status dp_route_topk(const float* logits, int64_t ld, float* gates
   a.renormalize = renormalize, a.gates = gates, a.choice = choice;
   const unsigned grid = static_cast<unsigned>((T + kWarps - 1) / kWarps);
   by_width(E, [&](auto v) {
-    route_kernel<decltype(v)::value><<<grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    st = launch_dependent(route_kernel<decltype(v)::value>, grid, kWarps * 32, 0, stream, a);
   });
-  return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+  return st;
 }
 
 extern "C" dp_status dp_route_topk_bwd(const float* dgates, const float* logits, int64_t ld, const float* gates,
@@ -276,7 +279,7 @@ extern "C" dp_status dp_route_topk_bwd(const float* dgates, const float* logits,
   a.dgates = dgates, a.dlogits = dlogits, a.ldd = ldd;
   const unsigned grid = static_cast<unsigned>((T + kWarps - 1) / kWarps);
   by_width(E, [&](auto v) {
-    route_bwd_kernel<decltype(v)::value><<<grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    st = launch_dependent(route_bwd_kernel<decltype(v)::value>, grid, kWarps * 32, 0, stream, a);
   });
-  return cudaGetLastError() == cudaSuccess ? DP_OK : DP_ERR_LAUNCH;
+  return st;
 }

@@ -15,12 +15,14 @@ struct Raw8 {
   uint4 v[F32 ? 2 : 1];
 };
 
-template <bool F32>
+// (COHERENT: behind pdl_wait.  Loads of read-only data ask that nobody writes it while the kernel lives, and the grid before
+// may, up to there.)
+template <bool F32, bool COHERENT = false>
 __device__ __forceinline__ Raw8<F32> load_raw8(const void* base, int64_t at) {
   Raw8<F32> r;
   const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + at * (F32 ? 4 : 2));
 #pragma unroll
-  for (int i = 0; i < (F32 ? 2 : 1); ++i) r.v[i] = __ldg(p + i);
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) r.v[i] = COHERENT ? p[i] : __ldg(p + i);
   return r;
 }
 
@@ -54,9 +56,9 @@ __device__ __forceinline__ void unpack8(const Raw8<F32>& r, float (&x)[8]) {
   }
 }
 
-template <bool F32>
+template <bool F32, bool COHERENT = false>
 __device__ __forceinline__ void load8(const void* base, int64_t at, float (&x)[8]) {
-  unpack8<F32>(load_raw8<F32>(base, at), x);
+  unpack8<F32>(load_raw8<F32, COHERENT>(base, at), x);
 }
 
 // Eight FP32 values, rounded once to BF16 (nearest-even) or stored as they are.

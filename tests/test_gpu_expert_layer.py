@@ -126,3 +126,37 @@ def test_training_behind_a_layer_norm(layer, T):
     for got, ref in zip((d_x, d_w1, d_w2, d_gamma, d_beta, d_router), grads):
         assert off(got, ref) <= TOL
     assert dp.device_error() == 0
+
+
+@pytest.mark.parametrize("T", [8, 700])
+def test_calls_one_after_another_share_buffers(T):
+    """Launches that begin while the ones before them end: many steps through the same buffers give what steps
+    with a pause after each call give, bit for bit."""
+    E, k, C, steps = 64, 4, 1024, 40
+    g = torch.Generator(device=DEV).manual_seed(T)
+    logits = torch.randn(steps, T, E, device=DEV, generator=g)
+    x = torch.randn(steps, T, C, device=DEV, generator=g).bfloat16()
+    rows = torch.empty(T * k, C, device=DEV, dtype=torch.bfloat16)
+    d_rows = torch.empty_like(rows)
+
+    def run(pause):
+        outs = torch.empty(steps, T, C, device=DEV, dtype=torch.bfloat16)
+        d_logits = torch.empty(steps, T, E, device=DEV)
+        for i in range(steps):
+            for call in (lambda: state.update(zip(("gates", "choice"), dp.route_topk(logits[i], k))),
+                         lambda: state.update(row_of=dp.expert_sort(state["choice"], E)[1]),
+                         lambda: dp.expert_gather(x[i], state["row_of"], out=rows),
+                         lambda: dp.expert_combine(rows, state["row_of"], state["gates"], out=outs[i]),
+                         lambda: state.update(d_gates=dp.expert_combine_bwd(outs[i], rows, state["row_of"], state["gates"], d_y=d_rows)[1]),
+                         lambda: dp.route_topk_bwd(state["d_gates"], logits[i], state["gates"], state["choice"], out=d_logits[i])):
+                call()
+                if pause:
+                    torch.cuda.synchronize()
+        return outs, d_logits
+
+    state = {}
+    want = run(True)
+    for _ in range(3):
+        got = run(False)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert dp.device_error() == 0
