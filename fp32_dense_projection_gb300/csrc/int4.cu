@@ -4,9 +4,9 @@
 //
 // Products of few rows, plain or grouped by expert:  Y[t][n] = sum over groups of s sum x[t][k] (q - z)
 //
-// Bound: the codes' bytes from HBM, and beside them the instructions that unpack them (118 of the 194 that a block of 16 x
-// 128 codes takes are the products; 55% of the issue slots; 64 experts of 1024 x 4096 with 64 rows: 26.4 us,
-// 3.4 TB/s).  Two chains of MMA sums in place of one: 27.0.  A unit of work is
+// Bound: the codes' bytes from HBM, and beside them the instructions that unpack them (118 a block
+// of 16 x 128 codes).  64 experts of 1024 x 4096 with 64 rows: 24.3 us, 3.7 TB/s (26.4 and, with groups of 32, 78 in place of 41
+// when scales were loaded one by one three stages ahead, in registers that spilled).  A unit of work is
 // 16 rows of weights (the MMA's rows) times the tokens of their group (its 8 columns, once or twice).
 // One CTA an SM goes over a contiguous range of units, so the tokens stay in shared memory while the
 // codes stream past.  Teams of warps take the units in turn (four teams of four warps, or one of sixteen
@@ -41,7 +41,6 @@ constexpr int kMaxInt4Experts = 1024;
 constexpr int64_t kMaxInt4K = 32768;
 constexpr int kUserWarps = 16, kHelpers = 4;  // the warps that multiply, and those that load for them
 constexpr int kUsers = kUserWarps * 32, kThreads = kUsers + kHelpers * 32, kWarps = kThreads / 32;
-constexpr int kAhead = 3;    // stages whose scales are on their way
 constexpr int kRows = 16;    // of weights in a unit
 constexpr int kPiece = 256;  // contraction elements in 128 bytes of codes, the width of a swizzled row
 constexpr int kPieceBytes = kRows * 128;
@@ -58,6 +57,7 @@ struct ProductArgs {
   const void* s;     // [E][N][K / G]
   const uint8_t* z;  // the same shape, or null
   int s_f32;
+  int wide;    // scales and zero points lie so that several of a row are loaded at once
   int pieces;  // 1: the codes' map is [rows][K / 2], 128 bytes wide boxes; else [pieces][rows][128] with a stage a box
   const void* offsets;  // null: one group of all T rows
   int offsets64;
@@ -242,6 +242,23 @@ __device__ __forceinline__ void store_out(const ProductArgs& a, int32_t t, int32
     static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16_rn(v);
 }
 
+// N neighbouring words in as few loads as their alignment (that of all of them, up to 16 bytes) allows.
+template <int N, int M>
+__device__ __forceinline__ void load_words(uint32_t (&v)[M], const uint32_t* p) {
+  if (N == 1) {
+    v[0] = __ldg(p);
+  } else if (N == 2) {
+    const uint2 t = __ldg(reinterpret_cast<const uint2*>(p));
+    v[0] = t.x, v[1] = t.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 t = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      v[4 * i] = t.x, v[4 * i + 1] = t.y, v[4 * i + 2] = t.z, v[4 * i + 3] = t.w;
+    }
+  }
+}
+
 template <int G, int NT, int TEAMS>
 __global__ void __launch_bounds__(kThreads, 1)
     int4_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ CUtensorMap codes_map) {
@@ -293,15 +310,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kUserWarps) {
     // --------------------------------------------------- codes, scales and zero points of a ring
-    // Scales are [group][row] (scale, twice -z / 64), some rows a helper; their loads are some stages ahead.
-    // (Helpers that took stages by turns could be two rounds from a barrier.)
+    // Scales are [group][row] (scale, twice -z / 64), some rows a helper; a lane has PER neighbouring groups of one row, in
+    // one or two loads where they lie so, and the next stage's are on their way.  (Two stages: spills, 47 us for 41 with groups
+    // of 32.  Helpers that took stages by turns could be two rounds from a barrier.)
     constexpr int ROWS = kRows / HELPERS, PER = CHUNK / G * ROWS / 32;
     const int team = (warp - kUserWarps) / HELPERS, helper = (warp - kUserWarps) % HELPERS;
     const int groups = a.K / G, in_stage = a.chunk / G;  // (a power of two)
     const int shift = 31 - __clz(in_stage);
-    uint32_t held_s[kAhead][PER], held_z[kAhead][PER];
-    int held_row[kAhead], held_k0[kAhead];
+    uint32_t held_s[PER], held_z[PER];  // of the next stage, as they come: a conversion would wait for them
+    int held_row = 0, held_k0 = 0;
     int k0 = 0, pending = 0, tile = 0;
+    const int own_r = (lane * PER) >> shift, own_g = (lane * PER) & (in_stage - 1);
+    const bool wide = a.wide && groups % PER == 0;
     auto settle = [&]() {  // the ring's next unit, from this pass on
       while (!pass.done() && tile >= pass.end) {
         phase = (phase + pass.end - pass.tile) % TEAMS;
@@ -309,19 +329,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         tile = pass.tile + (team - phase + TEAMS) % TEAMS;
       }
     };
-    auto fetch = [&](uint32_t (&hs)[PER], uint32_t (&hz)[PER], int& row, int& from_k) {  // the next stage's, if there is one
+    auto fetch = [&]() {  // the next stage's, if there is one
       if (pass.done()) return;
-      const int n0 = tile * kRows + helper * ROWS;
-      row = pass.e * a.N + tile * kRows, from_k = k0;
+      const int n0 = tile * kRows + helper * ROWS, g0 = k0 / G;
+      held_row = pass.e * a.N + tile * kRows, held_k0 = k0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int r = (i * 32 + lane) >> shift, gi = k0 / G + ((i * 32 + lane) & (in_stage - 1));
-        hs[i] = 0, hz[i] = 8;
-        if (r < ROWS && n0 + r < a.N && gi < groups) {
-          const int64_t p = static_cast<int64_t>(pass.e * a.N + n0 + r) * groups + gi;
-          // (as they come: a shift here would wait for them)
-          hs[i] = a.s_f32 ? __ldg(static_cast<const uint32_t*>(a.s) + p) : __ldg(static_cast<const uint16_t*>(a.s) + p);
-          if (a.z != nullptr) hz[i] = __ldg(a.z + p);
+      for (int i = 0; i < PER; ++i) held_s[i] = 0, held_z[i] = wide ? 0x08080808 : 8;
+      if (own_r < ROWS && n0 + own_r < a.N && g0 + own_g < groups) {
+        const int64_t p = static_cast<int64_t>(pass.e * a.N + n0 + own_r) * groups + g0 + own_g;
+        const uint16_t* const s16 = static_cast<const uint16_t*>(a.s) + p;
+        const uint32_t* const s32 = static_cast<const uint32_t*>(a.s) + p;
+        if (wide) {
+          if (a.s_f32)
+            load_words<PER>(held_s, s32);
+          else
+            load_words<PER / 2>(held_s, reinterpret_cast<const uint32_t*>(s16));
+          if (a.z != nullptr) {
+            if (PER >= 4)
+              load_words<PER / 4>(held_z, reinterpret_cast<const uint32_t*>(a.z + p));
+            else
+              held_z[0] = __ldg(reinterpret_cast<const uint16_t*>(a.z + p));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            if (g0 + own_g + i >= groups) continue;
+            held_s[i] = a.s_f32 ? __ldg(s32 + i) : __ldg(s16 + i);
+            if (a.z != nullptr) held_z[i] = __ldg(a.z + p + i);
+          }
         }
       }
       ++pending;
@@ -345,38 +380,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     tile = pass.tile + team;
     settle();
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d) fetch(held_s[d], held_z[d], held_row[d], held_k0[d]);
-    // the first stages' codes do not wait for scales
-    int early = min(pending, min(a.stages, kAhead));
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d)
-      if (d < early) load_codes(team * a.stages + d, held_row[d], held_k0[d]);
+    fetch();
     while (pending > 0 && !dead) {
+      const int stage = team * a.stages + at.slot;
+      wait(empty + 8 * stage, at.parity ^ 1);
+      if (dead) break;
+      load_codes(stage, held_row, held_k0);
+      uint2* meta = reinterpret_cast<uint2*>(smem + l.meta + stage * l.meta_bytes) + own_g * (kRows + 1) + helper * ROWS + own_r;
 #pragma unroll
-      for (int d = 0; d < kAhead; ++d) {
-        if (pending == 0 || dead) break;
-        const int stage = team * a.stages + at.slot;
-        wait(empty + 8 * stage, at.parity ^ 1);
-        if (dead) break;
-        if (early > 0)
-          --early;
-        else
-          load_codes(stage, held_row[d], held_k0[d]);
-        uint2* meta = reinterpret_cast<uint2*>(smem + l.meta + stage * l.meta_bytes) + helper * ROWS;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int r = (i * 32 + lane) >> shift, gi = (i * 32 + lane) & (in_stage - 1);
-          if (r < ROWS)
-            meta[gi * (kRows + 1) + r] = make_uint2(held_s[d][i] << (a.s_f32 ? 0 : 16),
-                                                    fma_bf16x2((held_z[d][i] & 15u) * 0x10001u, 0xFF00FF00u, 0));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full + 8 * stage);
-        at.advance(a.stages);
-        --pending;
-        fetch(held_s[d], held_z[d], held_row[d], held_k0[d]);
+      for (int i = 0; i < PER; ++i) {
+        uint32_t sc = held_s[i], z = held_z[i];
+        if (wide) z = held_z[i / 4] >> (8 * (i % 4));
+        if (!a.s_f32) sc = !wide ? sc << 16 : i % 2 ? held_s[i / 2] & 0xFFFF0000u : held_s[i / 2] << 16;
+        if (own_r < ROWS) meta[i * (kRows + 1)] = make_uint2(sc, fma_bf16x2((z & 15u) * 0x10001u, 0xFF00FF00u, 0));
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8 * stage);
+      at.advance(a.stages);
+      --pending;
+      fetch();
     }
     // (a CTA does not end before its copies: without a fault the team has waited for them all)
     for (int i = 0; dead && i < a.stages; ++i)  // stages before this place were filled in its round, the others in the one before
@@ -694,15 +716,19 @@ struct Int4Plan {
 
 // Tokens a pass: as many as shared memory holds beside two stages a ring, at most two MMAs' (16); one MMA's (8) where groups
 // have four and fewer on average, whose passes seldom need more.
-// Teams: one where an SM has fewer than 12 units, which four teams would share unevenly and whose sums they would begin
-// late.  One team / four (us): 12288 x 4096 of one token 11.3 / 11.0, 4096 x 4096 of 16 tokens 12.4 / 17.6, 64 experts of
-// 1024 x 4096 with 64 rows 29.4 / 26.8.
+// Teams: one where an SM has fewer than two units (eight where a pass has more than 8 tokens, whose room the rings lose),
+// which four teams would share unevenly and whose sums they would begin late.  One team / four (us):
+//   one token, groups of 128: 6144 x 4096 (2.5 units an SM) 7.0 / 6.2, 12288 x 4096 10.8 / 9.5; of 32: 4096 x 4096 (1.7) 6.4 / 7.9
+//   8 tokens, groups of 64: 6144 x 4096 7.8 / 7.0, 4096 x 12288 (1.7) 21.1 / 24.2
+//   16 tokens: 12288 x 4096 (5.1) 15.3 / 17.7, 16384 x 4096 (6.7) 17.0 / 18.6, 24576 x 2048 (10.1) 15.9 / 12.5
+//   64 experts of 1024 x 4096 with 64 rows (17) 30.7 / 24.3
 Int4Plan plan_int4(int64_t E, int64_t T, int64_t N, int64_t K, int64_t G, bool grouped, int sm_count) {
   Int4Plan p;
-  const int64_t tokens = grouped ? (T + E - 1) / E : T, units = (N + kRows - 1) / kRows * (grouped ? std::min(E, T) : 1);
+  const int64_t tokens = grouped ? (T + E - 1) / E : T, tiles = (N + kRows - 1) / kRows;
+  const int64_t units = tiles * (grouped ? std::min(E, T) : (T + 15) / 16);  // about
   const int want = tuning_override("DP_FORCE_INT4_TOKENS", 0), want_teams = tuning_override("DP_FORCE_INT4_TEAMS", 0);
   const int experts = grouped ? static_cast<int>(E) : 0, g = static_cast<int>(G), k = static_cast<int>(K);
-  p.teams = want_teams == 1 || want_teams == 4 ? want_teams : units < 12 * sm_count ? 1 : 4;
+  p.teams = want_teams == 1 || want_teams == 4 ? want_teams : units < (tokens <= 8 ? 2 : 8) * sm_count ? 1 : 4;
   p.x_rows = static_cast<int>(std::min<int64_t>(T, want > 0 && want <= 16 ? want : tokens <= 4 && grouped ? 8 : 16));
   for (;; p.x_rows = (p.x_rows + 1) / 2) {
     p.nt = p.x_rows <= 8 ? 1 : 2;
@@ -711,7 +737,7 @@ Int4Plan plan_int4(int64_t E, int64_t T, int64_t N, int64_t K, int64_t G, bool g
       p.stages = std::min(kMostStages, (kMaxShared - 1024 - none.bytes) / (p.teams * (none.code_bytes + none.meta_bytes)));
       if (p.stages >= (p.chunk > least_chunk(p.teams) ? 3 : 2)) {
         p.bytes = layout_of(g, k, p.teams, p.chunk, p.stages, p.x_rows, 8 * p.nt, experts).bytes + 1024;
-        p.grid = static_cast<int>(std::min<int64_t>(units * ((T + p.x_rows - 1) / p.x_rows), sm_count));
+        p.grid = static_cast<int>(std::min<int64_t>(tiles * (grouped ? std::min(E, T) : 1) * ((T + p.x_rows - 1) / p.x_rows), sm_count));
         return p;
       }
     }
@@ -750,6 +776,7 @@ dp_status run_product(const void* x, int64_t ldx, const void* q, const void* s, 
   const Int4Plan p = plan_int4(E, T, N, K, G, offsets != nullptr, ctx.sm_count);
   ProductArgs a = {};
   a.x = x, a.ldx = ldx, a.s = s, a.z = static_cast<const uint8_t*>(z), a.s_f32 = s_f32;
+  a.wide = is_aligned16(s) && is_aligned16(z);
   a.offsets = offsets, a.offsets64 = offset_bits == 64;
   a.E = static_cast<int32_t>(E), a.T = static_cast<int32_t>(T), a.N = static_cast<int32_t>(N), a.K = static_cast<int32_t>(K);
   a.x_rows = p.x_rows, a.chunk = p.chunk, a.stages = p.stages, a.tiles = static_cast<int32_t>((N + kRows - 1) / kRows);

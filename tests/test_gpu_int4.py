@@ -269,6 +269,28 @@ def test_no_rows():
     assert [t.shape for t in dp.int4_quantize(torch.empty(0, 128, device=DEV), 32)[:2]] == [(0, 64), (0, 4)]
 
 
+@pytest.mark.parametrize("K,group", [(4096, 32), (1088, 32), (192, 32), (2176, 64), (320, 64), (4096, 128), (384, 128)])
+@pytest.mark.parametrize("st", [BF16, F32])
+def test_scales_anywhere(K, group, st):
+    """Scales and zero points at any address of their type, and any number of groups, give the same bits."""
+    N, E = 72, 3
+    q, s, z = (torch.stack(t) for t in zip(*(problem(0, N, K, group, True, st, e, False) for e in range(E))))
+    X = rows(9, K, 3, False)
+    offsets = torch.tensor([0, 4, 4, 9], device=DEV, dtype=torch.int32)
+    want = dp.dp_gemm_fwd_int4(X, q[0], s[0], zeros=z[0]), dp.dp_gemm_fwd_int4_grouped(X, q, s, offsets, zeros=z)
+    for shift in (1, 2, 3, 8):
+        buf, bufz = torch.zeros(s.numel() + shift, device=DEV, dtype=st), torch.zeros(z.numel() + shift, device=DEV, dtype=torch.uint8)
+        s2, z2 = buf[shift:].view(s.shape), bufz[shift:].view(z.shape)
+        s2.copy_(s)
+        z2.copy_(z)
+        for sc, ze in ((s2, z), (s, z2), (s2, z2)):
+            assert torch.equal(dp.dp_gemm_fwd_int4(X, q[0], sc[0], zeros=ze[0]), want[0])
+            assert torch.equal(dp.dp_gemm_fwd_int4_grouped(X, q, sc, offsets, zeros=ze), want[1])
+    ref = X[:4].double() @ expand(q[0], s[0], z[0], group).T
+    check(want[1][:4], ref, X[:4].double().abs() @ expand(q[0], s[0], z[0], group).abs().T, group, K, False)
+    assert dp.device_error() == 0
+
+
 def test_experts_past_32_bits():
     """Codes of 2^31 bytes and more: the last expert's are read."""
     E, N, K = 260, 4096, 4096
