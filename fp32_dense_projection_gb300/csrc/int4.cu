@@ -546,15 +546,126 @@ __device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// The largest value and the largest negated one of a group of threads' pieces, and 0.
-template <bool F32, int WIDTH>
-__device__ __forceinline__ void group_range(const Raw8<F32>& raw, float& hi, float& minus_lo) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
-  if (F32) {
-    hi = minus_lo = 0.0f;
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A group's scale, zero point and the scale's reciprocal from its largest value and its largest negated one.
+struct Scale {
+  float s, z, inverse;
+};
+
+__device__ __forceinline__ Scale scale_of(const CodeArgs& a, float hi, float minus_lo) {
+  Scale v;
+  v.s = a.z != nullptr ? __fdiv_rn(hi + minus_lo, 15.0f) : __fdiv_rn(max_nan(hi, minus_lo), 7.0f);
+  v.s = max_nan(v.s, kTinyScale);
+  if (!a.s_f32) v.s = __bfloat162float(__float2bfloat16_rn(v.s));
+  v.z = 8.0f;
+  if (a.z != nullptr) v.z = fminf(fmaxf(rintf(__fdiv_rn(minus_lo, v.s)), 0.0f), 15.0f);
+  // No reciprocal where it might not be normal, or where both ends of a range may be rounded up and a code pass 15.
+  const float inverse = __frcp_rn(v.s);
+  v.inverse = v.s < 1e37f && fmaf(hi, inverse, v.z) < 15.49f ? inverse : __uint_as_float(0x7FC00000u);
+  return v;
+}
+
+__device__ __forceinline__ void put_scale(const CodeArgs& a, uint32_t group, const Scale& v) {
+  if (a.s_f32)
+    static_cast<float*>(a.s)[group] = v.s;
+  else
+    static_cast<__nv_bfloat16*>(a.s)[group] = __float2bfloat16_rn(v.s);
+  if (a.z != nullptr) a.z[group] = static_cast<uint8_t>(v.z);
+}
+
+// The codes of 8 values.  The rounded quotient rn(w / s) is that of w times 1 / s except next to a border between
+// two codes, where the division is done.
+__device__ __forceinline__ uint32_t codes_of(const Two (&w)[4], const Scale& v) {
+  constexpr float kRound = 12582912.0f;  // 1.5 2^23: adding it leaves the nearest integer, to even between two
+  constexpr float kInteger = 8388608.0f;  // 2^23: an integer's bits
+  float far = 0.0f, low = 0.0f, high = 0.0f;  // the farthest a quotient is from its integer; codes 0 to 3 and 4 to 7 as one number
+  auto add = [&](int j, float c0, float c1) {
+    float& sum = j < 2 ? low : high;
+    const float weight = j % 2 ? 256.0f : 1.0f;
+    sum = fmaf(c1, 16.0f * weight, fmaf(c0, weight, sum));
+  };
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const Two q = fma2(w[j], twice(v.inverse), twice(v.z)), c = (q + twice(kRound)) + twice(-kRound), off = fma2(c, twice(-1.0f), q);
+    far = fmaxf(far, fmaxf(fabsf(lo(off)), fabsf(dp::hi(off))));
+    add(j, lo(c), dp::hi(c));
+  }
+  // w (1 / s) + z is within 15 2^-22 + 2^-20 of w / s + z: another integer only next to a border between two
+  if (!(far <= 0.49999f) || v.inverse != v.inverse) {
+    low = high = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const Two n = (two(__fdiv_rn(lo(w[j]), v.s), __fdiv_rn(dp::hi(w[j]), v.s)) + twice(kRound)) + twice(-kRound), c = n + twice(v.z);
+      // (at least 0: rn(-lo / s) = -rn(lo / s))
+      add(j, fminf(lo(c), 15.0f), fminf(dp::hi(c), 15.0f));
+    }
+  }
+  return __byte_perm(__float_as_uint(low + kInteger), __float_as_uint(high + kInteger), 0x5410);
+}
+
+// BF16: a thread takes 32 neighbouring values, the WIDTH = G / 32 threads of a group share their range.  Their loads, 16 bytes
+// of every 64, meet in L1.  Bound: instructions and HBM bytes; 12288 x 4096 with zero points, groups of 128:
+// 30 us, 4.2 TB/s (38 with 8 values of each of four places a thread, whose ranges go over 16 threads; 100 so with a division
+// for every value).
+template <int WIDTH>
+__global__ void __launch_bounds__(256) int4_quantize_bf16_kernel(const __grid_constant__ CodeArgs a) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x, n = 4 * i;
+  const uint32_t r = (__umulhi(n, a.mul) + n) >> a.shift;
+  const bool in = n < a.pieces;  // (a row is whole groups: the threads of a group are in range together)
+  Raw8<false> raw[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    raw[k] = in ? load_raw8<false>(a.w, r * a.ldw + (n - r * a.per_row) * 8 + k * 8) : zero_raw8<false>();
+  uint32_t up = 0, down = 0;  // two at a time
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[k]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) up = max_nan2(up, w[j]), down = min_nan2(down, w[j]);
+  }
+  down ^= 0x80008000u;
+  uint32_t both = max_nan2(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));  // both maxima in one word
+#pragma unroll
+  for (int d = 1; d < WIDTH; d <<= 1) both = max_nan2(both, __shfl_xor_sync(kAll, both, d));
+  const Scale v = scale_of(a, __uint_as_float(both << 16), __uint_as_float(both & 0xFFFF0000u));
+  uint32_t word[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    Two w[4];
+    unpack8<false>(raw[k], w);
+    word[k] = codes_of(w, v);
+  }
+  if (!in) return;
+  reinterpret_cast<uint4*>(a.q)[i] = make_uint4(word[0], word[1], word[2], word[3]);
+  if ((threadIdx.x & (WIDTH - 1)) == 0) put_scale(a, i / WIDTH, v);
+}
+
+// FP32: a thread takes 8 neighbouring values of kPerThread places, the WIDTH = G / 8 threads of a group share their range.
+// Bound: HBM bytes; 12288 x 4096 with zero points, groups of 128: 38 us, 6.0 TB/s.
+template <int WIDTH>
+__global__ void __launch_bounds__(256) int4_quantize_f32_kernel(const __grid_constant__ CodeArgs a) {
+  const uint32_t first = blockIdx.x * (256u * kPerThread) + threadIdx.x;
+  Raw8<true> raw[kPerThread];
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const uint32_t i = first + k * 256, r = (__umulhi(i, a.mul) + i) >> a.shift;
+    raw[k] = i < a.pieces ? load_raw8<true>(a.w, r * a.ldw + (i - r * a.per_row) * 8) : zero_raw8<true>();
+  }
+  // Of a group's first four threads (and every four after them), each divides for one of the places.
+  static_assert(kPerThread == 4, "places are shared among four threads");
+  float its_hi = 0.0f, its_minus_lo = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[k]);
+    float hi = 0.0f, minus_lo = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float x = __uint_as_float(w[F32 ? j : 0]);
+      const float x = __uint_as_float(w[j]);
       hi = max_nan(hi, x);
       minus_lo = max_nan(minus_lo, -x);
     }
@@ -563,94 +674,19 @@ __device__ __forceinline__ void group_range(const Raw8<F32>& raw, float& hi, flo
       hi = max_nan(hi, __shfl_xor_sync(kAll, hi, d));
       minus_lo = max_nan(minus_lo, __shfl_xor_sync(kAll, minus_lo, d));
     }
-  } else {  // two at a time, and both maxima in one word
-    uint32_t up = 0, down = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      up = max_nan2(up, w[j]);
-      down = max_nan2(down, w[j] ^ 0x80008000u);
-    }
-    uint32_t both = max_nan2(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));
-#pragma unroll
-    for (int d = 1; d < WIDTH; d <<= 1) both = max_nan2(both, __shfl_xor_sync(kAll, both, d));
-    hi = __uint_as_float(both << 16);
-    minus_lo = __uint_as_float(both & 0xFFFF0000u);
-  }
-}
-
-// A thread takes 8 neighbouring values, the G / 8 threads of a group share their range.  The rounded
-// quotient rn(w / s) is that of w times 1 / s except next to a border between two codes, where
-// the division is done.  Bound: HBM bytes for FP32 (12288 x 4096 with zero points, groups of 128: 38 us, 6.0 TB/s),
-// instructions for BF16: 100 us with a division for every value, 78 with it at the borders only, 51 with one
-// thread of four dividing for a group, 46 with addresses counted in 32 bits, 38 with the zero point in the product's
-// addition, codes held to 15 where they can pass it only, and groups' widths known to the compiler.
-template <bool WF32, int WIDTH>
-__global__ void __launch_bounds__(256) int4_quantize_kernel(const __grid_constant__ CodeArgs a) {
-  constexpr float kRound = 12582912.0f;  // 1.5 2^23: adding it leaves the nearest integer, to even between two
-  constexpr float kInteger = 8388608.0f;  // 2^23: an integer's bits
-  const uint32_t first = blockIdx.x * (256u * kPerThread) + threadIdx.x;
-  Raw8<WF32> raw[kPerThread];
-#pragma unroll
-  for (int k = 0; k < kPerThread; ++k) {
-    const uint32_t i = first + k * 256, r = (__umulhi(i, a.mul) + i) >> a.shift;
-    raw[k] = i < a.pieces ? load_raw8<WF32>(a.w, r * a.ldw + (i - r * a.per_row) * 8) : zero_raw8<WF32>();
-  }
-  // (a row is whole groups: the threads of a group are in range together)
-  // Of a group's first four threads (and every four after them), each divides for one of the pieces.
-  static_assert(kPerThread == 4, "pieces are shared among four threads");
-  float its_hi = 0.0f, its_minus_lo = 0.0f;
-#pragma unroll
-  for (int k = 0; k < kPerThread; ++k) {
-    float hi, minus_lo;
-    group_range<WF32, WIDTH>(raw[k], hi, minus_lo);
     if ((threadIdx.x & 3) == k) its_hi = hi, its_minus_lo = minus_lo;
   }
-  float its_s = a.z != nullptr ? __fdiv_rn(its_hi + its_minus_lo, 15.0f) : __fdiv_rn(max_nan(its_hi, its_minus_lo), 7.0f);
-  its_s = max_nan(its_s, kTinyScale);
-  if (!a.s_f32) its_s = __bfloat162float(__float2bfloat16_rn(its_s));
-  float its_z = 8.0f;
-  if (a.z != nullptr) its_z = fminf(fmaxf(rintf(__fdiv_rn(its_minus_lo, its_s)), 0.0f), 15.0f);
-  // No reciprocal where it might not be normal, or where both ends of a range may be rounded up and a code pass 15.
-  const float its_inverse = its_s < 1e37f && fmaf(its_hi, __frcp_rn(its_s), its_z) < 15.49f ? __frcp_rn(its_s) : __uint_as_float(0x7FC00000u);
+  const Scale its = scale_of(a, its_hi, its_minus_lo);
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
     const int from = static_cast<int>(threadIdx.x & 28) + k;
-    const float s = __shfl_sync(kAll, its_s, from), z = __shfl_sync(kAll, its_z, from), inverse = __shfl_sync(kAll, its_inverse, from);
+    const Scale v = {__shfl_sync(kAll, its.s, from), __shfl_sync(kAll, its.z, from), __shfl_sync(kAll, its.inverse, from)};
     Two w[4];
-    unpack8<WF32>(raw[k], w);
-    float far = 0.0f, low = 0.0f, high = 0.0f;  // the farthest a quotient is from its integer; codes 0 to 3 and 4 to 7 as one number
-    auto add = [&](int j, float c0, float c1) {
-      float& sum = j < 2 ? low : high;
-      const float weight = j % 2 ? 256.0f : 1.0f;
-      sum = fmaf(c1, 16.0f * weight, fmaf(c0, weight, sum));
-    };
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const Two v = fma2(w[j], twice(inverse), twice(z)), c = (v + twice(kRound)) + twice(-kRound), off = fma2(c, twice(-1.0f), v);
-      far = fmaxf(far, fmaxf(fabsf(lo(off)), fabsf(dp::hi(off))));
-      add(j, lo(c), dp::hi(c));
-    }
-    // w (1 / s) + z is within 15 2^-22 + 2^-20 of w / s + z: another integer only next to a border between two
-    if (!(far <= 0.49999f) || inverse != inverse) {
-      low = high = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const Two n = (two(__fdiv_rn(lo(w[j]), s), __fdiv_rn(dp::hi(w[j]), s)) + twice(kRound)) + twice(-kRound), c = n + twice(z);
-        // (at least 0: rn(-lo / s) = -rn(lo / s))
-        add(j, fminf(lo(c), 15.0f), fminf(dp::hi(c), 15.0f));
-      }
-    }
-    const uint32_t i = first + k * 256;
+    unpack8<true>(raw[k], w);
+    const uint32_t word = codes_of(w, v), i = first + k * 256;
     if (i >= a.pieces) continue;
-    reinterpret_cast<uint32_t*>(a.q)[i] = __byte_perm(__float_as_uint(low + kInteger), __float_as_uint(high + kInteger), 0x5410);
-    if ((threadIdx.x & (WIDTH - 1)) == 0) {
-      const uint32_t g = i >> a.group_shift;  // (rows are whole groups, and packed)
-      if (a.s_f32)
-        static_cast<float*>(a.s)[g] = s;
-      else
-        static_cast<__nv_bfloat16*>(a.s)[g] = __float2bfloat16_rn(s);
-      if (a.z != nullptr) a.z[g] = static_cast<uint8_t>(z);
-    }
+    reinterpret_cast<uint32_t*>(a.q)[i] = word;
+    if ((threadIdx.x & (WIDTH - 1)) == 0) put_scale(a, i / WIDTH, v);
   }
 }
 
@@ -852,13 +888,14 @@ extern "C" dp_status dp_int4_quantize(const void* w, int64_t ldw, int w_f32, int
   CodeArgs a = {};
   a.w = w, a.ldw = ldw, a.q = static_cast<uint8_t*>(q), a.s = s, a.z = static_cast<uint8_t*>(z), a.s_f32 = s_f32;
   a.K = static_cast<int32_t>(K), a.G = static_cast<int32_t>(group);
+  static_assert(kPerThread == 4, "32 values a thread, of one place or of four");
   return run_codes(a, rows, w_f32 ? 4 : 2, s_f32 ? 4 : 2, [&](const CodeArgs& part, unsigned grid) {
     by_group(group, [&](auto g) {
-      constexpr int WIDTH = decltype(g)::value / 8;
+      constexpr int G = decltype(g)::value;
       if (w_f32)
-        int4_quantize_kernel<true, WIDTH><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(part);
+        int4_quantize_f32_kernel<G / 8><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(part);
       else
-        int4_quantize_kernel<false, WIDTH><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(part);
+        int4_quantize_bf16_kernel<G / 32><<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(part);
     });
   });
 }
