@@ -5,7 +5,7 @@
 // Products of few rows, plain or grouped by expert:  Y[t][n] = sum over groups of s sum x[t][k] (q - z)
 //
 // Bound: the codes' bytes from HBM, and beside them the instructions that unpack them (118 a block
-// of 16 x 128 codes).  64 experts of 1024 x 4096 with 64 rows: 24.3 us, 3.7 TB/s (26.4 and, with groups of 32, 78 in place of 41
+// of 16 x 128 codes).  64 experts of 1024 x 4096 with 64 rows: 23.8 us, 3.8 TB/s (24.4 with codes read word by word; 26.4 and, with groups of 32, 78 in place of 41
 // when scales were loaded one by one three stages ahead, in registers that spilled).  A unit of work is
 // 16 rows of weights (the MMA's rows) times the tokens of their group (its 8 columns, once or twice).
 // One CTA an SM goes over a contiguous range of units, so the tokens stay in shared memory while the
@@ -22,8 +22,8 @@
 // - the MMA's sums run over one group and meet the group's scale in FP32, so the product is as
 //   exact as with weights expanded in FP32 (sums below 2^-120 lose bits to the factor 64).
 // The order of the contraction within a group is free as long as both operands agree: the four threads
-// of a row take one word of 8 codes each, and each reads pairs (i, i + 4) of its word with one mask;
-// x is laid out in shared memory in the pairs' order.
+// of a row take G / 4 neighbouring codes each, in one load, and each reads pairs (i, i + 4) of a word of 8 with one mask;
+// x is laid out in shared memory in their order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -119,6 +119,20 @@ __device__ __forceinline__ void code_pairs(uint32_t word, uint32_t zero, uint32_
   p[1] = fma_bf16x2(word & 0x00F000F0u, kHigh, zero);
   p[2] = fma_bf16x2(upper & 0x000F000Fu, kLow, zero);
   p[3] = fma_bf16x2(upper & 0x00F000F0u, kHigh, zero);
+}
+
+// N words of shared memory at once.
+template <int N>
+__device__ __forceinline__ void take_words(uint32_t* w, const uint8_t* p) {
+  if (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
 }
 
 // The groups' table: start[i], offset i clamped to [0, T] and to the running maximum; list, the experts
@@ -408,10 +422,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ------------------------------------------------------------------ products
   const int team = warp / WAYS, way = warp % WAYS, g = lane >> 2, t = lane & 3;
   float* red = reinterpret_cast<float*>(smem + l.red) + team * (WAYS * TT * kRedStride);
-  // where in a swizzled piece this thread's words of row g lie (its blocks are all a piece's first or second half)
-  int32_t word[4];
+  // Of a group's bytes each thread of a row takes neighbouring ones, in one load.  The MMA's row g is the unit's row
+  // (0, 4, 2, 6, 1, 5, 3, 7)[g] (and g + 8 that + 8), so that what the threads of two or four rows read at a time
+  // lies in different banks of a swizzled piece (a warp's blocks are all a piece's first or second half).
+  const int row_g = (g & 1) << 2 | (g & 2) | g >> 2;
+  int32_t word[GROUPS];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) word[j] = way / 2 * kPieceBytes + g * 128 + (((way % 2 * 4 + j) ^ g) << 4) + t * 4;
+  for (int i = 0; i < GROUPS; ++i)
+    word[i] = way / 2 * kPieceBytes + row_g * 128 + (((way % 2 * 4 + i * STEPS + t * STEPS / 4) ^ row_g) << 4) + t * STEPS % 4 * 4;
   for (; !pass.done(); phase = (phase + pass.end - pass.tile) % TEAMS, pass.next(a, tab)) {
     const int count = pass.count;
     int32_t x_row[NT];  // this thread's rows of x (columns behind the last token: its row again, their sums are not used)
@@ -421,6 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     named_sync(1, kUsers);
     for (int c = tid; c < (a.K + 127) / 128 * 16; c += kUsers) {
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + pass.tok * a.ldx) + c;
+      // chunk (group, thread, step) of a block of 128 stands where that step's load of that thread finds it
+      const int to = (c & ~(4 * STEPS - 1)) + c % STEPS * 4 + c / STEPS % 4;
       for (int r0 = 0; r0 < count; r0 += 8) {
         uint4 v[8];
 #pragma unroll
@@ -429,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int r = 0; r < 8; ++r)
           if (r0 + r < count)
-            *reinterpret_cast<uint4*>(smem + l.x + (r0 + r) * l.x_stride + c * 16) =
+            *reinterpret_cast<uint4*>(smem + l.x + (r0 + r) * l.x_stride + to * 16) =
                 make_uint4(__byte_perm(v[r].x, v[r].z, 0x5410), __byte_perm(v[r].x, v[r].z, 0x7632),
                            __byte_perm(v[r].y, v[r].w, 0x5410), __byte_perm(v[r].y, v[r].w, 0x7632));
       }
@@ -445,15 +465,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k0 = 0; k0 < a.K; k0 += a.chunk) {
         const int stage = team * a.stages + at.slot;
         wait(full + 8 * stage, at.parity);
-        const uint2* meta = reinterpret_cast<const uint2*>(smem + l.meta + stage * l.meta_bytes) + way * (GROUPS * (kRows + 1)) + g;
+        const uint2* meta = reinterpret_cast<const uint2*>(smem + l.meta + stage * l.meta_bytes) + way * (GROUPS * (kRows + 1)) + row_g;
         const uint8_t* codes = smem + stage * l.code_bytes;
         const int left = min(a.chunk, a.K - k0);
         for (int k = way * 128; k < left; k += WAYS * 128) {
           uint32_t wa[4], wb[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            wa[j] = *reinterpret_cast<const uint32_t*>(codes + word[j]);
-            wb[j] = *reinterpret_cast<const uint32_t*>(codes + word[j] + 8 * 128);
+          for (int i = 0; i < GROUPS; ++i) {
+            take_words<STEPS>(wa + i * STEPS, codes + word[i]);
+            take_words<STEPS>(wb + i * STEPS, codes + word[i] + 8 * 128);
           }
 #pragma unroll
           for (int grp = 0; grp < GROUPS; ++grp) {
@@ -494,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_sync(2 + team, TEAM);  // (the sums of the team's last unit have been read)
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        float* d = red + (way * TT + i * 8 + 2 * t) * kRedStride + g;
+        float* d = red + (way * TT + i * 8 + 2 * t) * kRedStride + row_g;
         d[0] = acc[i][0];
         d[kRedStride] = acc[i][1];
         d[8] = acc[i][2];
