@@ -584,9 +584,7 @@ __device__ __forceinline__ Scale scale_of(const CodeArgs& a, float hi, float min
   if (!a.s_f32) v.s = __bfloat162float(__float2bfloat16_rn(v.s));
   v.z = 8.0f;
   if (a.z != nullptr) v.z = fminf(fmaxf(rintf(__fdiv_rn(minus_lo, v.s)), 0.0f), 15.0f);
-  // No reciprocal where it might not be normal, or where both ends of a range may be rounded up and a code pass 15.
-  const float inverse = __frcp_rn(v.s);
-  v.inverse = v.s < 1e37f && fmaf(hi, inverse, v.z) < 15.49f ? inverse : __uint_as_float(0x7FC00000u);
+  v.inverse = __frcp_rn(v.s);
   return v;
 }
 
@@ -598,40 +596,44 @@ __device__ __forceinline__ void put_scale(const CodeArgs& a, uint32_t group, con
   if (a.z != nullptr) a.z[group] = static_cast<uint8_t>(v.z);
 }
 
-// The codes of 8 values.  The rounded quotient rn(w / s) is that of w times 1 / s except next to a border between
-// two codes, where the division is done.
-__device__ __forceinline__ uint32_t codes_of(const Two (&w)[4], const Scale& v) {
+// The codes of 8 values, rn(rn(w / s)) + z.  The quotient is w times the rounded reciprocal, corrected twice by its remainder: the
+// first makes it one of its two neighbours in FP32, whose remainder is exact, the second the rounded quotient (P. Markstein,
+// Computation of elementary functions on the IBM RISC System/6000 processor, 1990).  The reciprocal is normal below 1e37,
+// and a remainder that underflows belongs to a quotient below 1/4 (s is 1e-30 at least).  Quotients halfway between
+// two integers are common where w and s are BF16: a product by the reciprocal alone, and divisions next to a border, took 30 us
+// in place of 24 for 12288 x 4096.
+__device__ __forceinline__ uint32_t codes_of(const CodeArgs& a, const Two (&w)[4], const Scale& v) {
   constexpr float kRound = 12582912.0f;  // 1.5 2^23: adding it leaves the nearest integer, to even between two
   constexpr float kInteger = 8388608.0f;  // 2^23: an integer's bits
-  float far = 0.0f, low = 0.0f, high = 0.0f;  // the farthest a quotient is from its integer; codes 0 to 3 and 4 to 7 as one number
-  auto add = [&](int j, float c0, float c1) {
+  float low = 0.0f, high = 0.0f;  // codes 0 to 3 and 4 to 7 as one number
+  auto add = [&](int j, Two q) {
+    const Two c = (q + twice(kRound)) + twice(v.z - kRound);
+    float c0 = lo(c), c1 = dp::hi(c);
+    // (at least 0: rn(-lo / s) = -rn(lo / s); above 15 only where both ends of a range are rounded up)
+    if (a.z != nullptr) c0 = fminf(c0, 15.0f), c1 = fminf(c1, 15.0f);
     float& sum = j < 2 ? low : high;
     const float weight = j % 2 ? 256.0f : 1.0f;
     sum = fmaf(c1, 16.0f * weight, fmaf(c0, weight, sum));
   };
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const Two q = fma2(w[j], twice(v.inverse), twice(v.z)), c = (q + twice(kRound)) + twice(-kRound), off = fma2(c, twice(-1.0f), q);
-    far = fmaxf(far, fmaxf(fabsf(lo(off)), fabsf(dp::hi(off))));
-    add(j, lo(c), dp::hi(c));
-  }
-  // w (1 / s) + z is within 15 2^-22 + 2^-20 of w / s + z: another integer only next to a border between two
-  if (!(far <= 0.49999f) || v.inverse != v.inverse) {
-    low = high = 0.0f;
+  if (v.s < 1e37f) {
+    const Two y = twice(v.inverse), minus_s = twice(-v.s);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const Two n = (two(__fdiv_rn(lo(w[j]), v.s), __fdiv_rn(dp::hi(w[j]), v.s)) + twice(kRound)) + twice(-kRound), c = n + twice(v.z);
-      // (at least 0: rn(-lo / s) = -rn(lo / s))
-      add(j, fminf(lo(c), 15.0f), fminf(dp::hi(c), 15.0f));
+      Two q = w[j] * y;
+      q = fma2(fma2(q, minus_s, w[j]), y, q);
+      add(j, fma2(fma2(q, minus_s, w[j]), y, q));
     }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) add(j, two(__fdiv_rn(lo(w[j]), v.s), __fdiv_rn(dp::hi(w[j]), v.s)));
   }
   return __byte_perm(__float_as_uint(low + kInteger), __float_as_uint(high + kInteger), 0x5410);
 }
 
 // BF16: a thread takes 32 neighbouring values, the WIDTH = G / 32 threads of a group share their range.  Their loads, 16 bytes
-// of every 64, meet in L1.  Bound: instructions and HBM bytes; 12288 x 4096 with zero points, groups of 128:
-// 30 us, 4.2 TB/s (38 with 8 values of each of four places a thread, whose ranges go over 16 threads; 100 so with a division
-// for every value).
+// of every 64, meet in L1.  Bound: HBM bytes and instructions; 12288 x 4096 with zero points, groups of 128:
+// 24 us, 5.3 TB/s (8 to 14 us more with 8 values of each of four places a thread, whose ranges go over 16 threads; 100 so
+// with a division for every value).
 template <int WIDTH>
 __global__ void __launch_bounds__(256) int4_quantize_bf16_kernel(const __grid_constant__ CodeArgs a) {
   const uint32_t i = blockIdx.x * 256u + threadIdx.x, n = 4 * i;
@@ -658,7 +660,7 @@ __global__ void __launch_bounds__(256) int4_quantize_bf16_kernel(const __grid_co
   for (int k = 0; k < 4; ++k) {
     Two w[4];
     unpack8<false>(raw[k], w);
-    word[k] = codes_of(w, v);
+    word[k] = codes_of(a, w, v);
   }
   if (!in) return;
   reinterpret_cast<uint4*>(a.q)[i] = make_uint4(word[0], word[1], word[2], word[3]);
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(256) int4_quantize_bf16_kernel(const __grid_co
 // FP32: a thread takes 8 neighbouring values of kPerThread places, the WIDTH = G / 8 threads of a group share their range.
 // Bound: HBM bytes; 12288 x 4096 with zero points, groups of 128: 38 us, 6.0 TB/s.
 template <int WIDTH>
-__global__ void __launch_bounds__(256) int4_quantize_f32_kernel(const __grid_constant__ CodeArgs a) {
+__global__ void __launch_bounds__(256, 4) int4_quantize_f32_kernel(const __grid_constant__ CodeArgs a) {
   const uint32_t first = blockIdx.x * (256u * kPerThread) + threadIdx.x;
   Raw8<true> raw[kPerThread];
 #pragma unroll
@@ -703,7 +705,7 @@ __global__ void __launch_bounds__(256) int4_quantize_f32_kernel(const __grid_con
     const Scale v = {__shfl_sync(kAll, its.s, from), __shfl_sync(kAll, its.z, from), __shfl_sync(kAll, its.inverse, from)};
     Two w[4];
     unpack8<true>(raw[k], w);
-    const uint32_t word = codes_of(w, v), i = first + k * 256;
+    const uint32_t word = codes_of(a, w, v), i = first + k * 256;
     if (i >= a.pieces) continue;
     reinterpret_cast<uint32_t*>(a.q)[i] = word;
     if ((threadIdx.x & (WIDTH - 1)) == 0) put_scale(a, i / WIDTH, v);

@@ -414,7 +414,7 @@ dp_status dp_layer_norm_bwd(const void* dy, int64_t ldg, int dy_f32, const void*
                             const float* mean, const float* rstd, const void* weight, int weight_f32, void* dx,
                             int64_t ld_dx, dp_out_dtype out, float* dw, float* db, int64_t T, int64_t C,
                             void* workspace, size_t workspace_bytes, dp_stream stream);
-/* Workspace of the backward pass (sm_count <= 0: the current device's). */
+/* Workspace of the backward pass, for one call at a time (sm_count <= 0: the current device's). */
 dp_status dp_layer_norm_workspace_size(int64_t T, int64_t C, int sm_count, size_t* bytes);
 
 /* ---------------------------------------------------- the router's choice of experts */
