@@ -160,3 +160,41 @@ def test_calls_one_after_another_share_buffers(T):
         got = run(False)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert dp.device_error() == 0
+
+
+def test_capture_on_two_streams():
+    """A graph that forks behind the sort, with torch's kernels and fills between the calls, follows its inputs."""
+    T, E, k, C = 300, 32, 2, 512
+    logits, x = normal((T, E), 1, 1.0, F32), normal((T, C), 2)
+    side = torch.cuda.Stream()
+
+    def work(fork):
+        gates, choice = dp.route_topk(logits, k)
+        _, row_of, _ = dp.expert_sort(choice, E)
+        halved = x * 0.5
+        main = torch.cuda.current_stream()
+        other = side if fork else main
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            rows = dp.expert_gather(halved, row_of)
+            first = dp.expert_combine(rows, row_of, gates, out_dtype=F32)
+        mine = dp.expert_gather(x, row_of, out=torch.zeros(T * k, C, device=DEV, dtype=BF16))
+        second = dp.expert_combine(mine, row_of, None, add=torch.zeros(T, C, device=DEV), out_dtype=F32)
+        main.wait_stream(other)
+        d = dp.route_topk_bwd(dp.expert_combine_bwd(first, mine, row_of, gates)[1], logits, gates, choice)
+        return first + second, d
+
+    work(True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work(True)
+    for i in range(5):
+        logits.copy_(normal((T, E), 10 + i, 1.0, F32))
+        x.copy_(normal((T, C), 20 + i))
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        want = work(False)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert dp.device_error() == 0
