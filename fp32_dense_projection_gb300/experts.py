@@ -74,8 +74,8 @@ def route_topk(logits, k, renormalize=True, stream=None):
         c.load()
 
     def work(st):
-        gates = torch.empty((T, k), dtype=c.F32, device=logits.device)
-        choice = torch.empty((T, k), dtype=_I32, device=logits.device)
+        gates = c.new((T, k), c.F32)
+        choice = c.new((T, k), _I32)
         code = _fn["dp_route_topk"](logits.data_ptr(), ld, gates.data_ptr(), choice.data_ptr(), T, E, k, bool(renormalize), st)
         if code:
             c.check(code, name)
@@ -136,9 +136,9 @@ def expert_sort(choice, E, workspace=None, stream=None):
         c.load()
 
     def work(st):
-        offsets = torch.empty((E + 1 if E > 0 else 1,), dtype=_I32, device=device)
-        row_of = torch.empty(choice.shape, dtype=_I32, device=device)
-        order = torch.empty((pairs,), dtype=_I32, device=device)
+        offsets = c.new_vector(E + 1 if E > 0 else 1, _I32)
+        row_of = c.new(choice.shape, _I32)
+        order = c.new_vector(pairs, _I32)
         buf, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
         args = (choice.data_ptr(), bits, pairs, E, offsets.data_ptr(), row_of.data_ptr(), order.data_ptr())
         code = _fn["dp_expert_sort"](*args, buf, size, st)
@@ -146,7 +146,7 @@ def expert_sort(choice, E, workspace=None, stream=None):
             n = ctypes.c_size_t(0)
             code = _fn["dp_expert_sort_workspace_size"](pairs, E, ctypes.byref(n))
             if not code:
-                buf = torch.empty((n.value,), dtype=torch.uint8, device=device)
+                buf = c.new_vector(n.value, torch.uint8)
                 code = _fn["dp_expert_sort"](*args, buf.data_ptr(), n.value, st)
         if code:
             c.check(code, name)
@@ -252,7 +252,7 @@ def expert_combine_bwd(d_out, y, row_of, gates, d_y=None, dy_dtype=c.BF16, strea
 
     def work(st):
         d, code, ld_dy = c.output_rows(d_y, shape, dy_dtype, index, y.device, name, "d_y")
-        d_gates = torch.empty((T, k), dtype=c.F32, device=y.device)
+        d_gates = c.new((T, k), c.F32)
         code = _fn["dp_expert_combine_bwd"](d_out.data_ptr(), ldd, d32, y.data_ptr(), ldy, y32, row_of.data_ptr(), gates.data_ptr(),
                                             d.data_ptr(), ld_dy, code, d_gates.data_ptr(), T, k, C, st)
         if code:

@@ -61,9 +61,9 @@ def int4_quantize(W, group=128, zeros=False, scale_dtype=c.BF16, stream=None):
         c.load()
 
     def work(st):
-        q = torch.empty((*front, K // 2), dtype=_U8, device=W.device)
-        s = torch.empty((*front, K // group), dtype=scale_dtype, device=W.device)
-        z = torch.empty((*front, K // group), dtype=_U8, device=W.device) if zeros else None
+        q = c.new((*front, K // 2), _U8)
+        s = c.new((*front, K // group), scale_dtype)
+        z = c.new((*front, K // group), _U8) if zeros else None
         code = _fn["dp_int4_quantize"](W.data_ptr(), ld, f32, front.numel(), K, group, q.data_ptr(), s.data_ptr(),
                                        scale_dtype is c.F32, None if z is None else z.data_ptr(), st)
         if code:

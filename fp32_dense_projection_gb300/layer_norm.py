@@ -64,8 +64,8 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=c.BF
 
     def work(st):
         y, code, ldy = c.output_rows(out, shape, out_dtype, index, x.device, name)
-        mean = torch.empty((T,), dtype=c.F32, device=x.device)
-        rstd = torch.empty((T,), dtype=c.F32, device=x.device)
+        mean = c.new_vector(T, c.F32)
+        rstd = c.new_vector(T, c.F32)
         code = _fn["dp_layer_norm_fwd"](x.data_ptr(), ldx, f32, None if weight is None else weight.data_ptr(),
                                         None if bias is None else bias.data_ptr(), w32, eps, y.data_ptr(), ldy,
                                         code, mean.data_ptr(), rstd.data_ptr(), T, C, st)
@@ -120,11 +120,11 @@ def layer_norm_bwd(dY, x, mean, rstd, weight=None, dX=None, dx_dtype=c.BF16, wor
         dW = dB = buf = None
         size = 0
         if weight is not None:
-            dW = torch.empty((C,), dtype=c.F32, device=dY.device)
-            dB = torch.empty((C,), dtype=c.F32, device=dY.device)
+            dW = c.new_vector(C, c.F32)
+            dB = c.new_vector(C, c.F32)
             if workspace is None:
                 size = _workspace_size(index, T, C)
-                buf = torch.empty((size,), dtype=torch.uint8, device=dY.device)
+                buf = c.new_vector(size, torch.uint8)
             else:
                 buf, size = workspace, workspace.nbytes
         status = _fn["dp_layer_norm_bwd"](dY.data_ptr(), ldg, g32, x.data_ptr(), ldx, x32, mean.data_ptr(), rstd.data_ptr(),
