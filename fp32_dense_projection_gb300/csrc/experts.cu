@@ -31,6 +31,7 @@ namespace {
 
 constexpr int64_t kMaxExpertCount = 1024;
 constexpr int64_t kMaxPairs = 0x7FFFFFFF - 256;
+constexpr int64_t kMaxColumns = 0x7FFFFFFF / 2048 * 2048;  // a thread's next column, up to 2048 further on, fits in 32 bits
 constexpr uint32_t kAll = 0xffffffffu;
 
 // ------------------------------------------------------------------------ sort
@@ -453,7 +454,7 @@ void by_bool(bool v, F f) {
 
 dp_status check_pairs(const int32_t* row_of, int64_t T, int64_t k, int64_t C) {
   if (T < 0 || k < 1 || C < 1) return DP_ERR_INVALID_ARG;
-  if (C % 8 != 0 || C > 0x7FFFFF00 || T > kMaxPairs || k > kMaxPairs || T * k > kMaxPairs) return DP_ERR_UNSUPPORTED;
+  if (C % 8 != 0 || C > kMaxColumns || T > kMaxPairs || k > kMaxPairs || T * k > kMaxPairs) return DP_ERR_UNSUPPORTED;
   if (T > 0 && row_of == nullptr) return DP_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(row_of) & 3) != 0) return DP_ERR_ALIGNMENT;
   return DP_OK;

@@ -447,7 +447,7 @@ dp_status dp_route_topk_bwd(const float* dgates, const float* logits, int64_t ld
  * Its gradient: dy[row_of[t][j]] = gate[t][j] dout[t] (zeros without an expert), dgates[t][j] =
  *   dout[t] . y[row_of[t][j]] (0 without).
  * An entry of row_of that names no row of the buffer is left out and reported as
- * DP_ERR_INVALID_ARG by dp_device_error(); two pairs must not name one row.  C a multiple of 8.
+ * DP_ERR_INVALID_ARG by dp_device_error(); two pairs must not name one row.  C a multiple of 8, at most 2^31 - 2048.
  * Outputs must not overlap inputs.  Deterministic. */
 dp_status dp_expert_sort(const void* choice, int choice_bits, int64_t pairs, int64_t E, int32_t* offsets, int32_t* row_of,
                          int32_t* order, void* workspace, size_t workspace_bytes, dp_stream stream);

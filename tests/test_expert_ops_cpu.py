@@ -135,6 +135,12 @@ def test_combine_bwd_refusals(L, kw, want):
     assert combine_bwd(L, **kw) == want
 
 
+@pytest.mark.parametrize("C", [0x7FFFF808, 0x7FFFFF00])
+def test_columns_that_a_counter_of_32_bits_would_pass(L, C):
+    """Threads go over a row up to 2048 columns at a time: from a last column C - 8 on the next must still fit."""
+    assert gather(L, C=C, T=1) == combine(L, C=C, T=1) == combine_bwd(L, C=C, T=1) == UNSUPPORTED
+
+
 def product(L, x=A, ldx=0, q=A, s=A, s32=0, z=None, group=32, offs=None, bits=32, y=A, ldy=0, E=1, T=4, N=64, K=128, out=0, grouped=False):
     if grouped:
         return L.dp_gemm_fwd_int4_grouped(x, ldx, q, s, s32, z, group, offs, bits, y, ldy, E, T, N, K, out, None)
