@@ -838,11 +838,11 @@ dp_status check_codes(const void* q, const void* s, const void* z, int s_f32, in
 dp_status run_product(const void* x, int64_t ldx, const void* q, const void* s, int s_f32, const void* z, int64_t G,
                       const void* offsets, int offset_bits, void* out, int64_t ldo, int64_t E, int64_t T, int64_t N, int64_t K,
                       int out_f32, dp_stream stream) {
-  if (!flag(out_f32) || E < 0 || T < 0 || N < 1 || K < 1) return DP_ERR_INVALID_ARG;
+  if (!flag(out_f32) || !flag(s_f32) || E < 0 || T < 0 || N < 1 || K < 1) return DP_ERR_INVALID_ARG;
   if (offset_bits != 32 && offset_bits != 64) return DP_ERR_INVALID_ARG;
-  dp_status st = check_codes(q, s, z, s_f32, E * N, K, G);
-  if (st != DP_OK) return st;
   if (N % 8 != 0 || N > 0x7FFFF || K > kMaxInt4K || E > kMaxInt4Experts || T > 0x7FFFFFFF - 256) return DP_ERR_UNSUPPORTED;
+  dp_status st = check_codes(q, s, z, s_f32, E * N, K, G);  // (each held to its range: the product fits)
+  if (st != DP_OK) return st;
   if ((st = check_operand(x, T, K, &ldx, 2)) != DP_OK) return st;
   if ((st = check_operand(out, T, N, &ldo, out_f32 ? 4 : 2)) != DP_OK) return st;
   if ((reinterpret_cast<uintptr_t>(offsets) & (offset_bits / 8 - 1)) != 0) return DP_ERR_ALIGNMENT;

@@ -165,6 +165,13 @@ def test_int4_grouped_refusals(L):
     assert product(L, grouped=True, offs=A + 2) == ALIGNMENT and product(L, grouped=True, offs=A + 4, bits=64) == ALIGNMENT
 
 
+@pytest.mark.parametrize("E,N", [(1 << 33, 1 << 30), (1 << 40, 1 << 30), (1 << 62, 8), (4, 1 << 61), ((1 << 63) - 1, 64)])
+def test_int4_rows_that_leave_64_bits(L, E, N):
+    """Experts times rows are counted after each of them has been held to its range."""
+    assert product(L, grouped=True, offs=A, E=E, N=N) == UNSUPPORTED
+    assert product(L, grouped=True, offs=A, E=E, N=N, q=None) == UNSUPPORTED  # (which asks whether there are rows)
+
+
 def test_int4_code_refusals(L):
     def quantize(w=A, ldw=0, w32=0, rows=4, K=128, group=32, q=A, s=A, s32=0, z=None):
         return L.dp_int4_quantize(w, ldw, w32, rows, K, group, q, s, s32, z, None)
