@@ -270,7 +270,9 @@ __global__ void __launch_bounds__(THREADS, bwd_per_sm(THREADS)) norm_bwd_kernel(
     }
     float s[2] = {lo(s0) + hi(s0), lo(s1) + hi(s1)};
     sum(s);
-    const Two c0 = twice(-s[0] * a.inv_c * rstd), c1 = twice(-s[1] * a.inv_c * rstd * (TWICE ? rstd : 1.0f));
+    // h is held, dx = g rs + (h c1 + c0); or, from x - mu and with as many operations, ((x - mu) c1 + (dy w + c0)) rs.  (c1 has rs once:
+    // its square could leave FP32's range.)
+    const Two c0 = twice(-s[0] * a.inv_c * (TWICE ? 1.0f : rstd)), c1 = twice(-s[1] * a.inv_c * rstd);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int col = (t + i * a.tpr) * 8;
@@ -286,10 +288,11 @@ __global__ void __launch_bounds__(THREADS, bwd_per_sm(THREADS)) norm_bwd_kernel(
         Two w[4];
         take_param(kept, a.tpr, t, i, w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) hx[j] = hx[j] + minus, gi[j] = gi[j] * w[j];
-      }
+        for (int j = 0; j < 4; ++j) gi[j] = fma2(hx[j] + minus, c1, fma2(gi[j], w[j], c0)) * scale;
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) gi[j] = fma2(gi[j], scale, fma2(hx[j], c1, c0));
+        for (int j = 0; j < 4; ++j) gi[j] = fma2(gi[j], scale, fma2(hx[j], c1, c0));
+      }
       store_row8(a, row * a.ldy + col, gi);
     }
     if (TWICE) {

@@ -282,3 +282,12 @@ def test_refusals():
     ]:
         with pytest.raises(kind, match=text):
             call()
+
+
+@pytest.mark.parametrize("T,C,xt,gt", [(5, 8192, F32, F32), (5, 8200, F32, F32), (3, 16384, F32, BF16), (4, 4096, BF16, BF16), (7, 4104, BF16, BF16)])
+@pytest.mark.parametrize("sigma,dy", [(1e-20, 1.0), (1e-22, 1.0), (1e17, 1e-6)])
+def test_gradient_of_tiny_and_large_deviations(T, C, xt, gt, sigma, dy):
+    """rs of 1e20, 1e22 and 1e-17, whose squares leave FP32's range or its normal numbers: only rs itself may meet a row's values."""
+    x, g, w = rows(T, C, xt, 1, sigma), rows(T, C, gt, 2, dy), rows(1, C, F32, 3)[0] + 1
+    mean, rs = reference(x, None, None, 0.0)[:2]
+    check_bwd(g, x, w, mean[:, 0].float(), rs[:, 0].float(), F32)
