@@ -93,9 +93,10 @@ def _workspace_size(index, T, C):
     return size
 
 
-def layer_norm_bwd(dY, x, mean, rstd, weight=None, dX=None, dx_dtype=c.BF16, workspace=None, stream=None):
+def layer_norm_bwd(dY, x, mean, rstd, weight=None, dX=None, dx_dtype=c.BF16, workspace=None, stream=None, param_grads=None):
     """(dX [T,C], dW [C], dB [C]) from dY [T,C] and what the forward pass read and returned.
-    Without a weight, dW and dB are None."""
+    dW and dB are made where there is a weight, or as ``param_grads`` says (True: also without one, for a
+    bias alone, dW as of a weight of ones; False: None)."""
     name = "layer_norm_bwd"
     index = dY.get_device()
     if (index < 0 or x.get_device() != index or mean.get_device() != index or rstd.get_device() != index or
@@ -112,6 +113,8 @@ def layer_norm_bwd(dY, x, mean, rstd, weight=None, dX=None, dx_dtype=c.BF16, wor
         _vector(weight, C, _PARAMS, name, "weight")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError(f"{name}: workspace must be contiguous")
+    if param_grads is None:
+        param_grads = weight is not None
     if not _fn:
         c.load()
 
@@ -119,7 +122,7 @@ def layer_norm_bwd(dY, x, mean, rstd, weight=None, dX=None, dx_dtype=c.BF16, wor
         d, code, ld_dx = c.output_rows(dX, shape, dx_dtype, index, dY.device, name, "dX")
         dW = dB = buf = None
         size = 0
-        if weight is not None:
+        if param_grads:
             dW = c.new_vector(C, c.F32)
             dB = c.new_vector(C, c.F32)
             if workspace is None:

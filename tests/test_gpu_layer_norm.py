@@ -291,3 +291,24 @@ def test_gradient_of_tiny_and_large_deviations(T, C, xt, gt, sigma, dy):
     x, g, w = rows(T, C, xt, 1, sigma), rows(T, C, gt, 2, dy), rows(1, C, F32, 3)[0] + 1
     mean, rs = reference(x, None, None, 0.0)[:2]
     check_bwd(g, x, w, mean[:, 0].float(), rs[:, 0].float(), F32)
+
+
+@pytest.mark.parametrize("T,C,xt,gt", [(1, 64, BF16, BF16), (200, 1000, BF16, F32), (50, 4096, F32, F32), (900, 4104, BF16, BF16), (3, 16384, F32, BF16)])
+def test_parameter_gradients_without_a_weight(T, C, xt, gt):
+    """A bias alone has its gradient, and a weight of ones that is not there too; with a weight they can be left out."""
+    x, dy = rows(T, C, xt, 1, shift=0.5), rows(T, C, gt, 2)
+    w, b = rows(1, C, F32, 3)[0], rows(1, C, F32, 4)[0]
+    _, mean, rstd = dp.layer_norm_fwd(x, None, b)
+    dx, dw, db = dp.layer_norm_bwd(dy, x, mean, rstd, param_grads=True)
+    ones = dp.layer_norm_bwd(dy, x, mean, rstd, torch.ones(C, device=DEV))
+    for got, same in zip((dx, dw, db), ones):
+        assert torch.equal(got, same)
+    d, h, depth = dy.double(), (x.double() - mean.double()[:, None]) * rstd.double()[:, None], T / 152 + 160
+    close(dw, (d * h).sum(0), (depth + 5) * U * (d * h).abs().sum(0))
+    close(db, d.sum(0), depth * U * d.abs().sum(0))
+    given = dp.layer_norm_bwd(dy, x, mean, rstd, param_grads=True, workspace=torch.empty(64 << 20, dtype=torch.uint8, device=DEV))
+    assert torch.equal(given[1], dw) and torch.equal(given[2], db)
+    got = dp.layer_norm_bwd(dy, x, mean, rstd, w, param_grads=False)
+    assert got[1] is None and got[2] is None and torch.equal(got[0], dp.layer_norm_bwd(dy, x, mean, rstd, w)[0])
+    empty = dp.layer_norm_bwd(dy[:0], x[:0], mean[:0], rstd[:0], param_grads=True)
+    assert empty[0].shape == (0, C) and not empty[1].any() and not empty[2].any()
