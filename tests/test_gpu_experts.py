@@ -128,6 +128,27 @@ def test_route_closed_experts(renormalize):
     assert torch.equal(choice[40], torch.arange(8, device=DEV, dtype=torch.int32))
 
 
+@pytest.mark.parametrize("T,E,k", [(3, 1, 1), (300, 64, 8), (300, 64, 20), (100, 250, 16), (50, 1000, 8), (50, 1024, 32)])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_gates_far_below_the_largest(T, E, k, renormalize):
+    """Logits up to 80 apart whose distances are exact in FP32 (multiples of 1/64), so that the exponential's own error is what is
+    left: 2 ulp, 4 u of a term at any distance.  The sum of at most E / 32 terms a lane and 5 steps over the warp: 4 + E / 32 + 5
+    u, the quotient 1: a gate is off by (14 + E / 32) u of itself, and one u for the products of these.
+    Gradient over all, of an expert that is not chosen: p s with s = sum dg gate of gates this far off, k <= 32 products and
+    5 steps; of a chosen one gate (dg - s), two steps more.  Below FP32's normal numbers each of two products is off by half
+    their spacing."""
+    l = torch.randint(-80 * 64, 1, (T, E), device=DEV, generator=gen(E + k)).float() / 64
+    l[:, 0] = 0.0  # (the largest, so that the others are as far below as they say)
+    gates, choice = dp.route_topk(l, k, renormalize=renormalize)
+    want, at = plain_route(l, k, renormalize)
+    rel = (15 + E / 32) * U
+    assert torch.equal(choice, at)
+    close(gates, want, rel * want)
+    dg = normal((T, k), 1)
+    ref, mag = plain_route_bwd(dg, l, want, at, renormalize)
+    close(dp.route_topk_bwd(dg, l, gates, choice, renormalize=renormalize), ref, (2 * rel + 9 * U) * mag + 2.0 ** -149)
+
+
 @pytest.mark.parametrize("renormalize", [True, False])
 def test_route_nan_and_infinity(renormalize):
     """A NaN is the largest, its row's gates are NaN; +infinity likewise; other rows do not notice."""
