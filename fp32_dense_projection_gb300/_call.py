@@ -1,4 +1,4 @@
-"""Marshalling shared by the grouped, 8-bit and AdamW bindings.
+"""Marshalling shared by the bindings of the grouped, 8-bit and 4-bit products, AdamW, layer norm and the experts' operators.
 
 A call of a few microseconds on the GPU is bound by what the host does before it, so checks
 are plain comparisons, and their messages are put together only when one of them fails.
@@ -15,11 +15,37 @@ OUT_CODES = {BF16: 0, F32: 1}  # dp_out_dtype
 
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_deterministic = torch.are_deterministic_algorithms_enabled
+
+
+def _public(shape, strides, dtype):
+    return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+
+def _choose(found):
+    """The function found if it makes what the public one makes (without dispatch: 0.9 for 1.5 us by itself, a call of layer norm
+    13.8 for 17.6, of the choice 8.8 for 12.6)."""
+    try:
+        t = found((2, 3), (3, 1), BF16)
+        ok = t.shape == (2, 3) and t.stride() == (3, 1) and t.dtype is BF16 and t.get_device() == _current_device()
+    except Exception:  # something else has its name
+        ok = False
+    return found if ok else _public
+
+
+def _direct(shape, strides, dtype):
+    """An uninitialised tensor on the current device.  (The first one; from then on, what _choose gives.)"""
+    global _direct
+    _direct = _choose(_found)
+    return _direct(shape, strides, dtype)
+
+
 try:
-    from torch._C._dynamo.guards import _empty_strided_cuda as _empty  # (torch.empty without its dispatch: 0.9 for 1.5 us)
-except ImportError:
-    def _empty(shape, strides, dtype):
-        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+    from torch._C import _len_torch_dispatch_stack as _modes
+    from torch._C._dynamo.guards import _empty_strided_cuda as _found
+    _modes()
+except Exception:  # not in this torch: the public function alone
+    _modes, _direct = int, _public
 
 
 def load():
@@ -59,19 +85,21 @@ def ld(t: torch.Tensor, name: str, what: str, shape=None) -> int:
 
 
 def new(shape, dtype):
-    """A new contiguous tensor on the current device."""
+    """A new contiguous tensor on the current device.  What watches torch's allocations (dispatch modes, the filling of new
+    memory that goes with deterministic algorithms) gets the public function's."""
+    empty = _public if _deterministic() or _modes() else _direct
     if len(shape) == 2:
         rows, cols = shape
-        return _empty((rows, cols), (cols, 1), dtype)
+        return empty((rows, cols), (cols, 1), dtype)
     strides, step = [], 1
     for n in reversed(shape):
         strides.append(step)
         step *= max(n, 1)
-    return _empty(tuple(shape), tuple(reversed(strides)), dtype)
+    return empty(tuple(shape), tuple(reversed(strides)), dtype)
 
 
 def new_vector(n, dtype):
-    return _empty((n,), (1,), dtype)
+    return (_public if _deterministic() or _modes() else _direct)((n,), (1,), dtype)
 
 
 def output(out, shape, dtype, index: int, device, name: str):
