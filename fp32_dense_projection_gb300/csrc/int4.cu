@@ -902,7 +902,8 @@ dp_status run_codes(CodeArgs a, int64_t rows, int w_size, int s_size, F launch) 
   a.shift = 0;
   while ((uint64_t{1} << a.shift) < a.per_row) ++a.shift;
   a.mul = static_cast<uint32_t>((((uint64_t{1} << a.shift) - a.per_row) << 32) / a.per_row + 1);
-  const int64_t most = 0x7FFFFF00 / a.per_row;
+  int64_t most = 0x7FFFFF00 / a.per_row;
+  if (const int want = tuning_override("DP_FORCE_INT4_ROWS", 0); want > 0) most = std::min<int64_t>(most, want);
   for (int64_t row = 0; row < rows; row += most) {
     const int64_t n = std::min(most, rows - row);
     a.pieces = static_cast<uint32_t>(n * a.per_row);

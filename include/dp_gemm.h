@@ -514,8 +514,9 @@ dp_status dp_gemm_fwd_int4_grouped(const void* X, int64_t ldx, const void* Wq, c
  * split; 2 to 8: clusters of that many CTAs share a tile's contraction); a call that
  * has no such form is refused with DP_ERR_UNSUPPORTED.  The products with 4-bit weights read
  * DP_FORCE_INT4_TEAMS (1 / 4: how an SM's warps share its work) and DP_FORCE_INT4_TOKENS (1 to 16
- * tokens a pass, fewer where shared memory does not hold them); dp_expert_sort reads
- * DP_FORCE_SORT_CLUSTER (0: two launches, 1: one of a cluster).
+ * tokens a pass, fewer where shared memory does not hold them), their quantisation and expansion
+ * DP_FORCE_INT4_ROWS (rows a launch, at most as many as are counted in 31 bits); dp_expert_sort
+ * reads DP_FORCE_SORT_CLUSTER (0: two launches, 1: one of a cluster).
  * A forced plan is still deterministic and keeps the accumulation-length bound. */
 
 /* The plan the library uses for one call.  The planner is a pure function of

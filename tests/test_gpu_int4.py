@@ -97,6 +97,27 @@ def test_quantize_padded_rows_and_bad_values():
         assert torch.equal(q[rows], clean[0][rows])
 
 
+@pytest.mark.parametrize("rows", ["1", "3", "16", "50"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("wt,st", [(BF16, BF16), (F32, F32), (F32, BF16), (BF16, F32)])
+def test_quantize_and_dequantize_in_parts(rows, group, zeros, wt, st, monkeypatch):
+    """More rows than a launch counts (here: a few): each part's pointers, of padded rows too, follow the last one's."""
+    K, pad = 640 if group < 128 else 384, 24
+    W = normal((50, K + pad), 1, wt, 0.05)[:, :K]
+    want = dp.int4_quantize(W, group, zeros=zeros, scale_dtype=st)
+    wide = [dp.int4_dequantize(*want, out_dtype=out) for out in (BF16, F32)]
+    monkeypatch.setenv("DP_FORCE_INT4_ROWS", rows)
+    got = dp.int4_quantize(W, group, zeros=zeros, scale_dtype=st)
+    assert all(torch.equal(a, b) if zeros or i < 2 else a is None for i, (a, b) in enumerate(zip(got, want)))
+    assert torch.equal(dp.int4_quantize(W.contiguous().view(5, 10, K), group, zeros=zeros, scale_dtype=st)[0], want[0].view(5, 10, K // 2))
+    for w in wide:
+        buf = torch.full((50, K + pad), 7.0, device=DEV, dtype=w.dtype)
+        dp.int4_dequantize(*want, out=buf[:, :K])
+        assert torch.equal(buf[:, :K], w) and bool((buf[:, K:] == 7).all())
+        assert torch.equal(dp.int4_dequantize(*want, out_dtype=w.dtype), w)
+
+
 def problem(E, N, K, group, zeros, st, seed, exact):
     """Codes, scales and zero points of E experts (0: none)."""
     front = (E, N) if E else (N,)
