@@ -420,14 +420,13 @@ void by_fwd_shape(int threads, bool x_f32, F f) {
   });
 }
 
-template <typename F>
+// (pieces, threads) of the backward pass; F32: of FP32 rows or gradients, which alone take two pieces above 4096 columns
+template <bool F32, typename F>
 void by_bwd_shape(const Shape& s, F f) {
-  if (s.threads == 256)
-    f(std::integral_constant<int, 2>(), std::integral_constant<int, 256>());
-  else if (s.pieces == 2)
-    f(std::integral_constant<int, 2>(), std::integral_constant<int, 512>());
-  else
-    f(std::integral_constant<int, 4>(), std::integral_constant<int, 512>());
+  if (s.threads == 256) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 256>());
+  if constexpr (F32)
+    if (s.pieces == 2) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 512>());
+  f(std::integral_constant<int, 4>(), std::integral_constant<int, 512>());
 }
 
 dp_status check_vector(const void* p) { return is_aligned16(p) ? DP_OK : DP_ERR_ALIGNMENT; }
@@ -467,8 +466,8 @@ cudaError_t set_attributes_layer_norm() {
     s.pieces = i / 4 == 2 ? 4 : 2, s.threads = i / 4 == 0 ? 256 : 512;
     by_bool(i & 1, [&](auto xf) {
       by_bool(i & 2, [&](auto gf) {
-        by_bwd_shape(s, [&](auto pieces, auto threads) {
-          constexpr bool X = decltype(xf)::value, G = decltype(gf)::value;
+        constexpr bool X = decltype(xf)::value, G = decltype(gf)::value;
+        by_bwd_shape<X || G>(s, [&](auto pieces, auto threads) {
           set(reinterpret_cast<const void*>(&norm_bwd_kernel<X, G, decltype(pieces)::value, decltype(threads)::value>));
         });
       });
@@ -565,8 +564,8 @@ extern "C" dp_status dp_layer_norm_bwd(const void* dy, int64_t ldg, int dy_f32, 
   const unsigned grid = static_cast<unsigned>(s.blocks);
   by_bool(x_f32, [&](auto xf) {
     by_bool(dy_f32, [&](auto gf) {
-      by_bwd_shape(s, [&](auto pieces, auto threads) {
-        constexpr bool X = decltype(xf)::value, G = decltype(gf)::value;
+      constexpr bool X = decltype(xf)::value, G = decltype(gf)::value;
+      by_bwd_shape<X || G>(s, [&](auto pieces, auto threads) {
         constexpr int CH = decltype(pieces)::value, N = decltype(threads)::value;
         norm_bwd_kernel<X, G, CH, N><<<grid, s.block, s.smem, str>>>(a);
       });
