@@ -42,7 +42,7 @@ struct SortArgs {
   int32_t P, E;
   int32_t per_block, per_warp;  // pairs, multiples of 32
   int32_t bits;                 // of the keys 0 .. E
-  int32_t* counts;              // [blocks][E + 1], more than one block
+  int32_t* counts;              // [blocks][E + 1], of two launches
   int32_t* offsets;
   int32_t* row_of;
   int32_t* order;
@@ -119,13 +119,9 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const __grid_constant_
         warp_counts[w * n + e] = own;
         own += c;
       }
-      total = own;
-      if (gridDim.x > 1) {
-        total = 0;
-        for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-          if (b == static_cast<int>(blockIdx.x)) before = total;
-          total += a.counts[static_cast<int64_t>(b) * n + e];
-        }
+      for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+        if (b == static_cast<int>(blockIdx.x)) before = total;
+        total += a.counts[static_cast<int64_t>(b) * n + e];
       }
     }
     int32_t incl = total;
@@ -270,7 +266,7 @@ __global__ void __launch_bounds__(1024) sort_cluster_kernel(const __grid_constan
 
 struct SortShape {
   int ranks;  // of the cluster that sorts alone (0: two launches)
-  int warps, blocks;
+  int warps, blocks;  // (of the two)
   int32_t per_warp, per_block;
   size_t smem;
 };
@@ -287,7 +283,6 @@ SortShape sort_shape(int64_t P, int64_t E) {
     s.warps = all <= 16 ? 8 : 32;
     s.per_warp = static_cast<int32_t>((all + s.ranks * s.warps - 1) / (s.ranks * s.warps) * 32);
     s.per_block = s.per_warp * s.warps;
-    s.blocks = 1;  // (no workspace)
     s.smem = (static_cast<size_t>(s.warps) * ((E + 1) | 1) + 2 * (E + 1)) * 4;
     return s;
   }
@@ -483,7 +478,7 @@ extern "C" dp_status dp_expert_sort_workspace_size(int64_t pairs, int64_t E, siz
   if (bytes == nullptr || pairs < 0 || E < 1) return DP_ERR_INVALID_ARG;
   if (E > kMaxExpertCount || pairs > kMaxPairs) return DP_ERR_UNSUPPORTED;
   const SortShape s = sort_shape(pairs, E);
-  *bytes = s.blocks > 1 ? static_cast<size_t>(s.blocks) * (E + 1) * 4 : 0;
+  *bytes = static_cast<size_t>(s.blocks) * (E + 1) * 4;  // (0 for a cluster)
   return DP_OK;
 }
 
@@ -499,7 +494,7 @@ extern "C" dp_status dp_expert_sort(const void* choice, int choice_bits, int64_t
         reinterpret_cast<uintptr_t>(workspace)) & 3) != 0)
     return DP_ERR_ALIGNMENT;
   const SortShape s = sort_shape(pairs, E);
-  if (s.blocks > 1 && (workspace == nullptr || workspace_bytes < static_cast<size_t>(s.blocks) * (E + 1) * 4))
+  if (s.ranks == 0 && (workspace == nullptr || workspace_bytes < static_cast<size_t>(s.blocks) * (E + 1) * 4))
     return DP_ERR_WORKSPACE;
   DeviceContext ctx;
   const dp_status st = device_context(&ctx);
@@ -526,10 +521,8 @@ extern "C" dp_status dp_expert_sort(const void* choice, int choice_bits, int64_t
     cudaGetLastError();
     return DP_ERR_LAUNCH;
   }
-  if (s.blocks > 1) {
-    const dp_status counted = launch_dependent(sort_count_kernel, s.blocks, s.warps * 32, s.smem, stream, a);
-    if (counted != DP_OK) return counted;
-  }
+  const dp_status counted = launch_dependent(sort_count_kernel, s.blocks, s.warps * 32, s.smem, stream, a);
+  if (counted != DP_OK) return counted;
   return launch_dependent(sort_place_kernel, s.blocks, s.warps * 32, s.smem, stream, a);
 }
 
