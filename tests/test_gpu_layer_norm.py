@@ -312,3 +312,20 @@ def test_parameter_gradients_without_a_weight(T, C, xt, gt):
     assert got[1] is None and got[2] is None and torch.equal(got[0], dp.layer_norm_bwd(dy, x, mean, rstd, w)[0])
     empty = dp.layer_norm_bwd(dy[:0], x[:0], mean[:0], rstd[:0], param_grads=True)
     assert empty[0].shape == (0, C) and not empty[1].any() and not empty[2].any()
+
+
+@pytest.mark.parametrize("T,C,block,tpr", [(16384, 4096, 256, 256), (20001, 2304, 160, 160), (30000, 1024, 256, 64), (60000, 72, 256, 8)])
+def test_parameter_gradients_at_the_blocks_own_bound(T, C, block, tpr):
+    """BF16 rows of two pieces of eight columns a thread: `block` threads, tpr for a row, 512 threads an SM.  Each group of tpr adds
+    n = T / groups rows one after the other (a fused step each), a block its groups, the second launch the blocks in 32 runs of
+    `per` and the runs in 5 steps; h itself has 2 roundings, and one is left for the products of these: n + groups a block + per + 8."""
+    x, dy = rows(T, C, BF16, 1, shift=0.5), rows(T, C, BF16, 2)
+    w = rows(1, C, F32, 3)[0]
+    _, mean, rstd = dp.layer_norm_fwd(x, w, w)
+    _, dw, db = dp.layer_norm_bwd(dy, x, mean, rstd, w)
+    at_a_time = block // tpr
+    blocks = min(-(-T // at_a_time), torch.cuda.get_device_properties(0).multi_processor_count * (512 // block))
+    steps = -(-T // (blocks * at_a_time)) + at_a_time + -(-blocks // 32) + 8
+    d, h = dy.double(), (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    close(dw, (d * h).sum(0), steps * U * (d * h).abs().sum(0))
+    close(db, d.sum(0), steps * U * d.abs().sum(0))
