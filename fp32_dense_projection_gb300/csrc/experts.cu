@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const __grid_constant_
 }
 
 // The same in one launch, for pairs that one cluster can go through: the blocks read each other's
-// counts from their shared memory.  Latency: 16384 pairs over 64 experts 8 us (22 in two launches of
-// four blocks; 11 with keys that meet by the hardware's match), 64 pairs 3 us.
+// counts from their shared memory.  Latency: 16384 pairs over 64 experts 6.1 us (14.1 in two launches; 11 with keys that
+// meet by the hardware's match, in an earlier form of 8 us), 64 pairs 3 us.
 __global__ void __launch_bounds__(1024) sort_cluster_kernel(const __grid_constant__ SortArgs a) {
   extern __shared__ int32_t warp_counts[];  // [warps][E + 1], then the block's totals [E + 1] and base [E + 1]
   __shared__ int32_t scan[32];
@@ -272,7 +272,12 @@ struct SortShape {
 };
 
 constexpr int kSortBlocks = 128;
-constexpr int64_t kClusterPairs = 1 << 18;  // 32 runs a warp; from there on two launches of many blocks are as fast
+// Up to 2^18 pairs (32 runs a warp) a cluster, which needs no workspace.  One launch of a cluster / two launches, us:
+//   8 experts     32768 pairs 5.9 / 11.8, 65536 11.1 / 12.5, 131072 21.2 / 14.0, 262144 41.0 / 17.2
+//   64 experts    32768 8.1 / 14.2, 65536 15.3 / 15.0, 131072 28.1 / 16.1, 262144 52.3 / 18.5
+//   1024 experts  32768 16.0 / 24.2, 65536 24.6 / 34.6, 131072 39.8 / 53.4, 262144 69.8 / 67.9
+// so that between 2^16 and 2^18 pairs of few experts two launches would be faster, for callers who bring their workspace.
+constexpr int64_t kClusterPairs = 1 << 18;
 
 SortShape sort_shape(int64_t P, int64_t E) {
   SortShape s = {};
@@ -350,7 +355,8 @@ constexpr int kBatch = 4;  // rows of a token whose loads are in flight together
 
 // (With loads for no more rows than there are: 8192 tokens of 2 rows of 4096 in BF16 36.5 us, 38.8 with room for four;
 // 16384 of one row of 1024 16.4, 19.2.  BF16 rows, five blocks an SM: 2048 tokens of 8 rows of 4096 26.3 us, 4096 of 3 rows
-// 26.3; with six 27.6 and 25.4; with the four that 50 registers leave 28.4 and 26.  FP32 rows need their registers: 27 us, 40 with 40.)
+// 26.3; with six 27.6 and 25.4; with the four that 50 registers leave 28.4 and 26.  At five, 48 registers, the form for four BF16
+// rows spills two words, and it is the faster one all the same.  FP32 rows need their registers: 27 us, 40 with 40.)
 template <bool YF32, bool OF32, int BATCH>
 __global__ void __launch_bounds__(256, YF32 ? 4 : 5) combine_kernel(const __grid_constant__ RowArgs a) {
   const int sub = static_cast<int>(threadIdx.x) / a.tpr, lane = static_cast<int>(threadIdx.x) % a.tpr;

@@ -21,6 +21,8 @@
 //   (q - z) / 64 of two codes;
 // - the MMA's sums run over one group and meet the group's scale in FP32, so the product is as
 //   exact as with weights expanded in FP32 (sums below 2^-120 lose bits to the factor 64).
+// The threads of a CTA leave 96 registers each.  With one MMA a step nothing spills; with two (9 to 16 tokens) 44 to 144 bytes a
+// thread are loaded back (groups of 32: 144 as one team, 124 as four; of 64: 44, 56; of 128: none, 48).
 // The order of the contraction within a group is free as long as both operands agree: the four threads
 // of a row take G / 4 neighbouring codes each, in one load, and each reads pairs (i, i + 4) of a word of 8 with one mask;
 // x is laid out in shared memory in their order.

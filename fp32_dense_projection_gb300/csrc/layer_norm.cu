@@ -13,14 +13,14 @@
 // to the workspace, and a second launch adds them in block order: no atomics, the same bits every time.
 // The shape depends on C and the types alone, so that a row's result does not depend on how many there are.
 //
-// Four pieces of eight columns a thread halve the warps of a row against two (with 96 MB of x in BF16, us):
-//   forward, BF16     256 columns 34 / 45, 1024  39 / 48, 4096  46 / 55, 5120 53 / 74: always four;
-//   forward, FP32     256         26 / 28, 1024  31 / 32, 4096  36 / 36, 5120 34 / 57: four above 4096 (two leave
-//                     shorter tails of few rows: 16173 x 1024 forward and backward 57, 60 with four);
-//   backward, BF16    1024        59 / 56, 4096  60 / 57, 5120 67 / 75, 8192 67 / 66: four above 4096;
-//   backward, FP32 x  1024        47 / 38, 4096  48 / 41, 5120 55 / 49, 8192 58 / 46: two up to 8192.
-// Above 8192 columns four it is (one thread of 512 has no more than four): 16384 in BF16 75 us, 135 with 1024 threads
-// that held dw and db in shared memory.  16384 x 4096 in BF16 backward: 72.7 us, 5.5 TB/s.
+// Four pieces of eight columns a thread halve the warps of a row against two (with 96 MB of x, four / two, us):
+//   forward, BF16     256 columns 32.6 / 41.9, 1024 37.7 / 47.6, 4096 44.4 / 53.9, 5120 50.0 / 84.0, 8192 50.3 / 65.2: always four;
+//   forward, FP32     256 25.4 / 26.9, 1024 29.1 / 30.8, 4096 34.1 / 34.6, 5120 33.3 / 46.9, 8192 32.8 / 39.6: four above 4096 (two
+//                     leave shorter tails of few rows: 16173 x 1024 forward and backward 57, 60 with four);
+//   backward, BF16    1024 59.6 / 53.8, 4096 61.5 / 55.2, 5120 63.7 / 69.7, 8192 63.3 / 60.8: four above 4096;
+//   backward, FP32 x  1024 51.2 / 36.4, 4096 54.0 / 39.8, 5120 49.1 / 46.8, 8192 49.2 / 44.4: two up to 8192.
+// Above 8192 columns four it is (one thread of 512 has no more than four): 3000 rows of 16384 in BF16 backward 71.5 us (with 1024
+// threads that held dw and db in shared memory 1.8 times that).  16384 x 4096 in BF16 backward: 72.7 us, 5.5 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -7,16 +7,21 @@
 //   over the chosen:  dl_e = gate_e (dg_e - s), 0 for the others
 //   over all:         dl_e = p_e ([e chosen] dg_e - s)
 //
-// Exponentials are expf's, within 2 ulp at any distance from the largest (__expf's error grows with it: 3e-6 of a gate 80 below).
+// Exponentials are expf's, within 2 ulp at any distance from the largest (__expf's grows with it: 3.8e-6 of a gate 60 to 80
+// below, 2.9e-7 now).
 //
 // Bound: instructions (16384 tokens of 256 experts, k = 8, over all: 10.1 us and 6.4 the gradient, 2.5 of them the
 // logits' bytes); a few rows are latency.  One warp a token holds its logits in registers, so they are read
 // once.  Keys order floats as integers: -0 as +0, NaN above all.
 // 3 to 16 choices: the k-th of the lanes' largest keys is a lower bound of the k-th of all; what is above it goes
-// to shared memory in the order of indexes, and if a warp's lanes can hold it, each counts how many come before its own
-// (15.6 us with a search for each choice; of one choice 8.2 against 7.2).
+// to shared memory in the order of indexes, and if a warp's lanes can hold it, each counts how many come before its own.
 // Otherwise a choice is a warp-wide maximum and the votes for it, register by register, up to the first that has it.
-// (Whether the gradient's choices differ, each lane sees from who holds its expert: 7.2 us, 8.8 by matching lanes.)
+// By the bound / by the search, 16384 tokens, us (more choices leave more above the bound than lanes):
+//   64 experts    k = 1 4.1 / 3.7, 3 4.9 / 4.7, 8 6.8 / 7.0, 16 10.0 / 10.9, 20 12.2 / 12.8, 24 17.0 / 14.8
+//   256 experts   k = 1 7.3 / 6.1, 3 8.1 / 8.2, 8 10.1 / 13.5, 16 13.9 / 21.8, 20 22.5 / 26.0, 24 35.1 / 30.1
+//   1024 experts  k = 1 21.3 / 17.7, 3 22.4 / 26.5, 8 24.6 / 46.8, 16 38.0 / 77.7, 20 110 / 93
+// (Whether the gradient's choices differ, each lane sees from who holds its expert: 7.2 us, 8.8 by matching lanes, both before
+// closed experts lost their selections.)
 #include <cuda_runtime.h>
 
 #include <cstdint>
